@@ -16,3 +16,12 @@ from .binding import (  # noqa: F401
     CONV_IM2COL, CONV_IMPLICIT, CONV_IMPLICIT_NHWC, conv2d, conv2d_algorithm, conv2d_workspace, conv_params,
     variant_name,
 )
+
+
+def __getattr__(name):
+    # the layers import torch, which the host-only uses of this package do not need
+    if name in ("gated", "gated_backward", "layer_norm", "layer_norm_backward", "linear", "linear_backward"):
+        from . import layers
+        globals()[name] = getattr(layers, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -35,6 +35,7 @@ GEMM_ERR_RUNTIME = -6
 GEMM_ERR_INVALID_LAYOUT = -7
 GEMM_ERR_WORKSPACE = -8
 GEMM_ERR_SCRATCH_LIMIT = -9
+GEMM_ERR_INVALID_ACTIVATION = -10
 GEMM_OP_N, GEMM_OP_T = 0, 1
 
 AUTO = -1
@@ -55,6 +56,13 @@ EXPORTS = ("gemm_f32", "gemm_f16_f32acc", "gemm_bf16_f32acc",
            "gemm_f32_ex", "gemm_f16_f32acc_ex", "gemm_bf16_f32acc_ex",
            "gemm_conv2d_workspace", "gemm_conv2d_algorithm", "gemm_conv2d_f32", "gemm_conv2d_f16_f32acc", "gemm_conv2d_bf16_f32acc",
            "gemm_conv2d_f16_f32acc_noalloc",
+           "gemm_linear_workspace", "gemm_linear_f16", "gemm_linear_bf16",
+           "gemm_linear_backward_workspace", "gemm_linear_backward_f16", "gemm_linear_backward_bf16",
+           "gemm_gated_workspace", "gemm_gated_f16", "gemm_gated_bf16",
+           "gemm_gated_backward_workspace", "gemm_gated_backward_f16", "gemm_gated_backward_bf16",
+           "gemm_layer_norm_f32", "gemm_layer_norm_f16", "gemm_layer_norm_bf16",
+           "gemm_layer_norm_backward_workspace", "gemm_layer_norm_backward_f32",
+           "gemm_layer_norm_backward_f16", "gemm_layer_norm_backward_bf16",
            "gemm_status_string", "gemm_variant_name")
 
 # Entry-point name stem per input format.
@@ -88,6 +96,48 @@ class ConvParams(ctypes.Structure):
 
 
 _CONV_STEM = {"f32": "gemm_conv2d_f32", "f16": "gemm_conv2d_f16_f32acc", "bf16": "gemm_conv2d_bf16_f32acc"}
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # gemm_activation
+
+
+class LinearParams(ctypes.Structure):
+    """gemm_linear_params of include/gemm.h."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "M", "N", "K", "op_w", "ldx", "ldw", "ldy", "ldr", "ldp", "activation", "y_f32")]
+
+
+class LinearBackwardParams(ctypes.Structure):
+    """gemm_linear_backward_params."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "M", "N", "K", "op_w", "lddy", "ldx", "ldw", "ldp", "lddx", "lddw", "activation")]
+
+
+class GatedParams(ctypes.Structure):
+    """gemm_gated_params."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "M", "F", "K", "op_w", "ldx", "ldw", "ldh", "ldp", "activation")]
+
+
+class GatedBackwardParams(ctypes.Structure):
+    """gemm_gated_backward_params."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "M", "F", "K", "op_w", "lddh", "ldx", "ldw", "ldp", "lddx", "lddw", "activation")]
+
+
+class LayerNormParams(ctypes.Structure):
+    """gemm_layer_norm_params."""
+    _fields_ = [(n, ctypes.c_int) for n in ("M", "N", "ldx", "ldy", "lddx", "weight_f32")] + [("eps", ctypes.c_float)]
+
+
+# Parameter struct, pointer arguments (workspace apart), workspace or not, and
+# element formats of the layer entry points.
+_LAYERS = {"gemm_linear": (LinearParams, 6, True, ("f16", "bf16")),
+           "gemm_linear_backward": (LinearBackwardParams, 7, True, ("f16", "bf16")),
+           "gemm_gated": (GatedParams, 6, True, ("f16", "bf16")),
+           "gemm_gated_backward": (GatedBackwardParams, 9, True, ("f16", "bf16")),
+           "gemm_layer_norm": (LayerNormParams, 6, False, ("f32", "f16", "bf16")),
+           "gemm_layer_norm_backward": (LayerNormParams, 8, True, ("f32", "f16", "bf16"))}
 
 
 class Plan(ctypes.Structure):
@@ -149,6 +199,15 @@ def _configure(path: str):
         f.restype = i
     lib.gemm_conv2d_f16_f32acc_noalloc.argtypes = [ctypes.POINTER(ConvParams), p, p, p, p]
     lib.gemm_conv2d_f16_f32acc_noalloc.restype = i
+    for stem, (params, pointers, workspace, kinds) in _LAYERS.items():
+        for kind in kinds:
+            f = getattr(lib, f"{stem}_{kind}")
+            f.argtypes = [ctypes.POINTER(params)] + [p] * pointers + ([p, ctypes.c_size_t] if workspace else []) + [p]
+            f.restype = i
+        if workspace:
+            f = getattr(lib, stem + "_workspace")
+            f.argtypes = [ctypes.POINTER(params), ctypes.POINTER(ctypes.c_size_t)]
+            f.restype = i
     lib.gemm_status_string.argtypes = [i]
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_variant_name.argtypes = [i]
@@ -402,6 +461,24 @@ def gemm_e5m2_f32acc_variant(variant, A, B, C=None, stream=None):
 
 def gemm_i8_i32acc_variant(variant, A, B, C=None, stream=None):
     return _call("i8", int(variant), A, B, C, stream)
+
+
+# ------------------------------------------------------------------ layers --
+
+def layer_workspace(stem: str, params) -> int:
+    """Workspace bytes of a layer entry point (``gemm_linear``, ...) with these
+    parameters (host arithmetic; raises on bad ones)."""
+    out = ctypes.c_size_t()
+    rc = getattr(load(), stem + "_workspace")(ctypes.byref(params), ctypes.byref(out))
+    if rc != GEMM_OK:
+        raise GemmError(rc, stem + "_workspace")
+    return int(out.value)
+
+
+def raw_layer(stem: str, kind, params, *args) -> int:
+    """A layer entry point with plain integers (device pointers in the order
+    of include/gemm.h, workspace, its size, stream); returns the status code."""
+    return int(getattr(load(), f"{stem}_{kind_of(kind)}")(ctypes.byref(params), *args))
 
 
 # ------------------------------------------------------------- convolution --

@@ -1,0 +1,150 @@
+// The element-wise part of the dense layers' backward passes: the gradient
+// of the pre-activations, rounded to the 16-bit format that the matrix
+// cores take, and the bias gradient's column sums of the unrounded values.
+//
+// Bound by memory: each value is read and written once.  A workgroup covers
+// kGradRows rows x 256 columns, 32 lanes of eight columns times 8 rows at a
+// time, so a row's accesses are 512 contiguous bytes and the column sums of a
+// workgroup need one pass through LDS.  The sums go out per row block and are
+// added in block order by a second kernel, so they do not depend on which
+// workgroup finished first.
+#include "linear.h"
+
+namespace dgor {
+namespace {
+
+constexpr int kCols = 256;
+
+template <class Fmt>
+__global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint16_t *__restrict__ dy, int lddy,
+                                                       const uint16_t *__restrict__ z, int ldz,
+                                                       uint16_t *__restrict__ dz, int lddz, int act,
+                                                       float *__restrict__ sums)
+{
+    __shared__ float part[8][kCols + 8];
+    const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
+    const int strips = (N + kCols - 1) / kCols, strip = blockIdx.x % strips, block = blockIdx.x / strips;
+    const int col = strip * kCols + 8 * lane, n = N - col;
+    const int row0 = block * kGradRows;
+    float total[8] = {};
+    if (n > 0) {
+#pragma unroll 4
+        for (int i = 0; i < kGradRows / 8; ++i) {
+            const int row = row0 + 8 * i + r8;
+            if (row >= M)
+                continue;
+            float d[8];
+            unpack8<Fmt>(load8_16(dy + (size_t)row * lddy + col, n), d);
+            if (z) {
+                float x[8];
+                unpack8<Fmt>(load8_16(z + (size_t)row * ldz + col, n), x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float value, slope;
+                    activate_slope(act, x[e], value, slope);
+                    d[e] *= slope;
+                }
+            }
+            if (dz)
+                store8_16(dz + (size_t)row * lddz + col, n, pack8<Fmt>(d));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                total[e] += d[e];
+        }
+    }
+    if (!sums)
+        return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        part[r8][8 * lane + e] = total[e];
+    __syncthreads();
+    const int c = strip * kCols + threadIdx.x;
+    if (c < N) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            s += part[r][threadIdx.x];
+        sums[(size_t)block * N + c] = s;
+    }
+}
+
+template <class Fmt>
+__global__ __launch_bounds__(256) void sum_blocks_kernel(int blocks, int N, const float *__restrict__ sums,
+                                                         uint16_t *__restrict__ out)
+{
+    // 64 columns x 4 threads over the blocks
+    __shared__ float part[4][64];
+    const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+    float s = 0.f;
+    if (c < N)
+        for (int b = w; b < blocks; b += 4)
+            s += sums[(size_t)b * N + c];
+    part[w][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (w == 0 && c < N)
+        out[c] = Fmt::down((part[0][threadIdx.x] + part[1][threadIdx.x]) +
+                           (part[2][threadIdx.x] + part[3][threadIdx.x]));
+}
+
+template <class Fmt>
+__global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint16_t *__restrict__ dh, int lddh,
+                                                        const uint16_t *__restrict__ g,
+                                                        const uint16_t *__restrict__ u, int ldp,
+                                                        uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int ldd,
+                                                        int act)
+{
+    const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
+    const int strips = (F + kCols - 1) / kCols;
+    const int col = (blockIdx.x % strips) * kCols + 8 * lane, n = F - col;
+    if (n <= 0)
+        return;
+    const int row0 = (blockIdx.x / strips) * kGradRows;
+#pragma unroll 2
+    for (int i = 0; i < kGradRows / 8; ++i) {
+        const int row = row0 + 8 * i + r8;
+        if (row >= M)
+            return;
+        float d[8], x[8], y[8], a[8], b[8];
+        unpack8<Fmt>(load8_16(dh + (size_t)row * lddh + col, n), d);
+        unpack8<Fmt>(load8_16(g + (size_t)row * ldp + col, n), x);
+        unpack8<Fmt>(load8_16(u + (size_t)row * ldp + col, n), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float value, slope;
+            activate_slope(act, x[e], value, slope);
+            a[e] = d[e] * y[e] * slope;
+            b[e] = d[e] * value;
+        }
+        store8_16(dg + (size_t)row * ldd + col, n, pack8<Fmt>(a));
+        store8_16(du + (size_t)row * ldd + col, n, pack8<Fmt>(b));
+    }
+}
+
+}  // namespace
+
+hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
+                           int lddz, int act, float *sums, bool bf16, hipStream_t s)
+{
+    const dim3 grid((unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + kGradRows - 1) / kGradRows));
+    hipLaunchKernelGGL((bf16 ? act_grad_kernel<Brain16> : act_grad_kernel<Half16>), grid, dim3(256), 0, s, M, N, dy,
+                       lddy, z, ldz, dz, lddz, act, sums);
+    return hipGetLastError();
+}
+
+hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out, bool bf16, hipStream_t s)
+{
+    hipLaunchKernelGGL((bf16 ? sum_blocks_kernel<Brain16> : sum_blocks_kernel<Half16>), dim3((N + 63) / 64),
+                       dim3(256), 0, s, blocks, N, sums, out);
+    return hipGetLastError();
+}
+
+hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u, int ldp,
+                            uint16_t *dg, uint16_t *du, int ldd, int act, bool bf16, hipStream_t s)
+{
+    const dim3 grid((unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + kGradRows - 1) / kGradRows));
+    hipLaunchKernelGGL((bf16 ? gate_grad_kernel<Brain16> : gate_grad_kernel<Half16>), grid, dim3(256), 0, s, M, F, dh,
+                       lddh, g, u, ldp, dg, du, ldd, act);
+    return hipGetLastError();
+}
+
+}  // namespace dgor

@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "linear.h"
 
 namespace {
 
@@ -46,6 +47,12 @@ int check_device()
         g_dev_state[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
     return ok ? GEMM_OK : GEMM_ERR_UNSUPPORTED_DEVICE;
 }
+
+}  // namespace
+
+int dgor::device_status() { return check_device(); }
+
+namespace {
 
 void clear(gemm_plan *p)
 {
@@ -895,6 +902,7 @@ const char *gemm_status_string(int status)
     case GEMM_ERR_RUNTIME: return "HIP runtime query failed";
     case GEMM_ERR_INVALID_LAYOUT: return "invalid operand layout (op flag or leading dimension)";
     case GEMM_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case GEMM_ERR_INVALID_ACTIVATION: return "unknown activation";
     case GEMM_ERR_SCRATCH_LIMIT: return "needs more scratch than the no-allocation entry point's fixed array (16 MiB)";
     default: return "unknown status";
     }

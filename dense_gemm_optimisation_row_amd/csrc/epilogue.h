@@ -1,0 +1,249 @@
+// What the dense-layer kernels do with a finished sum: bias, saved
+// pre-activation, activation (or the gate's product), residual and the
+// rounding to the output type.  Internal header.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm.h"
+
+namespace dgor {
+
+// The 16-bit input formats: conversion to and from binary32.
+struct Half16 {
+    static __device__ __forceinline__ float up(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
+    static __device__ __forceinline__ uint16_t down(float f)
+    {
+        return __builtin_bit_cast(uint16_t, (_Float16)f);   // round to nearest even, overflow to infinity
+    }
+};
+struct Brain16 {
+    static __device__ __forceinline__ float up(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+    static __device__ __forceinline__ uint16_t down(float f)
+    {
+        return __builtin_bit_cast(uint16_t, (__bf16)f);     // round to nearest even
+    }
+};
+
+// Vectors at their element's alignment: global memory takes 16-byte accesses
+// at any element address, so rows of any length move eight elements at a time.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
+
+// Eight (or the first n) elements of a 16-bit array, the rest zero.
+__device__ __forceinline__ u32x4 load8_16(const uint16_t *p, int n)
+{
+    if (n >= 8)
+        return *reinterpret_cast<const u32x4_at2 *>(p);
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    return v;
+}
+__device__ __forceinline__ void store8_16(uint16_t *p, int n, u32x4 v)
+{
+    if (n >= 8) {
+        *reinterpret_cast<u32x4_at2 *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+}
+template <class Fmt>
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = Fmt::up((uint16_t)(v[e >> 1] >> (16 * (e & 1))));
+}
+template <class Fmt>
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8])
+{
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = (uint32_t)Fmt::down(f[2 * e]) | ((uint32_t)Fmt::down(f[2 * e + 1]) << 16);
+    return v;
+}
+__device__ __forceinline__ void load8_f32(const float *p, int n, float (&f)[8])
+{
+    if (n >= 8) {
+        const f32x4 a = *reinterpret_cast<const f32x4_at4 *>(p), b = *reinterpret_cast<const f32x4_at4 *>(p + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[e] = a[e];
+            f[4 + e] = b[e];
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = e < n ? p[e] : 0.f;
+}
+__device__ __forceinline__ void store8_f32(float *p, int n, const float (&f)[8])
+{
+    if (n >= 8) {
+        *reinterpret_cast<f32x4_at4 *>(p) = f32x4{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4_at4 *>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            p[e] = f[e];
+}
+
+// ---- activations, in binary32.  exp is the hardware's base-2 exponential
+// (one unit in the last place; the scaled argument adds |z| 2^-24 relative);
+// the logistic function's quotient the hardware reciprocal.  A large
+// negative z gives exp = infinity and a quotient of exactly zero.
+__device__ __forceinline__ float act_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.f + act_exp(-x)); }
+
+// z held to [-m, m]; a NaN stays one.  The slopes saturate long before m, and
+// stay finite at the largest finite z.
+__device__ __forceinline__ float held(float z, float m) { return z > m ? m : (z < -m ? -m : z); }
+
+// The normal distribution function and e^(-z^2/2).  The tail is
+// erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) e^(-x^2), t = 1 / (1 + p x),
+// from Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26
+// (absolute error at most 1.5e-7), at x = |z| / sqrt(2).
+__device__ __forceinline__ float normal_cdf(float z, float &bell)
+{
+    const float x = fabsf(z) * 0.70710678118654752440f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.f));
+    bell = act_exp(-x * x);
+    const float poly =
+        t * __builtin_fmaf(t, __builtin_fmaf(t, __builtin_fmaf(t, __builtin_fmaf(t, 1.061405429f, -1.453152027f),
+                                                               1.421413741f), -0.284496736f), 0.254829592f);
+    const float tail = 0.5f * poly * bell;
+    return z > 0.f ? 1.f - tail : tail;
+}
+
+constexpr float kTanhScale = 1.59576912160573071176f;   // 2 sqrt(2 / pi)
+constexpr float kTanhCubic = 0.044715f;
+
+__device__ __forceinline__ float activate(int act, float z)
+{
+    switch (act) {
+    case GEMM_ACT_RELU: return z <= 0.f ? 0.f : z;
+    case GEMM_ACT_GELU: {
+        float bell;
+        return z * normal_cdf(z, bell);
+    }
+    case GEMM_ACT_GELU_TANH: {   // z (1 + tanh(y)) / 2 = z logistic(2 y)
+        const float c = held(z, 64.f);
+        return z * logistic(kTanhScale * c * __builtin_fmaf(kTanhCubic * c, c, 1.f));
+    }
+    case GEMM_ACT_SILU: return z * logistic(z);
+    default: return z;
+    }
+}
+
+// The activation's value and slope.
+__device__ __forceinline__ void activate_slope(int act, float z, float &value, float &slope)
+{
+    switch (act) {
+    case GEMM_ACT_RELU:
+        value = z <= 0.f ? 0.f : z;
+        slope = z <= 0.f ? 0.f : 1.f;
+        return;
+    case GEMM_ACT_GELU: {
+        float bell;
+        const float c = held(z, 64.f), p = normal_cdf(c, bell);
+        value = z * p;
+        slope = __builtin_fmaf(c * 0.39894228040143267794f, bell, p);
+        return;
+    }
+    case GEMM_ACT_GELU_TANH: {
+        const float c = held(z, 64.f), s = logistic(kTanhScale * c * __builtin_fmaf(kTanhCubic * c, c, 1.f));
+        value = z * s;
+        slope = __builtin_fmaf(c * s * (1.f - s) * kTanhScale, __builtin_fmaf(3.f * kTanhCubic * c, c, 1.f), s);
+        return;
+    }
+    case GEMM_ACT_SILU: {
+        const float c = held(z, 128.f), s = logistic(c);
+        value = z * s;
+        slope = s * __builtin_fmaf(c, 1.f - s, 1.f);
+        return;
+    }
+    default:
+        value = z;
+        slope = 1.f;
+    }
+}
+
+// Where a finished tile goes.  Y is M x N in FP32 (y_f32) or the input
+// format; the rest may be null.  Gated products have two sums an element and
+// two saved pre-activations.
+struct Epilogue {
+    void *Y;
+    const uint16_t *bias;
+    const void *R;         // residual, in Y's format
+    uint16_t *pre, *pre2;
+    int ldy, ldr, ldp;
+    int act, y_f32;
+};
+
+// Eight neighbouring outputs (n of them inside the matrix): v the sums, u
+// the up projection's (gated only).  The residual is read by the lane that
+// writes the same elements of Y, so Y may be the residual itself.
+template <class Fmt, bool GATED>
+__device__ __forceinline__ void emit8(const Epilogue &e, int row, int col, int n, float (&v)[8], const float (&u)[8])
+{
+    if (!GATED && e.bias) {
+        float b[8];
+        unpack8<Fmt>(load8_16(e.bias + col, n), b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += b[i];
+    }
+    if (e.pre) {
+        store8_16(e.pre + (size_t)row * e.ldp + col, n, pack8<Fmt>(v));
+        if (GATED)
+            store8_16(e.pre2 + (size_t)row * e.ldp + col, n, pack8<Fmt>(u));
+    }
+    // one uniform branch on the activation, not one an element
+    switch (e.act) {
+#define DGOR_ACT_CASE(A)                          \
+    case A:                                       \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = activate(A, v[i]); \
+        break;
+        DGOR_ACT_CASE(GEMM_ACT_RELU)
+        DGOR_ACT_CASE(GEMM_ACT_GELU)
+        DGOR_ACT_CASE(GEMM_ACT_GELU_TANH)
+        DGOR_ACT_CASE(GEMM_ACT_SILU)
+#undef DGOR_ACT_CASE
+    default: break;
+    }
+    if (GATED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] *= u[i];
+    }
+    const size_t at = (size_t)row * e.ldy + col;
+    if (!GATED && e.R) {
+        float r[8];
+        const size_t ra = (size_t)row * e.ldr + col;
+        if (e.y_f32)
+            load8_f32((const float *)e.R + ra, n, r);
+        else
+            unpack8<Fmt>(load8_16((const uint16_t *)e.R + ra, n), r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += r[i];
+    }
+    if (!GATED && e.y_f32)
+        store8_f32((float *)e.Y + at, n, v);
+    else
+        store8_16((uint16_t *)e.Y + at, n, pack8<Fmt>(v));
+}
+
+}  // namespace dgor

@@ -1,0 +1,59 @@
+// Launches of the dense-layer, gated and layer-norm kernels, between the C
+// entry points (linear.hip, norm.hip) and the kernel files.  Internal header.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "epilogue.h"
+
+namespace dgor {
+
+// One product Y = epilogue(op(A) op(B)) of 16-bit operands, op(A) M x K and
+// op(B) K x N.  A is M x K (lda >= K) or, with trans_a, K x M; B is K x N or,
+// with trans_b, N x K.
+//   gated:  two products of one A, with B[0] and B[1]; the epilogue gets both
+//           sums of an element.
+//   nseg 2: the sum runs over two pairs, A[0] B[0] + A[1] B[1].
+//   nbatch 2: two products A[i] B[i] into e.Y and Y1 in one launch.
+// At most one of the three.
+// Split over k (splits > 1): split s covers stages [s chunk, (s + 1) chunk)
+// of 64 k each (counted over both segments) and writes its FP32 sums to
+// part: ((batch or gate/up) * splits + s) * M * N; launch_join adds them in
+// that order and applies the epilogue.
+struct Product {
+    int M, N, K;
+    const uint16_t *A[2];
+    const uint16_t *B[2];
+    int lda, ldb;
+    bool bf16, trans_a, trans_b, gated;
+    int nseg, nbatch;
+    Epilogue e;
+    void *Y1;
+    int splits, chunk;
+    float *part;
+    int tiles_m, tiles_n, group_m;   // filled by the launcher
+};
+
+constexpr int kStageDepth = 64;   // k per stage, the unit of Product::chunk
+inline int product_stages(const Product &p) { return p.nseg * ((p.K + kStageDepth - 1) / kStageDepth); }
+
+hipError_t launch_tile(const Product &p, int tile, hipStream_t stream);
+hipError_t launch_join(const Product &p, hipStream_t stream);
+
+// dZ = dY act'(Z) (Z null: dZ = dY, nothing written unless dz) and, with
+// sums, each row block's column sums of the unrounded dZ in FP32 to
+// sums[block][N], blocks of kGradRows rows.
+constexpr int kGradRows = 64;
+hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
+                           int lddz, int act, float *sums, bool bf16, hipStream_t stream);
+// out[c] = sum over blocks of sums[block][c], in the input format.
+hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out, bool bf16, hipStream_t stream);
+// dG = dH U act'(G), dU = dH act(G).
+hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u,
+                            int ldp, uint16_t *dg, uint16_t *du, int ldd, int act, bool bf16, hipStream_t stream);
+
+// Device check of the C entry points (api.hip): GEMM_OK on gfx950.
+int device_status();
+
+}  // namespace dgor

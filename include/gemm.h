@@ -51,7 +51,8 @@ typedef enum {
     GEMM_ERR_RUNTIME = -6,
     GEMM_ERR_INVALID_LAYOUT = -7,
     GEMM_ERR_WORKSPACE = -8,
-    GEMM_ERR_SCRATCH_LIMIT = -9
+    GEMM_ERR_SCRATCH_LIMIT = -9,
+    GEMM_ERR_INVALID_ACTIVATION = -10
 } gemm_status;
 
 /*
@@ -332,6 +333,152 @@ int gemm_conv2d_bf16_f32acc(const gemm_conv2d_params *params, const uint16_t *x,
  * threads without ordering -- race on it. */
 int gemm_conv2d_f16_f32acc_noalloc(const gemm_conv2d_params *params, const uint16_t *x, const uint16_t *w,
                                    float *y, void *stream);
+
+/*
+ * The products of a transformer's feed-forward sublayer, with what surrounds
+ * them done while the sums are still on the chip: the dense layer with bias,
+ * activation and residual, the gated up-projection, and layer norm, each with
+ * its backward pass.  16-bit operands (binary16 or bfloat16 patterns), exact
+ * products, FP32 sums; a result is rounded once, to nearest even, where it
+ * is written.
+ *
+ * Conventions beyond those above:
+ *   - Matrices are row-major with the given row strides (ld..., in elements,
+ *     at least the row length); any element alignment, row length and stride
+ *     is taken.  16-byte aligned operands whose strides and row lengths are
+ *     multiples of 8 take the faster kernels.
+ *   - W holds K inputs x N outputs: stored K x N (op_w GEMM_OP_N) or N x K
+ *     (GEMM_OP_T); weight gradients come in the storage of their weight.
+ *   - Outputs must not overlap inputs or each other, except that Y may be the
+ *     residual itself (same pointer, same stride).
+ *   - The workspace (device memory, 256-byte aligned, any contents, at least
+ *     the size that the _workspace function of the same parameters reports;
+ *     NULL where that is 0) must not be used by anything else until the
+ *     call's work completes.
+ *   - Results do not depend on timing: sums are added in a fixed order.
+ *   - Errors: NULL params or a NULL required pointer of nonzero extent ->
+ *     GEMM_ERR_NULL_PTR; a negative size, or a matrix of more than 2^22
+ *     blocks of 128 x 64 -> GEMM_ERR_INVALID_DIM; an op flag or stride outside its range
+ *     -> GEMM_ERR_INVALID_LAYOUT; an unknown activation ->
+ *     GEMM_ERR_INVALID_ACTIVATION; a workspace that is missing, misaligned or
+ *     too small -> GEMM_ERR_WORKSPACE; otherwise as gemm_f32.  A size of zero
+ *     writes what an empty sum gives: nothing, or zeros.
+ */
+typedef enum {
+    GEMM_ACT_NONE = 0,       /* z */
+    GEMM_ACT_RELU = 1,       /* max(z, 0) */
+    GEMM_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution function */
+    GEMM_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    GEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} gemm_activation;
+
+/* Dense layer: Z = X W + bias, Y = act(Z) + R.  X is M x K, W K x N, Y and R
+ * M x N; bias (N), R and pre may be NULL.  Y and R are FP32 (y_f32 nonzero)
+ * or in X's format; pre, when given, receives Z in X's format, which the
+ * backward pass takes.  ldr and ldp are read only with R and pre. */
+typedef struct {
+    int M, N, K;
+    int op_w;
+    int ldx, ldw, ldy, ldr, ldp;
+    int activation;
+    int y_f32;
+} gemm_linear_params;
+int gemm_linear_workspace(const gemm_linear_params *params, size_t *bytes);
+int gemm_linear_f16(const gemm_linear_params *params, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
+                    const void *R, void *Y, uint16_t *pre, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_linear_bf16(const gemm_linear_params *params, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
+                     const void *R, void *Y, uint16_t *pre, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Its backward pass: dZ = dY act'(Z), dX = dZ W^T, dW = X^T dZ, dbias = the
+ * column sums of dZ (R's gradient is dY itself).  Each of dX, dW and dbias
+ * may be NULL: it is then not computed.  pre is the forward pass's Z (not
+ * read without an activation).  dZ is rounded to the input format for the
+ * two products, not for dbias.  W is read for dX only, X for dW only. */
+typedef struct {
+    int M, N, K;
+    int op_w;
+    int lddy, ldx, ldw, ldp, lddx, lddw;
+    int activation;
+} gemm_linear_backward_params;
+int gemm_linear_backward_workspace(const gemm_linear_backward_params *params, size_t *bytes);
+int gemm_linear_backward_f16(const gemm_linear_backward_params *params, const uint16_t *dY, const uint16_t *X,
+                             const uint16_t *W, const uint16_t *pre, uint16_t *dX, uint16_t *dW, uint16_t *dbias,
+                             void *workspace, size_t workspace_bytes, void *stream);
+int gemm_linear_backward_bf16(const gemm_linear_backward_params *params, const uint16_t *dY, const uint16_t *X,
+                              const uint16_t *W, const uint16_t *pre, uint16_t *dX, uint16_t *dW, uint16_t *dbias,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gated up-projection: G = X Wg, U = X Wu, H = act(G) U, both products and
+ * what follows them in one kernel.  X is M x K, Wg and Wu K x F (both in the
+ * storage op_w names, with one stride ldw: the halves of one K x 2F matrix
+ * will do), H M x F.  G and U (both or neither) receive the two products in
+ * X's format, with the stride ldp, for the backward pass. */
+typedef struct {
+    int M, F, K;
+    int op_w;
+    int ldx, ldw, ldh, ldp;
+    int activation;
+} gemm_gated_params;
+int gemm_gated_workspace(const gemm_gated_params *params, size_t *bytes);
+int gemm_gated_f16(const gemm_gated_params *params, const uint16_t *X, const uint16_t *Wg, const uint16_t *Wu,
+                   uint16_t *H, uint16_t *G, uint16_t *U, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_gated_bf16(const gemm_gated_params *params, const uint16_t *X, const uint16_t *Wg, const uint16_t *Wu,
+                    uint16_t *H, uint16_t *G, uint16_t *U, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Its backward pass: dG = dH U act'(G), dU = dH act(G), dX = dG Wg^T + dU
+ * Wu^T, dWg = X^T dG, dWu = X^T dU.  dX may be NULL, and dWg and dWu both. */
+typedef struct {
+    int M, F, K;
+    int op_w;
+    int lddh, ldx, ldw, ldp, lddx, lddw;
+    int activation;
+} gemm_gated_backward_params;
+int gemm_gated_backward_workspace(const gemm_gated_backward_params *params, size_t *bytes);
+int gemm_gated_backward_f16(const gemm_gated_backward_params *params, const uint16_t *dH, const uint16_t *X,
+                            const uint16_t *Wg, const uint16_t *Wu, const uint16_t *G, const uint16_t *U,
+                            uint16_t *dX, uint16_t *dWg, uint16_t *dWu, void *workspace, size_t workspace_bytes,
+                            void *stream);
+int gemm_gated_backward_bf16(const gemm_gated_backward_params *params, const uint16_t *dH, const uint16_t *X,
+                             const uint16_t *Wg, const uint16_t *Wu, const uint16_t *G, const uint16_t *U,
+                             uint16_t *dX, uint16_t *dWg, uint16_t *dWu, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/* Layer norm of each of M rows of N elements:
+ *   mean = sum x / N, rstd = 1 / sqrt(sum (x - mean)^2 / N + eps),
+ *   y = (x - mean) rstd weight + bias.
+ * weight and bias (N elements; NULL: ones, zeros) are in x's format, or FP32
+ * (weight_f32 nonzero).  mean and rstd (M FP32 values) may be NULL. eps
+ * negative or NaN -> GEMM_ERR_INVALID_DIM. */
+typedef struct {
+    int M, N;
+    int ldx, ldy;       /* rows of x; rows of y, or of dy in the backward pass */
+    int lddx;           /* rows of dx (backward pass only) */
+    int weight_f32;
+    float eps;          /* forward pass only */
+} gemm_layer_norm_params;
+int gemm_layer_norm_f32(const gemm_layer_norm_params *params, const float *x, const float *weight, const float *bias,
+                        float *y, float *mean, float *rstd, void *stream);
+int gemm_layer_norm_f16(const gemm_layer_norm_params *params, const uint16_t *x, const void *weight, const void *bias,
+                        uint16_t *y, float *mean, float *rstd, void *stream);
+int gemm_layer_norm_bf16(const gemm_layer_norm_params *params, const uint16_t *x, const void *weight,
+                         const void *bias, uint16_t *y, float *mean, float *rstd, void *stream);
+
+/* Its backward pass, from the forward pass's mean and rstd: with
+ * xh = (x - mean) rstd and t = dy weight,
+ *   dx = rstd (t - sum t / N - xh sum (t xh) / N),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy,
+ * the last two in weight's format; each of them may be NULL (with both NULL
+ * no workspace is needed). */
+int gemm_layer_norm_backward_workspace(const gemm_layer_norm_params *params, size_t *bytes);
+int gemm_layer_norm_backward_f32(const gemm_layer_norm_params *params, const float *dy, const float *x,
+                                 const float *weight, const float *mean, const float *rstd, float *dx,
+                                 float *dweight, float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_layer_norm_backward_f16(const gemm_layer_norm_params *params, const uint16_t *dy, const uint16_t *x,
+                                 const void *weight, const float *mean, const float *rstd, uint16_t *dx,
+                                 void *dweight, void *dbias, void *workspace, size_t workspace_bytes, void *stream);
+int gemm_layer_norm_backward_bf16(const gemm_layer_norm_params *params, const uint16_t *dy, const uint16_t *x,
+                                  const void *weight, const float *mean, const float *rstd, uint16_t *dx,
+                                  void *dweight, void *dbias, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, NUL-terminated descriptions; never NULL ("unknown ..." for values
  * outside the enums). */
