@@ -38,7 +38,11 @@ struct Product {
 constexpr int kStageDepth = 64;   // k per stage, the unit of Product::chunk
 inline int product_stages(const Product &p) { return p.nseg * ((p.K + kStageDepth - 1) / kStageDepth); }
 
+// The register-staged tiles (64 or 128; any operands), and the rings (128 or
+// 256; 16-byte aligned operands whose rows are whole 16-byte units, strides
+// below 2^22).
 hipError_t launch_tile(const Product &p, int tile, hipStream_t stream);
+hipError_t launch_linear_ring(const Product &p, int tile, hipStream_t stream);
 hipError_t launch_join(const Product &p, hipStream_t stream);
 
 // dZ = dY act'(Z) (Z null: dZ = dY, nothing written unless dz) and, with

@@ -1,6 +1,7 @@
 // C entry points of the dense layer and the gated up-projection (declared in
 // include/gemm.h): argument checks, choice of kernel, workspace layout.
-// Host code only; the kernels live in linear_tile.hip and act_grad.hip.
+// Host code only; the kernels live in linear_ring.hip, linear_tile.hip and
+// act_grad.hip.
 #include <stdint.h>
 
 #include "linear.h"
@@ -21,9 +22,11 @@ bool op_ok(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 bool act_ok(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
 bool missing(const void *p, long long rows, long long cols) { return rows > 0 && cols > 0 && !p; }
 
-// How a product runs: the tile and, where its tiles leave compute units
-// idle, into how many parts the sum over k is split.
+// How a product runs: on the register-staged tiles or the rings, the tile
+// and, where its tiles leave compute units idle, into how many parts the sum
+// over k is split.
 struct Way {
+    bool ring;
     int tile, splits, chunk;
 };
 
@@ -33,34 +36,67 @@ long long tiles(const Product &p, int t)
     return (long long)ceil_div(p.M, t) * ceil_div(p.N, ft) * p.nbatch;
 }
 
-Way choose(const Product &p)
+// Whether sizes and strides let the rings run (the addresses apart): rows of
+// whole 16-byte units, lane offsets within a tile below 2^31.
+bool ring_sizes(const Product &p)
 {
-    Way w{128, 1, 0};
-    if (tiles(p, 128) < 512)
-        w.tile = 64;
-    // fewer tiles than compute units: split k until two workgroups a unit,
-    // keeping at least four stages a part
+    const auto ok = [](int ld) { return ld % 8 == 0 && ld < (1 << 22); };
+    const int a_row = p.trans_a ? p.M : p.K, b_row = p.trans_b ? p.K : p.N;
+    return ok(p.lda) && ok(p.ldb) && a_row % 8 == 0 && b_row % 8 == 0;
+}
+bool ring_addresses(const Product &p)
+{
+    return (((uintptr_t)p.A[0] | (uintptr_t)p.A[1] | (uintptr_t)p.B[0] | (uintptr_t)p.B[1]) & 15) == 0;
+}
+
+// Fewer tiles than compute units: split k until two workgroups a unit,
+// keeping at least four stages a part.
+void split_over_k(const Product &p, Way &w)
+{
     const long long n = tiles(p, w.tile);
     const int stages = dgor::product_stages(p);
-    if (n > 0 && n < 256 && stages >= 8) {
-        long long want = 512 / n;
-        want = want < stages / 4 ? want : stages / 4;
-        want = want < 16 ? want : 16;
-        if (want > 1) {
-            w.chunk = ceil_div(stages, want);
-            w.splits = ceil_div(stages, w.chunk);
-        }
+    if (n <= 0 || n >= 256 || stages < 8)
+        return;
+    long long want = 512 / n;
+    want = want < stages / 4 ? want : stages / 4;
+    want = want < 16 ? want : 16;
+    if (want > 1) {
+        w.chunk = ceil_div(stages, want);
+        w.splits = ceil_div(stages, w.chunk);
     }
+}
+
+Way choose(const Product &p, bool ring)
+{
+    Way w{ring, 128, 1, 0};
+    if (ring) {
+        // cycles of a compute unit: a 256 tile's stage of 32 k is 1024 of its
+        // matrix cores, four 128 tiles' the same at a lower rate, two at a time
+        const long long stages = 2LL * dgor::product_stages(p), n256 = tiles(p, 256), n128 = tiles(p, 128);
+        const long long c256 = (n256 + 255) / 256 * (stages * 1024 + 4000);
+        const long long c128 = n128 <= 256 ? stages * 420 + 3000 : (n128 + 511) / 512 * (stages * 660 + 3000);
+        if (c256 <= c128) {
+            w.tile = 256;
+            return w;
+        }
+    } else if (tiles(p, 128) < 512) {
+        w.tile = 64;
+    }
+    split_over_k(p, w);
     return w;
 }
 
-// FP32 partial sums of a split product.
+// FP32 partial sums of a split product, on whichever kernel the operands'
+// addresses will give it.
 size_t part_bytes(const Product &p)
 {
-    const Way w = choose(p);
-    if (w.splits <= 1)
-        return 0;
-    return round_up((size_t)(p.gated ? 2 : p.nbatch) * w.splits * p.M * p.N * sizeof(float), kWsAlign);
+    size_t most = 0;
+    for (int ring = 0; ring < (ring_sizes(p) ? 2 : 1); ++ring) {
+        const Way w = choose(p, ring);
+        const size_t b = w.splits <= 1 ? 0 : (size_t)(p.gated ? 2 : p.nbatch) * w.splits * p.M * p.N * sizeof(float);
+        most = b > most ? b : most;
+    }
+    return round_up(most, kWsAlign);
 }
 
 // Runs a product; ws has part_bytes(p) bytes.
@@ -68,43 +104,46 @@ hipError_t run_product(Product p, void *ws, hipStream_t s)
 {
     if (p.M == 0 || p.N == 0)
         return hipSuccess;
-    const Way w = choose(p);
+    const Way w = choose(p, ring_sizes(p) && ring_addresses(p));
     p.splits = w.splits;
     p.chunk = w.chunk;
     p.part = (float *)ws;
-    const hipError_t err = dgor::launch_tile(p, w.tile, s);
+    const hipError_t err = w.ring ? dgor::launch_linear_ring(p, w.tile, s) : dgor::launch_tile(p, w.tile, s);
     if (err != hipSuccess || p.splits <= 1)
         return err;
     return dgor::launch_join(p, s);
 }
 
-Product plain_product(int M, int N, int K, bool bf16)
+Product plain_product(int M, int N, int K)
 {
     Product p{};
-    p.M = M, p.N = N, p.K = K, p.bf16 = bf16;
+    p.M = M, p.N = N, p.K = K;
     p.nseg = p.nbatch = 1;
     return p;
 }
 
 // The three products of a layer with n weights W (1, or 2 for the gated one)
 // of K inputs x N outputs.
-Product forward_product(int M, int N, int K, int op_w, bool gated, bool bf16)
+Product forward_product(int M, int N, int K, int op_w, int ldx, int ldw, bool gated)
 {
-    Product p = plain_product(M, N, K, bf16);
+    Product p = plain_product(M, N, K);
+    p.lda = ldx, p.ldb = ldw;
     p.trans_b = op_w == GEMM_OP_T;
     p.gated = gated;
     return p;
 }
-Product input_gradient_product(int M, int N, int K, int op_w, int n, bool bf16)   // dX = sum of dZ W^T
+Product input_gradient_product(int M, int N, int K, int op_w, int lddz, int ldw, int n)   // dX = sum of dZ W^T
 {
-    Product p = plain_product(M, K, N, bf16);
+    Product p = plain_product(M, K, N);
+    p.lda = lddz, p.ldb = ldw;
     p.trans_b = op_w == GEMM_OP_N;
     p.nseg = n;
     return p;
 }
-Product weight_gradient_product(int M, int N, int K, int op_w, int n, bool bf16)   // X^T dZ, or dZ^T X
+Product weight_gradient_product(int M, int N, int K, int op_w, int ldx, int lddz, int n)   // X^T dZ, or dZ^T X
 {
-    Product p = op_w == GEMM_OP_N ? plain_product(K, N, M, bf16) : plain_product(N, K, M, bf16);
+    Product p = op_w == GEMM_OP_N ? plain_product(K, N, M) : plain_product(N, K, M);
+    p.lda = op_w == GEMM_OP_N ? ldx : lddz, p.ldb = op_w == GEMM_OP_N ? lddz : ldx;
     p.trans_a = true;
     p.nbatch = n;
     return p;
@@ -129,7 +168,7 @@ int check_linear(const gemm_linear_params *q, Product &p)
         return GEMM_ERR_INVALID_LAYOUT;
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
-    p = forward_product(q->M, q->N, q->K, q->op_w, false, false);
+    p = forward_product(q->M, q->N, q->K, q->op_w, q->ldx, q->ldw, false);
     return GEMM_OK;
 }
 
@@ -152,8 +191,8 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
     if (dev != GEMM_OK)
         return dev;
     p.bf16 = bf16;
-    p.A[0] = p.A[1] = X, p.lda = q->ldx;
-    p.B[0] = p.B[1] = W, p.ldb = q->ldw;
+    p.A[0] = p.A[1] = X;
+    p.B[0] = p.B[1] = W;
     p.e.Y = Y, p.e.ldy = q->ldy, p.e.y_f32 = q->y_f32 != 0;
     p.e.bias = bias, p.e.act = q->activation;
     p.e.R = R, p.e.ldr = q->ldr;
@@ -180,9 +219,9 @@ int check_linear_backward(const gemm_linear_backward_params *q, Product &px, Pro
         return GEMM_ERR_INVALID_LAYOUT;
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
-    px = input_gradient_product(q->M, q->N, q->K, q->op_w, 1, false);
-    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, 1, false);
-    l.lddz = (int)round_up((size_t)q->N, 8);
+    l.lddz = q->activation == GEMM_ACT_NONE ? q->lddy : (int)round_up((size_t)q->N, 8);
+    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, q->ldw, 1);
+    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, q->ldx, l.lddz, 1);
     l.dz = 0;
     l.sums = q->activation == GEMM_ACT_NONE ? 0 : round_up((size_t)q->M * l.lddz * 2, kWsAlign);
     l.part = l.sums + round_up((size_t)row_blocks(q->M) * q->N * sizeof(float), kWsAlign);
@@ -216,7 +255,6 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
     const uint16_t *dZ = dY;
-    int lddz = q->lddy;
     float *sums = dbias ? (float *)(base + l.sums) : nullptr;
     if (q->M > 0 && q->N > 0 && ((act && (dX || dW)) || dbias)) {
         uint16_t *out = act && (dX || dW) ? (uint16_t *)(base + l.dz) : nullptr;
@@ -224,26 +262,24 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
                                                    q->activation, sums, bf16, s);
         if (e != hipSuccess)
             return GEMM_ERR_LAUNCH;
-        if (out) {
+        if (out)
             dZ = out;
-            lddz = l.lddz;
-        }
     }
     if (dbias && q->N > 0 &&
         dgor::launch_sum_blocks(row_blocks(q->M), q->N, sums, dbias, bf16, s) != hipSuccess)
         return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
     if (dX) {
-        px.A[0] = px.A[1] = dZ, px.lda = lddz;
-        px.B[0] = px.B[1] = W, px.ldb = q->ldw;
+        px.A[0] = px.A[1] = dZ;
+        px.B[0] = px.B[1] = W;
         px.e.Y = dX, px.e.ldy = q->lddx;
         if (run_product(px, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     if (dW) {
         const bool t = q->op_w == GEMM_OP_T;
-        pw.A[0] = pw.A[1] = t ? dZ : X, pw.lda = t ? lddz : q->ldx;
-        pw.B[0] = pw.B[1] = t ? X : dZ, pw.ldb = t ? q->ldx : lddz;
+        pw.A[0] = pw.A[1] = t ? dZ : X;
+        pw.B[0] = pw.B[1] = t ? X : dZ;
         pw.e.Y = dW, pw.e.ldy = q->lddw;
         if (run_product(pw, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
@@ -263,7 +299,7 @@ int check_gated(const gemm_gated_params *q, Product &p)
         return GEMM_ERR_INVALID_LAYOUT;
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
-    p = forward_product(q->M, q->F, q->K, q->op_w, true, false);
+    p = forward_product(q->M, q->F, q->K, q->op_w, q->ldx, q->ldw, true);
     return GEMM_OK;
 }
 
@@ -287,8 +323,8 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
     if (dev != GEMM_OK)
         return dev;
     p.bf16 = bf16;
-    p.A[0] = p.A[1] = X, p.lda = q->ldx;
-    p.B[0] = Wg, p.B[1] = Wu, p.ldb = q->ldw;
+    p.A[0] = p.A[1] = X;
+    p.B[0] = Wg, p.B[1] = Wu;
     p.e.Y = H, p.e.ldy = q->ldh, p.e.act = q->activation;
     p.e.pre = G, p.e.pre2 = U, p.e.ldp = q->ldp;
     return done(run_product(p, ws, (hipStream_t)stream));
@@ -311,9 +347,9 @@ int check_gated_backward(const gemm_gated_backward_params *q, Product &px, Produ
         return GEMM_ERR_INVALID_LAYOUT;
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
-    px = input_gradient_product(q->M, q->F, q->K, q->op_w, 2, false);
-    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, 2, false);
     l.ldd = (int)round_up((size_t)q->F, 8);
+    px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, q->ldw, 2);
+    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, q->ldx, l.ldd, 2);
     l.du = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
     l.part = 2 * l.du;
     const size_t a = part_bytes(px), b = part_bytes(pw);
@@ -354,16 +390,16 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
         return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
     if (dX) {
-        px.A[0] = dG, px.A[1] = dU, px.lda = l.ldd;
-        px.B[0] = Wg, px.B[1] = Wu, px.ldb = q->ldw;
+        px.A[0] = dG, px.A[1] = dU;
+        px.B[0] = Wg, px.B[1] = Wu;
         px.e.Y = dX, px.e.ldy = q->lddx;
         if (run_product(px, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     if (dWg) {
         const bool t = q->op_w == GEMM_OP_T;
-        pw.A[0] = t ? dG : X, pw.A[1] = t ? dU : X, pw.lda = t ? l.ldd : q->ldx;
-        pw.B[0] = t ? X : dG, pw.B[1] = t ? X : dU, pw.ldb = t ? q->ldx : l.ldd;
+        pw.A[0] = t ? dG : X, pw.A[1] = t ? dU : X;
+        pw.B[0] = t ? X : dG, pw.B[1] = t ? X : dU;
         pw.e.Y = dWg, pw.Y1 = dWu, pw.e.ldy = q->lddw;
         if (run_product(pw, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;

@@ -1,0 +1,433 @@
+// The dense-layer products of 16-byte aligned operands: square tiles of 256
+// or 128, loaded straight from global memory into LDS rings 32 k deep, FP32
+// sums on v_mfma_f32_16x16x32, and the epilogue of epilogue.h on whole rows.
+//
+// Four wavefronts, each a quarter of the tile: 8 x 8 (tile 256, all 256
+// accumulator registers, one workgroup a compute unit) or 4 x 4 blocks of
+// 16 x 16 (tile 128, two workgroups a unit, which cover each other's waits).
+// Loads: one instruction moves 64 lanes x 16 bytes into 1 KB of LDS, lane p
+// at byte 16 p; the layout is chosen by permuting the sources, and a lane
+// whose offset is out of range writes zeros, which fills every edge.
+//
+// A stage of an operand whose rows run along the outputs (B as K x N, A as
+// K x M) is kept as two halves of tile / 2 columns, each 32 k rows of W =
+// tile / 16 units of 16 bytes, unit u of row k at W k + (u ^ x(k)), x(k) =
+// 2 (k & 3) + 8 ((k >> 3) & 1) for W = 16 and 2 ((k >> 1) & 1) + 4 ((k >> 3) & 1)
+// for W = 8, which puts the eight k rows that a cycle of a transposing read
+// takes two units of on distinct banks.  B as N x K is two halves of tile / 2
+// rows of four units, unit c of row r at 4 r + (c ^ 2 ((r >> 2) & 1)).  The
+// halves may come from two matrices: a gated product's tile is the gate's
+// columns and the up projection's same columns, so that a wavefront has both
+// sums of its elements.  A as M x K is staged two stages at a time, whole
+// 128-byte lines: rows of eight units, unit c of row r at 8 r + (c ^ ((r >> 1) & 7)).
+//
+// Pipeline.  B has four stage buffers, A as K x M too, A as M x K three
+// buffers of two stages.  During stage t the fragments of stage t + 1 are
+// read and the loads of B stage t + 3 and A stage t + 3 (half of pair
+// t / 2 + 2) issued, spread between the MFMAs.  Each stage begins with a wait
+// for this wavefront's loads of two stages before and a barrier: then stage
+// t + 1 has landed, and the buffers that are refilled were last read by
+// fragments that every wavefront has since consumed.
+//
+// Bound by the matrix cores where there are tiles for every compute unit.
+#include "common.h"
+#include "lds_dma.h"
+#include "linear.h"
+
+namespace dgor {
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
+
+struct OpHalf : Half16 {
+    static __device__ __forceinline__ floatx4 mfma(halfx8 a, halfx8 b, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+struct OpBrain : Brain16 {
+    static __device__ __forceinline__ floatx4 mfma(halfx8 a, halfx8 b, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+};
+
+constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descriptor's range
+
+template <int W>
+__device__ __forceinline__ int row_swizzle(int k)
+{
+    return W == 16 ? 2 * (k & 3) + 8 * ((k >> 3) & 1) : 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1);
+}
+
+// Descriptor range in bytes of `rows` rows of `cols` elements: what is past
+// it reads as zero.
+__device__ __forceinline__ int range_of(int rows, int cols, int ld)
+{
+    return rows <= 0 || cols <= 0 ? 0 : (int)(((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)cols) * 2u);
+}
+
+template <class Op, int BT, bool TA, bool TB, bool GATED>
+__global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
+{
+    constexpr int BK = 32;
+    constexpr int HW = BT / 2, FB = HW / 16;       // a wavefront's square, and its 16-wide blocks
+    constexpr int W = HW / 8;                      // units of a half's k row
+    constexpr int LPW = BT / 64;                   // a wavefront's loads of one operand and stage
+    constexpr int HALF = BK * HW * 2, STAGE = 2 * HALF, PAIR = 2 * STAGE;
+    constexpr int A_BYTES = TA ? 4 * STAGE : 3 * PAIR;
+    constexpr int LDS_BYTES = A_BYTES + 4 * STAGE;
+    constexpr int FT = GATED ? HW : BT;            // output columns of a tile
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_BYTES];
+    const uint32_t ring = lds_address(lds);
+
+    const int per = p.tiles_m * p.tiles_n;
+    const int batch = blockIdx.x >= (unsigned)per ? 1 : 0;
+    int tm, tn;
+    dgor_tile_of_block((int)blockIdx.x - batch * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    const int m0 = tm * BT, n0 = tn * FT;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int M = p.M, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;
+    // stages of 32 k; a segment's are a whole number of pairs
+    const int seg_stages = 2 * ((K + 2 * BK - 1) / (2 * BK));
+    const int total = p.nseg == 2 ? 2 * seg_stages : (K + BK - 1) / BK;
+    const int s0 = p.splits > 1 ? (int)blockIdx.y * p.chunk * 2 : 0;
+    const int steps = (p.splits > 1 ? min(s0 + p.chunk * 2, total) : total) - s0;
+
+    // ---- loads.  Wavefronts 0 and 1 fill half 0 of a stage, 2 and 3 half 1.
+    const int lhalf = wave >> 1, lid0 = LPW * (wave & 1);
+    const int bcol = GATED ? n0 : n0 + HW * lhalf;            // first column of this wavefront's half of B
+    const int b_left = N - bcol;
+    const uint16_t *const B0 = p.B[GATED ? lhalf : batch], *const B1 = p.B[GATED ? lhalf : 1];
+    uint32_t b_off[LPW];
+    const int b_kc = 8 * ((lane & 3) ^ (2 * ((lane >> 4) & 1)));
+#pragma unroll
+    for (int q = 0; q < LPW; ++q) {
+        if (TB) {
+            b_off[q] = (uint32_t)((16 * (lid0 + q) + (lane >> 2)) * ldb + b_kc) * 2u;
+        } else {
+            const int k = (64 / W) * (lid0 + q) + lane / W, u = (lane % W) ^ row_swizzle<W>(k);
+            b_off[q] = 8 * u < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
+        }
+    }
+    const uint32_t lds_b = ring + (uint32_t)(A_BYTES + lhalf * HALF + lid0 * 1024);
+    struct Loads {
+        intx4 r;
+        int k_left;
+        uint32_t dst;
+    };
+    // stage st, counted over the segments
+    auto place = [&](int st, int &seg) {
+        seg = p.nseg == 2 && st >= seg_stages ? 1 : 0;
+        return BK * (st - seg * seg_stages);
+    };
+    auto b_loads = [&](int t) {
+        Loads L;
+        int seg;
+        const int k0 = place(s0 + t, seg);
+        const uint16_t *B = seg ? B1 : B0;
+        L.k_left = K - k0;
+        L.r = rsrc_words(TB ? B + (size_t)bcol * ldb + k0 : B + (size_t)k0 * ldb + bcol, 0);
+        if (TB)
+            L.r.z = L.k_left <= 0 ? 0 : (b_left >= HW ? 0x7fffffff : range_of(b_left, L.k_left, ldb));
+        else
+            L.r.z = L.k_left >= BK ? 0x7fffffff : range_of(L.k_left, b_left, ldb);
+        L.dst = lds_b + (uint32_t)((t & 3) * STAGE);
+        return L;
+    };
+    auto load_b = [&](const Loads &L, int q) {
+        load_to_lds(L.r, L.dst + (uint32_t)(q * 1024), TB && b_kc >= L.k_left ? kOutside : b_off[q]);
+    };
+    const uint16_t *const A0 = p.A[batch], *const A1 = p.A[1];
+    // A as M x K: a wavefront loads its HW / 2 rows of the tile, eight a load
+    uint32_t a_off[TA ? LPW : 2];
+    int a_kc[2] = {0, 0};
+    const int arow = TA ? m0 + HW * lhalf : m0;
+    const int a_left = M - arow;
+#pragma unroll
+    for (int j = 0; j < (TA ? LPW : 2); ++j) {
+        if (TA) {
+            const int k = (64 / W) * (lid0 + j) + lane / W, u = (lane % W) ^ row_swizzle<W>(k);
+            a_off[j] = 8 * u < a_left ? (uint32_t)(k * lda + 8 * u) * 2u : kOutside;
+        } else {
+            const int r = (HW / 2) * wave + 8 * j + (lane >> 3);
+            const int c = (lane & 7) ^ ((4 * j + (lane >> 4)) & 7);
+            a_off[j] = (uint32_t)(r * lda + 8 * c) * 2u;
+            a_kc[j] = 8 * c;
+        }
+    }
+    const uint32_t a_row16 = (uint32_t)(16 * lda) * 2u;
+    const uint32_t lds_a = ring + (uint32_t)(TA ? lhalf * HALF + lid0 * 1024 : 2 * LPW * wave * 1024);
+    // loads of A stage t (A as K x M), or of the pair that begins at stage t
+    auto a_loads = [&](int t, uint32_t buf) {
+        Loads L;
+        int seg;
+        const int k0 = place(s0 + t, seg);
+        const uint16_t *A = seg ? A1 : A0;
+        L.k_left = K - k0;
+        L.r = rsrc_words(TA ? A + (size_t)k0 * lda + arow : A + (size_t)m0 * lda + k0, 0);
+        if (TA)
+            L.r.z = L.k_left >= BK ? 0x7fffffff : range_of(L.k_left, a_left, lda);
+        else
+            L.r.z = L.k_left <= 0 ? 0 : (a_left >= BT ? 0x7fffffff : range_of(a_left, L.k_left, lda));
+        L.dst = lds_a + buf;
+        return L;
+    };
+    auto load_a = [&](const Loads &L, int j) {
+        uint32_t off;
+        if (TA)
+            off = a_off[j];
+        else
+            off = a_kc[j & 1] >= L.k_left ? kOutside : a_off[j & 1] + (uint32_t)(j >> 1) * a_row16;
+        load_to_lds(L.r, L.dst + (uint32_t)(j * 1024), off);
+    };
+
+    // ---- fragments.  Lane (g, s) = (lane / 16, lane % 16).
+    const int s16 = lane & 15, g = lane >> 4;
+    const int wrow = (wave >> 1) * HW;
+    // k rows 8 g + s / 4 and four further: both have this swizzle
+    const int ks_x = row_swizzle<W>(8 * g + (s16 >> 2));
+    const uint32_t ks_lane = (uint32_t)((8 * g + (s16 >> 2)) * (HW * 2) + 8 * (s16 & 1));
+    constexpr int FU = GATED ? FB / 2 : FB;        // distinct column blocks of B
+    uint32_t b_unit[TB ? 1 : FU], a_unit[TA ? FB : 1];
+    if (!TB)
+#pragma unroll
+        for (int j = 0; j < FU; ++j)
+            b_unit[TB ? 0 : j] =
+                (uint32_t)(((2 * ((GATED ? (wave & 1) * FU : 0) + j) + ((s16 & 3) >> 1)) ^ ks_x) * 16);
+    if (TA)
+#pragma unroll
+        for (int i = 0; i < FB; ++i)
+            a_unit[TA ? i : 0] = (uint32_t)(((2 * i + ((s16 & 3) >> 1)) ^ ks_x) * 16);
+    const uint32_t kc_lane = (uint32_t)(s16 * 64 + ((g ^ (2 * ((s16 >> 2) & 1))) * 16));
+    const uint32_t b_lane = (uint32_t)A_BYTES + (TB ? kc_lane : ks_lane) +
+                            (GATED ? (TB ? (uint32_t)((wave & 1) * FU * 1024) : 0u) : (uint32_t)((wave & 1) * HALF));
+    const uint32_t a_lane = TA ? ks_lane + (uint32_t)((wave >> 1) * HALF)
+                               : (uint32_t)((wrow + s16) * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
+    auto transposed = [&](uint32_t at) -> halfx8 {
+        const uint8_t *q = lds + at;
+        const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
+        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * HW * 2));
+        return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    struct Source {
+        uint32_t a;      // byte offset of the stage's A buffer
+        int odd;         // second stage of its pair (A as M x K)
+        uint32_t b;      // and of its B buffer
+    };
+    auto read_a = [&](const Source &S, int i) -> halfx8 {
+        if (TA)
+            return transposed(a_lane + S.a + a_unit[TA ? i : 0]);
+        return *reinterpret_cast<const halfx8 *>(lds + ((a_lane ^ (uint32_t)(64 * S.odd)) + S.a + (uint32_t)(i * 2048)));
+    };
+    auto read_b = [&](const Source &S, int j) -> halfx8 {
+        const uint32_t at = b_lane + S.b + (GATED ? (uint32_t)((j / FU) * HALF) : 0u);
+        if (TB)
+            return *reinterpret_cast<const halfx8 *>(lds + at + (uint32_t)((j % FU) * 1024));
+        return transposed(at + b_unit[TB ? 0 : j % FU]);
+    };
+    // A block 0, the B blocks, then the other A blocks: as the MFMAs want them
+    auto fread = [&](const Source &S, int r, halfx8 *fa, halfx8 *fb) {
+        if (r == 0 || r > FB)
+            fa[r == 0 ? 0 : r - FB] = read_a(S, r == 0 ? 0 : r - FB);
+        else
+            fb[r - 1] = read_b(S, r - 1);
+    };
+
+    floatx4 acc[FB][FB];
+#pragma unroll
+    for (int i = 0; i < FB; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                asm("v_accvgpr_write_b32 %0, 0" : "=a"(acc[i][j][r]));   // keeps the array in the accumulators
+
+    // One stage: its MFMAs from (ca, cb), the next stage's 2 FB fragment reads
+    // after the first of them, then its 2 LPW loads evenly over the rest.
+    auto stage = [&](int par, const Loads &LA, const Loads &LB, const Source &S, halfx8 *ca, halfx8 *cb, halfx8 *na,
+                     halfx8 *nb) {
+        constexpr int EVERY = (FB * FB - 2 * FB) / (2 * LPW);
+#pragma unroll
+        for (int m = 0; m < FB * FB; ++m) {
+            const int i = m / FB, j = m % FB;
+            acc[i][j] = Op::mfma(ca[i], cb[j], acc[i][j]);
+            if (m < 2 * FB)
+                fread(S, m, na, nb);
+            if (m >= 2 * FB && (m - 2 * FB) % EVERY == EVERY - 1) {
+                const int ld = (m - 2 * FB) / EVERY;
+                if (ld < LPW)
+                    load_b(LB, ld);
+                else if (ld < 2 * LPW)
+                    load_a(LA, (TA ? 0 : LPW * par) + ld - LPW);
+            }
+            // keep this order: the compiler would otherwise cluster the reads
+            // and loads, and move MFMAs across the barrier
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto next_pair = [](uint32_t b) { return b == (uint32_t)(2 * PAIR) ? 0u : b + PAIR; };
+    auto buf = [](int t) { return (uint32_t)((t & 3) * STAGE); };
+
+    halfx8 fa0[FB], fa1[FB], fb0[FB], fb1[FB];
+    if (TA) {
+#pragma unroll
+        for (int st = 0; st < 3; ++st) {
+            const Loads LA = a_loads(st, buf(st)), LB = b_loads(st);
+#pragma unroll
+            for (int q = 0; q < LPW; ++q)
+                load_a(LA, q);
+#pragma unroll
+            for (int q = 0; q < LPW; ++q)
+                load_b(LB, q);
+        }
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(4 * LPW));
+    } else {
+        const Loads P0 = a_loads(0, 0), P1 = a_loads(2, PAIR);
+#pragma unroll
+        for (int j = 0; j < 2 * LPW; ++j)
+            load_a(P0, j);
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const Loads LB = b_loads(st);
+#pragma unroll
+            for (int q = 0; q < LPW; ++q)
+                load_b(LB, q);
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * LPW; ++j)
+            load_a(P1, j);
+        const Loads LB = b_loads(2);
+#pragma unroll
+        for (int q = 0; q < LPW; ++q)
+            load_b(LB, q);
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(4 * LPW));
+    }
+    __builtin_amdgcn_s_barrier();
+    {
+        const Source S{0u, 0, 0u};
+#pragma unroll
+        for (int r = 0; r < 2 * FB; ++r)
+            fread(S, r, fa0, fb0);
+    }
+    auto wait = [&](int t) {
+        // the loads of the stage before may stay in flight (at stage 0: A pair
+        // 1 and B stage 2)
+        if (!TA && t == 0)
+            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(3 * LPW));
+        else
+            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(2 * LPW));
+        __builtin_amdgcn_s_barrier();
+    };
+    uint32_t pa = 0;   // the pair's buffer
+    for (int t = 0; t < steps; t += 2) {
+        const uint32_t pa1 = next_pair(pa), pa2 = next_pair(pa1);
+        wait(t);
+        {
+            const Loads LA = TA ? a_loads(t + 3, buf(t + 3)) : a_loads(t + 4, pa2), LB = b_loads(t + 3);
+            __builtin_amdgcn_sched_barrier(0);
+            stage(0, LA, LB, TA ? Source{buf(t + 1), 0, buf(t + 1)} : Source{pa, 1, buf(t + 1)}, fa0, fb0, fa1, fb1);
+        }
+        if (t + 1 < steps) {
+            wait(t + 1);
+            const Loads LA = TA ? a_loads(t + 4, buf(t + 4)) : a_loads(t + 4, pa2), LB = b_loads(t + 4);
+            __builtin_amdgcn_sched_barrier(0);
+            stage(1, LA, LB, TA ? Source{buf(t + 2), 0, buf(t + 2)} : Source{pa1, 0, buf(t + 2)}, fa1, fb1, fa0, fb0);
+        }
+        pa = pa1;
+    }
+    // no load may still be writing LDS, nor a wavefront reading the ring
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
+    __builtin_amdgcn_s_barrier();
+    dgor_acc_hazard_wait();
+
+    // Epilogue: 32 rows at a time through the wavefront's own part of LDS, so
+    // that a lane holds eight neighbouring columns of one row.  Rows are padded
+    // by 16 bytes, which puts the 64 lanes of each write on distinct banks.
+    constexpr int ROW = HW + 4;                                   // floats
+    constexpr int COLS = GATED ? HW / 2 : HW, LANES = COLS / 8;
+    static_assert(4 * 32 * ROW * 4 <= LDS_BYTES, "the epilogue uses the ring's LDS");
+    float *w = reinterpret_cast<float *>(lds) + wave * 32 * ROW;
+    const int c0 = n0 + (wave & 1) * COLS;
+    Epilogue e = p.e;
+    if (batch)
+        e.Y = p.Y1;
+#pragma unroll
+    for (int round = 0; round < FB / 2; ++round) {
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+            for (int j = 0; j < FB; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    w[(16 * ii + 4 * g + r) * ROW + 16 * j + s16] = dgor_acc_read(acc[2 * round + ii][j][r]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int q = 0; q < 32 * LANES / 64; ++q) {
+            const int id = lane + 64 * q, r = id / LANES, c = 8 * (id % LANES);
+            const int row = m0 + wrow + 32 * round + r, col = c0 + c;
+            if (row < M && col < N) {
+                float v[8], u[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    v[x] = w[r * ROW + c + x];
+                    u[x] = GATED ? w[r * ROW + COLS + c + x] : 0.f;
+                }
+                if (p.splits > 1) {
+                    const size_t MN = (size_t)M * N, at = (size_t)row * N + col;
+                    store8_f32(p.part + ((size_t)batch * p.splits + blockIdx.y) * MN + at, N - col, v);
+                    if (GATED)
+                        store8_f32(p.part + ((size_t)p.splits + blockIdx.y) * MN + at, N - col, u);
+                } else {
+                    emit8<Op, GATED>(e, row, col, N - col, v, u);
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <class Op, int BT>
+hipError_t launch_ring_as(const Product &p, hipStream_t s)
+{
+    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n * p.nbatch), (unsigned)(p.splits > 1 ? p.splits : 1));
+    if (p.gated) {
+        if (p.trans_b)
+            hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, true, true>), grid, dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, false, true>), grid, dim3(256), 0, s, p);
+    } else if (p.trans_a) {
+        hipLaunchKernelGGL((linear_ring_kernel<Op, BT, true, false, false>), grid, dim3(256), 0, s, p);
+    } else if (p.trans_b) {
+        hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, true, false>), grid, dim3(256), 0, s, p);
+    } else {
+        hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, false, false>), grid, dim3(256), 0, s, p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linear_ring(const Product &q, int tile, hipStream_t s)
+{
+    Product p = q;
+    if ((p.trans_a && p.trans_b) || (tile != 256 && tile != 128))
+        return hipErrorInvalidValue;
+    const int ft = p.gated ? tile / 2 : tile;
+    p.tiles_m = (p.M + tile - 1) / tile;
+    p.tiles_n = (p.N + ft - 1) / ft;
+    p.group_m = 4;
+    if (tile == 256)
+        return p.bf16 ? launch_ring_as<OpBrain, 256>(p, s) : launch_ring_as<OpHalf, 256>(p, s);
+    return p.bf16 ? launch_ring_as<OpBrain, 128>(p, s) : launch_ring_as<OpHalf, 128>(p, s);
+}
+
+}  // namespace dgor
