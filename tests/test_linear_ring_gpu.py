@@ -30,10 +30,12 @@ def library(request):
         return
     lib, load, kept = binding.load(build.POISON_LIB), binding.load, dict(layers._functions)
     layers._functions.clear()
+    layers._FORMS.clear()
     binding.load = lambda *a: lib
     yield request.param
     binding.load = load
     layers._functions.clear()
+    layers._FORMS.clear()
     layers._functions.update(kept)
 
 
