@@ -26,7 +26,7 @@ OBJDIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libdgor_gemm.so")
 
 SOURCES = ["api.hip", "ladder.hip", "mfma_f32.hip", "mfma_f16.hip", "mfma_8bit.hip", "conv.hip", "conv_nhwc.hip",
-           "linear.hip", "linear_ring.hip", "linear_tile.hip", "act_grad.hip", "norm.hip"]
+           "linear.hip", "linear_ring.hip", "linear_skinny.hip", "linear_tile.hip", "act_grad.hip", "norm.hip"]
 # The matrix-core rate calibration kernel: a library of its own, which the
 # GEMM library never loads (only the benchmark's calibration leg calls it).
 CAL_SOURCES = ["calibrate.hip"]

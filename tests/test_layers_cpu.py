@@ -111,8 +111,9 @@ def test_missing_operands_are_refused(stem, required):
                                   "gemm_layer_norm_backward"])
 def test_workspace_is_checked(stem):
     make, pointers = CALLS[stem]
-    # few outputs and a long sum: the forward products are split over k
-    long = dict(K=4096, ldx=4096, lddx=4096) if "norm" not in stem else {}
+    # few outputs and a long sum: the forward products are split over k (those
+    # of few rows are not, and need none)
+    long = dict(M=100, K=4096, ldx=4096, lddx=4096) if "norm" not in stem else {}
     if "backward" not in stem and "norm" not in stem:
         long["ldw"] = 8
     names = {n for n, _ in type(make())._fields_}
