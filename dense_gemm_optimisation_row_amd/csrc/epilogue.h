@@ -56,6 +56,36 @@ __device__ __forceinline__ void store8_16(uint16_t *p, int n, u32x4 v)
         if (e < n)
             p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
 }
+// Eight elements of row r from column c of a rows x cols matrix (neither
+// zero), zero outside.  Without a branch on the lane, so that a wavefront's
+// loads stay in flight together: a unit that an edge cuts is read from where
+// its row still holds eight elements and shifted into place.
+__device__ __forceinline__ u32x4 load_unit(const uint16_t *p, size_t ld, int r, int rows, int c, int cols)
+{
+    const uint16_t *row = p + (size_t)(r < rows ? r : rows - 1) * ld;
+    u32x4 v;
+    if (cols < 8) {   // shorter rows than a unit: the same for every lane
+        v = load8_16(row, cols);
+        if (c > 0)    // c is a multiple of 8
+            v = u32x4{0u, 0u, 0u, 0u};
+    } else {
+        const int at = c < cols - 8 ? c : cols - 8, off = c - at;
+        v = *reinterpret_cast<const u32x4_at2 *>(row + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = off & 1 ? __builtin_amdgcn_alignbit(i < 3 ? v[i < 3 ? i + 1 : 3] : 0u, v[i], 16) : v[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = off & 2 ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = off & 4 ? (i < 2 ? v[i < 2 ? i + 2 : 3] : 0u) : v[i];
+        if (off >= 8)
+            v = u32x4{0u, 0u, 0u, 0u};
+    }
+    return r < rows ? v : u32x4{0u, 0u, 0u, 0u};
+}
+
 template <class Fmt>
 __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8])
 {

@@ -43,10 +43,9 @@ inline int product_stages(const Product &p) { return p.nseg * ((p.K + kStageDept
 // below 2^22).
 hipError_t launch_tile(const Product &p, int tile, hipStream_t stream);
 hipError_t launch_linear_ring(const Product &p, int tile, hipStream_t stream);
-// Few rows (at most kSkinnyRows, A as M x K, one product): strips of 16 columns, or
-// 32 (not gated).
+// Few rows (at most kSkinnyRows, A as M x K, one product).
 constexpr int kSkinnyRows = 64;
-hipError_t launch_linear_skinny(const Product &p, int strip, hipStream_t stream);
+hipError_t launch_linear_skinny(const Product &p, hipStream_t stream);
 hipError_t launch_join(const Product &p, hipStream_t stream);
 
 // dZ = dY act'(Z) (Z null: dZ = dY, nothing written unless dz) and, with

@@ -22,7 +22,7 @@ bool op_ok(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 bool act_ok(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
 bool missing(const void *p, long long rows, long long cols) { return rows > 0 && cols > 0 && !p; }
 
-// How a product runs: the kernel, the tile (or strip) and, where its tiles
+// How a product runs: the kernel, the tile and, where its tiles
 // leave compute units idle, into how many parts the sum over k is split.
 enum Kernel { kSkinny, kRing, kTile };
 struct Way {
@@ -69,12 +69,8 @@ void split_over_k(const Product &p, Way &w)
 Way choose(const Product &p, bool ring)
 {
     Way w{ring ? kRing : kTile, 128, 1, 0};
-    if (!p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows) {
-        // a strip of 32 halves the reads of A and pays where those are of
-        // several row blocks and there are strips for every compute unit
-        const bool wide = !p.gated && p.M > 16 && p.N >= 32 * 256;
-        return Way{kSkinny, wide ? 32 : 16, 1, 0};
-    }
+    if (!p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows)
+        return Way{kSkinny, 0, 1, 0};
     if (ring) {
         // cycles of a compute unit: a 256 tile's stage of 32 k is 1024 of its
         // matrix cores, four 128 tiles' the same at a lower rate, two at a time
@@ -115,7 +111,7 @@ hipError_t run_product(Product p, void *ws, hipStream_t s)
     p.chunk = w.chunk;
     p.part = (float *)ws;
     if (w.kernel == kSkinny)
-        return dgor::launch_linear_skinny(p, w.tile, s);
+        return dgor::launch_linear_skinny(p, s);
     const hipError_t err =
         w.kernel == kRing ? dgor::launch_linear_ring(p, w.tile, s) : dgor::launch_tile(p, w.tile, s);
     if (err != hipSuccess || p.splits <= 1)

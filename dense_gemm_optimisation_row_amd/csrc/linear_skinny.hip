@@ -2,19 +2,25 @@
 // for M of at most 64.
 //
 // Bound by reading B once.  A workgroup of eight wavefronts takes a strip of
-// 16 (or 32) columns and the whole sum over k, so there is one launch and
-// nothing to join: wavefront w takes the 64-deep chunks w, w + 8, ... and has
-// the loads of UNROLL of them in flight at once; the eight sums meet in LDS,
-// in wavefront order.  Operands go from memory to registers; A, which every
-// workgroup reads, comes from the caches.  FP32 sums on v_mfma_f32_16x16x32:
-// lane (g, s) = (lane / 16, lane % 16) supplies k 8 g .. 8 g + 7 of row s of A
-// and of column s of B.  B as N x K has those eight k together: one 16-byte
-// load.  Of B as K x N a lane loads eight columns of one k row, and the
-// wavefront passes 32 rows x 16 columns through 1 KB of LDS to transposing
-// reads; row positions 4 g + j and 16 + 4 g + j hold k 8 g + j and 8 g + 4 + j,
-// so that each read is of contiguous bytes.  A strip's 32-byte row pieces of
-// a K x N matrix are parts of lines that the strips beside it want too: these
-// run on the same XCD, which fetches each line once.
+// columns and the whole sum over k, so there is one launch and nothing to
+// join: wavefront w takes the 64-deep chunks w, w + 8, ... and has the loads of
+// UNROLL of them in flight at once; the eight sums meet in LDS, in wavefront
+// order.  FP32 sums on v_mfma_f32_16x16x32: lane (g, s) = (lane / 16, lane % 16)
+// supplies k 8 g .. 8 g + 7 of row s of A and of column s of B.
+//
+// What the caches serve is counted in pieces that neighbouring lanes ask for
+// together, so every load takes whole rows of a chunk (of A, and of B as
+// N x K: 8 rows x 128 bytes; of B as K x N: 16 rows x the strip's 64 bytes)
+// and the wavefront passes the units through its own part of LDS into the
+// lanes that multiply them.  Loaded in the multiplying lanes' order, 16 bytes
+// from each of 16 rows, a 48 x 4096 by 4096 x 4096 product took 18.6 us.
+//   16 rows x 64 k (2 KB): unit c of row r at 8 r + (c ^ ((r >> 1) & 7)), read
+//     128 bits a lane;
+//   64 k x 32 columns (4 KB, in 16-row loads j): the load's rows 4 q + i hold
+//     k 32 (j / 2) + 4 (j % 2) + 8 q + i, unit u of row r at 4 r + (u ^ 2 ((r >> 2) & 1)),
+//     read transposing, the eight rows of a cycle on distinct banks.
+// Strips: 16 columns of B as N x K, 32 as K x N; the strips beside it, which
+// share its lines, run on the same XCD.
 #include "common.h"
 #include "linear.h"
 
@@ -42,14 +48,6 @@ struct OpBrain : Brain16 {
     }
 };
 
-// Eight elements of row r from column c of a rows x cols matrix, zero outside.
-__device__ __forceinline__ u32x4 load_unit(const uint16_t *p, size_t ld, int r, int rows, int c, int cols)
-{
-    if (r >= rows || c >= cols)
-        return u32x4{0u, 0u, 0u, 0u};
-    return load8_16(p + (size_t)r * ld + c, cols - c);
-}
-
 constexpr int kWaves = 8;
 
 // RB: 16-row blocks of A; CB: 16-column blocks of a strip.  A gated product's
@@ -57,11 +55,12 @@ constexpr int kWaves = 8;
 template <class Op, int RB, int CB, bool TB, bool GATED, int UNROLL>
 __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
 {
-    constexpr int NB = GATED ? 2 * CB : CB;
+    constexpr int NM = GATED ? 2 : 1, NB = NM * CB;         // matrices B, column blocks
+    static_assert(TB || CB == 2, "a K x N strip is 32 columns");
     constexpr int PITCH = 16 * NB + 4;                      // floats; spreads four-row groups over the banks
     constexpr int SUMS = kWaves * RB * 16 * PITCH * 4;      // bytes
-    constexpr int TURN = TB ? 0 : kWaves * 2 * NB * 1024;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[SUMS > TURN ? SUMS : TURN];
+    constexpr int TURN = (RB + NB) * 2048;                  // a wavefront's chunk
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[SUMS > kWaves * TURN ? SUMS : kWaves * TURN];
     const int M = p.M, N = p.N, K = p.K;
     int none, strip;
     dgor_tile_of_block((int)blockIdx.x, 1, p.tiles_n, 1, none, strip);
@@ -69,39 +68,46 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
     const int lane = threadIdx.x & 63, s16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int per_seg = (K + 63) / 64, chunks = p.nseg * per_seg;
-    const int pos = lane >> 1;                              // row position of this lane's piece of B as K x N
-    const int krow = pos < 16 ? 8 * (pos >> 2) + (pos & 3) : 8 * ((pos - 16) >> 2) + 4 + (pos & 3);
+    const int r8 = lane >> 3, c8 = 8 * (lane & 7);          // of 8 rows x 64 k
+    const int r16 = lane >> 2, c4 = 8 * (lane & 3);         // of 16 rows x 32 columns
 
-    u32x4 w[UNROLL][2][NB], x[UNROLL][2][RB];
+    u32x4 w[UNROLL][2 * NB], x[UNROLL][2 * RB];
     auto fetch = [&](int c0, bool whole) {
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int c = c0 + kWaves * u, seg = c >= per_seg ? p.nseg - 1 : 0;
             const int k0 = 64 * (c - seg * per_seg);
             const uint16_t *A = p.A[seg];
+            if (!whole && c >= chunks) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = k0 + 32 * h;
+                for (int i = 0; i < 2 * NB; ++i)
+                    w[u][i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint16_t *B = p.B[GATED ? b / CB : seg];
-                    const int n = n0 + 16 * (b % CB);
-                    if (TB) {
-                        w[u][h][b] = whole ? load8_16(B + (size_t)(n + s16) * p.ldb + k + 8 * g, 8)
-                                           : load_unit(B, p.ldb, n + s16, N, k + 8 * g, K);
-                    } else {
-                        const int col = n + 8 * (lane & 1);
-                        w[u][h][b] = whole ? load8_16(B + (size_t)(k + krow) * p.ldb + col, 8)
-                                           : load_unit(B, p.ldb, k + krow, K, col, N);
-                    }
-                }
+                for (int i = 0; i < 2 * RB; ++i)
+                    x[u][i] = u32x4{0u, 0u, 0u, 0u};
+                continue;
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 2 * NB; ++i) {
+                // TB: rows 8 (i % 2 CB) .. of matrix i / (2 CB); else load i % 4 of matrix i / 4
+                const uint16_t *B = p.B[GATED ? i / (2 * CB) : seg];
+                const int j = i % (2 * CB);
+                const int row = TB ? n0 + 8 * j + r8 : k0 + 32 * (j >> 1) + 4 * (j & 1) + 8 * (r16 >> 2) + (r16 & 3);
+                const int col = TB ? k0 + c8 : n0 + c4;
+                w[u][i] = whole ? load8_16(B + (size_t)row * p.ldb + col, 8)
+                                : load_unit(B, p.ldb, row, TB ? N : K, col, TB ? K : N);
+            }
 #pragma unroll
-                for (int i = 0; i < RB; ++i)
-                    x[u][h][i] = load_unit(A, p.lda, 16 * i + s16, M, k0 + 32 * h + 8 * g,
-                                           whole ? 0x7fffffff : K);
+            for (int i = 0; i < 2 * RB; ++i) {
+                const int row = 8 * i + r8;
+                if (whole) {
+                    x[u][i] = u32x4{0u, 0u, 0u, 0u};
+                    if (row < M)
+                        x[u][i] = load8_16(A + (size_t)row * p.lda + k0 + c8, 8);
+                } else {
+                    x[u][i] = load_unit(A, p.lda, row, M, k0 + c8, K);
+                }
+            }
         }
     };
     floatx4 acc[RB][NB];
@@ -110,6 +116,8 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
             acc[i][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+    uint8_t *const xl = lds + wave * TURN, *const wl = xl + RB * 2048;
+    auto row_slot = [&](int r) { return 16 * (8 * r + ((lane & 7) ^ ((r >> 1) & 7))); };
     for (int c0 = wave; c0 < chunks; c0 += kWaves * UNROLL) {
         const int last = c0 + kWaves * (UNROLL - 1);
         const bool full_k = p.nseg == 1 ? 64 * (last + 1) <= K : K % 64 == 0 && last < chunks;
@@ -119,41 +127,50 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
             fetch(c0, false);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            if (!TB) {
-                uint8_t *mine = lds + wave * 2 * NB * 1024;
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 2 * NB; ++i)
+                *reinterpret_cast<u32x4 *>(wl + (TB ? row_slot(8 * i + r8)
+                                                    : 1024 * i + 64 * r16 + 16 * ((lane & 3) ^ (2 * ((r16 >> 2) & 1))))) =
+                    w[u][i];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<u32x4 *>(mine + (h * NB + b) * 1024 + 16 * lane) = w[u][h][b];
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
+            for (int i = 0; i < 2 * RB; ++i)
+                *reinterpret_cast<u32x4 *>(xl + row_slot(8 * i + r8)) = x[u][i];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                auto of_rows = [&](const uint8_t *at) {
+                    return *reinterpret_cast<const u32x4 *>(at + 16 * (8 * s16 + ((4 * h + g) ^ ((s16 >> 1) & 7))));
+                };
+                u32x4 a[RB], b[NB];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint8_t *q = mine + (h * NB + b) * 1024 + 8 * lane;
+                for (int i = 0; i < RB; ++i)
+                    a[i] = of_rows(xl + 2048 * i);
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    if (TB) {
+                        b[j] = of_rows(wl + 2048 * j);
+                    } else {
+                        const uint8_t *q = wl + 4096 * (j / 2) + 2048 * h + 64 * (4 * g + (s16 >> 2)) +
+                                           16 * ((2 * (j % 2) + ((s16 & 3) >> 1)) ^ (2 * (g & 1))) + 8 * (s16 & 1);
                         const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
-                        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 512));
-                        w[u][h][b] =
-                            __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 1024));
+                        b[j] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                     }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+                }
 #pragma unroll
                 for (int i = 0; i < RB; ++i)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        acc[i][b] = Op::mfma(x[u][h][i], w[u][h][b], acc[i][b]);
+                    for (int j = 0; j < NB; ++j)
+                        acc[i][j] = Op::mfma(a[i], b[j], acc[i][j]);
+            }
         }
     }
 
     // the wavefronts' sums, added in their order
-    if (!TB)
-        __syncthreads();
+    __syncthreads();
     float *sums = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int i = 0; i < RB; ++i)
@@ -186,49 +203,48 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
     }
 }
 
-template <class Op, int RB, int CB, bool TB, bool GATED>
+template <class Op, int RB, bool TB, bool GATED>
 hipError_t launch_rows(const Product &p, hipStream_t s)
 {
-    // loads in flight: 16 of B and as many of A for one row block, what the
-    // registers hold beyond it
-    constexpr int UNROLL = RB == 1 && CB == 1 && !GATED ? 8 : 4;
+    // 16-byte loads in flight, a lane: up to 40, what the registers hold
+    constexpr int CB = TB ? 1 : 2, EACH = 2 * (RB + CB * (GATED ? 2 : 1));
+    constexpr int UNROLL = EACH <= 4 ? 8 : (EACH <= 10 ? 4 : (EACH <= 14 ? 2 : 1));
     hipLaunchKernelGGL((linear_skinny_kernel<Op, RB, CB, TB, GATED, UNROLL>), dim3((unsigned)p.tiles_n),
                        dim3(64 * kWaves), 0, s, p);
     return hipGetLastError();
 }
 
-template <class Op, int CB, bool TB, bool GATED>
+template <class Op, bool TB, bool GATED>
 hipError_t launch_blocks(const Product &p, hipStream_t s)
 {
     switch ((p.M + 15) / 16) {
-    case 1: return launch_rows<Op, 1, CB, TB, GATED>(p, s);
-    case 2: return launch_rows<Op, 2, CB, TB, GATED>(p, s);
-    case 3: return launch_rows<Op, 3, CB, TB, GATED>(p, s);
-    case 4: return launch_rows<Op, 4, CB, TB, GATED>(p, s);
+    case 1: return launch_rows<Op, 1, TB, GATED>(p, s);
+    case 2: return launch_rows<Op, 2, TB, GATED>(p, s);
+    case 3: return launch_rows<Op, 3, TB, GATED>(p, s);
+    case 4: return launch_rows<Op, 4, TB, GATED>(p, s);
     default: return hipErrorInvalidValue;
     }
 }
 
 template <class Op>
-hipError_t launch_op(const Product &p, int strip, hipStream_t s)
+hipError_t launch_op(const Product &p, hipStream_t s)
 {
     if (p.gated)
-        return p.trans_b ? launch_blocks<Op, 1, true, true>(p, s) : launch_blocks<Op, 1, false, true>(p, s);
-    if (strip == 32)
-        return p.trans_b ? launch_blocks<Op, 2, true, false>(p, s) : launch_blocks<Op, 2, false, false>(p, s);
-    return p.trans_b ? launch_blocks<Op, 1, true, false>(p, s) : launch_blocks<Op, 1, false, false>(p, s);
+        return p.trans_b ? launch_blocks<Op, true, true>(p, s) : launch_blocks<Op, false, true>(p, s);
+    return p.trans_b ? launch_blocks<Op, true, false>(p, s) : launch_blocks<Op, false, false>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_linear_skinny(const Product &q, int strip, hipStream_t s)
+hipError_t launch_linear_skinny(const Product &q, hipStream_t s)
 {
     Product p = q;
-    if (p.trans_a || p.nbatch != 1 || p.M > kSkinnyRows || (strip != 16 && (strip != 32 || p.gated)))
+    if (p.trans_a || p.nbatch != 1 || p.M > kSkinnyRows)
         return hipErrorInvalidValue;
+    const int strip = p.trans_b ? 16 : 32;
     p.tiles_m = 1;
     p.tiles_n = (p.N + strip - 1) / strip;
-    return p.bf16 ? launch_op<OpBrain>(p, strip, s) : launch_op<OpHalf>(p, strip, s);
+    return p.bf16 ? launch_op<OpBrain>(p, s) : launch_op<OpHalf>(p, s);
 }
 
 }  // namespace dgor

@@ -11,8 +11,8 @@
 //     2 ((k >> 1) & 1) + 4 ((k >> 3) & 1) for W = 8: the eight k rows that a
 //     cycle of a transposing read takes two units of fall on distinct units
 //     modulo 16.
-// Global loads take 16 bytes at any element address; only the units that an
-// edge of the matrix cuts are read element by element.
+// Global loads take 16 bytes at any element address; a stage that an edge of
+// the matrix cuts masks them, without a branch on the lane.
 #include "common.h"
 #include "linear.h"
 
@@ -38,14 +38,6 @@ struct OpBrain : Brain16 {
                                                        c, 0, 0, 0);
     }
 };
-
-// Eight elements of row r from column c of a rows x cols matrix, zero outside.
-__device__ __forceinline__ u32x4 load_unit(const uint16_t *p, size_t ld, int r, int rows, int c, int cols)
-{
-    if (r >= rows || c >= cols)
-        return u32x4{0u, 0u, 0u, 0u};
-    return load8_16(p + (size_t)r * ld + c, cols - c);
-}
 
 template <int W>
 __device__ __forceinline__ int strided_swizzle(int k)
@@ -86,26 +78,33 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
         return n0 + (GATED ? (j / WT) * (WT / 2) + j % (WT / 2) : j);
     };
     u32x4 ra[UNITS], rb[UNITS];
-    auto load_stage = [&](int t) {
-        const int seg = t >= per_seg ? 1 : 0;
-        const int k0 = (t - seg * per_seg) * BK;
-        const uint16_t *A = p.A[seg | batch];
+    const bool inside = m0 + BT <= M && n0 + FT <= N;
+    auto fetch = [&](const uint16_t *A, const uint16_t *B0, const uint16_t *B1, int k0, bool whole) {
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             const int u = tid + 256 * i;
-            if (TA)
-                ra[i] = load_unit(A, p.lda, k0 + u / W, K, m0 + 8 * (u % W), M);
-            else
-                ra[i] = load_unit(A, p.lda, m0 + u / 8, M, k0 + 8 * (u % 8), K);
             int which;
-            if (TB) {
-                const int n = b_col(u / 8, which);
-                rb[i] = load_unit(p.B[GATED ? which : seg | batch], p.ldb, n, N, k0 + 8 * (u % 8), K);
+            const int n = TB ? b_col(u / 8, which) : b_col(8 * (u % W), which);
+            const int ar = TA ? k0 + u / W : m0 + u / 8, ac = TA ? m0 + 8 * (u % W) : k0 + 8 * (u % 8);
+            const int br = TB ? n : k0 + u / W, bc = TB ? k0 + 8 * (u % 8) : n;
+            const uint16_t *B = GATED && which ? B1 : B0;
+            if (whole) {
+                ra[i] = load8_16(A + (size_t)ar * p.lda + ac, 8);
+                rb[i] = load8_16(B + (size_t)br * p.ldb + bc, 8);
             } else {
-                const int n = b_col(8 * (u % W), which);
-                rb[i] = load_unit(p.B[GATED ? which : seg | batch], p.ldb, k0 + u / W, K, n, N);
+                ra[i] = load_unit(A, p.lda, ar, TA ? K : M, ac, TA ? M : K);
+                rb[i] = load_unit(B, p.ldb, br, TB ? N : K, bc, TB ? K : N);
             }
         }
+    };
+    auto load_stage = [&](int t) {
+        const int seg = t >= per_seg ? 1 : 0;
+        const int k0 = (t - seg * per_seg) * BK;
+        const uint16_t *A = p.A[seg | batch], *B0 = p.B[GATED ? 0 : seg | batch];
+        if (inside && k0 + BK <= K)
+            fetch(A, B0, p.B[1], k0, true);
+        else
+            fetch(A, B0, p.B[1], k0, false);
     };
     auto slot = [&](bool strided, int u) {
         return strided ? W * (u / W) + ((u % W) ^ strided_swizzle<W>(u / W)) : 8 * (u / 8) + ((u % 8) ^ ((u / 16) & 7));
