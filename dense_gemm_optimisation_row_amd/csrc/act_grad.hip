@@ -1,4 +1,5 @@
-// The element-wise part of the dense layers' backward passes: the gradient
+// The element-wise work around the dense layers' products: copies of operands
+// whose rows are not whole 16-byte units, and of the backward passes the gradient
 // of the pre-activations, rounded to the 16-bit format that the matrix
 // cores take, and the bias gradient's column sums of the unrounded values.
 //
@@ -45,8 +46,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint1
                     d[e] *= slope;
                 }
             }
-            if (dz)
-                store8_16(dz + (size_t)row * lddz + col, n, pack8<Fmt>(d));
+            if (dz)   // past N zeros: its rows are padded to whole units
+                store8_16(dz + (size_t)row * lddz + col, 8, pack8<Fmt>(d));
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 total[e] += d[e];
@@ -115,12 +116,41 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
             a[e] = d[e] * y[e] * slope;
             b[e] = d[e] * value;
         }
-        store8_16(dg + (size_t)row * ldd + col, n, pack8<Fmt>(a));
-        store8_16(du + (size_t)row * ldd + col, n, pack8<Fmt>(b));
+        store8_16(dg + (size_t)row * ldd + col, 8, pack8<Fmt>(a));   // past F zeros
+        store8_16(du + (size_t)row * ldd + col, 8, pack8<Fmt>(b));
     }
 }
 
+// Eight elements a thread: a unit read at any alignment, written whole.
+__global__ __launch_bounds__(256) void repack_kernel(Repack r, unsigned units)
+{
+    const unsigned id = blockIdx.x * 256 + threadIdx.x;
+    if (id >= units)
+        return;
+    Repack::Job j = r.job[0];
+#pragma unroll
+    for (int i = 1; i < 3; ++i)
+        if (i < r.jobs && id >= r.job[i].first)
+            j = r.job[i];
+    const unsigned per = (unsigned)(j.cols + 7) / 8, u = id - j.first, row = u / per;
+    const int col = 8 * (int)(u - row * per);
+    store8_16(j.to + (size_t)row * j.ld_to + col, 8, load8_16(j.from + (size_t)row * j.ld + col, j.cols - col));
+}
+
 }  // namespace
+
+hipError_t launch_repack(const Repack &q, hipStream_t s)
+{
+    Repack r = q;
+    unsigned units = 0;
+    for (int i = 0; i < r.jobs; ++i) {
+        r.job[i].first = units;
+        units += (unsigned)r.job[i].rows * (unsigned)((r.job[i].cols + 7) / 8);
+    }
+    if (units)
+        hipLaunchKernelGGL(repack_kernel, dim3((units + 255) / 256), dim3(256), 0, s, r, units);
+    return hipGetLastError();
+}
 
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
                            int lddz, int act, float *sums, bool bf16, hipStream_t s)

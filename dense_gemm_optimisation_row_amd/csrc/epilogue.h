@@ -56,35 +56,61 @@ __device__ __forceinline__ void store8_16(uint16_t *p, int n, u32x4 v)
         if (e < n)
             p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
 }
-// Eight elements of row r from column c of a rows x cols matrix (neither
-// zero), zero outside.  Without a branch on the lane, so that a wavefront's
-// loads stay in flight together: a unit that an edge cuts is read from where
-// its row still holds eight elements and shifted into place.
-__device__ __forceinline__ u32x4 load_unit(const uint16_t *p, size_t ld, int r, int rows, int c, int cols)
-{
-    const uint16_t *row = p + (size_t)(r < rows ? r : rows - 1) * ld;
-    u32x4 v;
-    if (cols < 8) {   // shorter rows than a unit: the same for every lane
-        v = load8_16(row, cols);
-        if (c > 0)    // c is a multiple of 8
-            v = u32x4{0u, 0u, 0u, 0u};
-    } else {
-        const int at = c < cols - 8 ? c : cols - 8, off = c - at;
-        v = *reinterpret_cast<const u32x4_at2 *>(row + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = off & 1 ? __builtin_amdgcn_alignbit(i < 3 ? v[i < 3 ? i + 1 : 3] : 0u, v[i], 16) : v[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = off & 2 ? (i < 3 ? v[i < 3 ? i + 1 : 3] : 0u) : v[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = off & 4 ? (i < 2 ? v[i < 2 ? i + 2 : 3] : 0u) : v[i];
-        if (off >= 8)
-            v = u32x4{0u, 0u, 0u, 0u};
+// A 16-bit operand as its units are loaded: rows x cols, at least eight
+// elements from its first to its last.
+//
+// A unit is eight elements of row r from column c, a multiple of 8; what is
+// outside the matrix counts as zero.  load reads the unit from the nearest
+// place where the matrix holds eight elements (of the row, or across rows
+// shorter than a unit); settle, when the load has arrived, shifts it into
+// place and clears what is outside.  The load has no branch, so that a
+// wavefront's loads stay in flight together, and a unit inside the matrix
+// needs no settling.
+struct Operand {
+    const uint16_t *p;
+    int rows, cols;
+    size_t ld;
+
+    __device__ __forceinline__ size_t row_at(int r) const { return (size_t)min(r, rows - 1) * ld; }
+    __device__ __forceinline__ size_t last() const { return (size_t)(rows - 1) * ld + cols - 8; }
+    __device__ __forceinline__ u32x4 load(int r, int c) const
+    {
+        size_t at = row_at(r);
+        if (cols >= 8)
+            at += min(c, cols - 8);
+        else
+            at = min(at, last());
+        return *reinterpret_cast<const u32x4_at2 *>(p + at);
     }
-    return r < rows ? v : u32x4{0u, 0u, 0u, 0u};
-}
+    __device__ __forceinline__ u32x4 settle(u32x4 v, int r, int c) const
+    {
+        int off;
+        bool keep = r < rows;
+        if (cols >= 8) {
+            off = c - min(c, cols - 8);
+            keep = keep && off < 8;
+        } else {
+            off = (int)(row_at(r) - min(row_at(r), last()));
+            keep = keep && c == 0;
+        }
+        const uint32_t half = 16u * (off & 1), m2 = -(uint32_t)(off >> 1 & 1), m4 = -(uint32_t)(off >> 2 & 1);
+        uint32_t d[8] = {v[0], v[1], v[2], v[3], 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] = (d[i + 1] & m2) | (d[i] & ~m2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = keep ? (d[i + 2] & m4) | (d[i] & ~m4) : 0u;
+        if (cols < 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] &= 2 * i + 1 < cols ? ~0u : (2 * i < cols ? 0xffffu : 0u);
+        return v;
+    }
+};
 
 template <class Fmt>
 __device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8])

@@ -27,6 +27,7 @@ struct Product {
     const uint16_t *B[2];
     int lda, ldb;
     bool bf16, trans_a, trans_b, gated;
+    bool units;   // the operands' rows are whole 16-byte units, or padded to them
     int nseg, nbatch;
     Epilogue e;
     void *Y1;
@@ -38,17 +39,44 @@ struct Product {
 constexpr int kStageDepth = 64;   // k per stage, the unit of Product::chunk
 inline int product_stages(const Product &p) { return p.nseg * ((p.K + kStageDepth - 1) / kStageDepth); }
 
-// The register-staged tiles (64 or 128; any operands), and the rings (128 or
-// 256; 16-byte aligned operands whose rows are whole 16-byte units, strides
-// below 2^22).
-hipError_t launch_tile(const Product &p, int tile, hipStream_t stream);
-hipError_t launch_linear_ring(const Product &p, int tile, hipStream_t stream);
-// Few rows (at most kSkinnyRows, A as M x K, one product).
+// The register-staged tile (any operands).
+constexpr int kTile = 64;
+hipError_t launch_tile(const Product &p, hipStream_t stream);
+
+// The rings: 16-byte aligned operands, rows of whole units of eight elements
+// (or padded to them: the padding is read, zeros along k), strides below
+// 2^22 and multiples of 8.
+enum RingTile { kRing256, kRing256x128, kRing128, kRing64 };
+constexpr int ring_tile_m(RingTile t) { return t == kRing64 ? 64 : (t == kRing128 ? 128 : 256); }
+constexpr int ring_tile_n(RingTile t) { return t == kRing64 ? 64 : (t == kRing256 ? 256 : 128); }
+hipError_t launch_linear_ring(const Product &p, RingTile tile, hipStream_t stream);
+
+// Few rows (at most kSkinnyRows, A as M x K, one product); each operand at
+// least eight elements from its first to its last.
 constexpr int kSkinnyRows = 64;
+inline bool spans_a_unit(const Product &p)
+{
+    const long long b_rows = p.trans_b ? p.N : p.K, b_cols = p.trans_b ? p.K : p.N;
+    return (long long)(p.M - 1) * p.lda + p.K >= 8 && (b_rows - 1) * p.ldb + b_cols >= 8;
+}
 hipError_t launch_linear_skinny(const Product &p, hipStream_t stream);
+
+// Copies of operands whose rows are not whole units, padded to them with zeros.
+struct Repack {
+    int jobs;
+    struct Job {
+        const uint16_t *from;
+        uint16_t *to;
+        int rows, cols, ld, ld_to;
+        unsigned first;   // the job's first unit in the launch; filled by the launcher
+    } job[3];
+};
+hipError_t launch_repack(const Repack &r, hipStream_t stream);
+
 hipError_t launch_join(const Product &p, hipStream_t stream);
 
-// dZ = dY act'(Z) (Z null: dZ = dY, nothing written unless dz) and, with
+// dZ = dY act'(Z) (Z null: dZ = dY, nothing written unless dz; rows padded
+// with zeros to whole units) and, with
 // sums, each row block's column sums of the unrounded dZ in FP32 to
 // sums[block][N], blocks of kGradRows rows.
 constexpr int kGradRows = 64;
@@ -56,7 +84,7 @@ hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uin
                            int lddz, int act, float *sums, bool bf16, hipStream_t stream);
 // out[c] = sum over blocks of sums[block][c], in the input format.
 hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out, bool bf16, hipStream_t stream);
-// dG = dH U act'(G), dU = dH act(G).
+// dG = dH U act'(G), dU = dH act(G), padded likewise.
 hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u,
                             int ldp, uint16_t *dg, uint16_t *du, int ldd, int act, bool bf16, hipStream_t stream);
 

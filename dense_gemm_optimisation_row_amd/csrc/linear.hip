@@ -22,69 +22,110 @@ bool op_ok(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 bool act_ok(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
 bool missing(const void *p, long long rows, long long cols) { return rows > 0 && cols > 0 && !p; }
 
-// How a product runs: the kernel, the tile and, where its tiles
-// leave compute units idle, into how many parts the sum over k is split.
-enum Kernel { kSkinny, kRing, kTile };
+// How a product runs: the kernel, a ring's tile and, where its tiles leave
+// compute units idle, into how many parts the sum over k is split.
+enum class Kernel { Rows, Ring, Tile };
 struct Way {
     Kernel kernel;
-    int tile, splits, chunk;
+    dgor::RingTile tile;
+    int splits, chunk;
 };
 
-long long tiles(const Product &p, int t)
+long long tiles(const Product &p, int tm, int tn)
 {
-    const int ft = p.gated ? t / 2 : t;
-    return (long long)ceil_div(p.M, t) * ceil_div(p.N, ft) * p.nbatch;
+    return (long long)ceil_div(p.M, tm) * ceil_div(p.N, p.gated ? tn / 2 : tn) * p.nbatch;
 }
 
-// Whether sizes and strides let the rings run (the addresses apart): rows of
-// whole 16-byte units, lane offsets within a tile below 2^31.
+// Whether the few-row kernel takes a product.
+bool few_rows(const Product &p)
+{
+    return !p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows && dgor::spans_a_unit(p);
+}
+
+// Whether sizes and strides let the rings run (the addresses apart).
 bool ring_sizes(const Product &p)
 {
     const auto ok = [](int ld) { return ld % 8 == 0 && ld < (1 << 22); };
-    const int a_row = p.trans_a ? p.M : p.K, b_row = p.trans_b ? p.K : p.N;
-    return ok(p.lda) && ok(p.ldb) && a_row % 8 == 0 && b_row % 8 == 0;
+    return p.units && ok(p.lda) && ok(p.ldb);
 }
 bool ring_addresses(const Product &p)
 {
     return (((uintptr_t)p.A[0] | (uintptr_t)p.A[1] | (uintptr_t)p.B[0] | (uintptr_t)p.B[1]) & 15) == 0;
 }
 
-// Fewer tiles than compute units: split k until two workgroups a unit,
-// keeping at least four stages a part.
-void split_over_k(const Product &p, Way &w)
+void split(const Product &p, long long parts, Way &w)
 {
-    const long long n = tiles(p, w.tile);
-    const int stages = dgor::product_stages(p);
-    if (n <= 0 || n >= 256 || stages < 8)
-        return;
-    long long want = 512 / n;
-    want = want < stages / 4 ? want : stages / 4;
-    want = want < 16 ? want : 16;
-    if (want > 1) {
-        w.chunk = ceil_div(stages, want);
-        w.splits = ceil_div(stages, w.chunk);
+    w.splits = 1, w.chunk = 0;
+    if (parts > 1) {
+        w.chunk = ceil_div(dgor::product_stages(p), parts);
+        w.splits = ceil_div(dgor::product_stages(p), w.chunk);
     }
+}
+
+// Estimated cycles of a product on a ring's tile with its sum in `parts`: each
+// compute unit holds `share` workgroups of the tile at once, a stage of 32 k
+// of one takes `alone` cycles by itself and `full` of the unit when its share
+// is there, a workgroup's beginning and end `ends`; parts are written in
+// FP32 and joined by another launch (measured: 1500 bytes a cycle there and
+// back, and 9000 cycles).
+struct RingCost {
+    dgor::RingTile tile;
+    int share, alone, full, ends;
+};
+constexpr RingCost kRings[] = {
+    {dgor::kRing256, 1, 1150, 1150, 7000},
+    {dgor::kRing256x128, 1, 640, 640, 5000},
+    {dgor::kRing128, 2, 420, 340, 4000},
+    {dgor::kRing64, 4, 260, 110, 3000},
+};
+double cycles(const Product &p, const RingCost &c, int parts)
+{
+    const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
+    const double stages = 2.0 * dgor::product_stages(p) / parts;
+    const long long rounds = n / (256LL * c.share), rest = n - rounds * 256LL * c.share;
+    const double whole = c.full * c.share > c.alone ? c.full * c.share : c.alone;
+    const double last = c.full * ceil_div(rest, 256);
+    double t = rounds * (stages * whole + c.ends);
+    if (rest)
+        t += stages * (last > c.alone ? last : c.alone) + c.ends;
+    if (parts > 1)
+        t += 9000 + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / 1500;
+    return t;
 }
 
 Way choose(const Product &p, bool ring)
 {
-    Way w{ring ? kRing : kTile, 128, 1, 0};
-    if (!p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows)
-        return Way{kSkinny, 0, 1, 0};
+    Way w{Kernel::Rows, dgor::kRing64, 1, 0};
+    if (few_rows(p))
+        return w;
+    const int stages = dgor::product_stages(p);
     if (ring) {
-        // cycles of a compute unit: a 256 tile's stage of 32 k is 1024 of its
-        // matrix cores, four 128 tiles' the same at a lower rate, two at a time
-        const long long stages = 2LL * dgor::product_stages(p), n256 = tiles(p, 256), n128 = tiles(p, 128);
-        const long long c256 = (n256 + 255) / 256 * (stages * 1024 + 4000);
-        const long long c128 = n128 <= 256 ? stages * 420 + 3000 : (n128 + 511) / 512 * (stages * 660 + 3000);
-        if (c256 <= c128) {
-            w.tile = 256;
-            return w;
+        w.kernel = Kernel::Ring;
+        double best = 0;
+        int best_parts = 1;
+        for (const RingCost &c : kRings) {
+            // parts until two workgroups wait for each place, at least four
+            // stages of 64 k each
+            const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile));
+            for (int parts = 1; parts == 1 || (parts <= 16 && 4 * parts <= stages && n * parts <= 512 * c.share);
+                 ++parts) {
+                const double t = cycles(p, c, parts);
+                if (best == 0 || t < best)
+                    best = t, best_parts = parts, w.tile = c.tile;
+            }
         }
-    } else if (tiles(p, 128) < 512) {
-        w.tile = 64;
+        split(p, best_parts, w);
+        return w;
     }
-    split_over_k(p, w);
+    // the plain tile: split until two workgroups a compute unit, keeping at
+    // least four stages a part
+    w.kernel = Kernel::Tile;
+    const long long n = tiles(p, dgor::kTile, dgor::kTile);
+    if (n > 0 && n < 256 && stages >= 8) {
+        long long want = 512 / n;
+        want = want < stages / 4 ? want : stages / 4;
+        split(p, want < 16 ? want : 16, w);
+    }
     return w;
 }
 
@@ -110,14 +151,59 @@ hipError_t run_product(Product p, void *ws, hipStream_t s)
     p.splits = w.splits;
     p.chunk = w.chunk;
     p.part = (float *)ws;
-    if (w.kernel == kSkinny)
+    if (w.kernel == Kernel::Rows)
         return dgor::launch_linear_skinny(p, s);
     const hipError_t err =
-        w.kernel == kRing ? dgor::launch_linear_ring(p, w.tile, s) : dgor::launch_tile(p, w.tile, s);
+        w.kernel == Kernel::Ring ? dgor::launch_linear_ring(p, w.tile, s) : dgor::launch_tile(p, s);
     if (err != hipSuccess || p.splits <= 1)
         return err;
     return dgor::launch_join(p, s);
 }
+
+// Operands that are copied at the front of the workspace, their rows padded
+// to whole units for the rings: those whose rows or strides are not.  (1000 x
+// 777 by 777 x 1033 on the plain tile, whose loads then fall off dwords: 22
+// us; copied and on the ring: see kRings' figures.)
+struct Copies {
+    dgor::Repack r{};
+    size_t at[3] = {}, bytes = 0;
+    bool units = true;   // the operands' rows are whole units, or padded to them
+
+    // A stored matrix; returns its index here, -1 where it is used as it is.
+    // ld becomes the stride of what the products will read.
+    int add(int rows, int cols, int &ld)
+    {
+        if ((ld % 8 == 0 && cols % 8 == 0 && ld < (1 << 22)) || rows == 0 || cols == 0)
+            return -1;
+        if ((long long)rows * ceil_div(cols, 8) >= (1LL << 30)) {   // a launch's units are counted in 32 bits
+            units = false;
+            return -1;
+        }
+        const int i = r.jobs++;
+        r.job[i] = {nullptr, nullptr, rows, cols, ld, (int)round_up((size_t)cols, 8), 0u};
+        at[i] = bytes;
+        bytes += round_up((size_t)rows * r.job[i].ld_to * 2, kWsAlign);
+        ld = r.job[i].ld_to;
+        return i;
+    }
+    // Marks copy i (or none) for launch; returns where the operand will be.
+    const uint16_t *use(int i, const uint16_t *from, uint8_t *ws)
+    {
+        if (i < 0)
+            return from;
+        r.job[i].from = from;
+        r.job[i].to = (uint16_t *)(ws + at[i]);
+        return r.job[i].to;
+    }
+    hipError_t launch(hipStream_t s)
+    {
+        dgor::Repack q{};
+        for (int i = 0; i < r.jobs; ++i)
+            if (r.job[i].from)
+                q.job[q.jobs++] = r.job[i];
+        return q.jobs ? dgor::launch_repack(q, s) : hipSuccess;
+    }
+};
 
 Product plain_product(int M, int N, int K)
 {
@@ -154,6 +240,22 @@ Product weight_gradient_product(int M, int N, int K, int op_w, int ldx, int lddz
     return p;
 }
 
+// The copies of a forward product's A and its one or two B.
+void copy_operands(Product &p, Copies &c, int (&copy)[3])
+{
+    copy[0] = copy[1] = copy[2] = -1;
+    if (p.M == 0 || p.N == 0 || few_rows(p))
+        return;
+    const int rows = p.trans_b ? p.N : p.K, cols = p.trans_b ? p.K : p.N, ld = p.ldb;
+    copy[0] = c.add(p.M, p.K, p.lda);
+    copy[1] = c.add(rows, cols, p.ldb);
+    if (p.gated) {
+        int again = ld;
+        copy[2] = c.add(rows, cols, again);
+    }
+    p.units = c.units;
+}
+
 bool workspace_ok(const void *ws, size_t have, size_t need)
 {
     return need == 0 || (ws && have >= need && ((uintptr_t)ws & (kWsAlign - 1)) == 0);
@@ -163,7 +265,7 @@ int done(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
 // ------------------------------------------------------------ dense layer --
 
-int check_linear(const gemm_linear_params *q, Product &p)
+int check_linear(const gemm_linear_params *q, Product &p, Copies &c, int (&copy)[3])
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
@@ -174,6 +276,7 @@ int check_linear(const gemm_linear_params *q, Product &p)
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
     p = forward_product(q->M, q->N, q->K, q->op_w, q->ldx, q->ldw, false);
+    copy_operands(p, c, copy);
     return GEMM_OK;
 }
 
@@ -181,7 +284,9 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
                const void *R, void *Y, uint16_t *pre, void *ws, size_t ws_bytes, void *stream)
 {
     Product p;
-    const int rc = check_linear(q, p);
+    Copies c;
+    int copy[3];
+    const int rc = check_linear(q, p, c, copy);
     if (rc != GEMM_OK)
         return rc;
     if ((R && !ld_ok(q->ldr, q->N)) || (pre && !ld_ok(q->ldp, q->N)))
@@ -190,24 +295,29 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
         return GEMM_ERR_NULL_PTR;
     if (q->M == 0 || q->N == 0)
         return GEMM_OK;
-    if (!workspace_ok(ws, ws_bytes, part_bytes(p)))
+    if (!workspace_ok(ws, ws_bytes, c.bytes + part_bytes(p)))
         return GEMM_ERR_WORKSPACE;
     const int dev = dgor::device_status();
     if (dev != GEMM_OK)
         return dev;
+    uint8_t *base = (uint8_t *)ws;
+    hipStream_t s = (hipStream_t)stream;
     p.bf16 = bf16;
-    p.A[0] = p.A[1] = X;
-    p.B[0] = p.B[1] = W;
+    p.A[0] = p.A[1] = c.use(copy[0], X, base);
+    p.B[0] = p.B[1] = c.use(copy[1], W, base);
     p.e.Y = Y, p.e.ldy = q->ldy, p.e.y_f32 = q->y_f32 != 0;
     p.e.bias = bias, p.e.act = q->activation;
     p.e.R = R, p.e.ldr = q->ldr;
     p.e.pre = pre, p.e.ldp = q->ldp;
-    return done(run_product(p, ws, (hipStream_t)stream));
+    const hipError_t err = c.launch(s);
+    return done(err == hipSuccess ? run_product(p, base + c.bytes, s) : err);
 }
 
-// Workspace of the dense layer's backward pass: dZ, the column sums of each
-// row block, and the partial sums of whichever product is running.
+// Workspace of the dense layer's backward pass: copies, dZ, the column sums of
+// each row block, and the partial sums of whichever product is running.
 struct BackwardLayout {
+    Copies c;
+    int copy_dy, copy_x, copy_w;
     int lddz;
     size_t dz, sums, part, bytes;   // offsets, and the whole size
 };
@@ -224,11 +334,18 @@ int check_linear_backward(const gemm_linear_backward_params *q, Product &px, Pro
         return GEMM_ERR_INVALID_LAYOUT;
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
-    l.lddz = q->activation == GEMM_ACT_NONE ? q->lddy : (int)round_up((size_t)q->N, 8);
-    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, q->ldw, 1);
-    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, q->ldx, l.lddz, 1);
-    l.dz = 0;
-    l.sums = q->activation == GEMM_ACT_NONE ? 0 : round_up((size_t)q->M * l.lddz * 2, kWsAlign);
+    const bool act = q->activation != GEMM_ACT_NONE, t = q->op_w == GEMM_OP_T;
+    int ldx = q->ldx, ldw = q->ldw;
+    l.lddz = act ? (int)round_up((size_t)q->N, 8) : q->lddy;
+    l.copy_dy = act ? -1 : l.c.add(q->M, q->N, l.lddz);
+    l.copy_x = l.c.add(q->M, q->K, ldx);
+    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1);
+    l.copy_w = few_rows(px) ? -1 : l.c.add(t ? q->N : q->K, t ? q->K : q->N, ldw);
+    px.ldb = ldw;
+    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1);
+    px.units = pw.units = l.c.units;
+    l.dz = l.c.bytes;
+    l.sums = l.dz + (act ? round_up((size_t)q->M * l.lddz * 2, kWsAlign) : 0);
     l.part = l.sums + round_up((size_t)row_blocks(q->M) * q->N * sizeof(float), kWsAlign);
     const size_t a = part_bytes(px), b = part_bytes(pw);
     l.bytes = l.part + (a > b ? a : b);
@@ -274,17 +391,21 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
         dgor::launch_sum_blocks(row_blocks(q->M), q->N, sums, dbias, bf16, s) != hipSuccess)
         return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
+    dZ = l.c.use(dX || dW ? l.copy_dy : -1, dZ, base);
+    const uint16_t *Xs = l.c.use(dW ? l.copy_x : -1, X, base), *Ws = l.c.use(dX ? l.copy_w : -1, W, base);
+    if (l.c.launch(s) != hipSuccess)
+        return GEMM_ERR_LAUNCH;
     if (dX) {
         px.A[0] = px.A[1] = dZ;
-        px.B[0] = px.B[1] = W;
+        px.B[0] = px.B[1] = Ws;
         px.e.Y = dX, px.e.ldy = q->lddx;
         if (run_product(px, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     if (dW) {
         const bool t = q->op_w == GEMM_OP_T;
-        pw.A[0] = pw.A[1] = t ? dZ : X;
-        pw.B[0] = pw.B[1] = t ? X : dZ;
+        pw.A[0] = pw.A[1] = t ? dZ : Xs;
+        pw.B[0] = pw.B[1] = t ? Xs : dZ;
         pw.e.Y = dW, pw.e.ldy = q->lddw;
         if (run_product(pw, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
@@ -294,7 +415,7 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
 
 // ---------------------------------------------------- gated up-projection --
 
-int check_gated(const gemm_gated_params *q, Product &p)
+int check_gated(const gemm_gated_params *q, Product &p, Copies &c, int (&copy)[3])
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
@@ -305,6 +426,7 @@ int check_gated(const gemm_gated_params *q, Product &p)
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
     p = forward_product(q->M, q->F, q->K, q->op_w, q->ldx, q->ldw, true);
+    copy_operands(p, c, copy);
     return GEMM_OK;
 }
 
@@ -312,7 +434,9 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
               uint16_t *H, uint16_t *G, uint16_t *U, void *ws, size_t ws_bytes, void *stream)
 {
     Product p;
-    const int rc = check_gated(q, p);
+    Copies c;
+    int copy[3];
+    const int rc = check_gated(q, p, c, copy);
     if (rc != GEMM_OK)
         return rc;
     if (G && !ld_ok(q->ldp, q->F))
@@ -322,24 +446,29 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
         return GEMM_ERR_NULL_PTR;
     if (q->M == 0 || q->F == 0)
         return GEMM_OK;
-    if (!workspace_ok(ws, ws_bytes, part_bytes(p)))
+    if (!workspace_ok(ws, ws_bytes, c.bytes + part_bytes(p)))
         return GEMM_ERR_WORKSPACE;
     const int dev = dgor::device_status();
     if (dev != GEMM_OK)
         return dev;
+    uint8_t *base = (uint8_t *)ws;
+    hipStream_t s = (hipStream_t)stream;
     p.bf16 = bf16;
-    p.A[0] = p.A[1] = X;
-    p.B[0] = Wg, p.B[1] = Wu;
+    p.A[0] = p.A[1] = c.use(copy[0], X, base);
+    p.B[0] = c.use(copy[1], Wg, base), p.B[1] = c.use(copy[2], Wu, base);
     p.e.Y = H, p.e.ldy = q->ldh, p.e.act = q->activation;
     p.e.pre = G, p.e.pre2 = U, p.e.ldp = q->ldp;
-    return done(run_product(p, ws, (hipStream_t)stream));
+    const hipError_t err = c.launch(s);
+    return done(err == hipSuccess ? run_product(p, base + c.bytes, s) : err);
 }
 
-// Workspace of the gated backward pass: dG and dU, then the partial sums of
-// whichever product is running.
+// Workspace of the gated backward pass: copies, dG and dU, then the partial
+// sums of whichever product is running.
 struct GatedBackwardLayout {
+    Copies c;
+    int copy_x, copy_wg, copy_wu;
     int ldd;
-    size_t du, part, bytes;
+    size_t dg, du, part, bytes;
 };
 
 int check_gated_backward(const gemm_gated_backward_params *q, Product &px, Product &pw, GatedBackwardLayout &l)
@@ -353,10 +482,20 @@ int check_gated_backward(const gemm_gated_backward_params *q, Product &px, Produ
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
     l.ldd = (int)round_up((size_t)q->F, 8);
-    px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, q->ldw, 2);
-    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, q->ldx, l.ldd, 2);
-    l.du = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
-    l.part = 2 * l.du;
+    const bool t = q->op_w == GEMM_OP_T;
+    int ldx = q->ldx, ldw = q->ldw, ldu = q->ldw;
+    l.copy_x = l.c.add(q->M, q->K, ldx);
+    px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, ldw, 2);
+    const bool copy_w = !few_rows(px);
+    l.copy_wg = copy_w ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldw) : -1;
+    l.copy_wu = copy_w ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldu) : -1;
+    px.ldb = ldw;
+    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2);
+    px.units = pw.units = l.c.units;
+    const size_t d_bytes = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
+    l.dg = l.c.bytes;
+    l.du = l.dg + d_bytes;
+    l.part = l.du + d_bytes;
     const size_t a = part_bytes(px), b = part_bytes(pw);
     l.bytes = l.part + (a > b ? a : b);
     return GEMM_OK;
@@ -388,23 +527,27 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
         return dev;
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
-    uint16_t *dG = (uint16_t *)base, *dU = (uint16_t *)(base + l.du);
+    uint16_t *dG = (uint16_t *)(base + l.dg), *dU = (uint16_t *)(base + l.du);
     if (q->M > 0 && q->F > 0 &&
         dgor::launch_gate_grad(q->M, q->F, dH, q->lddh, G, U, q->ldp, dG, dU, l.ldd, q->activation, bf16, s) !=
             hipSuccess)
         return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
+    const uint16_t *Xs = l.c.use(dWg ? l.copy_x : -1, X, base);
+    const uint16_t *Gs = l.c.use(dX ? l.copy_wg : -1, Wg, base), *Us = l.c.use(dX ? l.copy_wu : -1, Wu, base);
+    if (l.c.launch(s) != hipSuccess)
+        return GEMM_ERR_LAUNCH;
     if (dX) {
         px.A[0] = dG, px.A[1] = dU;
-        px.B[0] = Wg, px.B[1] = Wu;
+        px.B[0] = Gs, px.B[1] = Us;
         px.e.Y = dX, px.e.ldy = q->lddx;
         if (run_product(px, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     if (dWg) {
         const bool t = q->op_w == GEMM_OP_T;
-        pw.A[0] = t ? dG : X, pw.A[1] = t ? dU : X;
-        pw.B[0] = t ? X : dG, pw.B[1] = t ? X : dU;
+        pw.A[0] = t ? dG : Xs, pw.A[1] = t ? dU : Xs;
+        pw.B[0] = t ? Xs : dG, pw.B[1] = t ? Xs : dU;
         pw.e.Y = dWg, pw.Y1 = dWu, pw.e.ldy = q->lddw;
         if (run_product(pw, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
@@ -421,9 +564,11 @@ int gemm_linear_workspace(const gemm_linear_params *params, size_t *bytes)
     if (!bytes)
         return GEMM_ERR_NULL_PTR;
     Product p;
-    const int rc = check_linear(params, p);
+    Copies c;
+    int copy[3];
+    const int rc = check_linear(params, p, c, copy);
     if (rc == GEMM_OK)
-        *bytes = p.M && p.N ? part_bytes(p) : 0;
+        *bytes = p.M && p.N ? c.bytes + part_bytes(p) : 0;
     return rc;
 }
 int gemm_linear_f16(const gemm_linear_params *params, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
@@ -466,9 +611,11 @@ int gemm_gated_workspace(const gemm_gated_params *params, size_t *bytes)
     if (!bytes)
         return GEMM_ERR_NULL_PTR;
     Product p;
-    const int rc = check_gated(params, p);
+    Copies c;
+    int copy[3];
+    const int rc = check_gated(params, p, c, copy);
     if (rc == GEMM_OK)
-        *bytes = p.M && p.N ? part_bytes(p) : 0;
+        *bytes = p.M && p.N ? c.bytes + part_bytes(p) : 0;
     return rc;
 }
 int gemm_gated_f16(const gemm_gated_params *params, const uint16_t *X, const uint16_t *Wg, const uint16_t *Wu,

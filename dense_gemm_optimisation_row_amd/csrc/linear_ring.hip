@@ -1,21 +1,22 @@
-// The dense-layer products of 16-byte aligned operands: square tiles of 256
-// or 128, loaded straight from global memory into LDS rings 32 k deep, FP32
-// sums on v_mfma_f32_16x16x32, and the epilogue of epilogue.h on whole rows.
+// The dense-layer products of 16-byte aligned operands: tiles of 256 x 256,
+// 256 x 128, 128 x 128 and 64 x 64, loaded straight from global memory into
+// LDS rings 32 k deep, FP32 sums on v_mfma_f32_16x16x32, and the epilogue of
+// epilogue.h on whole rows.
 //
-// Four wavefronts, each a quarter of the tile: 8 x 8 (tile 256, all 256
-// accumulator registers, one workgroup a compute unit) or 4 x 4 blocks of
-// 16 x 16 (tile 128, two workgroups a unit, which cover each other's waits).
+// Four wavefronts, each a quarter of the tile in 16 x 16 blocks: 8 x 8 of them
+// (all 256 accumulator registers, one workgroup a compute unit), 8 x 4 (one),
+// 4 x 4 (two workgroups a unit, which cover each other's waits) or 2 x 2 (four).
 // Loads: one instruction moves 64 lanes x 16 bytes into 1 KB of LDS, lane p
 // at byte 16 p; the layout is chosen by permuting the sources, and a lane
 // whose offset is out of range writes zeros, which fills every edge.
 //
 // A stage of an operand whose rows run along the outputs (B as K x N, A as
-// K x M) is kept as two halves of tile / 2 columns, each 32 k rows of W =
-// tile / 16 units of 16 bytes, unit u of row k at W k + (u ^ x(k)), x(k) =
-// 2 (k & 3) + 8 ((k >> 3) & 1) for W = 16 and 2 ((k >> 1) & 1) + 4 ((k >> 3) & 1)
-// for W = 8, which puts the eight k rows that a cycle of a transposing read
-// takes two units of on distinct banks.  B as N x K is two halves of tile / 2
-// rows of four units, unit c of row r at 4 r + (c ^ 2 ((r >> 2) & 1)).  The
+// K x M) is kept as two halves of the tile's columns, each 32 k rows of W units
+// of 16 bytes, unit u of row k at W k + (u ^ x(k)), x(k) = 2 (k & 3) + 8 ((k >> 3) & 1)
+// for W = 16, 2 ((k >> 1) & 1) + 4 ((k >> 3) & 1) for W = 8 and 2 ((k >> 3) & 1)
+// for W = 4, which puts the eight k rows that a cycle of a transposing read
+// takes two units of on distinct banks.  B as N x K is two halves of the
+// tile's rows of four units, unit c of row r at 4 r + (c ^ 2 ((r >> 2) & 1)).  The
 // halves may come from two matrices: a gated product's tile is the gate's
 // columns and the up projection's same columns, so that a wavefront has both
 // sums of its elements.  A as M x K is staged two stages at a time, whole
@@ -29,7 +30,9 @@
 // t + 1 has landed, and the buffers that are refilled were last read by
 // fragments that every wavefront has since consumed.
 //
-// Bound by the matrix cores where there are tiles for every compute unit.
+// Bound by the matrix cores where there are tiles for every compute unit; the
+// smaller tiles by LDS reads, 64, 96, 128 and 256 bytes a cycle and compute
+// unit of its 128 if the matrix cores never waited.
 #include "common.h"
 #include "lds_dma.h"
 #include "linear.h"
@@ -62,27 +65,32 @@ constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descrip
 template <int W>
 __device__ __forceinline__ int row_swizzle(int k)
 {
-    return W == 16 ? 2 * (k & 3) + 8 * ((k >> 3) & 1) : 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1);
+    return W == 16 ? 2 * (k & 3) + 8 * ((k >> 3) & 1)
+                   : (W == 8 ? 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1) : 2 * ((k >> 3) & 1));
 }
 
-// Descriptor range in bytes of `rows` rows of `cols` elements: what is past
-// it reads as zero.
+// Descriptor range in bytes of `rows` rows of `cols` elements in whole units:
+// what is past it reads as zero.
 __device__ __forceinline__ int range_of(int rows, int cols, int ld)
 {
-    return rows <= 0 || cols <= 0 ? 0 : (int)(((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)cols) * 2u);
+    return rows <= 0 || cols <= 0
+               ? 0
+               : (int)(((uint32_t)(rows - 1) * (uint32_t)ld + ((uint32_t)(cols + 7) & ~7u)) * 2u);
 }
 
-template <class Op, int BT, bool TA, bool TB, bool GATED>
+template <class Op, int BM, int BN, bool TA, bool TB, bool GATED>
 __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
 {
     constexpr int BK = 32;
-    constexpr int HW = BT / 2, FB = HW / 16;       // a wavefront's square, and its 16-wide blocks
-    constexpr int W = HW / 8;                      // units of a half's k row
-    constexpr int LPW = BT / 64;                   // a wavefront's loads of one operand and stage
-    constexpr int HALF = BK * HW * 2, STAGE = 2 * HALF, PAIR = 2 * STAGE;
-    constexpr int A_BYTES = TA ? 4 * STAGE : 3 * PAIR;
-    constexpr int LDS_BYTES = A_BYTES + 4 * STAGE;
-    constexpr int FT = GATED ? HW : BT;            // output columns of a tile
+    constexpr int HM = BM / 2, HN = BN / 2;        // a wavefront's part of the tile,
+    constexpr int FA = HM / 16, FB = HN / 16;      // and its 16-wide blocks
+    constexpr int WA = HM / 8, WB = HN / 8;        // units of a half's k row
+    constexpr int LPA = BM / 64, LPB = BN / 64;    // a wavefront's loads of each operand and stage
+    constexpr int HALF_A = BK * HM * 2, HALF_B = BK * HN * 2, STAGE_A = 2 * HALF_A, STAGE_B = 2 * HALF_B;
+    constexpr int PAIR = 2 * STAGE_A;
+    constexpr int A_BYTES = TA ? 4 * STAGE_A : 3 * PAIR;
+    constexpr int LDS_BYTES = A_BYTES + 4 * STAGE_B;
+    constexpr int FT = GATED ? HN : BN;            // output columns of a tile
     __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_BYTES];
     const uint32_t ring = lds_address(lds);
 
@@ -90,7 +98,7 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     const int batch = blockIdx.x >= (unsigned)per ? 1 : 0;
     int tm, tn;
     dgor_tile_of_block((int)blockIdx.x - batch * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    const int m0 = tm * BT, n0 = tn * FT;
+    const int m0 = tm * BM, n0 = tn * FT;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int M = p.M, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;
@@ -101,22 +109,22 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     const int steps = (p.splits > 1 ? min(s0 + p.chunk * 2, total) : total) - s0;
 
     // ---- loads.  Wavefronts 0 and 1 fill half 0 of a stage, 2 and 3 half 1.
-    const int lhalf = wave >> 1, lid0 = LPW * (wave & 1);
-    const int bcol = GATED ? n0 : n0 + HW * lhalf;            // first column of this wavefront's half of B
+    const int lhalf = wave >> 1, alid0 = LPA * (wave & 1), blid0 = LPB * (wave & 1);
+    const int bcol = GATED ? n0 : n0 + HN * lhalf;            // first column of this wavefront's half of B
     const int b_left = N - bcol;
     const uint16_t *const B0 = p.B[GATED ? lhalf : batch], *const B1 = p.B[GATED ? lhalf : 1];
-    uint32_t b_off[LPW];
+    uint32_t b_off[LPB];
     const int b_kc = 8 * ((lane & 3) ^ (2 * ((lane >> 4) & 1)));
 #pragma unroll
-    for (int q = 0; q < LPW; ++q) {
+    for (int q = 0; q < LPB; ++q) {
         if (TB) {
-            b_off[q] = (uint32_t)((16 * (lid0 + q) + (lane >> 2)) * ldb + b_kc) * 2u;
+            b_off[q] = (uint32_t)((16 * (blid0 + q) + (lane >> 2)) * ldb + b_kc) * 2u;
         } else {
-            const int k = (64 / W) * (lid0 + q) + lane / W, u = (lane % W) ^ row_swizzle<W>(k);
+            const int k = (64 / WB) * (blid0 + q) + lane / WB, u = (lane % WB) ^ row_swizzle<WB>(k);
             b_off[q] = 8 * u < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
         }
     }
-    const uint32_t lds_b = ring + (uint32_t)(A_BYTES + lhalf * HALF + lid0 * 1024);
+    const uint32_t lds_b = ring + (uint32_t)(A_BYTES + lhalf * HALF_B + blid0 * 1024);
     struct Loads {
         intx4 r;
         int k_left;
@@ -135,35 +143,35 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
         L.k_left = K - k0;
         L.r = rsrc_words(TB ? B + (size_t)bcol * ldb + k0 : B + (size_t)k0 * ldb + bcol, 0);
         if (TB)
-            L.r.z = L.k_left <= 0 ? 0 : (b_left >= HW ? 0x7fffffff : range_of(b_left, L.k_left, ldb));
+            L.r.z = L.k_left <= 0 ? 0 : (b_left >= HN ? 0x7fffffff : range_of(b_left, L.k_left, ldb));
         else
             L.r.z = L.k_left >= BK ? 0x7fffffff : range_of(L.k_left, b_left, ldb);
-        L.dst = lds_b + (uint32_t)((t & 3) * STAGE);
+        L.dst = lds_b + (uint32_t)((t & 3) * STAGE_B);
         return L;
     };
     auto load_b = [&](const Loads &L, int q) {
         load_to_lds(L.r, L.dst + (uint32_t)(q * 1024), TB && b_kc >= L.k_left ? kOutside : b_off[q]);
     };
     const uint16_t *const A0 = p.A[batch], *const A1 = p.A[1];
-    // A as M x K: a wavefront loads its HW / 2 rows of the tile, eight a load
-    uint32_t a_off[TA ? LPW : 2];
+    // A as M x K: a wavefront loads a quarter of the tile's rows, eight a load
+    uint32_t a_off[TA ? LPA : 2];
     int a_kc[2] = {0, 0};
-    const int arow = TA ? m0 + HW * lhalf : m0;
+    const int arow = TA ? m0 + HM * lhalf : m0;
     const int a_left = M - arow;
 #pragma unroll
-    for (int j = 0; j < (TA ? LPW : 2); ++j) {
+    for (int j = 0; j < (TA ? LPA : 2); ++j) {
         if (TA) {
-            const int k = (64 / W) * (lid0 + j) + lane / W, u = (lane % W) ^ row_swizzle<W>(k);
+            const int k = (64 / WA) * (alid0 + j) + lane / WA, u = (lane % WA) ^ row_swizzle<WA>(k);
             a_off[j] = 8 * u < a_left ? (uint32_t)(k * lda + 8 * u) * 2u : kOutside;
         } else {
-            const int r = (HW / 2) * wave + 8 * j + (lane >> 3);
+            const int r = (HM / 2) * wave + 8 * j + (lane >> 3);
             const int c = (lane & 7) ^ ((4 * j + (lane >> 4)) & 7);
             a_off[j] = (uint32_t)(r * lda + 8 * c) * 2u;
             a_kc[j] = 8 * c;
         }
     }
     const uint32_t a_row16 = (uint32_t)(16 * lda) * 2u;
-    const uint32_t lds_a = ring + (uint32_t)(TA ? lhalf * HALF + lid0 * 1024 : 2 * LPW * wave * 1024);
+    const uint32_t lds_a = ring + (uint32_t)(TA ? lhalf * HALF_A + alid0 * 1024 : 2 * LPA * wave * 1024);
     // loads of A stage t (A as K x M), or of the pair that begins at stage t
     auto a_loads = [&](int t, uint32_t buf) {
         Loads L;
@@ -175,7 +183,7 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
         if (TA)
             L.r.z = L.k_left >= BK ? 0x7fffffff : range_of(L.k_left, a_left, lda);
         else
-            L.r.z = L.k_left <= 0 ? 0 : (a_left >= BT ? 0x7fffffff : range_of(a_left, L.k_left, lda));
+            L.r.z = L.k_left <= 0 ? 0 : (a_left >= BM ? 0x7fffffff : range_of(a_left, L.k_left, lda));
         L.dst = lds_a + buf;
         return L;
     };
@@ -190,30 +198,29 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
 
     // ---- fragments.  Lane (g, s) = (lane / 16, lane % 16).
     const int s16 = lane & 15, g = lane >> 4;
-    const int wrow = (wave >> 1) * HW;
+    const int wrow = (wave >> 1) * HM;
     // k rows 8 g + s / 4 and four further: both have this swizzle
-    const int ks_x = row_swizzle<W>(8 * g + (s16 >> 2));
-    const uint32_t ks_lane = (uint32_t)((8 * g + (s16 >> 2)) * (HW * 2) + 8 * (s16 & 1));
+    const int kr = 8 * g + (s16 >> 2), a_x = row_swizzle<WA>(kr), b_x = row_swizzle<WB>(kr);
     constexpr int FU = GATED ? FB / 2 : FB;        // distinct column blocks of B
-    uint32_t b_unit[TB ? 1 : FU], a_unit[TA ? FB : 1];
+    uint32_t b_unit[TB ? 1 : FU], a_unit[TA ? FA : 1];
     if (!TB)
 #pragma unroll
         for (int j = 0; j < FU; ++j)
             b_unit[TB ? 0 : j] =
-                (uint32_t)(((2 * ((GATED ? (wave & 1) * FU : 0) + j) + ((s16 & 3) >> 1)) ^ ks_x) * 16);
+                (uint32_t)(((2 * ((GATED ? (wave & 1) * FU : 0) + j) + ((s16 & 3) >> 1)) ^ b_x) * 16);
     if (TA)
 #pragma unroll
-        for (int i = 0; i < FB; ++i)
-            a_unit[TA ? i : 0] = (uint32_t)(((2 * i + ((s16 & 3) >> 1)) ^ ks_x) * 16);
+        for (int i = 0; i < FA; ++i)
+            a_unit[TA ? i : 0] = (uint32_t)(((2 * i + ((s16 & 3) >> 1)) ^ a_x) * 16);
     const uint32_t kc_lane = (uint32_t)(s16 * 64 + ((g ^ (2 * ((s16 >> 2) & 1))) * 16));
-    const uint32_t b_lane = (uint32_t)A_BYTES + (TB ? kc_lane : ks_lane) +
-                            (GATED ? (TB ? (uint32_t)((wave & 1) * FU * 1024) : 0u) : (uint32_t)((wave & 1) * HALF));
-    const uint32_t a_lane = TA ? ks_lane + (uint32_t)((wave >> 1) * HALF)
+    const uint32_t b_lane = (uint32_t)A_BYTES + (TB ? kc_lane : (uint32_t)(kr * (HN * 2) + 8 * (s16 & 1))) +
+                            (GATED ? (TB ? (uint32_t)((wave & 1) * FU * 1024) : 0u) : (uint32_t)((wave & 1) * HALF_B));
+    const uint32_t a_lane = TA ? (uint32_t)(kr * (HM * 2) + 8 * (s16 & 1) + (wave >> 1) * HALF_A)
                                : (uint32_t)((wrow + s16) * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
-    auto transposed = [&](uint32_t at) -> halfx8 {
+    auto transposed = [&](uint32_t at, int row) -> halfx8 {   // row: bytes of a k row
         const uint8_t *q = lds + at;
         const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
-        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * HW * 2));
+        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * row));
         return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     struct Source {
@@ -223,14 +230,14 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     };
     auto read_a = [&](const Source &S, int i) -> halfx8 {
         if (TA)
-            return transposed(a_lane + S.a + a_unit[TA ? i : 0]);
+            return transposed(a_lane + S.a + a_unit[TA ? i : 0], HM * 2);
         return *reinterpret_cast<const halfx8 *>(lds + ((a_lane ^ (uint32_t)(64 * S.odd)) + S.a + (uint32_t)(i * 2048)));
     };
     auto read_b = [&](const Source &S, int j) -> halfx8 {
-        const uint32_t at = b_lane + S.b + (GATED ? (uint32_t)((j / FU) * HALF) : 0u);
+        const uint32_t at = b_lane + S.b + (GATED ? (uint32_t)((j / FU) * HALF_B) : 0u);
         if (TB)
             return *reinterpret_cast<const halfx8 *>(lds + at + (uint32_t)((j % FU) * 1024));
-        return transposed(at + b_unit[TB ? 0 : j % FU]);
+        return transposed(at + b_unit[TB ? 0 : j % FU], HN * 2);
     };
     // A block 0, the B blocks, then the other A blocks: as the MFMAs want them
     auto fread = [&](const Source &S, int r, halfx8 *fa, halfx8 *fb) {
@@ -240,89 +247,98 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
             fb[r - 1] = read_b(S, r - 1);
     };
 
-    floatx4 acc[FB][FB];
+    floatx4 acc[FA][FB];
 #pragma unroll
-    for (int i = 0; i < FB; ++i)
+    for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FB; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 asm("v_accvgpr_write_b32 %0, 0" : "=a"(acc[i][j][r]));   // keeps the array in the accumulators
 
-    // One stage: its MFMAs from (ca, cb), the next stage's 2 FB fragment reads
-    // after the first of them, then its 2 LPW loads evenly over the rest.
+    // One stage: its MFMAs from (ca, cb), the next stage's fragment reads after
+    // the first of them, then its loads evenly over the rest.
     auto stage = [&](int par, const Loads &LA, const Loads &LB, const Source &S, halfx8 *ca, halfx8 *cb, halfx8 *na,
                      halfx8 *nb) {
-        constexpr int EVERY = (FB * FB - 2 * FB) / (2 * LPW);
+        constexpr int READS = FA + FB, LOADS = LPA + LPB, EVERY = (FA * FB - READS) / LOADS;
+        auto issue = [&](int ld) {
+            if (ld < LPB)
+                load_b(LB, ld);
+            else if (ld < LOADS)
+                load_a(LA, (TA ? 0 : LPA * par) + ld - LPB);
+        };
 #pragma unroll
-        for (int m = 0; m < FB * FB; ++m) {
+        for (int m = 0; m < FA * FB; ++m) {
             const int i = m / FB, j = m % FB;
             acc[i][j] = Op::mfma(ca[i], cb[j], acc[i][j]);
-            if (m < 2 * FB)
+            if (m < READS)
                 fread(S, m, na, nb);
-            if (m >= 2 * FB && (m - 2 * FB) % EVERY == EVERY - 1) {
-                const int ld = (m - 2 * FB) / EVERY;
-                if (ld < LPW)
-                    load_b(LB, ld);
-                else if (ld < 2 * LPW)
-                    load_a(LA, (TA ? 0 : LPW * par) + ld - LPW);
-            }
+            if (EVERY > 0 && m >= READS && (m - READS) % (EVERY > 0 ? EVERY : 1) == EVERY - 1)
+                issue((m - READS) / (EVERY > 0 ? EVERY : 1));
             // keep this order: the compiler would otherwise cluster the reads
             // and loads, and move MFMAs across the barrier
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (EVERY == 0) {   // as many reads as MFMAs
+#pragma unroll
+            for (int ld = 0; ld < LOADS; ++ld)
+                issue(ld);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     auto next_pair = [](uint32_t b) { return b == (uint32_t)(2 * PAIR) ? 0u : b + PAIR; };
-    auto buf = [](int t) { return (uint32_t)((t & 3) * STAGE); };
+    auto a_buf = [](int t) { return (uint32_t)((t & 3) * STAGE_A); };
+    auto b_buf = [](int t) { return (uint32_t)((t & 3) * STAGE_B); };
 
-    halfx8 fa0[FB], fa1[FB], fb0[FB], fb1[FB];
+    halfx8 fa0[FA], fa1[FA], fb0[FB], fb1[FB];
     if (TA) {
 #pragma unroll
         for (int st = 0; st < 3; ++st) {
-            const Loads LA = a_loads(st, buf(st)), LB = b_loads(st);
+            const Loads LA = a_loads(st, a_buf(st)), LB = b_loads(st);
 #pragma unroll
-            for (int q = 0; q < LPW; ++q)
+            for (int q = 0; q < LPA; ++q)
                 load_a(LA, q);
 #pragma unroll
-            for (int q = 0; q < LPW; ++q)
+            for (int q = 0; q < LPB; ++q)
                 load_b(LB, q);
         }
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(4 * LPW));
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * (LPA + LPB)));
     } else {
         const Loads P0 = a_loads(0, 0), P1 = a_loads(2, PAIR);
 #pragma unroll
-        for (int j = 0; j < 2 * LPW; ++j)
+        for (int j = 0; j < 2 * LPA; ++j)
             load_a(P0, j);
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const Loads LB = b_loads(st);
 #pragma unroll
-            for (int q = 0; q < LPW; ++q)
+            for (int q = 0; q < LPB; ++q)
                 load_b(LB, q);
         }
 #pragma unroll
-        for (int j = 0; j < 2 * LPW; ++j)
+        for (int j = 0; j < 2 * LPA; ++j)
             load_a(P1, j);
         const Loads LB = b_loads(2);
 #pragma unroll
-        for (int q = 0; q < LPW; ++q)
+        for (int q = 0; q < LPB; ++q)
             load_b(LB, q);
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(4 * LPW));
+        // A pair 0 and B stage 0 have landed
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * LPA + 2 * LPB));
     }
     __builtin_amdgcn_s_barrier();
     {
         const Source S{0u, 0, 0u};
 #pragma unroll
-        for (int r = 0; r < 2 * FB; ++r)
+        for (int r = 0; r < FA + FB; ++r)
             fread(S, r, fa0, fb0);
     }
     auto wait = [&](int t) {
         // the loads of the stage before may stay in flight (at stage 0: A pair
         // 1 and B stage 2)
         if (!TA && t == 0)
-            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(3 * LPW));
+            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(2 * LPA + LPB));
         else
-            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(2 * LPW));
+            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(LPA + LPB));
         __builtin_amdgcn_s_barrier();
     };
     uint32_t pa = 0;   // the pair's buffer
@@ -330,15 +346,15 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
         const uint32_t pa1 = next_pair(pa), pa2 = next_pair(pa1);
         wait(t);
         {
-            const Loads LA = TA ? a_loads(t + 3, buf(t + 3)) : a_loads(t + 4, pa2), LB = b_loads(t + 3);
+            const Loads LA = TA ? a_loads(t + 3, a_buf(t + 3)) : a_loads(t + 4, pa2), LB = b_loads(t + 3);
             __builtin_amdgcn_sched_barrier(0);
-            stage(0, LA, LB, TA ? Source{buf(t + 1), 0, buf(t + 1)} : Source{pa, 1, buf(t + 1)}, fa0, fb0, fa1, fb1);
+            stage(0, LA, LB, TA ? Source{a_buf(t + 1), 0, b_buf(t + 1)} : Source{pa, 1, b_buf(t + 1)}, fa0, fb0, fa1, fb1);
         }
         if (t + 1 < steps) {
             wait(t + 1);
-            const Loads LA = TA ? a_loads(t + 4, buf(t + 4)) : a_loads(t + 4, pa2), LB = b_loads(t + 4);
+            const Loads LA = TA ? a_loads(t + 4, a_buf(t + 4)) : a_loads(t + 4, pa2), LB = b_loads(t + 4);
             __builtin_amdgcn_sched_barrier(0);
-            stage(1, LA, LB, TA ? Source{buf(t + 2), 0, buf(t + 2)} : Source{pa1, 0, buf(t + 2)}, fa1, fb1, fa0, fb0);
+            stage(1, LA, LB, TA ? Source{a_buf(t + 2), 0, b_buf(t + 2)} : Source{pa1, 0, b_buf(t + 2)}, fa1, fb1, fa0, fb0);
         }
         pa = pa1;
     }
@@ -350,8 +366,8 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     // Epilogue: 32 rows at a time through the wavefront's own part of LDS, so
     // that a lane holds eight neighbouring columns of one row.  Rows are padded
     // by 16 bytes, which puts the 64 lanes of each write on distinct banks.
-    constexpr int ROW = HW + 4;                                   // floats
-    constexpr int COLS = GATED ? HW / 2 : HW, LANES = COLS / 8;
+    constexpr int ROW = HN + 4;                                   // floats
+    constexpr int COLS = GATED ? HN / 2 : HN, LANES = COLS / 8;
     static_assert(4 * 32 * ROW * 4 <= LDS_BYTES, "the epilogue uses the ring's LDS");
     float *w = reinterpret_cast<float *>(lds) + wave * 32 * ROW;
     const int c0 = n0 + (wave & 1) * COLS;
@@ -359,7 +375,7 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     if (batch)
         e.Y = p.Y1;
 #pragma unroll
-    for (int round = 0; round < FB / 2; ++round) {
+    for (int round = 0; round < FA / 2; ++round) {
 #pragma unroll
         for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -395,39 +411,44 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     }
 }
 
-template <class Op, int BT>
+template <class Op, int BM, int BN>
 hipError_t launch_ring_as(const Product &p, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n * p.nbatch), (unsigned)(p.splits > 1 ? p.splits : 1));
     if (p.gated) {
         if (p.trans_b)
-            hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, true, true>), grid, dim3(256), 0, s, p);
+            hipLaunchKernelGGL((linear_ring_kernel<Op, BM, BN, false, true, true>), grid, dim3(256), 0, s, p);
         else
-            hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, false, true>), grid, dim3(256), 0, s, p);
+            hipLaunchKernelGGL((linear_ring_kernel<Op, BM, BN, false, false, true>), grid, dim3(256), 0, s, p);
     } else if (p.trans_a) {
-        hipLaunchKernelGGL((linear_ring_kernel<Op, BT, true, false, false>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((linear_ring_kernel<Op, BM, BN, true, false, false>), grid, dim3(256), 0, s, p);
     } else if (p.trans_b) {
-        hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, true, false>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((linear_ring_kernel<Op, BM, BN, false, true, false>), grid, dim3(256), 0, s, p);
     } else {
-        hipLaunchKernelGGL((linear_ring_kernel<Op, BT, false, false, false>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((linear_ring_kernel<Op, BM, BN, false, false, false>), grid, dim3(256), 0, s, p);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear_ring(const Product &q, int tile, hipStream_t s)
+hipError_t launch_linear_ring(const Product &q, RingTile tile, hipStream_t s)
 {
     Product p = q;
-    if ((p.trans_a && p.trans_b) || (tile != 256 && tile != 128))
+    if (p.trans_a && p.trans_b)
         return hipErrorInvalidValue;
-    const int ft = p.gated ? tile / 2 : tile;
-    p.tiles_m = (p.M + tile - 1) / tile;
+    const int bm = ring_tile_m(tile), bn = ring_tile_n(tile), ft = p.gated ? bn / 2 : bn;
+    p.tiles_m = (p.M + bm - 1) / bm;
     p.tiles_n = (p.N + ft - 1) / ft;
     p.group_m = 4;
-    if (tile == 256)
-        return p.bf16 ? launch_ring_as<OpBrain, 256>(p, s) : launch_ring_as<OpHalf, 256>(p, s);
-    return p.bf16 ? launch_ring_as<OpBrain, 128>(p, s) : launch_ring_as<OpHalf, 128>(p, s);
+    switch (tile) {
+    case kRing256: return p.bf16 ? launch_ring_as<OpBrain, 256, 256>(p, s) : launch_ring_as<OpHalf, 256, 256>(p, s);
+    case kRing256x128:
+        return p.bf16 ? launch_ring_as<OpBrain, 256, 128>(p, s) : launch_ring_as<OpHalf, 256, 128>(p, s);
+    case kRing128: return p.bf16 ? launch_ring_as<OpBrain, 128, 128>(p, s) : launch_ring_as<OpHalf, 128, 128>(p, s);
+    case kRing64: return p.bf16 ? launch_ring_as<OpBrain, 64, 64>(p, s) : launch_ring_as<OpHalf, 64, 64>(p, s);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace dgor

@@ -72,43 +72,26 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
     const int r16 = lane >> 2, c4 = 8 * (lane & 3);         // of 16 rows x 32 columns
 
     u32x4 w[UNROLL][2 * NB], x[UNROLL][2 * RB];
-    auto fetch = [&](int c0, bool whole) {
+    // where chunk c begins, and its operands
+    struct Chunk {
+        int k0;
+        Operand a, b[NM];
+    };
+    auto chunk_of = [&](int c) {
+        const int seg = c >= per_seg ? p.nseg - 1 : 0;
+        Chunk s;
+        s.k0 = 64 * (c - seg * per_seg);
+        s.a = Operand{p.A[seg], M, K, (size_t)p.lda};
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int c = c0 + kWaves * u, seg = c >= per_seg ? p.nseg - 1 : 0;
-            const int k0 = 64 * (c - seg * per_seg);
-            const uint16_t *A = p.A[seg];
-            if (!whole && c >= chunks) {
-#pragma unroll
-                for (int i = 0; i < 2 * NB; ++i)
-                    w[u][i] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int i = 0; i < 2 * RB; ++i)
-                    x[u][i] = u32x4{0u, 0u, 0u, 0u};
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) {
-                // TB: rows 8 (i % 2 CB) .. of matrix i / (2 CB); else load i % 4 of matrix i / 4
-                const uint16_t *B = p.B[GATED ? i / (2 * CB) : seg];
-                const int j = i % (2 * CB);
-                const int row = TB ? n0 + 8 * j + r8 : k0 + 32 * (j >> 1) + 4 * (j & 1) + 8 * (r16 >> 2) + (r16 & 3);
-                const int col = TB ? k0 + c8 : n0 + c4;
-                w[u][i] = whole ? load8_16(B + (size_t)row * p.ldb + col, 8)
-                                : load_unit(B, p.ldb, row, TB ? N : K, col, TB ? K : N);
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * RB; ++i) {
-                const int row = 8 * i + r8;
-                if (whole) {
-                    x[u][i] = u32x4{0u, 0u, 0u, 0u};
-                    if (row < M)
-                        x[u][i] = load8_16(A + (size_t)row * p.lda + k0 + c8, 8);
-                } else {
-                    x[u][i] = load_unit(A, p.lda, row, M, k0 + c8, K);
-                }
-            }
-        }
+        for (int i = 0; i < NM; ++i)
+            s.b[i] = Operand{p.B[GATED ? i : seg], TB ? N : K, TB ? K : N, (size_t)p.ldb};
+        return s;
+    };
+    // load i of B: TB rows 8 (i % 2) of matrix i / 2, else load i % 4 of matrix i / 4
+    auto b_place = [&](int i, int k0, int &row, int &col) {
+        const int j = i % (2 * CB);
+        row = TB ? n0 + 8 * j + r8 : k0 + 32 * (j >> 1) + 4 * (j & 1) + 8 * (r16 >> 2) + (r16 & 3);
+        col = TB ? k0 + c8 : n0 + c4;
     };
     floatx4 acc[RB][NB];
 #pragma unroll
@@ -119,14 +102,39 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
     uint8_t *const xl = lds + wave * TURN, *const wl = xl + RB * 2048;
     auto row_slot = [&](int r) { return 16 * (8 * r + ((lane & 7) ^ ((r >> 1) & 7))); };
     for (int c0 = wave; c0 < chunks; c0 += kWaves * UNROLL) {
-        const int last = c0 + kWaves * (UNROLL - 1);
-        const bool full_k = p.nseg == 1 ? 64 * (last + 1) <= K : K % 64 == 0 && last < chunks;
-        if (full_k && n0 + 16 * CB <= N)
-            fetch(c0, true);
-        else
-            fetch(c0, false);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
+            const Chunk s = chunk_of(c0 + kWaves * u);
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+                int row, col;
+                b_place(i, s.k0, row, col);
+                w[u][i] = s.b[i / (2 * CB)].load(row, col);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * RB; ++i) {
+                x[u][i] = u32x4{0u, 0u, 0u, 0u};
+                if (8 * i + r8 < M)
+                    x[u][i] = s.a.load(8 * i + r8, s.k0 + c8);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int c = c0 + kWaves * u;
+            if (c >= chunks)
+                break;
+            const Chunk s = chunk_of(c);
+            if (s.k0 + 64 > K || n0 + 16 * CB > N) {
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i) {
+                    int row, col;
+                    b_place(i, s.k0, row, col);
+                    w[u][i] = s.b[0].settle(w[u][i], row, col);
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * RB; ++i)
+                    x[u][i] = s.a.settle(x[u][i], 8 * i + r8, s.k0 + c8);
+            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -206,9 +214,9 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
 template <class Op, int RB, bool TB, bool GATED>
 hipError_t launch_rows(const Product &p, hipStream_t s)
 {
-    // 16-byte loads in flight, a lane: up to 40, what the registers hold
+    // 16-byte loads in flight, a lane: up to 32, what the registers hold
     constexpr int CB = TB ? 1 : 2, EACH = 2 * (RB + CB * (GATED ? 2 : 1));
-    constexpr int UNROLL = EACH <= 4 ? 8 : (EACH <= 10 ? 4 : (EACH <= 14 ? 2 : 1));
+    constexpr int UNROLL = EACH <= 4 ? 8 : (EACH <= 8 ? 4 : (EACH <= 12 ? 2 : 1));
     hipLaunchKernelGGL((linear_skinny_kernel<Op, RB, CB, TB, GATED, UNROLL>), dim3((unsigned)p.tiles_n),
                        dim3(64 * kWaves), 0, s, p);
     return hipGetLastError();
@@ -239,7 +247,7 @@ hipError_t launch_op(const Product &p, hipStream_t s)
 hipError_t launch_linear_skinny(const Product &q, hipStream_t s)
 {
     Product p = q;
-    if (p.trans_a || p.nbatch != 1 || p.M > kSkinnyRows)
+    if (p.trans_a || p.nbatch != 1 || p.M > kSkinnyRows || !spans_a_unit(p))
         return hipErrorInvalidValue;
     const int strip = p.trans_b ? 16 : 32;
     p.tiles_m = 1;

@@ -1,18 +1,20 @@
-// The dense-layer product for operands of any size, stride and alignment:
-// square tiles staged through registers into LDS, FP32 sums on
-// v_mfma_f32_16x16x32, and the epilogue of epilogue.h on whole rows.
+// The dense-layer product for operands that neither the rings nor the few-row
+// kernel take (addresses off 16 bytes under strides on it, strides of 2^22 and
+// more, matrices smaller than a 16-byte unit): 64 x 64 tiles staged through
+// registers into LDS, FP32 sums on v_mfma_f32_16x16x32, and the epilogue of
+// epilogue.h on whole rows.  Any size, stride and alignment; written to be
+// short rather than fast.
 //
 // Both operands may be k-contiguous (A as M x K, B as N x K) or k-strided (A
 // as K x M, B as K x N).  A stage is 64 k.  In 16-byte units (8 elements):
 //   k-contiguous: rows of 8 units, unit c of row r at 8 r + (c ^ ((r >> 1) & 7));
 //     a fragment is one 128-bit read of a row;
-//   k-strided: 64 k rows of W = BT / 8 units, unit u of row k at
-//     W k + (u ^ x(k)), x(k) = 2 (k & 3) + 8 ((k >> 3) & 1) for W = 16 and
-//     2 ((k >> 1) & 1) + 4 ((k >> 3) & 1) for W = 8: the eight k rows that a
-//     cycle of a transposing read takes two units of fall on distinct units
-//     modulo 16.
-// Global loads take 16 bytes at any element address; a stage that an edge of
-// the matrix cuts masks them, without a branch on the lane.
+//   k-strided: 64 k rows of W = 8 units, unit u of row k at W k + (u ^ x(k)),
+//     x(k) = 2 ((k >> 1) & 1) + 4 ((k >> 3) & 1): the eight k rows that a cycle
+//     of a transposing read takes two units of fall on distinct units modulo
+//     16.
+// Global loads take 16 bytes at any element address; only the units that an
+// edge of the matrix cuts are read element by element.
 #include "common.h"
 #include "linear.h"
 
@@ -39,16 +41,20 @@ struct OpBrain : Brain16 {
     }
 };
 
-template <int W>
-__device__ __forceinline__ int strided_swizzle(int k)
+// Eight elements of row r from column c of a rows x cols matrix, zero outside.
+__device__ __forceinline__ u32x4 load_unit(const uint16_t *p, size_t ld, int r, int rows, int c, int cols)
 {
-    return W == 16 ? 2 * (k & 3) + 8 * ((k >> 3) & 1) : 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1);
+    if (r >= rows || c >= cols)
+        return u32x4{0u, 0u, 0u, 0u};
+    return load8_16(p + (size_t)r * ld + c, cols - c);
 }
 
-template <class Op, int BT, bool TA, bool TB, bool GATED>
+__device__ __forceinline__ int strided_swizzle(int k) { return 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1); }
+
+template <class Op, bool TA, bool TB, bool GATED>
 __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
 {
-    constexpr int BK = kStageDepth;
+    constexpr int BT = kTile, BK = kStageDepth;
     constexpr int W = BT / 8;                    // units of a k-strided row
     constexpr int UNITS = BT * BK / 8 / 256;     // units a thread loads of each operand and stage
     constexpr int FT = GATED ? BT / 2 : BT;      // output columns of a tile
@@ -78,36 +84,29 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
         return n0 + (GATED ? (j / WT) * (WT / 2) + j % (WT / 2) : j);
     };
     u32x4 ra[UNITS], rb[UNITS];
-    const bool inside = m0 + BT <= M && n0 + FT <= N;
-    auto fetch = [&](const uint16_t *A, const uint16_t *B0, const uint16_t *B1, int k0, bool whole) {
-#pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            const int u = tid + 256 * i;
-            int which;
-            const int n = TB ? b_col(u / 8, which) : b_col(8 * (u % W), which);
-            const int ar = TA ? k0 + u / W : m0 + u / 8, ac = TA ? m0 + 8 * (u % W) : k0 + 8 * (u % 8);
-            const int br = TB ? n : k0 + u / W, bc = TB ? k0 + 8 * (u % 8) : n;
-            const uint16_t *B = GATED && which ? B1 : B0;
-            if (whole) {
-                ra[i] = load8_16(A + (size_t)ar * p.lda + ac, 8);
-                rb[i] = load8_16(B + (size_t)br * p.ldb + bc, 8);
-            } else {
-                ra[i] = load_unit(A, p.lda, ar, TA ? K : M, ac, TA ? M : K);
-                rb[i] = load_unit(B, p.ldb, br, TB ? N : K, bc, TB ? K : N);
-            }
-        }
-    };
     auto load_stage = [&](int t) {
         const int seg = t >= per_seg ? 1 : 0;
         const int k0 = (t - seg * per_seg) * BK;
-        const uint16_t *A = p.A[seg | batch], *B0 = p.B[GATED ? 0 : seg | batch];
-        if (inside && k0 + BK <= K)
-            fetch(A, B0, p.B[1], k0, true);
-        else
-            fetch(A, B0, p.B[1], k0, false);
+        const uint16_t *A = p.A[seg | batch];
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            const int u = tid + 256 * i;
+            if (TA)
+                ra[i] = load_unit(A, p.lda, k0 + u / W, K, m0 + 8 * (u % W), M);
+            else
+                ra[i] = load_unit(A, p.lda, m0 + u / 8, M, k0 + 8 * (u % 8), K);
+            int which;
+            if (TB) {
+                const int n = b_col(u / 8, which);
+                rb[i] = load_unit(p.B[GATED ? which : seg | batch], p.ldb, n, N, k0 + 8 * (u % 8), K);
+            } else {
+                const int n = b_col(8 * (u % W), which);
+                rb[i] = load_unit(p.B[GATED ? which : seg | batch], p.ldb, k0 + u / W, K, n, N);
+            }
+        }
     };
     auto slot = [&](bool strided, int u) {
-        return strided ? W * (u / W) + ((u % W) ^ strided_swizzle<W>(u / W)) : 8 * (u / 8) + ((u % 8) ^ ((u / 16) & 7));
+        return strided ? W * (u / W) + ((u % W) ^ strided_swizzle(u / W)) : 8 * (u / 8) + ((u % 8) ^ ((u / 16) & 7));
     };
     auto store_stage = [&](int buf) {
         uint8_t *base = lds + buf * 2 * OPERAND;
@@ -127,9 +126,9 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
         }
         const int k = 32 * half + 8 * g + (s16 >> 2);
         const int u = at / 8 + ((s16 & 3) >> 1);
-        const uint8_t *lo = op + 16 * (W * k + (u ^ strided_swizzle<W>(k))) + 8 * (s16 & 1);
+        const uint8_t *lo = op + 16 * (W * k + (u ^ strided_swizzle(k))) + 8 * (s16 & 1);
         const int k4 = k + 4;
-        const uint8_t *hi = op + 16 * (W * k4 + (u ^ strided_swizzle<W>(k4))) + 8 * (s16 & 1);
+        const uint8_t *hi = op + 16 * (W * k4 + (u ^ strided_swizzle(k4))) + 8 * (s16 & 1);
         const shortx4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)lo);
         const shortx4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)hi);
         return __builtin_bit_cast(halfx8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -249,39 +248,37 @@ __global__ __launch_bounds__(256) void linear_join_kernel(Product p)
     emit8<Op, GATED>(e, row, col, n, v, u);
 }
 
-template <class Op, int BT>
+template <class Op>
 hipError_t launch_tile_as(const Product &p, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n * p.nbatch), (unsigned)(p.splits > 1 ? p.splits : 1));
     if (p.gated) {
         if (p.trans_b)
-            hipLaunchKernelGGL((linear_tile_kernel<Op, BT, false, true, true>), grid, dim3(256), 0, s, p);
+            hipLaunchKernelGGL((linear_tile_kernel<Op, false, true, true>), grid, dim3(256), 0, s, p);
         else
-            hipLaunchKernelGGL((linear_tile_kernel<Op, BT, false, false, true>), grid, dim3(256), 0, s, p);
+            hipLaunchKernelGGL((linear_tile_kernel<Op, false, false, true>), grid, dim3(256), 0, s, p);
     } else if (p.trans_a) {
-        hipLaunchKernelGGL((linear_tile_kernel<Op, BT, true, false, false>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((linear_tile_kernel<Op, true, false, false>), grid, dim3(256), 0, s, p);
     } else if (p.trans_b) {
-        hipLaunchKernelGGL((linear_tile_kernel<Op, BT, false, true, false>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((linear_tile_kernel<Op, false, true, false>), grid, dim3(256), 0, s, p);
     } else {
-        hipLaunchKernelGGL((linear_tile_kernel<Op, BT, false, false, false>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((linear_tile_kernel<Op, false, false, false>), grid, dim3(256), 0, s, p);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_tile(const Product &q, int tile, hipStream_t s)
+hipError_t launch_tile(const Product &q, hipStream_t s)
 {
     Product p = q;
-    const int ft = p.gated ? tile / 2 : tile;
-    p.tiles_m = (p.M + tile - 1) / tile;
+    const int ft = p.gated ? kTile / 2 : kTile;
+    p.tiles_m = (p.M + kTile - 1) / kTile;
     p.tiles_n = (p.N + ft - 1) / ft;
     p.group_m = 4;
-    if ((p.trans_a && p.trans_b) || (tile != 64 && tile != 128))
+    if (p.trans_a && p.trans_b)
         return hipErrorInvalidValue;
-    if (tile == 128)
-        return p.bf16 ? launch_tile_as<OpBrain, 128>(p, s) : launch_tile_as<OpHalf, 128>(p, s);
-    return p.bf16 ? launch_tile_as<OpBrain, 64>(p, s) : launch_tile_as<OpHalf, 64>(p, s);
+    return p.bf16 ? launch_tile_as<OpBrain>(p, s) : launch_tile_as<OpHalf>(p, s);
 }
 
 hipError_t launch_join(const Product &p, hipStream_t s)

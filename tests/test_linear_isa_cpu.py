@@ -33,9 +33,9 @@ def ring(tmp_path_factory):
 
 
 def test_every_layout_is_generated(ring):
-    # two formats, two tiles; M x K with K x N and N x K, K x M with K x N,
+    # two formats, four tiles; M x K with K x N and N x K, K x M with K x N,
     # gated with K x N and N x K
-    assert len(ring[1]) == 20
+    assert len(ring[1]) == 40
 
 
 def test_m0_is_touched_only_by_the_loads(ring):
@@ -58,4 +58,5 @@ def test_nothing_spills(ring):
             return int(re.search(rf"^\s*\.set\s+{re.escape(sym)}\.{name},\s*(\d+)", asm, flags=re.M).group(1))
         assert resource("private_seg_size") == 0, sym
         assert "scratch_" not in body, sym
-        assert resource("num_agpr") >= (256 if "ELi256E" in sym else 64), sym
+        bm, bn = (int(v) for v in re.search(r"ELi(\d+)ELi(\d+)E", sym).groups())
+        assert resource("num_agpr") >= bm * bn // 256, sym   # the accumulators of 256 lanes

@@ -82,3 +82,29 @@ def test_gated_rows(M, dtype, transposed):
             x2 = ints(g, M, F, T, pad)
             dx = dg.gated_backward(dh, x2, wg, wu, g2, u2, activation="relu", need_weight=False)[0]
             same(dx, gated_grads("relu", *(t.double() for t in (dh, x2, wg, wu, g2, u2)))[0], "dx")
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["KxN", "NxK"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [65, 130, 300])
+def test_tiles_with_narrow_and_cut_operands(M, dtype, transposed):
+    """More rows than the strips take, with rows shorter than a 16-byte unit
+    or cut by one, of each operand of the three products."""
+    T = DTYPES[dtype]
+    for K in (1, 3, 7, 8, 9, 15, 63, 65, 130, 329):
+        for N in (1, 7, 8, 15, 65, 131):
+            pad = (K + N) % 4
+            say("narrow", M, K, N, dtype, transposed, pad)
+            g = torch.Generator(device="cuda").manual_seed(K * 31 + N)
+            x, w, dy = ints(g, M, K, T, pad), weight(g, K, N, T, transposed, pad), ints(g, M, N, T, pad)
+            same(dg.linear(x, w, out_dtype=torch.float32), x.double() @ w.double(), "y")
+            want = linear_grads("none", dy.double(), x.double(), w.double(), dy.double())
+            for got, ref, name in zip(dg.linear_backward(dy, x, w), want, ("dx", "dw", "dbias")):
+                same(got, ref, name)
+            wu, gs, us = weight(g, K, N, T, transposed, pad), ints(g, M, N, T, pad), ints(g, M, N, T, pad)
+            h = dg.gated(x, w, wu, activation="none")
+            same(h, ((x.double() @ w.double()) * (x.double() @ wu.double())).float(), "h")
+            want = gated_grads("relu", *(t.double() for t in (dy, x, w, wu, gs, us)))
+            for got, ref, name in zip(dg.gated_backward(dy, x, w, wu, gs, us, activation="relu"), want,
+                                      ("dx", "dwg", "dwu")):
+                same(got, ref, name)
