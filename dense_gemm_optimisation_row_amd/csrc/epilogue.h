@@ -10,19 +10,27 @@
 
 namespace dgor {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 // The 16-bit input formats: conversion to and from binary32.
 struct Half16 {
     static __device__ __forceinline__ float up(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
-    static __device__ __forceinline__ uint16_t down(float f)
+    // round to nearest even, overflow to infinity
+    static __device__ __forceinline__ uint16_t down(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+    static __device__ __forceinline__ uint32_t down2(float a, float b)
     {
-        return __builtin_bit_cast(uint16_t, (_Float16)f);   // round to nearest even, overflow to infinity
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, f16x2));
     }
 };
 struct Brain16 {
     static __device__ __forceinline__ float up(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
-    static __device__ __forceinline__ uint16_t down(float f)
+    // round to nearest even
+    static __device__ __forceinline__ uint16_t down(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+    static __device__ __forceinline__ uint32_t down2(float a, float b)
     {
-        return __builtin_bit_cast(uint16_t, (__bf16)f);     // round to nearest even
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
     }
 };
 
@@ -125,7 +133,7 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8])
     u32x4 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        v[e] = (uint32_t)Fmt::down(f[2 * e]) | ((uint32_t)Fmt::down(f[2 * e + 1]) << 16);
+        v[e] = Fmt::down2(f[2 * e], f[2 * e + 1]);
     return v;
 }
 __device__ __forceinline__ void load8_f32(const float *p, int n, float (&f)[8])
@@ -248,58 +256,103 @@ struct Epilogue {
     int act, y_f32;
 };
 
-// Eight neighbouring outputs (n of them inside the matrix): v the sums, u
-// the up projection's (gated only).  The residual is read by the lane that
-// writes the same elements of Y, so Y may be the residual itself.
-template <class Fmt, bool GATED>
-__device__ __forceinline__ void emit8(const Epilogue &e, int row, int col, int n, float (&v)[8], const float (&u)[8])
+// The bias of eight neighbouring columns, n of them inside the matrix.
+template <class Fmt>
+__device__ __forceinline__ void load_bias(const Epilogue &e, int col, int n, float (&b)[8])
 {
-    if (!GATED && e.bias) {
-        float b[8];
-        unpack8<Fmt>(load8_16(e.bias + col, n), b);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (e.bias)
+        v = load8_16(e.bias + col, n);
+    unpack8<Fmt>(v, b);
+}
+
+// Eight neighbouring outputs (n of them inside the matrix) of each of the rows
+// row, row + step, ... below M: v the sums, u the up projection's (gated only).
+// The residual is read by the lane that writes the same elements of Y, so Y
+// may be the residual itself; all rows' residuals are read before the first
+// row is written, so that their loads are in flight together.  WHOLE: n is 8
+// for every lane, so no access branches on it.  ACT: the activation, or
+// kAnyActivation for e's.  bias: zeros without one (a sum is never -0: adding
+// them changes nothing).
+constexpr int kAnyActivation = -1;
+template <class Fmt, bool GATED, bool WHOLE, int ACT, int ROWS>
+__device__ __forceinline__ void emit_rows(const Epilogue &e, int row, int step, int M, int col, int inside,
+                                          float (&v)[ROWS][8], const float (&u)[ROWS][8], const float (&bias)[8])
+{
+    const int n = WHOLE ? 8 : inside;
+    float r[ROWS][8];
+    if (!GATED && e.R) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] += b[i];
+        for (int i = 0; i < ROWS; ++i) {
+            const int at = row + i * step;
+            const size_t ra = (size_t)(at < M ? at : row) * e.ldr + col;
+            if (e.y_f32)
+                load8_f32((const float *)e.R + ra, n, r[i]);
+            else
+                unpack8<Fmt>(load8_16((const uint16_t *)e.R + ra, n), r[i]);
+        }
     }
+    if (!GATED)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[i][c] += bias[c];
     if (e.pre) {
-        store8_16(e.pre + (size_t)row * e.ldp + col, n, pack8<Fmt>(v));
-        if (GATED)
-            store8_16(e.pre2 + (size_t)row * e.ldp + col, n, pack8<Fmt>(u));
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (row + i * step < M) {
+                const size_t at = (size_t)(row + i * step) * e.ldp + col;
+                store8_16(e.pre + at, n, pack8<Fmt>(v[i]));
+                if (GATED)
+                    store8_16(e.pre2 + at, n, pack8<Fmt>(u[i]));
+            }
     }
+    auto apply = [&](int act) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[i][c] = activate(act, v[i][c]);
+    };
     // one uniform branch on the activation, not one an element
-    switch (e.act) {
-#define DGOR_ACT_CASE(A)                          \
-    case A:                                       \
-        _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = activate(A, v[i]); \
-        break;
-        DGOR_ACT_CASE(GEMM_ACT_RELU)
-        DGOR_ACT_CASE(GEMM_ACT_GELU)
-        DGOR_ACT_CASE(GEMM_ACT_GELU_TANH)
-        DGOR_ACT_CASE(GEMM_ACT_SILU)
-#undef DGOR_ACT_CASE
+    switch (ACT == kAnyActivation ? e.act : ACT) {
+    case GEMM_ACT_RELU: apply(GEMM_ACT_RELU); break;
+    case GEMM_ACT_GELU: apply(GEMM_ACT_GELU); break;
+    case GEMM_ACT_GELU_TANH: apply(GEMM_ACT_GELU_TANH); break;
+    case GEMM_ACT_SILU: apply(GEMM_ACT_SILU); break;
     default: break;
     }
-    if (GATED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] *= u[i];
-    }
-    const size_t at = (size_t)row * e.ldy + col;
-    if (!GATED && e.R) {
-        float r[8];
-        const size_t ra = (size_t)row * e.ldr + col;
-        if (e.y_f32)
-            load8_f32((const float *)e.R + ra, n, r);
-        else
-            unpack8<Fmt>(load8_16((const uint16_t *)e.R + ra, n), r);
+    for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] += r[i];
+        for (int c = 0; c < 8; ++c) {
+            if (GATED)
+                v[i][c] *= u[i][c];
+            else if (e.R)
+                v[i][c] += r[i][c];
+        }
+        if (row + i * step < M) {
+            const size_t at = (size_t)(row + i * step) * e.ldy + col;
+            if (!GATED && e.y_f32)
+                store8_f32((float *)e.Y + at, n, v[i]);
+            else
+                store8_16((uint16_t *)e.Y + at, n, pack8<Fmt>(v[i]));
+        }
     }
-    if (!GATED && e.y_f32)
-        store8_f32((float *)e.Y + at, n, v);
-    else
-        store8_16((uint16_t *)e.Y + at, n, pack8<Fmt>(v));
+}
+
+// One row's.
+template <class Fmt, bool GATED>
+__device__ __forceinline__ void emit8(const Epilogue &e, int row, int col, int n, const float (&v)[8],
+                                      const float (&u)[8])
+{
+    float b[8], v1[1][8], u1[1][8];
+    load_bias<Fmt>(e, col, n, b);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        v1[0][c] = v[c], u1[0][c] = u[c];
+    emit_rows<Fmt, GATED, false, kAnyActivation, 1>(e, row, 0, row + 1, col, n, v1, u1, b);
 }
 
 }  // namespace dgor

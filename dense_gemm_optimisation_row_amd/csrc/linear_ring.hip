@@ -22,12 +22,13 @@
 // sums of its elements.  A as M x K is staged two stages at a time, whole
 // 128-byte lines: rows of eight units, unit c of row r at 8 r + (c ^ ((r >> 1) & 7)).
 //
-// Pipeline.  B has four stage buffers, A as K x M too, A as M x K three
-// buffers of two stages.  During stage t the fragments of stage t + 1 are
-// read and the loads of B stage t + 3 and A stage t + 3 (half of pair
-// t / 2 + 2) issued, spread between the MFMAs.  Each stage begins with a wait
-// for this wavefront's loads of two stages before and a barrier: then stage
-// t + 1 has landed, and the buffers that are refilled were last read by
+// Pipeline.  Loads run D stages ahead: 3, and 7 on the 64 x 64 tile, whose
+// stages are shorter.  B has D + 1 stage buffers, A as K x M too, A as M x K
+// (D + 3) / 2 buffers of two stages.  During stage t the fragments of stage
+// t + 1 are read and the loads of B stage t + D and A stage t + D (half of
+// pair (t + D + 1) / 2) issued, spread between the MFMAs.  Each stage begins
+// with a wait for this wavefront's loads of stage t + 1 and a barrier: then all
+// of that stage has landed, and the buffers that are refilled were last read by
 // fragments that every wavefront has since consumed.
 //
 // Bound by the matrix cores where there are tiles for every compute unit; the
@@ -88,8 +89,10 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     constexpr int LPA = BM / 64, LPB = BN / 64;    // a wavefront's loads of each operand and stage
     constexpr int HALF_A = BK * HM * 2, HALF_B = BK * HN * 2, STAGE_A = 2 * HALF_A, STAGE_B = 2 * HALF_B;
     constexpr int PAIR = 2 * STAGE_A;
-    constexpr int A_BYTES = TA ? 4 * STAGE_A : 3 * PAIR;
-    constexpr int LDS_BYTES = A_BYTES + 4 * STAGE_B;
+    constexpr int D = BM == 64 ? 7 : 3;            // stages that a load is ahead of its fragments' stage
+    constexpr int A_PAIRS = (D + 1) / 2 + 1;
+    constexpr int A_BYTES = TA ? (D + 1) * STAGE_A : A_PAIRS * PAIR;
+    constexpr int LDS_BYTES = A_BYTES + (D + 1) * STAGE_B;
     constexpr int FT = GATED ? HN : BN;            // output columns of a tile
     __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_BYTES];
     const uint32_t ring = lds_address(lds);
@@ -146,7 +149,7 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
             L.r.z = L.k_left <= 0 ? 0 : (b_left >= HN ? 0x7fffffff : range_of(b_left, L.k_left, ldb));
         else
             L.r.z = L.k_left >= BK ? 0x7fffffff : range_of(L.k_left, b_left, ldb);
-        L.dst = lds_b + (uint32_t)((t & 3) * STAGE_B);
+        L.dst = lds_b + (uint32_t)((t & D) * STAGE_B);
         return L;
     };
     auto load_b = [&](const Loads &L, int q) {
@@ -286,14 +289,14 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    auto next_pair = [](uint32_t b) { return b == (uint32_t)(2 * PAIR) ? 0u : b + PAIR; };
-    auto a_buf = [](int t) { return (uint32_t)((t & 3) * STAGE_A); };
-    auto b_buf = [](int t) { return (uint32_t)((t & 3) * STAGE_B); };
+    auto next_pair = [](uint32_t b) { return b == (uint32_t)((A_PAIRS - 1) * PAIR) ? 0u : b + PAIR; };
+    auto a_buf = [](int t) { return (uint32_t)((t & D) * STAGE_A); };   // D + 1 is a power of two
+    auto b_buf = [](int t) { return (uint32_t)((t & D) * STAGE_B); };
 
     halfx8 fa0[FA], fa1[FA], fb0[FB], fb1[FB];
     if (TA) {
 #pragma unroll
-        for (int st = 0; st < 3; ++st) {
+        for (int st = 0; st < D; ++st) {
             const Loads LA = a_loads(st, a_buf(st)), LB = b_loads(st);
 #pragma unroll
             for (int q = 0; q < LPA; ++q)
@@ -302,28 +305,24 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
             for (int q = 0; q < LPB; ++q)
                 load_b(LB, q);
         }
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * (LPA + LPB)));
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt((D - 1) * (LPA + LPB)));
     } else {
-        const Loads P0 = a_loads(0, 0), P1 = a_loads(2, PAIR);
+        // in the order of their stages: pair 0, B 0; B 1; pair 1, B 2; B 3; ...
 #pragma unroll
-        for (int j = 0; j < 2 * LPA; ++j)
-            load_a(P0, j);
+        for (int st = 0; st < D; ++st) {
+            if (st % 2 == 0) {
+                const Loads LA = a_loads(st, (uint32_t)(st / 2 * PAIR));
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+                for (int j = 0; j < 2 * LPA; ++j)
+                    load_a(LA, j);
+            }
             const Loads LB = b_loads(st);
 #pragma unroll
             for (int q = 0; q < LPB; ++q)
                 load_b(LB, q);
         }
-#pragma unroll
-        for (int j = 0; j < 2 * LPA; ++j)
-            load_a(P1, j);
-        const Loads LB = b_loads(2);
-#pragma unroll
-        for (int q = 0; q < LPB; ++q)
-            load_b(LB, q);
         // A pair 0 and B stage 0 have landed
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * LPA + 2 * LPB));
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt((D - 1) * (LPA + LPB)));
     }
     __builtin_amdgcn_s_barrier();
     {
@@ -332,31 +331,36 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
         for (int r = 0; r < FA + FB; ++r)
             fread(S, r, fa0, fb0);
     }
-    auto wait = [&](int t) {
-        // the loads of the stage before may stay in flight (at stage 0: A pair
-        // 1 and B stage 2)
-        if (!TA && t == 0)
-            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(2 * LPA + LPB));
+    // Before stage t: B stage t + 1 and the A it reads have landed.  Loads are
+    // in the order of their stages, each stage's B first; an even stage's next
+    // stage is of the pair it already reads.
+    auto wait = [&](int par) {
+        if (!TA && par == 0)
+            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0((D - 2) * (LPA + LPB) + LPA));
         else
-            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(LPA + LPB));
+            __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0((D - 2) * (LPA + LPB)));
         __builtin_amdgcn_s_barrier();
     };
-    uint32_t pa = 0;   // the pair's buffer
+    uint32_t pa = 0, pl = (uint32_t)((A_PAIRS - 1) * PAIR);   // the pair's buffer, and that of the pair to load
     for (int t = 0; t < steps; t += 2) {
-        const uint32_t pa1 = next_pair(pa), pa2 = next_pair(pa1);
-        wait(t);
+        const uint32_t pa1 = next_pair(pa);
+        wait(0);
         {
-            const Loads LA = TA ? a_loads(t + 3, a_buf(t + 3)) : a_loads(t + 4, pa2), LB = b_loads(t + 3);
+            const Loads LA = TA ? a_loads(t + D, a_buf(t + D)) : a_loads(t + D + 1, pl), LB = b_loads(t + D);
             __builtin_amdgcn_sched_barrier(0);
-            stage(0, LA, LB, TA ? Source{a_buf(t + 1), 0, b_buf(t + 1)} : Source{pa, 1, b_buf(t + 1)}, fa0, fb0, fa1, fb1);
+            stage(0, LA, LB, TA ? Source{a_buf(t + 1), 0, b_buf(t + 1)} : Source{pa, 1, b_buf(t + 1)}, fa0, fb0, fa1,
+                  fb1);
         }
         if (t + 1 < steps) {
-            wait(t + 1);
-            const Loads LA = TA ? a_loads(t + 4, a_buf(t + 4)) : a_loads(t + 4, pa2), LB = b_loads(t + 4);
+            wait(1);
+            const Loads LA = TA ? a_loads(t + D + 1, a_buf(t + D + 1)) : a_loads(t + D + 1, pl),
+                        LB = b_loads(t + D + 1);
             __builtin_amdgcn_sched_barrier(0);
-            stage(1, LA, LB, TA ? Source{a_buf(t + 2), 0, b_buf(t + 2)} : Source{pa1, 0, b_buf(t + 2)}, fa1, fb1, fa0, fb0);
+            stage(1, LA, LB, TA ? Source{a_buf(t + 2), 0, b_buf(t + 2)} : Source{pa1, 0, b_buf(t + 2)}, fa1, fb1, fa0,
+                  fb0);
         }
         pa = pa1;
+        pl = next_pair(pl);
     }
     // no load may still be writing LDS, nor a wavefront reading the ring
     __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
@@ -374,36 +378,80 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     Epilogue e = p.e;
     if (batch)
         e.Y = p.Y1;
-#pragma unroll
+    // a lane keeps its columns through all rounds, every STEP-th row of each
+    constexpr int STEP = 64 / LANES, TURNS = 32 / STEP, TOGETHER = TURNS < 2 ? 1 : 2;
+    const int r0 = lane / LANES, c = 8 * (lane % LANES), col = c0 + c, cols = N - col;
+    const bool mine = cols > 0, whole = n0 + FT <= N;
+    float bias[8] = {};
+    if (!GATED && mine && p.splits <= 1)
+        load_bias<Op>(e, col, cols, bias);
+    // one copy of the code behind the accumulators: unrolled, its first run
+    // waits for instructions longer than it works (256 x 256 tile: 10 us)
+#pragma unroll 1
     for (int round = 0; round < FA / 2; ++round) {
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii)
+        for (int k = 0; k < FA / 2; ++k)
+            if (round == k) {
 #pragma unroll
-            for (int j = 0; j < FB; ++j)
+                for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    w[(16 * ii + 4 * g + r) * ROW + 16 * j + s16] = dgor_acc_read(acc[2 * round + ii][j][r]);
+                    for (int j = 0; j < FB; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            w[(16 * ii + 4 * g + r) * ROW + 16 * j + s16] = dgor_acc_read(acc[2 * k + ii][j][r]);
+            }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
+        // the round's rows, TOGETHER at a time, to take(first row, v, u)
+        auto rows = [&](auto take) {
 #pragma unroll 1
-        for (int q = 0; q < 32 * LANES / 64; ++q) {
-            const int id = lane + 64 * q, r = id / LANES, c = 8 * (id % LANES);
-            const int row = m0 + wrow + 32 * round + r, col = c0 + c;
-            if (row < M && col < N) {
-                float v[8], u[8];
+            for (int q0 = 0; q0 < TURNS; q0 += TOGETHER) {
+                const int lr = r0 + STEP * q0, row = m0 + wrow + 32 * round + lr;
+                if (!mine || row >= M)
+                    break;
+                float v[TOGETHER][8], u[TOGETHER][8];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    v[x] = w[r * ROW + c + x];
-                    u[x] = GATED ? w[r * ROW + COLS + c + x] : 0.f;
-                }
-                if (p.splits > 1) {
-                    const size_t MN = (size_t)M * N, at = (size_t)row * N + col;
-                    store8_f32(p.part + ((size_t)batch * p.splits + blockIdx.y) * MN + at, N - col, v);
-                    if (GATED)
-                        store8_f32(p.part + ((size_t)p.splits + blockIdx.y) * MN + at, N - col, u);
-                } else {
-                    emit8<Op, GATED>(e, row, col, N - col, v, u);
-                }
+                for (int q = 0; q < TOGETHER; ++q)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        v[q][x] = w[(lr + STEP * q) * ROW + c + x];
+                        u[q][x] = GATED ? w[(lr + STEP * q) * ROW + COLS + c + x] : 0.f;
+                    }
+                take(row, v, u);
+            }
+        };
+        typedef float Rows[TOGETHER][8];
+        if (p.splits > 1) {
+            rows([&](int row, Rows &v, Rows &u) {
+                const size_t MN = (size_t)M * N;
+                float *part = p.part + ((size_t)batch * p.splits + blockIdx.y) * MN + (size_t)row * N + col;
+#pragma unroll
+                for (int q = 0; q < TOGETHER; ++q)
+                    if (row + STEP * q < M) {
+                        store8_f32(part + (size_t)(STEP * q) * N, cols, v[q]);
+                        if (GATED)
+                            store8_f32(part + p.splits * MN + (size_t)(STEP * q) * N, cols, u[q]);
+                    }
+            });
+        } else if (!whole) {
+            rows([&](int row, Rows &v, Rows &u) {
+                emit_rows<Op, GATED, false, kAnyActivation, TOGETHER>(e, row, STEP, M, col, cols, v, u, bias);
+            });
+        } else {
+            // a copy for each activation: the branch is taken once a round,
+            // and the values stay in their registers
+            switch (e.act) {
+#define DGOR_ROWS(A)                                                                              \
+    rows([&](int row, Rows &v, Rows &u) {                                                         \
+        emit_rows<Op, GATED, true, A, TOGETHER>(e, row, STEP, M, col, 8, v, u, bias);             \
+    });                                                                                           \
+    break
+            case GEMM_ACT_RELU: DGOR_ROWS(GEMM_ACT_RELU);
+            case GEMM_ACT_GELU: DGOR_ROWS(GEMM_ACT_GELU);
+            case GEMM_ACT_GELU_TANH: DGOR_ROWS(GEMM_ACT_GELU_TANH);
+            case GEMM_ACT_SILU: DGOR_ROWS(GEMM_ACT_SILU);
+            default: DGOR_ROWS(GEMM_ACT_NONE);
+#undef DGOR_ROWS
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
