@@ -62,34 +62,34 @@ void split(const Product &p, long long parts, Way &w)
     }
 }
 
-// Estimated cycles of a product on a ring's tile with its sum in `parts`: each
-// compute unit holds `share` workgroups of the tile at once, a stage of 32 k
-// of one takes `alone` cycles by itself and `full` of the unit when its share
-// is there, a workgroup's beginning and end `ends`; parts are written in
-// FP32 and joined by another launch (measured: 1500 bytes a cycle there and
-// back, and 9000 cycles).
+// Time of a product on a ring's tile with its sum in `parts`.  Up to `share`
+// workgroups of the tile run on a compute unit at once; a round of them takes
+// `ends` and, for each 32 k, `alone` (at most one a unit) or `full`.  Parts are
+// written in FP32 and joined by another launch.  Microseconds, fitted to 16 to
+// 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N): within
+// 10% of the times measured.  Full rates: 1470, 1280, 1180 and 570 TFLOP/s.
 struct RingCost {
     dgor::RingTile tile;
-    int share, alone, full, ends;
+    int share;
+    double ends, alone, full, n_by_k;   // the last: times as long with B as N x K, whose loads take half lines
 };
 constexpr RingCost kRings[] = {
-    {dgor::kRing256, 1, 1150, 1150, 7000},
-    {dgor::kRing256x128, 1, 640, 640, 5000},
-    {dgor::kRing128, 2, 420, 340, 4000},
-    {dgor::kRing64, 4, 260, 110, 3000},
+    {dgor::kRing256, 1, 14.5, 0.73, 0.73, 1.0},
+    {dgor::kRing256x128, 1, 9.8, 0.42, 0.42, 1.3},
+    {dgor::kRing128, 2, 6.8, 0.295, 0.455, 1.17},
+    {dgor::kRing64, 2, 4.0, 0.158, 0.235, 1.08},
 };
-double cycles(const Product &p, const RingCost &c, int parts)
+constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
+double microseconds(const Product &p, const RingCost &c, int parts)
 {
     const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
-    const double stages = 2.0 * dgor::product_stages(p) / parts;
-    const long long rounds = n / (256LL * c.share), rest = n - rounds * 256LL * c.share;
-    const double whole = c.full * c.share > c.alone ? c.full * c.share : c.alone;
-    const double last = c.full * ceil_div(rest, 256);
-    double t = rounds * (stages * whole + c.ends);
+    const double stages = 2.0 * dgor::product_stages(p) / parts * (p.trans_b ? c.n_by_k : 1.0);
+    const long long rounds = n / (256LL * c.share), rest = n % (256LL * c.share);
+    double t = rounds * (c.ends + stages * c.full);
     if (rest)
-        t += stages * (last > c.alone ? last : c.alone) + c.ends;
+        t += c.ends + stages * (rest <= 256 ? c.alone : c.full);
     if (parts > 1)
-        t += 9000 + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / 1500;
+        t += kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes;
     return t;
 }
 
@@ -104,12 +104,11 @@ Way choose(const Product &p, bool ring)
         double best = 0;
         int best_parts = 1;
         for (const RingCost &c : kRings) {
-            // parts until two workgroups wait for each place, at least four
-            // stages of 64 k each
+            // parts until two rounds are full, at least two stages of 64 k each
             const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile));
-            for (int parts = 1; parts == 1 || (parts <= 16 && 4 * parts <= stages && n * parts <= 512 * c.share);
+            for (int parts = 1; parts == 1 || (parts <= 16 && 2 * parts <= stages && n * parts <= 512 * c.share);
                  ++parts) {
-                const double t = cycles(p, c, parts);
+                const double t = microseconds(p, c, parts);
                 if (best == 0 || t < best)
                     best = t, best_parts = parts, w.tile = c.tile;
             }
