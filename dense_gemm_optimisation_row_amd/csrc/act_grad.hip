@@ -73,18 +73,19 @@ template <class Fmt>
 __global__ __launch_bounds__(256) void sum_blocks_kernel(int blocks, int N, const float *__restrict__ sums,
                                                          uint16_t *__restrict__ out)
 {
-    // 64 columns x 4 threads over the blocks
-    __shared__ float part[4][64];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+    // 32 columns x 8 threads over the blocks
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < N)
-        for (int b = w; b < blocks; b += 4)
+#pragma unroll 4
+        for (int b = w; b < blocks; b += 8)
             s += sums[(size_t)b * N + c];
-    part[w][threadIdx.x & 63] = s;
+    part[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < N)
-        out[c] = Fmt::down((part[0][threadIdx.x] + part[1][threadIdx.x]) +
-                           (part[2][threadIdx.x] + part[3][threadIdx.x]));
+        out[c] = Fmt::down(((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])) +
+                           ((part[4][lane] + part[5][lane]) + (part[6][lane] + part[7][lane])));
 }
 
 template <class Fmt>
@@ -163,7 +164,7 @@ hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uin
 
 hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out, bool bf16, hipStream_t s)
 {
-    hipLaunchKernelGGL((bf16 ? sum_blocks_kernel<Brain16> : sum_blocks_kernel<Half16>), dim3((N + 63) / 64),
+    hipLaunchKernelGGL((bf16 ? sum_blocks_kernel<Brain16> : sum_blocks_kernel<Half16>), dim3((N + 31) / 32),
                        dim3(256), 0, s, blocks, N, sums, out);
     return hipGetLastError();
 }

@@ -7,15 +7,19 @@
 //   dw_j = sum over rows of dy_j xh_j,  db_j = sum over rows of dy_j.
 //
 // Bound by memory.  A row is held in registers, eight elements of a thread
-// at a time, so it is read once: rows of up to 1024 elements by one wavefront
-// (four rows a workgroup, no barrier), up to 16384 by a workgroup of 256.
-// The variance is the second pass over the registers, around the mean, so
-// it loses nothing where the mean is large.  Longer rows are read again for
-// each pass (the second read comes from the caches).
-// The weight gradients: a workgroup takes every gridDim-th row and keeps its
-// columns' sums in registers, so dy and x are read once for dx, dw and db
-// together; the workgroups' sums are added in a fixed order by a second
-// kernel.
+// at a time, so it is read once: in the forward pass rows of up to 1024
+// elements by one wavefront (four rows a workgroup, no barrier), up to 16384 by
+// a workgroup of 256; all of a row's loads, the weights' among them, are
+// issued before the first sum.  Sums within a wavefront are shifts on the
+// vector ALUs.  The variance is the second pass over the registers, around the
+// mean, so it loses nothing where the mean is large.  Longer rows are read
+// again for each pass (the second read comes from the caches).
+// 8192 x 4096 BF16: 29.4 us, 4.6 TB/s, where a copy of it takes 26.5; with sums
+// through LDS shuffles and the weights loaded after them it took 37.
+// The weight gradients: a workgroup, one for each compute unit, takes every
+// gridDim-th rows and keeps its columns' sums in registers, so dy and x are
+// read once for dx, dw and db together; the workgroups' sums are added in a
+// fixed order by a second kernel.
 #include "common.h"
 #include "linear.h"
 
@@ -24,6 +28,22 @@ namespace {
 
 struct Single {
     using T = float;
+    // eight elements as they are loaded, and opened
+    struct Raw {
+        float f[8];
+    };
+    static __device__ __forceinline__ Raw fetch(const float *p, int n)
+    {
+        Raw r;
+        load8_f32(p, n, r.f);
+        return r;
+    }
+    static __device__ __forceinline__ void open(const Raw &r, float (&f)[8])
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = r.f[e];
+    }
     static __device__ __forceinline__ void load8(const float *p, int n, float (&f)[8]) { load8_f32(p, n, f); }
     static __device__ __forceinline__ void store8(float *p, int n, const float (&f)[8]) { store8_f32(p, n, f); }
     static __device__ __forceinline__ float down(float f) { return f; }
@@ -31,6 +51,9 @@ struct Single {
 template <class Fmt>
 struct Short {
     using T = uint16_t;
+    using Raw = u32x4;
+    static __device__ __forceinline__ Raw fetch(const uint16_t *p, int n) { return load8_16(p, n); }
+    static __device__ __forceinline__ void open(const Raw &r, float (&f)[8]) { unpack8<Fmt>(r, f); }
     static __device__ __forceinline__ void load8(const uint16_t *p, int n, float (&f)[8])
     {
         unpack8<Fmt>(load8_16(p, n), f);
@@ -42,16 +65,45 @@ struct Short {
     static __device__ __forceinline__ uint16_t down(float f) { return Fmt::down(f); }
 };
 
+// A wavefront's sum, in every lane: four shifts within rows of 16 lanes, two
+// across them, all on the vector ALUs.
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ float add_shifted(float v)
+{
+    const int t = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CONTROL, ROWS, 0xf, false);
+    return v + __builtin_bit_cast(float, t);
+}
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int m = 32; m; m >>= 1)
-        v += __shfl_xor(v, m);
-    return v;
+    v = add_shifted<0x111, 0xf>(v);   // row_shr:1, 2, 4, 8; lanes without a source add zero
+    v = add_shifted<0x112, 0xf>(v);
+    v = add_shifted<0x114, 0xf>(v);
+    v = add_shifted<0x118, 0xf>(v);
+    v = add_shifted<0x142, 0xa>(v);   // row_bcast:15 into rows 1 and 3
+    v = add_shifted<0x143, 0xc>(v);   // row_bcast:31 into rows 2 and 3
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// The sums of a and b over the RT threads of a row, in every one of them.
-// slots: 8 floats of LDS, not read since the last barrier.
+// The sum of a over the RT threads of a row, in every one of them.
+// slots: a float of LDS for each of the row's wavefronts, not read since the
+// last barrier.
+template <int RT>
+__device__ __forceinline__ float row_sum(float a, float *slots)
+{
+    a = wave_sum(a);
+    if (RT == 64)
+        return a;
+    if ((threadIdx.x & 63) == 0)
+        slots[threadIdx.x % RT / 64] = a;
+    __syncthreads();
+    a = slots[0];
+#pragma unroll
+    for (int i = 1; i < RT / 64; ++i)
+        a += slots[i];
+    return a;
+}
+
+// The sums of a and b likewise; slots: two floats a wavefront.
 template <int RT>
 __device__ __forceinline__ void row_sum2(float &a, float &b, float *slots)
 {
@@ -59,58 +111,79 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float *slots)
     b = wave_sum(b);
     if (RT == 64)
         return;
-    const int wave = threadIdx.x >> 6;
+    const int wave = threadIdx.x % RT / 64;
     if ((threadIdx.x & 63) == 0) {
-        slots[wave] = a;
-        slots[4 + wave] = b;
+        slots[2 * wave] = a;
+        slots[2 * wave + 1] = b;
     }
     __syncthreads();
-    a = (slots[0] + slots[1]) + (slots[2] + slots[3]);
-    b = (slots[4] + slots[5]) + (slots[6] + slots[7]);
+    a = slots[0];
+    b = slots[1];
+#pragma unroll
+    for (int i = 1; i < RT / 64; ++i) {
+        a += slots[2 * i];
+        b += slots[2 * i + 1];
+    }
 }
 
-template <class X, class W, int RT, int V>
+// WHOLE: N is a multiple of 8, so no access branches on a row's end.
+template <class X, class W, int RT, int V, bool WHOLE>
 __global__ __launch_bounds__(256) void layer_norm_kernel(int M, int N, const typename X::T *__restrict__ x, int ldx,
                                                          const typename W::T *__restrict__ weight,
                                                          const typename W::T *__restrict__ bias, float eps,
                                                          typename X::T *__restrict__ y, int ldy,
                                                          float *__restrict__ mean_out, float *__restrict__ rstd_out)
 {
-    __shared__ float slots[2][8];
+    __shared__ float slots[2][4];
     constexpr int ROWS = 256 / RT;
     const int at = threadIdx.x % RT;
     // a row's two sums use a slot each, with a barrier between any write of a
     // slot and its last readers; with a row a wavefront there is no barrier
     for (long long row = blockIdx.x * ROWS + (RT == 64 ? (int)(threadIdx.x >> 6) : 0); row < M;
          row += (long long)gridDim.x * ROWS) {
-        float v[V][8], sum = 0.f, none = 0.f;
+        // all of the row's loads first, the weights' among them
+        typename X::Raw xr[V];
+        typename W::Raw wr[V], br[V];
+        float v[V][8], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i);
-            if (c < N)
-                X::load8(x + (size_t)row * ldx + c, N - c, v[i]);
+            const int c = 8 * (at + RT * i), n = WHOLE ? 8 : N - c;
+            if (c < N) {
+                xr[i] = X::fetch(x + (size_t)row * ldx + c, n);   // elements past the row are zero
+                if (weight)
+                    wr[i] = W::fetch(weight + c, n);
+                if (bias)
+                    br[i] = W::fetch(bias + c, n);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (8 * (at + RT * i) < N)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum += v[i][e];   // elements past the row are zero
-        row_sum2<RT>(sum, none, slots[0]);
-        const float mean = sum / (float)N;
+        for (int i = 0; i < V; ++i) {
+            if (8 * (at + RT * i) >= N)
+                continue;
+            X::open(xr[i], v[i]);
+            sum += ((v[i][0] + v[i][1]) + (v[i][2] + v[i][3])) + ((v[i][4] + v[i][5]) + (v[i][6] + v[i][7]));
+        }
+        const float mean = row_sum<RT>(sum, slots[0]) / (float)N;
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (at + RT * i);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 8; ++e)
                 v[i][e] -= mean;
-                if (c + e < N)
-                    sq = __builtin_fmaf(v[i][e], v[i][e], sq);
+            if (WHOLE) {
+                if (c < N)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sq = __builtin_fmaf(v[i][e], v[i][e], sq);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < N)
+                        sq = __builtin_fmaf(v[i][e], v[i][e], sq);
             }
         }
-        row_sum2<RT>(sq, none, slots[1]);
-        const float rstd = 1.f / sqrtf(sq / (float)N + eps);
+        const float rstd = 1.f / sqrtf(row_sum<RT>(sq, slots[1]) / (float)N + eps);
         if (at == 0) {
             if (mean_out)
                 mean_out[row] = mean;
@@ -119,20 +192,18 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(int M, int N, const typ
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i), n = N - c;
-            if (n <= 0)
-                break;
-            float w[8], b[8];
-            if (weight)
-                W::load8(weight + c, n, w);
-            if (bias)
-                W::load8(bias + c, n, b);
+            const int c = 8 * (at + RT * i);
+            if (c < N) {
+                float w[8], b[8];
+                if (weight)
+                    W::open(wr[i], w);
+                if (bias)
+                    W::open(br[i], b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float h = v[i][e] * rstd;
-                v[i][e] = __builtin_fmaf(h, weight ? w[e] : 1.f, bias ? b[e] : 0.f);
+                for (int e = 0; e < 8; ++e)
+                    v[i][e] = __builtin_fmaf(v[i][e] * rstd, weight ? w[e] : 1.f, bias ? b[e] : 0.f);
+                X::store8(y + (size_t)row * ldy + c, WHOLE ? 8 : N - c, v[i]);
             }
-            X::store8(y + (size_t)row * ldy + c, n, v[i]);
         }
     }
 }
@@ -147,17 +218,16 @@ __global__ __launch_bounds__(256) void layer_norm_long_kernel(int M, int N, cons
                                                               float *__restrict__ mean_out,
                                                               float *__restrict__ rstd_out)
 {
-    __shared__ float slots[2][8];
+    __shared__ float slots[2][4];
     for (size_t row = blockIdx.x; row < (size_t)M; row += gridDim.x) {
         const typename X::T *x = xs + row * ldx;
         typename X::T *y = ys + row * ldy;
-        float sum = 0.f, none = 0.f, sq = 0.f, v[8], w[8], b[8];
+        float sum = 0.f, sq = 0.f, v[8], w[8], b[8];
         for (int c = 8 * threadIdx.x; c < N; c += 2048) {
             X::load8(x + c, N - c, v);
             sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
-        row_sum2<256>(sum, none, slots[0]);
-        const float mean = sum / (float)N;
+        const float mean = row_sum<256>(sum, slots[0]) / (float)N;
         for (int c = 8 * threadIdx.x; c < N; c += 2048) {
             X::load8(x + c, N - c, v);
 #pragma unroll
@@ -165,8 +235,7 @@ __global__ __launch_bounds__(256) void layer_norm_long_kernel(int M, int N, cons
                 if (c + e < N)
                     sq = __builtin_fmaf(v[e] - mean, v[e] - mean, sq);
         }
-        row_sum2<256>(sq, none, slots[1]);
-        const float rstd = 1.f / sqrtf(sq / (float)N + eps);
+        const float rstd = 1.f / sqrtf(row_sum<256>(sq, slots[1]) / (float)N + eps);
         if (threadIdx.x == 0) {
             if (mean_out)
                 mean_out[row] = mean;
@@ -187,108 +256,149 @@ __global__ __launch_bounds__(256) void layer_norm_long_kernel(int M, int N, cons
     }
 }
 
-template <class X, class W, int RT, int V>
-__global__ __launch_bounds__(256) void layer_norm_backward_kernel(
+// G rows at a time, by RT threads each, 1024 in all (256 with eight
+// units a thread); a workgroup takes rows blockIdx.x G + g, then gridDim.x G
+// further on.  With one unit a thread, the next row's loads are issued before a
+// row is worked on; with more the registers do not hold them.  The groups' sums of dw and db meet in LDS, halves of the groups
+// at a time in a fixed order; they go to sums[block][2][N] or, with one
+// workgroup, straight to dweight and dbias.
+template <class X, class W, int RT, int V, int G, bool WHOLE>
+__global__ __launch_bounds__(RT * G) void layer_norm_backward_kernel(
     int M, int N, const typename X::T *__restrict__ dy, int lddy, const typename X::T *__restrict__ x, int ldx,
     const typename W::T *__restrict__ weight, const float *__restrict__ mean, const float *__restrict__ rstd,
-    typename X::T *__restrict__ dx, int lddx, float *__restrict__ sums)
+    typename X::T *__restrict__ dx, int lddx, float *__restrict__ sums, typename W::T *__restrict__ dweight,
+    typename W::T *__restrict__ dbias)
 {
-    constexpr int ROWS = 256 / RT;
-    __shared__ float slots[2][8];
-    const int at = threadIdx.x % RT, sub = RT == 64 ? (int)(threadIdx.x >> 6) : 0;
-    float w[V][8], dw[V][8], db[V][8];
+    __shared__ float slots[2][RT / 32 * G];
+    const int at = threadIdx.x % RT, group = threadIdx.x / RT;
+    typename W::Raw wr[V];
+    float dw[V][8], db[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (at + RT * i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 8; ++e)
             dw[i][e] = db[i][e] = 0.f;
-            w[i][e] = 1.f;
-        }
         if (weight && c < N)
-            W::load8(weight + c, N - c, w[i]);
+            wr[i] = W::fetch(weight + c, WHOLE ? 8 : N - c);
     }
+    typename X::Raw xr[V], tr[V];
+    float mu = 0.f, rs = 0.f;
+    auto fetch = [&](long long row) {
+        if (row >= M)
+            return;
+        mu = mean[row];
+        rs = rstd[row];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (at + RT * i), n = WHOLE ? 8 : N - c;
+            if (c < N) {
+                xr[i] = X::fetch(x + (size_t)row * ldx + c, n);
+                tr[i] = X::fetch(dy + (size_t)row * lddy + c, n);   // zero past the row
+            }
+        }
+    };
     const float inv = 1.f / (float)N;
+    const long long step = (long long)gridDim.x * G;
+    if (V == 1)
+        fetch((long long)blockIdx.x * G + group);
     int turn = 0;
-    // every wavefront of a workgroup that shares a row runs the same trips
-    for (long long row = blockIdx.x * ROWS + sub; row < M; row += gridDim.x * ROWS, turn ^= 1) {
+    // every wavefront of the workgroup runs the same trips
+    for (long long first = (long long)blockIdx.x * G; first < M; first += step, turn ^= 1) {
+        const long long row = first + group;
         float h[V][8], t[V][8], a = 0.f, b = 0.f;
-        const float mu = mean[row], rs = rstd[row];
+        if (V > 1)
+            fetch(row);
+        const float rs_row = rs;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (at + RT * i);
-            if (c < N) {
-                X::load8(x + (size_t)row * ldx + c, N - c, h[i]);
-                X::load8(dy + (size_t)row * lddy + c, N - c, t[i]);   // zero past the row
+            if (row < M && c < N) {
+                X::open(xr[i], h[i]);
+                X::open(tr[i], t[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[i][e] = (h[i][e] - mu) * rs;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     h[i][e] = t[i][e] = 0.f;
             }
         }
+        if (V == 1)
+            fetch(row + step);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            float w[8];
+            if (weight)
+                W::open(wr[i], w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                h[i][e] = (h[i][e] - mu) * rs;
                 dw[i][e] = __builtin_fmaf(t[i][e], h[i][e], dw[i][e]);
                 db[i][e] += t[i][e];
-                t[i][e] *= w[i][e];
+                if (weight)
+                    t[i][e] = 8 * (at + RT * i) < N ? t[i][e] * w[e] : 0.f;
                 a += t[i][e];
                 b = __builtin_fmaf(t[i][e], h[i][e], b);
             }
-        row_sum2<RT>(a, b, slots[turn]);
+        }
+        row_sum2<RT>(a, b, slots[turn] + RT / 32 * group);
         a *= inv;
         b *= inv;
+        if (row < M)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i);
-            if (c < N) {
+            for (int i = 0; i < V; ++i) {
+                const int c = 8 * (at + RT * i);
+                if (c < N) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[i][e] = rs * (t[i][e] - a - h[i][e] * b);
-                X::store8(dx + (size_t)row * lddx + c, N - c, t[i]);
+                    for (int e = 0; e < 8; ++e)
+                        t[i][e] = rs_row * (t[i][e] - a - h[i][e] * b);
+                    X::store8(dx + (size_t)row * lddx + c, WHOLE ? 8 : N - c, t[i]);
+                }
             }
-        }
     }
-    if (!sums)
+    if (!sums && !dweight && !dbias)
         return;
-    float *out = sums + (size_t)blockIdx.x * 2 * N;
-    if constexpr (RT == 64) {
-        // the four wavefronts' sums, added in LDS in their order
-        __shared__ float part[3][V * 512];
+    if constexpr (G > 1) {
+        __shared__ float part[G / 2][2][V * 8 * RT];
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            float(&mine)[V][8] = pass ? db : dw;
-            __syncthreads();
-            if (sub > 0)
+        for (int half = G / 2; half; half /= 2) {
+            __syncthreads();   // the part's readers are done
+            if (group >= half && group < 2 * half)
 #pragma unroll
                 for (int i = 0; i < V; ++i)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        part[sub - 1][(i * 8 + e) * 64 + at] = mine[i][e];
+                    for (int e = 0; e < 8; ++e) {
+                        part[group - half][0][(i * 8 + e) * RT + at] = dw[i][e];
+                        part[group - half][1][(i * 8 + e) * RT + at] = db[i][e];
+                    }
             __syncthreads();
-            if (sub == 0)
+            if (group < half)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = 8 * (at + RT * i);
+                for (int i = 0; i < V; ++i)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int k = (i * 8 + e) * 64 + at;
-                        mine[i][e] = ((mine[i][e] + part[0][k]) + part[1][k]) + part[2][k];
+                        dw[i][e] += part[group][0][(i * 8 + e) * RT + at];
+                        db[i][e] += part[group][1][(i * 8 + e) * RT + at];
                     }
-                    if (c < N)
-                        store8_f32(out + pass * N + c, N - c, mine[i]);
-                }
         }
-    } else {
+        if (group)
+            return;
+    }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i);
-            if (c < N) {
-                store8_f32(out + c, N - c, dw[i]);
-                store8_f32(out + N + c, N - c, db[i]);
-            }
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (at + RT * i), n = WHOLE ? 8 : N - c;
+        if (c >= N)
+            continue;
+        if (sums) {
+            float *out = sums + (size_t)blockIdx.x * 2 * N;
+            store8_f32(out + c, n, dw[i]);
+            store8_f32(out + N + c, n, db[i]);
+        } else {
+            if (dweight)
+                W::store8(dweight + c, n, dw[i]);
+            if (dbias)
+                W::store8(dbias + c, n, db[i]);
         }
     }
 }
@@ -401,7 +511,7 @@ __global__ __launch_bounds__(256) void layer_norm_join_kernel(int blocks, int N,
 }
 
 constexpr int kMaxHeld = 16384;   // longest row that a workgroup holds
-constexpr int kBackwardGroups = 512;   // workgroups of the backward kernel: two a compute unit
+constexpr int kUnits = 256;       // compute units
 
 struct NormArgs {
     int M, N;
@@ -421,9 +531,11 @@ unsigned most(long long rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 <
 template <class X, class W, int RT, int V>
 hipError_t forward_as(const NormArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((layer_norm_kernel<X, W, RT, V>), dim3(most(((long long)a.M + 256 / RT - 1) / (256 / RT))), dim3(256), 0, s, a.M,
-                       a.N, (const typename X::T *)a.x, a.ldx, (const typename W::T *)a.weight,
-                       (const typename W::T *)a.bias, a.eps, (typename X::T *)a.out, a.ldout, a.mean, a.rstd);
+    const dim3 grid(most(((long long)a.M + 256 / RT - 1) / (256 / RT)));
+    hipLaunchKernelGGL((a.N % 8 == 0 ? layer_norm_kernel<X, W, RT, V, true> : layer_norm_kernel<X, W, RT, V, false>),
+                       grid, dim3(256), 0, s, a.M, a.N, (const typename X::T *)a.x, a.ldx,
+                       (const typename W::T *)a.weight, (const typename W::T *)a.bias, a.eps,
+                       (typename X::T *)a.out, a.ldout, a.mean, a.rstd);
     return hipGetLastError();
 }
 
@@ -448,13 +560,23 @@ hipError_t forward(const NormArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <class X, class W, int RT, int V>
+template <class X, class W, int RT, int V, int G>
 hipError_t backward_as(const NormArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((layer_norm_backward_kernel<X, W, RT, V>), dim3(a.blocks), dim3(256), 0, s, a.M, a.N,
-                       (const typename X::T *)a.dy, a.lddy, (const typename X::T *)a.x, a.ldx,
-                       (const typename W::T *)a.weight, a.mean, a.rstd, (typename X::T *)a.out, a.ldout, a.sums);
+    using WT = typename W::T;
+    hipLaunchKernelGGL((a.N % 8 == 0 ? layer_norm_backward_kernel<X, W, RT, V, G, true>
+                                     : layer_norm_backward_kernel<X, W, RT, V, G, false>),
+                       dim3(a.blocks), dim3(RT * G), 0, s, a.M, a.N, (const typename X::T *)a.dy, a.lddy,
+                       (const typename X::T *)a.x, a.ldx, (const WT *)a.weight, a.mean, a.rstd,
+                       (typename X::T *)a.out, a.ldout, a.sums, a.sums ? nullptr : (WT *)a.dweight,
+                       a.sums ? nullptr : (WT *)a.dbias);
     return hipGetLastError();
+}
+
+// Rows that a workgroup of the backward kernel works on at once.
+int rows_at_once(int N)
+{
+    return N <= 512 ? 16 : (N <= 1024 ? 8 : (N <= 2048 ? 4 : (N <= 4096 ? 2 : 1)));
 }
 
 template <class X, class W>
@@ -462,17 +584,17 @@ hipError_t backward(const NormArgs &a, hipStream_t s)
 {
     hipError_t err;
     if (a.N <= 512)
-        err = backward_as<X, W, 64, 1>(a, s);
+        err = backward_as<X, W, 64, 1, 16>(a, s);
     else if (a.N <= 1024)
-        err = backward_as<X, W, 64, 2>(a, s);
+        err = backward_as<X, W, 128, 1, 8>(a, s);
     else if (a.N <= 2048)
-        err = backward_as<X, W, 256, 1>(a, s);
+        err = backward_as<X, W, 256, 1, 4>(a, s);
     else if (a.N <= 4096)
-        err = backward_as<X, W, 256, 2>(a, s);
+        err = backward_as<X, W, 512, 1, 2>(a, s);
     else if (a.N <= 8192)
-        err = backward_as<X, W, 256, 4>(a, s);
+        err = backward_as<X, W, 1024, 1, 1>(a, s);
     else if (a.N <= kMaxHeld)
-        err = backward_as<X, W, 256, 8>(a, s);
+        err = backward_as<X, W, 256, 8, 1>(a, s);
     else {
         hipLaunchKernelGGL((layer_norm_backward_long_kernel<X, W>), dim3(most(a.M)), dim3(256), 0, s, a.M, a.N,
                            (const typename X::T *)a.dy, a.lddy, (const typename X::T *)a.x, a.ldx,
@@ -516,14 +638,19 @@ int check(const gemm_layer_norm_params *p)
     return GEMM_OK;
 }
 
-// Workgroups of the backward kernel, each with its 2 N sums: no more than
-// there are rows for.
+// Workgroups of the backward kernel, each with its 2 N sums: one for each
+// compute unit, no more than there are rows for, and a single one, whose sums
+// need no joining, for up to four turns.
 int backward_blocks(int M, int N)
 {
-    const int rows = N <= 1024 ? 4 : 1;
+    const int rows = rows_at_once(N);
+    if (M <= 4 * rows && N <= kMaxHeld)
+        return 1;
     const int want = M / rows + (M % rows != 0);
-    return want < kBackwardGroups ? want : kBackwardGroups;
+    return want < kUnits ? want : kUnits;
 }
+// Whether the sums of the weights' gradients pass through the workspace.
+bool joined(int M, int N) { return backward_blocks(M, N) > 1 || N > kMaxHeld; }
 
 int run_forward(Type t, const gemm_layer_norm_params *p, const void *x, const void *weight, const void *bias, void *y,
                 float *mean, float *rstd, void *stream)
@@ -566,7 +693,7 @@ int run_backward(Type t, const gemm_layer_norm_params *p, const void *dy, const 
     a.dweight = dweight, a.dbias = dbias;
     a.blocks = backward_blocks(p->M, p->N);
     const bool grads = dweight || dbias, empty = p->M == 0;   // no rows: the weight gradients are empty sums
-    if (grads && !empty) {
+    if (grads && !empty && joined(p->M, p->N)) {
         if (!ws || ((uintptr_t)ws & 255) || ws_bytes < (size_t)a.blocks * 2 * p->N * sizeof(float))
             return GEMM_ERR_WORKSPACE;
         a.sums = (float *)ws;
@@ -615,7 +742,9 @@ int gemm_layer_norm_backward_workspace(const gemm_layer_norm_params *params, siz
         return GEMM_ERR_NULL_PTR;
     const int rc = dgor::check(params);
     if (rc == GEMM_OK)
-        *bytes = (size_t)dgor::backward_blocks(params->M, params->N) * 2 * params->N * sizeof(float);
+        *bytes = dgor::joined(params->M, params->N)
+                     ? (size_t)dgor::backward_blocks(params->M, params->N) * 2 * params->N * sizeof(float)
+                     : 0;
     return rc;
 }
 int gemm_layer_norm_backward_f32(const gemm_layer_norm_params *params, const float *dy, const float *x,

@@ -361,7 +361,9 @@ def test_gated_backward_is_exact_on_integers(shape, dtype, transposed):
 # --------------------------------------------------------------- layer norm --
 
 NORM_SHAPES = [(1, 1), (1, 64), (3, 7), (5, 513), (70, 512), (9, 1000), (130, 1024), (3, 1500), (700, 777),
-               (1100, 2048), (4, 4096), (600, 4097), (3, 8000), (2, 16384), (2, 16385), (40, 20001)]
+               (1100, 2048), (4, 4096), (600, 4097), (3, 8000), (2, 16384), (2, 16385), (40, 20001),
+               # several turns of each form of the backward kernel
+               (300, 9000), (5000, 513), (5000, 200), (700, 8192), (700, 3000)]
 
 
 @pytest.mark.parametrize("dtype,weight_f32", [("f32", True), ("f16", False), ("f16", True), ("bf16", False),
