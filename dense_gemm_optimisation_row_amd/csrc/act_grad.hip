@@ -16,6 +16,25 @@ namespace {
 
 constexpr int kCols = 256;
 
+// x to act'(x): one uniform branch on the activation, not one an element.
+__device__ __forceinline__ void slopes(int act, float (&x)[8])
+{
+    auto apply = [&](int a) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float value;
+            activate_slope(a, x[e], value, x[e]);
+        }
+    };
+    switch (act) {
+    case GEMM_ACT_RELU: apply(GEMM_ACT_RELU); break;
+    case GEMM_ACT_GELU: apply(GEMM_ACT_GELU); break;
+    case GEMM_ACT_GELU_TANH: apply(GEMM_ACT_GELU_TANH); break;
+    case GEMM_ACT_SILU: apply(GEMM_ACT_SILU); break;
+    default: apply(GEMM_ACT_NONE);
+    }
+}
+
 template <class Fmt>
 __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint16_t *__restrict__ dy, int lddy,
                                                        const uint16_t *__restrict__ z, int ldz,
@@ -28,23 +47,32 @@ __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint1
     const int col = strip * kCols + 8 * lane, n = N - col;
     const int row0 = block * kGradRows;
     float total[8] = {};
-    if (n > 0) {
-#pragma unroll 4
-        for (int i = 0; i < kGradRows / 8; ++i) {
+    // all of a thread's rows are loaded before the first is worked on; rows
+    // past M are read from the last and not used
+    auto rows = [&](auto load) {
+        constexpr int R = kGradRows / 8;
+        u32x4 dv[R], zv[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const size_t row = (size_t)min(row0 + 8 * i + r8, M - 1);
+            dv[i] = load(dy + row * lddy + col);
+            if (z)
+                zv[i] = load(z + row * ldz + col);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
             const int row = row0 + 8 * i + r8;
             if (row >= M)
-                continue;
+                break;
             float d[8];
-            unpack8<Fmt>(load8_16(dy + (size_t)row * lddy + col, n), d);
+            unpack8<Fmt>(dv[i], d);
             if (z) {
                 float x[8];
-                unpack8<Fmt>(load8_16(z + (size_t)row * ldz + col, n), x);
+                unpack8<Fmt>(zv[i], x);
+                slopes(act, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float value, slope;
-                    activate_slope(act, x[e], value, slope);
-                    d[e] *= slope;
-                }
+                for (int e = 0; e < 8; ++e)
+                    d[e] *= x[e];
             }
             if (dz)   // past N zeros: its rows are padded to whole units
                 store8_16(dz + (size_t)row * lddz + col, 8, pack8<Fmt>(d));
@@ -52,7 +80,11 @@ __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint1
             for (int e = 0; e < 8; ++e)
                 total[e] += d[e];
         }
-    }
+    };
+    if (n >= 8)
+        rows([](const uint16_t *p) { return load8_16(p, 8); });
+    else if (n > 0)
+        rows([&](const uint16_t *p) { return load8_16(p, n); });
     if (!sums)
         return;
 #pragma unroll
@@ -95,31 +127,46 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
                                                         uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int ldd,
                                                         int act)
 {
+    // a unit a thread, 32 units x 8 rows a workgroup
     const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
     const int strips = (F + kCols - 1) / kCols;
-    const int col = (blockIdx.x % strips) * kCols + 8 * lane, n = F - col;
-    if (n <= 0)
+    const int col = (int)(blockIdx.x % strips) * kCols + 8 * lane, n = F - col;
+    const int row = (int)(blockIdx.x / strips) * 8 + r8;
+    if (n <= 0 || row >= M)
         return;
-    const int row0 = (blockIdx.x / strips) * kGradRows;
-#pragma unroll 2
-    for (int i = 0; i < kGradRows / 8; ++i) {
-        const int row = row0 + 8 * i + r8;
-        if (row >= M)
-            return;
-        float d[8], x[8], y[8], a[8], b[8];
-        unpack8<Fmt>(load8_16(dh + (size_t)row * lddh + col, n), d);
-        unpack8<Fmt>(load8_16(g + (size_t)row * ldp + col, n), x);
-        unpack8<Fmt>(load8_16(u + (size_t)row * ldp + col, n), y);
+    u32x4 dv, gv, uv;
+    const size_t at = (size_t)row * ldp + col;
+    if (n >= 8) {
+        dv = load8_16(dh + (size_t)row * lddh + col, 8);
+        gv = load8_16(g + at, 8);
+        uv = load8_16(u + at, 8);
+    } else {
+        dv = load8_16(dh + (size_t)row * lddh + col, n);
+        gv = load8_16(g + at, n);
+        uv = load8_16(u + at, n);
+    }
+    float d[8], x[8], y[8], a[8], b[8];
+    unpack8<Fmt>(dv, d);
+    unpack8<Fmt>(gv, x);
+    unpack8<Fmt>(uv, y);
+    auto apply = [&](int which) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float value, slope;
-            activate_slope(act, x[e], value, slope);
+            activate_slope(which, x[e], value, slope);
             a[e] = d[e] * y[e] * slope;
             b[e] = d[e] * value;
         }
-        store8_16(dg + (size_t)row * ldd + col, 8, pack8<Fmt>(a));   // past F zeros
-        store8_16(du + (size_t)row * ldd + col, 8, pack8<Fmt>(b));
+    };
+    switch (act) {
+    case GEMM_ACT_RELU: apply(GEMM_ACT_RELU); break;
+    case GEMM_ACT_GELU: apply(GEMM_ACT_GELU); break;
+    case GEMM_ACT_GELU_TANH: apply(GEMM_ACT_GELU_TANH); break;
+    case GEMM_ACT_SILU: apply(GEMM_ACT_SILU); break;
+    default: apply(GEMM_ACT_NONE);
     }
+    store8_16(dg + (size_t)row * ldd + col, 8, pack8<Fmt>(a));   // past F zeros
+    store8_16(du + (size_t)row * ldd + col, 8, pack8<Fmt>(b));
 }
 
 // Eight elements a thread: a unit read at any alignment, written whole.
@@ -172,7 +219,7 @@ hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out
 hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u, int ldp,
                             uint16_t *dg, uint16_t *du, int ldd, int act, bool bf16, hipStream_t s)
 {
-    const dim3 grid((unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + kGradRows - 1) / kGradRows));
+    const dim3 grid((unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + 7) / 8));
     hipLaunchKernelGGL((bf16 ? gate_grad_kernel<Brain16> : gate_grad_kernel<Half16>), grid, dim3(256), 0, s, M, F, dh,
                        lddh, g, u, ldp, dg, du, ldd, act);
     return hipGetLastError();

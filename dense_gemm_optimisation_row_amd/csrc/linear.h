@@ -19,8 +19,8 @@ namespace dgor {
 // At most one of the three.
 // Split over k (splits > 1): split s covers stages [s chunk, (s + 1) chunk)
 // of 64 k each (counted over both segments) and writes its FP32 sums to
-// part: ((batch or gate/up) * splits + s) * M * N; launch_join adds them in
-// that order and applies the epilogue.
+// part: ((batch or gate/up) * splits + s) * part_size(p), rows padded to whole
+// units; launch_join adds them in that order and applies the epilogue.
 struct Product {
     int M, N, K;
     const uint16_t *A[2];
@@ -36,6 +36,8 @@ struct Product {
     int tiles_m, tiles_n, group_m;   // filled by the launcher
 };
 
+__host__ __device__ inline int part_stride(const Product &p) { return (p.N + 7) / 8 * 8; }
+__host__ __device__ inline size_t part_size(const Product &p) { return (size_t)p.M * part_stride(p); }
 constexpr int kStageDepth = 64;   // k per stage, the unit of Product::chunk
 inline int product_stages(const Product &p) { return p.nseg * ((p.K + kStageDepth - 1) / kStageDepth); }
 
@@ -59,6 +61,8 @@ inline bool spans_a_unit(const Product &p)
     const long long b_rows = p.trans_b ? p.N : p.K, b_cols = p.trans_b ? p.K : p.N;
     return (long long)(p.M - 1) * p.lda + p.K >= 8 && (b_rows - 1) * p.ldb + b_cols >= 8;
 }
+// Columns of a workgroup's strip, of the one or each of the two products.
+inline int skinny_strip(const Product &p, bool split) { return p.trans_b ? 16 : (split && !p.gated ? 64 : 32); }
 hipError_t launch_linear_skinny(const Product &p, hipStream_t stream);
 
 // Copies of operands whose rows are not whole units, padded to them with zeros.

@@ -68,6 +68,9 @@ void split(const Product &p, long long parts, Way &w)
 // written in FP32 and joined by another launch.  Microseconds, fitted to 16 to
 // 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N): within
 // 10% of the times measured.  Full rates: 1470, 1280, 1180 and 570 TFLOP/s.
+// An activation of exponentials adds to a tile's end what its outputs take on
+// the vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs: 236 us, 217
+// without).
 struct RingCost {
     dgor::RingTile tile;
     int share;
@@ -79,15 +82,18 @@ constexpr RingCost kRings[] = {
     {dgor::kRing128, 2, 6.8, 0.295, 0.455, 1.17},
     {dgor::kRing64, 2, 4.0, 0.158, 0.235, 1.08},
 };
+constexpr int kSplitRows = 40;   // stages of 64 k from which few rows' sums over a K x N matrix are split
 constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
 double microseconds(const Product &p, const RingCost &c, int parts)
 {
     const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
     const double stages = 2.0 * dgor::product_stages(p) / parts * (p.trans_b ? c.n_by_k : 1.0);
     const long long rounds = n / (256LL * c.share), rest = n % (256LL * c.share);
-    double t = rounds * (c.ends + stages * c.full);
+    const double outputs = (double)ring_tile_m(c.tile) * ring_tile_n(c.tile) / 65536;
+    const double ends = c.ends + (p.e.act > GEMM_ACT_RELU && parts == 1 ? 9.0 * outputs : 0.0);
+    double t = rounds * (ends + stages * c.full);
     if (rest)
-        t += c.ends + stages * (rest <= 256 ? c.alone : c.full);
+        t += ends + stages * (rest <= 256 ? c.alone : c.full);
     if (parts > 1)
         t += kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes;
     return t;
@@ -96,9 +102,18 @@ double microseconds(const Product &p, const RingCost &c, int parts)
 Way choose(const Product &p, bool ring)
 {
     Way w{Kernel::Rows, dgor::kRing64, 1, 0};
-    if (few_rows(p))
-        return w;
     const int stages = dgor::product_stages(p);
+    if (few_rows(p)) {
+        // a K x N matrix with a long sum and too few columns for the compute
+        // units: parts of at least eight stages, one for each wavefront
+        const long long strips = ceil_div(p.N, dgor::skinny_strip(p, true));
+        if (!p.trans_b && stages >= kSplitRows && strips < 256) {
+            long long want = (256 + strips - 1) / strips;
+            want = want < stages / 8 ? want : stages / 8;
+            split(p, want < 32 ? want : 32, w);
+        }
+        return w;
+    }
     if (ring) {
         w.kernel = Kernel::Ring;
         double best = 0;
@@ -135,7 +150,7 @@ size_t part_bytes(const Product &p)
     size_t most = 0;
     for (int ring = 0; ring < (ring_sizes(p) ? 2 : 1); ++ring) {
         const Way w = choose(p, ring);
-        const size_t b = w.splits <= 1 ? 0 : (size_t)(p.gated ? 2 : p.nbatch) * w.splits * p.M * p.N * sizeof(float);
+        const size_t b = w.splits <= 1 ? 0 : (size_t)(p.gated ? 2 : p.nbatch) * w.splits * dgor::part_size(p) * sizeof(float);
         most = b > most ? b : most;
     }
     return round_up(most, kWsAlign);
@@ -150,10 +165,9 @@ hipError_t run_product(Product p, void *ws, hipStream_t s)
     p.splits = w.splits;
     p.chunk = w.chunk;
     p.part = (float *)ws;
-    if (w.kernel == Kernel::Rows)
-        return dgor::launch_linear_skinny(p, s);
-    const hipError_t err =
-        w.kernel == Kernel::Ring ? dgor::launch_linear_ring(p, w.tile, s) : dgor::launch_tile(p, s);
+    const hipError_t err = w.kernel == Kernel::Rows   ? dgor::launch_linear_skinny(p, s)
+                           : w.kernel == Kernel::Ring ? dgor::launch_linear_ring(p, w.tile, s)
+                                                      : dgor::launch_tile(p, s);
     if (err != hipSuccess || p.splits <= 1)
         return err;
     return dgor::launch_join(p, s);
@@ -275,6 +289,7 @@ int check_linear(const gemm_linear_params *q, Product &p, Copies &c, int (&copy)
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
     p = forward_product(q->M, q->N, q->K, q->op_w, q->ldx, q->ldw, false);
+    p.e.act = q->activation;
     copy_operands(p, c, copy);
     return GEMM_OK;
 }
@@ -305,7 +320,7 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
     p.A[0] = p.A[1] = c.use(copy[0], X, base);
     p.B[0] = p.B[1] = c.use(copy[1], W, base);
     p.e.Y = Y, p.e.ldy = q->ldy, p.e.y_f32 = q->y_f32 != 0;
-    p.e.bias = bias, p.e.act = q->activation;
+    p.e.bias = bias;
     p.e.R = R, p.e.ldr = q->ldr;
     p.e.pre = pre, p.e.ldp = q->ldp;
     const hipError_t err = c.launch(s);
@@ -425,6 +440,7 @@ int check_gated(const gemm_gated_params *q, Product &p, Copies &c, int (&copy)[3
     if (!act_ok(q->activation))
         return GEMM_ERR_INVALID_ACTIVATION;
     p = forward_product(q->M, q->F, q->K, q->op_w, q->ldx, q->ldw, true);
+    p.e.act = q->activation;
     copy_operands(p, c, copy);
     return GEMM_OK;
 }
@@ -455,7 +471,7 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
     p.bf16 = bf16;
     p.A[0] = p.A[1] = c.use(copy[0], X, base);
     p.B[0] = c.use(copy[1], Wg, base), p.B[1] = c.use(copy[2], Wu, base);
-    p.e.Y = H, p.e.ldy = q->ldh, p.e.act = q->activation;
+    p.e.Y = H, p.e.ldy = q->ldh;
     p.e.pre = G, p.e.pre2 = U, p.e.ldp = q->ldp;
     const hipError_t err = c.launch(s);
     return done(err == hipSuccess ? run_product(p, base + c.bytes, s) : err);

@@ -426,14 +426,14 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
         typedef float Rows[TOGETHER][8];
         if (p.splits > 1) {
             rows([&](int row, Rows &v, Rows &u) {
-                const size_t MN = (size_t)M * N;
-                float *part = p.part + ((size_t)batch * p.splits + blockIdx.y) * MN + (size_t)row * N + col;
+                const int ld = part_stride(p);
+                float *part = p.part + ((size_t)batch * p.splits + blockIdx.y) * part_size(p) + (size_t)row * ld + col;
 #pragma unroll
                 for (int q = 0; q < TOGETHER; ++q)
                     if (row + STEP * q < M) {
-                        store8_f32(part + (size_t)(STEP * q) * N, cols, v[q]);
+                        store8_f32(part + (size_t)(STEP * q) * ld, 8, v[q]);
                         if (GATED)
-                            store8_f32(part + p.splits * MN + (size_t)(STEP * q) * N, cols, u[q]);
+                            store8_f32(part + p.splits * part_size(p) + (size_t)(STEP * q) * ld, 8, u[q]);
                     }
             });
         } else if (!whole) {

@@ -2,11 +2,11 @@
 // for M of at most 64.
 //
 // Bound by reading B once.  A workgroup of eight wavefronts takes a strip of
-// columns and the whole sum over k, so there is one launch and nothing to
-// join: wavefront w takes the 64-deep chunks w, w + 8, ... and has the loads of
-// UNROLL of them in flight at once; the eight sums meet in LDS, in wavefront
-// order.  FP32 sums on v_mfma_f32_16x16x32: lane (g, s) = (lane / 16, lane % 16)
-// supplies k 8 g .. 8 g + 7 of row s of A and of column s of B.
+// columns and, as a rule, the whole sum over k, so there is one launch and
+// nothing to join: wavefront w takes the 64-deep chunks w, w + 8, ... and has the
+// loads of UNROLL of them in flight at once; the eight sums meet in LDS, in
+// wavefront order.  FP32 sums on v_mfma_f32_16x16x32: lane (g, s) = (lane / 16,
+// lane % 16) supplies k 8 g .. 8 g + 7 of row s of A and of column s of B.
 //
 // What the caches serve is counted in pieces that neighbouring lanes ask for
 // together, so every load takes whole rows of a chunk (of A, and of B as
@@ -19,8 +19,12 @@
 //   64 k x 32 columns (4 KB, in 16-row loads j): the load's rows 4 q + i hold
 //     k 32 (j / 2) + 4 (j % 2) + 8 q + i, unit u of row r at 4 r + (u ^ 2 ((r >> 2) & 1)),
 //     read transposing, the eight rows of a cycle on distinct banks.
+//   64 k x 64 columns (8 KB): unit u of row k at 8 k + (u ^ x(k)).
 // Strips: 16 columns of B as N x K, 32 as K x N; the strips beside it, which
-// share its lines, run on the same XCD.
+// share its lines, run on the same XCD.  A compute unit takes about the same
+// number of pieces a microsecond whatever their size (K x N: 32 bytes each 19
+// GB/s, 64 bytes 33), so of a K x N matrix with a long sum the strips are 64
+// columns, whole lines, and the sum is split over workgroups and joined.
 #include "common.h"
 #include "linear.h"
 
@@ -50,13 +54,17 @@ struct OpBrain : Brain16 {
 
 constexpr int kWaves = 8;
 
+// Of 64 k rows of eight units: unit u of row k at 8 k + (u ^ this); k and k + 4
+// have the same.
+__device__ __forceinline__ int wide_swizzle(int k) { return 2 * ((k >> 1) & 1) + 4 * ((k >> 3) & 1); }
+
 // RB: 16-row blocks of A; CB: 16-column blocks of a strip.  A gated product's
 // blocks are CB of the gate and then the same CB of the up projection.
 template <class Op, int RB, int CB, bool TB, bool GATED, int UNROLL>
 __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
 {
     constexpr int NM = GATED ? 2 : 1, NB = NM * CB;         // matrices B, column blocks
-    static_assert(TB || CB == 2, "a K x N strip is 32 columns");
+    static_assert(TB || CB == 2 || CB == 4, "a K x N strip is 32 or 64 columns");
     constexpr int PITCH = 16 * NB + 4;                      // floats; spreads four-row groups over the banks
     constexpr int SUMS = kWaves * RB * 16 * PITCH * 4;      // bytes
     constexpr int TURN = (RB + NB) * 2048;                  // a wavefront's chunk
@@ -67,7 +75,9 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
     const int n0 = strip * 16 * CB;
     const int lane = threadIdx.x & 63, s16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int per_seg = (K + 63) / 64, chunks = p.nseg * per_seg;
+    const int per_seg = (K + 63) / 64;
+    const int first = p.splits > 1 ? (int)blockIdx.y * p.chunk : 0;
+    const int chunks = p.splits > 1 ? min(first + p.chunk, p.nseg * per_seg) : p.nseg * per_seg;
     const int r8 = lane >> 3, c8 = 8 * (lane & 7);          // of 8 rows x 64 k
     const int r16 = lane >> 2, c4 = 8 * (lane & 3);         // of 16 rows x 32 columns
 
@@ -87,11 +97,15 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
             s.b[i] = Operand{p.B[GATED ? i : seg], TB ? N : K, TB ? K : N, (size_t)p.ldb};
         return s;
     };
-    // load i of B: TB rows 8 (i % 2) of matrix i / 2, else load i % 4 of matrix i / 4
+    // load i of B: the (i % 2 CB)th of matrix i / (2 CB)
     auto b_place = [&](int i, int k0, int &row, int &col) {
         const int j = i % (2 * CB);
-        row = TB ? n0 + 8 * j + r8 : k0 + 32 * (j >> 1) + 4 * (j & 1) + 8 * (r16 >> 2) + (r16 & 3);
-        col = TB ? k0 + c8 : n0 + c4;
+        if (TB)
+            row = n0 + 8 * j + r8, col = k0 + c8;
+        else if (CB == 4)
+            row = k0 + 8 * j + r8, col = n0 + c8;
+        else
+            row = k0 + 32 * (j >> 1) + 4 * (j & 1) + 8 * (r16 >> 2) + (r16 & 3), col = n0 + c4;
     };
     floatx4 acc[RB][NB];
 #pragma unroll
@@ -101,7 +115,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
             acc[i][b] = floatx4{0.f, 0.f, 0.f, 0.f};
     uint8_t *const xl = lds + wave * TURN, *const wl = xl + RB * 2048;
     auto row_slot = [&](int r) { return 16 * (8 * r + ((lane & 7) ^ ((r >> 1) & 7))); };
-    for (int c0 = wave; c0 < chunks; c0 += kWaves * UNROLL) {
+    for (int c0 = first + wave; c0 < chunks; c0 += kWaves * UNROLL) {
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const Chunk s = chunk_of(c0 + kWaves * u);
@@ -139,9 +153,10 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i)
-                *reinterpret_cast<u32x4 *>(wl + (TB ? row_slot(8 * i + r8)
-                                                    : 1024 * i + 64 * r16 + 16 * ((lane & 3) ^ (2 * ((r16 >> 2) & 1))))) =
-                    w[u][i];
+                *reinterpret_cast<u32x4 *>(
+                    wl + (TB ? row_slot(8 * i + r8)
+                             : 1024 * i + (CB == 4 ? 128 * r8 + 16 * ((lane & 7) ^ wide_swizzle(8 * i + r8))
+                                                   : 64 * r16 + 16 * ((lane & 3) ^ (2 * ((r16 >> 2) & 1)))))) = w[u][i];
 #pragma unroll
             for (int i = 0; i < 2 * RB; ++i)
                 *reinterpret_cast<u32x4 *>(xl + row_slot(8 * i + r8)) = x[u][i];
@@ -161,10 +176,13 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
                     if (TB) {
                         b[j] = of_rows(wl + 2048 * j);
                     } else {
-                        const uint8_t *q = wl + 4096 * (j / 2) + 2048 * h + 64 * (4 * g + (s16 >> 2)) +
-                                           16 * ((2 * (j % 2) + ((s16 & 3) >> 1)) ^ (2 * (g & 1))) + 8 * (s16 & 1);
+                        const int unit = 2 * (j % CB) + ((s16 & 3) >> 1), kr = 8 * g + (s16 >> 2);
+                        const uint8_t *q = wl + 2048 * CB * (j / CB) + 1024 * CB * h + 8 * (s16 & 1) +
+                                           (CB == 4 ? 128 * kr + 16 * (unit ^ wide_swizzle(kr))
+                                                    : 64 * (4 * g + (s16 >> 2)) + 16 * (unit ^ (2 * (g & 1))));
                         const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
-                        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 1024));
+                        const shortx4 hi =
+                            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + (CB == 4 ? 512 : 1024)));
                         b[j] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                     }
                 }
@@ -206,40 +224,49 @@ __global__ __launch_bounds__(64 * kWaves) void linear_skinny_kernel(Product p)
                 v[o] = sums[row * PITCH + c + o];
                 u[o] = GATED ? sums[row * PITCH + 16 * CB + c + o] : 0.f;
             }
-            emit8<Op, GATED>(p.e, row, col, N - col, v, u);
+            if (p.splits > 1) {
+                float *part = p.part + blockIdx.y * part_size(p) + (size_t)row * part_stride(p) + col;
+                store8_f32(part, 8, v);
+                if (GATED)
+                    store8_f32(part + p.splits * part_size(p), 8, u);
+            } else {
+                emit8<Op, GATED>(p.e, row, col, N - col, v, u);
+            }
         }
     }
 }
 
-template <class Op, int RB, bool TB, bool GATED>
+template <class Op, int RB, int CB, bool TB, bool GATED>
 hipError_t launch_rows(const Product &p, hipStream_t s)
 {
     // 16-byte loads in flight, a lane: up to 32, what the registers hold
-    constexpr int CB = TB ? 1 : 2, EACH = 2 * (RB + CB * (GATED ? 2 : 1));
+    constexpr int EACH = 2 * (RB + CB * (GATED ? 2 : 1));
     constexpr int UNROLL = EACH <= 4 ? 8 : (EACH <= 8 ? 4 : (EACH <= 12 ? 2 : 1));
-    hipLaunchKernelGGL((linear_skinny_kernel<Op, RB, CB, TB, GATED, UNROLL>), dim3((unsigned)p.tiles_n),
-                       dim3(64 * kWaves), 0, s, p);
+    hipLaunchKernelGGL((linear_skinny_kernel<Op, RB, CB, TB, GATED, UNROLL>),
+                       dim3((unsigned)p.tiles_n, (unsigned)(p.splits > 1 ? p.splits : 1)), dim3(64 * kWaves), 0, s, p);
     return hipGetLastError();
 }
 
-template <class Op, bool TB, bool GATED>
+template <class Op, int CB, bool TB, bool GATED>
 hipError_t launch_blocks(const Product &p, hipStream_t s)
 {
     switch ((p.M + 15) / 16) {
-    case 1: return launch_rows<Op, 1, TB, GATED>(p, s);
-    case 2: return launch_rows<Op, 2, TB, GATED>(p, s);
-    case 3: return launch_rows<Op, 3, TB, GATED>(p, s);
-    case 4: return launch_rows<Op, 4, TB, GATED>(p, s);
+    case 1: return launch_rows<Op, 1, CB, TB, GATED>(p, s);
+    case 2: return launch_rows<Op, 2, CB, TB, GATED>(p, s);
+    case 3: return launch_rows<Op, 3, CB, TB, GATED>(p, s);
+    case 4: return launch_rows<Op, 4, CB, TB, GATED>(p, s);
     default: return hipErrorInvalidValue;
     }
 }
 
 template <class Op>
-hipError_t launch_op(const Product &p, hipStream_t s)
+hipError_t launch_op(const Product &p, int strip, hipStream_t s)
 {
     if (p.gated)
-        return p.trans_b ? launch_blocks<Op, true, true>(p, s) : launch_blocks<Op, false, true>(p, s);
-    return p.trans_b ? launch_blocks<Op, true, false>(p, s) : launch_blocks<Op, false, false>(p, s);
+        return p.trans_b ? launch_blocks<Op, 1, true, true>(p, s) : launch_blocks<Op, 2, false, true>(p, s);
+    if (p.trans_b)
+        return launch_blocks<Op, 1, true, false>(p, s);
+    return strip == 64 ? launch_blocks<Op, 4, false, false>(p, s) : launch_blocks<Op, 2, false, false>(p, s);
 }
 
 }  // namespace
@@ -249,10 +276,10 @@ hipError_t launch_linear_skinny(const Product &q, hipStream_t s)
     Product p = q;
     if (p.trans_a || p.nbatch != 1 || p.M > kSkinnyRows || !spans_a_unit(p))
         return hipErrorInvalidValue;
-    const int strip = p.trans_b ? 16 : 32;
+    const int strip = skinny_strip(p, p.splits > 1);
     p.tiles_m = 1;
     p.tiles_n = (p.N + strip - 1) / strip;
-    return p.bf16 ? launch_op<OpBrain>(p, s) : launch_op<OpHalf>(p, s);
+    return p.bf16 ? launch_op<OpBrain>(p, strip, s) : launch_op<OpHalf>(p, strip, s);
 }
 
 }  // namespace dgor

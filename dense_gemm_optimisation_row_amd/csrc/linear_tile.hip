@@ -201,10 +201,11 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
                     u[x] = GATED ? w[r * ROW + COLS + c + x] : 0.f;
                 }
                 if (p.splits > 1) {
-                    const size_t MN = (size_t)M * N, at = (size_t)row * N + col;
-                    store8_f32(p.part + ((size_t)batch * p.splits + blockIdx.y) * MN + at, N - col, v);
+                    float *part = p.part + ((size_t)batch * p.splits + blockIdx.y) * part_size(p) +
+                                  (size_t)row * part_stride(p) + col;
+                    store8_f32(part, 8, v);
                     if (GATED)
-                        store8_f32(p.part + ((size_t)p.splits + blockIdx.y) * MN + at, N - col, u);
+                        store8_f32(part + p.splits * part_size(p), 8, u);
                 } else {
                     emit8<Op, GATED>(e, row, col, N - col, v, u);
                 }
@@ -221,22 +222,23 @@ template <class Op, bool GATED>
 __global__ __launch_bounds__(256) void linear_join_kernel(Product p)
 {
     const int batch = blockIdx.y;
-    const size_t MN = (size_t)p.M * p.N;
-    const int groups = (p.N + 7) / 8;
-    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (size_t)p.M * groups)
+    const size_t size = part_size(p);
+    const unsigned groups = (unsigned)(p.N + 7) / 8;
+    const unsigned id = blockIdx.x * 256 + threadIdx.x;   // split products are small
+    if (id >= (unsigned)p.M * groups)
         return;
     const int row = (int)(id / groups), col = 8 * (int)(id % groups), n = p.N - col;
     float v[8] = {}, u[8] = {};
-    const float *q = p.part + (size_t)batch * p.splits * MN + (size_t)row * p.N + col;
+    const float *q = p.part + (size_t)batch * p.splits * size + (size_t)row * part_stride(p) + col;
+#pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
         float t[8];
-        load8_f32(q + s * MN, n, t);
+        load8_f32(q + s * size, 8, t);
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             v[x] += t[x];
         if (GATED) {
-            load8_f32(q + (p.splits + s) * MN, n, t);
+            load8_f32(q + (p.splits + s) * size, 8, t);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 u[x] += t[x];
