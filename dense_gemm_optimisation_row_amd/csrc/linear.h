@@ -62,7 +62,10 @@ inline bool spans_a_unit(const Product &p)
     return (long long)(p.M - 1) * p.lda + p.K >= 8 && (b_rows - 1) * p.ldb + b_cols >= 8;
 }
 // Columns of a workgroup's strip, of the one or each of the two products.
-inline int skinny_strip(const Product &p, bool split) { return p.trans_b ? 16 : (split && !p.gated ? 64 : 32); }
+inline int skinny_strip(const Product &p, bool split)
+{
+    return p.trans_b ? 16 : (split && (!p.gated || p.M <= 32) ? 64 : 32);   // a gated strip holds both products'
+}
 hipError_t launch_linear_skinny(const Product &p, hipStream_t stream);
 
 // Copies of operands whose rows are not whole units, padded to them with zeros.
@@ -80,12 +83,13 @@ hipError_t launch_repack(const Repack &r, hipStream_t stream);
 hipError_t launch_join(const Product &p, hipStream_t stream);
 
 // dZ = dY act'(Z) (Z null: dZ = dY, nothing written unless dz; rows padded
-// with zeros to whole units) and, with
-// sums, each row block's column sums of the unrounded dZ in FP32 to
-// sums[block][N], blocks of kGradRows rows.
-constexpr int kGradRows = 64;
+// with zeros to whole units) and each row block's column sums of the unrounded
+// dZ, rounded to dbias where there is one block, else in FP32 to sums[block][N]
+// (one of them, or neither).  Blocks of 64 rows, 16 where those would leave
+// compute units idle.
+inline int grad_rows(int M, int N) { return (M + 63LL) / 64 * ((N + 255) / 256) >= 1024 ? 64 : 16; }
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
-                           int lddz, int act, float *sums, bool bf16, hipStream_t stream);
+                           int lddz, int act, float *sums, uint16_t *dbias, bool bf16, hipStream_t stream);
 // out[c] = sum over blocks of sums[block][c], in the input format.
 hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out, bool bf16, hipStream_t stream);
 // dG = dH U act'(G), dU = dH act(G), padded likewise.

@@ -121,8 +121,9 @@ Way choose(const Product &p, bool ring)
         for (const RingCost &c : kRings) {
             // parts until two rounds are full, at least two stages of 64 k each
             const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile));
-            for (int parts = 1; parts == 1 || (parts <= 16 && 2 * parts <= stages && n * parts <= 512 * c.share);
-                 ++parts) {
+            for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+                if (parts > 1 && (2 * parts > stages || n * parts > 512 * c.share))
+                    break;
                 const double t = microseconds(p, c, parts);
                 if (best == 0 || t < best)
                     best = t, best_parts = parts, w.tile = c.tile;
@@ -143,25 +144,30 @@ Way choose(const Product &p, bool ring)
     return w;
 }
 
-// FP32 partial sums of a split product, on whichever kernel the operands'
-// addresses will give it.
-size_t part_bytes(const Product &p)
+// How a product runs off and on the rings, as the operands' addresses will
+// have it, and the bytes of its FP32 partial sums either way.
+struct Plan {
+    Way off, ring;
+    size_t part;
+};
+Plan plan(const Product &p)
 {
-    size_t most = 0;
-    for (int ring = 0; ring < (ring_sizes(p) ? 2 : 1); ++ring) {
-        const Way w = choose(p, ring);
-        const size_t b = w.splits <= 1 ? 0 : (size_t)(p.gated ? 2 : p.nbatch) * w.splits * dgor::part_size(p) * sizeof(float);
-        most = b > most ? b : most;
-    }
-    return round_up(most, kWsAlign);
+    const auto bytes = [&](const Way &w) {
+        return w.splits <= 1 ? 0 : (size_t)(p.gated ? 2 : p.nbatch) * w.splits * dgor::part_size(p) * sizeof(float);
+    };
+    Plan l;
+    l.off = choose(p, false);
+    l.ring = ring_sizes(p) ? choose(p, true) : l.off;
+    l.part = round_up(bytes(l.off) > bytes(l.ring) ? bytes(l.off) : bytes(l.ring), kWsAlign);
+    return l;
 }
 
-// Runs a product; ws has part_bytes(p) bytes.
-hipError_t run_product(Product p, void *ws, hipStream_t s)
+// Runs a product; ws has its plan's part bytes.
+hipError_t run_product(Product p, const Plan &l, void *ws, hipStream_t s)
 {
     if (p.M == 0 || p.N == 0)
         return hipSuccess;
-    const Way w = choose(p, ring_sizes(p) && ring_addresses(p));
+    const Way &w = ring_addresses(p) ? l.ring : l.off;
     p.splits = w.splits;
     p.chunk = w.chunk;
     p.part = (float *)ws;
@@ -172,6 +178,9 @@ hipError_t run_product(Product p, void *ws, hipStream_t s)
         return err;
     return dgor::launch_join(p, s);
 }
+
+// Whether rows are whole units at strides on them.
+bool whole_units(int cols, int ld) { return ld % 8 == 0 && cols % 8 == 0 && ld < (1 << 22); }
 
 // Operands that are copied at the front of the workspace, their rows padded
 // to whole units for the rings: those whose rows or strides are not.  (1000 x
@@ -186,7 +195,7 @@ struct Copies {
     // ld becomes the stride of what the products will read.
     int add(int rows, int cols, int &ld)
     {
-        if ((ld % 8 == 0 && cols % 8 == 0 && ld < (1 << 22)) || rows == 0 || cols == 0)
+        if (whole_units(cols, ld) || rows == 0 || cols == 0)
             return -1;
         if ((long long)rows * ceil_div(cols, 8) >= (1LL << 30)) {   // a launch's units are counted in 32 bits
             units = false;
@@ -253,12 +262,24 @@ Product weight_gradient_product(int M, int N, int K, int op_w, int ldx, int lddz
     return p;
 }
 
+// Whether operands off the units are worth a launch that copies them: not for
+// a sum of up to two stages of the plain tile over at most a round of its
+// tiles (100 x 100 by 100 x 100: 9 us against 12).
+bool worth_copies(const Product &p)
+{
+    return dgor::product_stages(p) > 2 || tiles(p, dgor::kTile, dgor::kTile) > 512;
+}
+
 // The copies of a forward product's A and its one or two B.
 void copy_operands(Product &p, Copies &c, int (&copy)[3])
 {
     copy[0] = copy[1] = copy[2] = -1;
     if (p.M == 0 || p.N == 0 || few_rows(p))
         return;
+    if (!worth_copies(p)) {
+        p.units = whole_units(p.K, p.lda) && whole_units(p.trans_b ? p.K : p.N, p.ldb);
+        return;
+    }
     const int rows = p.trans_b ? p.N : p.K, cols = p.trans_b ? p.K : p.N, ld = p.ldb;
     copy[0] = c.add(p.M, p.K, p.lda);
     copy[1] = c.add(rows, cols, p.ldb);
@@ -278,7 +299,7 @@ int done(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
 // ------------------------------------------------------------ dense layer --
 
-int check_linear(const gemm_linear_params *q, Product &p, Copies &c, int (&copy)[3])
+int check_linear(const gemm_linear_params *q, Product &p, Plan &l, Copies &c, int (&copy)[3])
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
@@ -291,6 +312,7 @@ int check_linear(const gemm_linear_params *q, Product &p, Copies &c, int (&copy)
     p = forward_product(q->M, q->N, q->K, q->op_w, q->ldx, q->ldw, false);
     p.e.act = q->activation;
     copy_operands(p, c, copy);
+    l = plan(p);
     return GEMM_OK;
 }
 
@@ -298,9 +320,10 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
                const void *R, void *Y, uint16_t *pre, void *ws, size_t ws_bytes, void *stream)
 {
     Product p;
+    Plan l;
     Copies c;
     int copy[3];
-    const int rc = check_linear(q, p, c, copy);
+    const int rc = check_linear(q, p, l, c, copy);
     if (rc != GEMM_OK)
         return rc;
     if ((R && !ld_ok(q->ldr, q->N)) || (pre && !ld_ok(q->ldp, q->N)))
@@ -309,7 +332,7 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
         return GEMM_ERR_NULL_PTR;
     if (q->M == 0 || q->N == 0)
         return GEMM_OK;
-    if (!workspace_ok(ws, ws_bytes, c.bytes + part_bytes(p)))
+    if (!workspace_ok(ws, ws_bytes, c.bytes + l.part))
         return GEMM_ERR_WORKSPACE;
     const int dev = dgor::device_status();
     if (dev != GEMM_OK)
@@ -324,19 +347,20 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
     p.e.R = R, p.e.ldr = q->ldr;
     p.e.pre = pre, p.e.ldp = q->ldp;
     const hipError_t err = c.launch(s);
-    return done(err == hipSuccess ? run_product(p, base + c.bytes, s) : err);
+    return done(err == hipSuccess ? run_product(p, l, base + c.bytes, s) : err);
 }
 
 // Workspace of the dense layer's backward pass: copies, dZ, the column sums of
 // each row block, and the partial sums of whichever product is running.
 struct BackwardLayout {
     Copies c;
+    Plan px, pw;
     int copy_dy, copy_x, copy_w;
     int lddz;
     size_t dz, sums, part, bytes;   // offsets, and the whole size
 };
 
-int row_blocks(int M) { return ceil_div(M, dgor::kGradRows); }
+int row_blocks(int M, int N) { return ceil_div(M, dgor::grad_rows(M, N)); }
 
 int check_linear_backward(const gemm_linear_backward_params *q, Product &px, Product &pw, BackwardLayout &l)
 {
@@ -351,18 +375,23 @@ int check_linear_backward(const gemm_linear_backward_params *q, Product &px, Pro
     const bool act = q->activation != GEMM_ACT_NONE, t = q->op_w == GEMM_OP_T;
     int ldx = q->ldx, ldw = q->ldw;
     l.lddz = act ? (int)round_up((size_t)q->N, 8) : q->lddy;
-    l.copy_dy = act ? -1 : l.c.add(q->M, q->N, l.lddz);
-    l.copy_x = l.c.add(q->M, q->K, ldx);
     px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1);
-    l.copy_w = few_rows(px) ? -1 : l.c.add(t ? q->N : q->K, t ? q->K : q->N, ldw);
-    px.ldb = ldw;
     pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1);
-    px.units = pw.units = l.c.units;
+    const bool for_x = !few_rows(px) && worth_copies(px), for_w = worth_copies(pw);
+    l.copy_dy = !act && (for_x || for_w) ? l.c.add(q->M, q->N, l.lddz) : -1;
+    l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
+    l.copy_w = for_x ? l.c.add(t ? q->N : q->K, t ? q->K : q->N, ldw) : -1;
+    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1);
+    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1);
+    const bool dz_units = act || for_x || for_w || whole_units(q->N, l.lddz);
+    px.units = l.c.units && dz_units && (for_x || whole_units(t ? q->K : q->N, ldw));
+    pw.units = l.c.units && dz_units && (for_w || whole_units(q->K, ldx));
     l.dz = l.c.bytes;
     l.sums = l.dz + (act ? round_up((size_t)q->M * l.lddz * 2, kWsAlign) : 0);
-    l.part = l.sums + round_up((size_t)row_blocks(q->M) * q->N * sizeof(float), kWsAlign);
-    const size_t a = part_bytes(px), b = part_bytes(pw);
-    l.bytes = l.part + (a > b ? a : b);
+    l.part = l.sums + round_up((size_t)row_blocks(q->M, q->N) * q->N * sizeof(float), kWsAlign);
+    l.px = plan(px);
+    l.pw = plan(pw);
+    l.bytes = l.part + (l.px.part > l.pw.part ? l.px.part : l.pw.part);
     return GEMM_OK;
 }
 
@@ -391,18 +420,20 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
     const uint16_t *dZ = dY;
-    float *sums = dbias ? (float *)(base + l.sums) : nullptr;
+    const int blocks = row_blocks(q->M, q->N);
+    float *sums = dbias && blocks != 1 ? (float *)(base + l.sums) : nullptr;
     if (q->M > 0 && q->N > 0 && ((act && (dX || dW)) || dbias)) {
         uint16_t *out = act && (dX || dW) ? (uint16_t *)(base + l.dz) : nullptr;
         const hipError_t e = dgor::launch_act_grad(q->M, q->N, dY, q->lddy, act ? pre : nullptr, q->ldp, out, l.lddz,
-                                                   q->activation, sums, bf16, s);
+                                                   q->activation, sums, blocks == 1 ? dbias : nullptr, bf16, s);
         if (e != hipSuccess)
             return GEMM_ERR_LAUNCH;
         if (out)
             dZ = out;
     }
-    if (dbias && q->N > 0 &&
-        dgor::launch_sum_blocks(row_blocks(q->M), q->N, sums, dbias, bf16, s) != hipSuccess)
+    // no rows: an empty sum, no workspace
+    if (dbias && blocks != 1 && q->N > 0 &&
+        dgor::launch_sum_blocks(blocks, q->N, sums, dbias, bf16, s) != hipSuccess)
         return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
     dZ = l.c.use(dX || dW ? l.copy_dy : -1, dZ, base);
@@ -413,7 +444,7 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
         px.A[0] = px.A[1] = dZ;
         px.B[0] = px.B[1] = Ws;
         px.e.Y = dX, px.e.ldy = q->lddx;
-        if (run_product(px, base + l.part, s) != hipSuccess)
+        if (run_product(px, l.px, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     if (dW) {
@@ -421,7 +452,7 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
         pw.A[0] = pw.A[1] = t ? dZ : Xs;
         pw.B[0] = pw.B[1] = t ? Xs : dZ;
         pw.e.Y = dW, pw.e.ldy = q->lddw;
-        if (run_product(pw, base + l.part, s) != hipSuccess)
+        if (run_product(pw, l.pw, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
@@ -429,7 +460,7 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
 
 // ---------------------------------------------------- gated up-projection --
 
-int check_gated(const gemm_gated_params *q, Product &p, Copies &c, int (&copy)[3])
+int check_gated(const gemm_gated_params *q, Product &p, Plan &l, Copies &c, int (&copy)[3])
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
@@ -442,6 +473,7 @@ int check_gated(const gemm_gated_params *q, Product &p, Copies &c, int (&copy)[3
     p = forward_product(q->M, q->F, q->K, q->op_w, q->ldx, q->ldw, true);
     p.e.act = q->activation;
     copy_operands(p, c, copy);
+    l = plan(p);
     return GEMM_OK;
 }
 
@@ -449,9 +481,10 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
               uint16_t *H, uint16_t *G, uint16_t *U, void *ws, size_t ws_bytes, void *stream)
 {
     Product p;
+    Plan l;
     Copies c;
     int copy[3];
-    const int rc = check_gated(q, p, c, copy);
+    const int rc = check_gated(q, p, l, c, copy);
     if (rc != GEMM_OK)
         return rc;
     if (G && !ld_ok(q->ldp, q->F))
@@ -461,7 +494,7 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
         return GEMM_ERR_NULL_PTR;
     if (q->M == 0 || q->F == 0)
         return GEMM_OK;
-    if (!workspace_ok(ws, ws_bytes, c.bytes + part_bytes(p)))
+    if (!workspace_ok(ws, ws_bytes, c.bytes + l.part))
         return GEMM_ERR_WORKSPACE;
     const int dev = dgor::device_status();
     if (dev != GEMM_OK)
@@ -474,13 +507,14 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
     p.e.Y = H, p.e.ldy = q->ldh;
     p.e.pre = G, p.e.pre2 = U, p.e.ldp = q->ldp;
     const hipError_t err = c.launch(s);
-    return done(err == hipSuccess ? run_product(p, base + c.bytes, s) : err);
+    return done(err == hipSuccess ? run_product(p, l, base + c.bytes, s) : err);
 }
 
 // Workspace of the gated backward pass: copies, dG and dU, then the partial
 // sums of whichever product is running.
 struct GatedBackwardLayout {
     Copies c;
+    Plan px, pw;
     int copy_x, copy_wg, copy_wu;
     int ldd;
     size_t dg, du, part, bytes;
@@ -499,20 +533,23 @@ int check_gated_backward(const gemm_gated_backward_params *q, Product &px, Produ
     l.ldd = (int)round_up((size_t)q->F, 8);
     const bool t = q->op_w == GEMM_OP_T;
     int ldx = q->ldx, ldw = q->ldw, ldu = q->ldw;
-    l.copy_x = l.c.add(q->M, q->K, ldx);
     px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, ldw, 2);
-    const bool copy_w = !few_rows(px);
-    l.copy_wg = copy_w ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldw) : -1;
-    l.copy_wu = copy_w ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldu) : -1;
+    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2);
+    const bool for_x = !few_rows(px) && worth_copies(px), for_w = worth_copies(pw);
+    l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
+    l.copy_wg = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldw) : -1;
+    l.copy_wu = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldu) : -1;
     px.ldb = ldw;
     pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2);
-    px.units = pw.units = l.c.units;
+    px.units = l.c.units && (for_x || whole_units(t ? q->K : q->F, ldw));
+    pw.units = l.c.units && (for_w || whole_units(q->K, ldx));
     const size_t d_bytes = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
     l.dg = l.c.bytes;
     l.du = l.dg + d_bytes;
     l.part = l.du + d_bytes;
-    const size_t a = part_bytes(px), b = part_bytes(pw);
-    l.bytes = l.part + (a > b ? a : b);
+    l.px = plan(px);
+    l.pw = plan(pw);
+    l.bytes = l.part + (l.px.part > l.pw.part ? l.px.part : l.pw.part);
     return GEMM_OK;
 }
 
@@ -556,7 +593,7 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
         px.A[0] = dG, px.A[1] = dU;
         px.B[0] = Gs, px.B[1] = Us;
         px.e.Y = dX, px.e.ldy = q->lddx;
-        if (run_product(px, base + l.part, s) != hipSuccess)
+        if (run_product(px, l.px, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     if (dWg) {
@@ -564,7 +601,7 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
         pw.A[0] = t ? dG : Xs, pw.A[1] = t ? dU : Xs;
         pw.B[0] = t ? Xs : dG, pw.B[1] = t ? Xs : dU;
         pw.e.Y = dWg, pw.Y1 = dWu, pw.e.ldy = q->lddw;
-        if (run_product(pw, base + l.part, s) != hipSuccess)
+        if (run_product(pw, l.pw, base + l.part, s) != hipSuccess)
             return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
@@ -579,11 +616,12 @@ int gemm_linear_workspace(const gemm_linear_params *params, size_t *bytes)
     if (!bytes)
         return GEMM_ERR_NULL_PTR;
     Product p;
+    Plan l;
     Copies c;
     int copy[3];
-    const int rc = check_linear(params, p, c, copy);
+    const int rc = check_linear(params, p, l, c, copy);
     if (rc == GEMM_OK)
-        *bytes = p.M && p.N ? c.bytes + part_bytes(p) : 0;
+        *bytes = p.M && p.N ? c.bytes + l.part : 0;
     return rc;
 }
 int gemm_linear_f16(const gemm_linear_params *params, const uint16_t *X, const uint16_t *W, const uint16_t *bias,
@@ -626,11 +664,12 @@ int gemm_gated_workspace(const gemm_gated_params *params, size_t *bytes)
     if (!bytes)
         return GEMM_ERR_NULL_PTR;
     Product p;
+    Plan l;
     Copies c;
     int copy[3];
-    const int rc = check_gated(params, p, c, copy);
+    const int rc = check_gated(params, p, l, c, copy);
     if (rc == GEMM_OK)
-        *bytes = p.M && p.N ? c.bytes + part_bytes(p) : 0;
+        *bytes = p.M && p.N ? c.bytes + l.part : 0;
     return rc;
 }
 int gemm_gated_f16(const gemm_gated_params *params, const uint16_t *X, const uint16_t *Wg, const uint16_t *Wu,

@@ -262,8 +262,13 @@ hipError_t launch_blocks(const Product &p, hipStream_t s)
 template <class Op>
 hipError_t launch_op(const Product &p, int strip, hipStream_t s)
 {
-    if (p.gated)
-        return p.trans_b ? launch_blocks<Op, 1, true, true>(p, s) : launch_blocks<Op, 2, false, true>(p, s);
+    if (p.gated) {
+        if (p.trans_b)
+            return launch_blocks<Op, 1, true, true>(p, s);
+        if (strip == 32)
+            return launch_blocks<Op, 2, false, true>(p, s);
+        return p.M <= 16 ? launch_rows<Op, 1, 4, false, true>(p, s) : launch_rows<Op, 2, 4, false, true>(p, s);
+    }
     if (p.trans_b)
         return launch_blocks<Op, 1, true, false>(p, s);
     return strip == 64 ? launch_blocks<Op, 4, false, false>(p, s) : launch_blocks<Op, 2, false, false>(p, s);
