@@ -48,9 +48,9 @@ hipError_t launch_tile(const Product &p, hipStream_t stream);
 // The rings: 16-byte aligned operands, rows of whole units of eight elements
 // (or padded to them: the padding is read, zeros along k), strides below
 // 2^22 and multiples of 8.
-enum RingTile { kRing256, kRing256x128, kRing128, kRing64 };
-constexpr int ring_tile_m(RingTile t) { return t == kRing64 ? 64 : (t == kRing128 ? 128 : 256); }
-constexpr int ring_tile_n(RingTile t) { return t == kRing64 ? 64 : (t == kRing256 ? 256 : 128); }
+enum RingTile { kRing256, kRing256x128, kRing128, kRing128x64, kRing64 };
+constexpr int ring_tile_m(RingTile t) { return t <= kRing256x128 ? 256 : (t == kRing64 ? 64 : 128); }
+constexpr int ring_tile_n(RingTile t) { return t == kRing256 ? 256 : (t <= kRing128 ? 128 : 64); }
 hipError_t launch_linear_ring(const Product &p, RingTile tile, hipStream_t stream);
 
 // Few rows (at most kSkinnyRows, A as M x K, one product); each operand at

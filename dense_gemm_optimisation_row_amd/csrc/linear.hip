@@ -63,37 +63,44 @@ void split(const Product &p, long long parts, Way &w)
 }
 
 // Time of a product on a ring's tile with its sum in `parts`.  Up to `share`
-// workgroups of the tile run on a compute unit at once; a round of them takes
-// `ends` and, for each 32 k, `alone` (at most one a unit) or `full`.  Parts are
-// written in FP32 and joined by another launch.  Microseconds, fitted to 16 to
-// 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N): within
-// 10% of the times measured.  Full rates: 1470, 1280, 1180 and 570 TFLOP/s.
-// An activation of exponentials adds to a tile's end what its outputs take on
-// the vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs: 236 us, 217
+// workgroups of the tile run on a compute unit at once.  A round of at most one
+// a unit takes ends + alone for each 32 k, a full one ends_full + full each.
+// Parts are written in FP32 and joined by another launch.  Microseconds, fitted
+// to 16 to 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N):
+// within 10% of the times measured.  Full rates: 1470, 1280, 1180, 890 and
+// 570 TFLOP/s.  An activation of exponentials adds what its outputs take on the
+// vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs: 236 us, 217
 // without).
 struct RingCost {
     dgor::RingTile tile;
     int share;
-    double ends, alone, full, n_by_k;   // the last: times as long with B as N x K, whose loads take half lines
+    double ends, alone, ends_full, full;
+    double halves;   // times as long a stage whose loads take half lines
 };
 constexpr RingCost kRings[] = {
-    {dgor::kRing256, 1, 14.5, 0.73, 0.73, 1.0},
-    {dgor::kRing256x128, 1, 9.8, 0.42, 0.42, 1.3},
-    {dgor::kRing128, 2, 6.8, 0.295, 0.455, 1.17},
-    {dgor::kRing64, 2, 4.0, 0.158, 0.235, 1.08},
+    {dgor::kRing256, 1, 14.5, 0.73, 14.5, 0.73, 1.0},
+    {dgor::kRing256x128, 1, 9.8, 0.42, 9.8, 0.42, 1.3},
+    {dgor::kRing128, 2, 6.8, 0.295, 7.5, 0.455, 1.17},
+    {dgor::kRing128x64, 2, 4.8, 0.243, 6.2, 0.33, 1.12},
+    {dgor::kRing64, 2, 4.0, 0.158, 4.2, 0.243, 1.08},
 };
 constexpr int kSplitRows = 40;   // stages of 64 k from which few rows' sums over a K x N matrix are split
 constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
 double microseconds(const Product &p, const RingCost &c, int parts)
 {
     const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
-    const double stages = 2.0 * dgor::product_stages(p) / parts * (p.trans_b ? c.n_by_k : 1.0);
+    // half lines: B as N x K, and each of two matrices' 32 columns
+    const bool halves = p.trans_b || (p.gated && ring_tile_n(c.tile) == 64);
+    const double stages = 2.0 * dgor::product_stages(p) / parts * (halves ? c.halves : 1.0);
     const long long rounds = n / (256LL * c.share), rest = n % (256LL * c.share);
-    const double outputs = (double)ring_tile_m(c.tile) * ring_tile_n(c.tile) / 65536;
-    const double ends = c.ends + (p.e.act > GEMM_ACT_RELU && parts == 1 ? 9.0 * outputs : 0.0);
-    double t = rounds * (ends + stages * c.full);
+    // an activation's time for a workgroup's outputs
+    const double act = p.e.act > GEMM_ACT_RELU && parts == 1
+                           ? 9.0 * ring_tile_m(c.tile) * ring_tile_n(c.tile) / (p.gated ? 131072 : 65536)
+                           : 0.0;
+    const double alone = c.ends + stages * c.alone + act, full = c.ends_full + stages * c.full + act * c.share;
+    double t = rounds * full;
     if (rest)
-        t += ends + stages * (rest <= 256 ? c.alone : c.full);
+        t += rest <= 256 ? alone : full;
     if (parts > 1)
         t += kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes;
     return t;

@@ -1,11 +1,11 @@
 // The dense-layer products of 16-byte aligned operands: tiles of 256 x 256,
-// 256 x 128, 128 x 128 and 64 x 64, loaded straight from global memory into
+// 256 x 128, 128 x 128, 128 x 64 and 64 x 64, loaded straight from global memory into
 // LDS rings 32 k deep, FP32 sums on v_mfma_f32_16x16x32, and the epilogue of
 // epilogue.h on whole rows.
 //
 // Four wavefronts, each a quarter of the tile in 16 x 16 blocks: 8 x 8 of them
 // (all 256 accumulator registers, one workgroup a compute unit), 8 x 4 (one),
-// 4 x 4 or 2 x 2 (two, which cover each other's waits).
+// 4 x 4, 4 x 2 or 2 x 2 (two, which cover each other's waits).
 // Loads: one instruction moves 64 lanes x 16 bytes into 1 KB of LDS, lane p
 // at byte 16 p; the layout is chosen by permuting the sources, and a lane
 // whose offset is out of range writes zeros, which fills every edge.
@@ -32,8 +32,8 @@
 // fragments that every wavefront has since consumed.
 //
 // Bound by the matrix cores where there are tiles for every compute unit; the
-// smaller tiles by LDS reads, 64, 96, 128 and 256 bytes a cycle and compute
-// unit of its 128 if the matrix cores never waited.
+// smaller tiles by LDS reads, 64, 96, 128, 192 and 256 bytes a cycle and
+// compute unit of its 128 if the matrix cores never waited.
 #include "common.h"
 #include "lds_dma.h"
 #include "linear.h"
@@ -286,9 +286,9 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     Loads LA, LB;
     auto stage = [&](int par, const Source &S, halfx8 *ca, halfx8 *cb, halfx8 *na, halfx8 *nb) {
         constexpr int MFMAS = FA * FB, READS = FA + FB, LOADS = LPA + LPB;
-        // a load every EVERY MFMAs: after the reads, or (as many reads as
-        // MFMAs: the 64 x 64 tile, 12% faster so) among them
-        constexpr int FIRST = MFMAS > READS ? READS : 2, EVERY = MFMAS > READS ? (MFMAS - READS) / LOADS : 1;
+        // a load every EVERY MFMAs: after the reads, or (too few MFMAs after
+        // them; the 64 x 64 tile is 12% faster so) among them
+        constexpr int FIRST = MFMAS - READS >= LOADS ? READS : 2, EVERY = (MFMAS - FIRST) / LOADS;
         auto issue = [&](int ld) {
             if (ld < LPB)
                 load_b(LB, ld);
@@ -497,6 +497,7 @@ hipError_t launch_linear_ring(const Product &q, RingTile tile, hipStream_t s)
     case kRing256x128:
         return p.bf16 ? launch_ring_as<OpBrain, 256, 128>(p, s) : launch_ring_as<OpHalf, 256, 128>(p, s);
     case kRing128: return p.bf16 ? launch_ring_as<OpBrain, 128, 128>(p, s) : launch_ring_as<OpHalf, 128, 128>(p, s);
+    case kRing128x64: return p.bf16 ? launch_ring_as<OpBrain, 128, 64>(p, s) : launch_ring_as<OpHalf, 128, 64>(p, s);
     case kRing64: return p.bf16 ? launch_ring_as<OpBrain, 64, 64>(p, s) : launch_ring_as<OpHalf, 64, 64>(p, s);
     }
     return hipErrorInvalidValue;

@@ -33,9 +33,9 @@ def ring(tmp_path_factory):
 
 
 def test_every_layout_is_generated(ring):
-    # two formats, four tiles; M x K with K x N and N x K, K x M with K x N,
+    # two formats, five tiles; M x K with K x N and N x K, K x M with K x N,
     # gated with K x N and N x K
-    assert len(ring[1]) == 40
+    assert len(ring[1]) == 50
 
 
 def test_m0_is_touched_only_by_the_loads(ring):
