@@ -9,17 +9,17 @@
 // Bound by memory.  A row is held in registers, eight elements of a thread
 // at a time, so it is read once: in the forward pass rows of up to 1024
 // elements by one wavefront (four rows a workgroup, no barrier), up to 16384 by
-// a workgroup of 256; all of a row's loads, the weights' among them, are
+// a workgroup of 256 to 1024; all of a row's loads, the weights' among them, are
 // issued before the first sum.  Sums within a wavefront are shifts on the
 // vector ALUs.  The variance is the second pass over the registers, around the
 // mean, so it loses nothing where the mean is large.  Longer rows are read
 // again for each pass (the second read comes from the caches).
-// 8192 x 4096 BF16: 29.4 us, 4.6 TB/s, where a copy of it takes 26.5; with sums
+// 8192 x 4096 BF16: 23.3 us, 5.8 TB/s (26.4 for torch's copy of it); with sums
 // through LDS shuffles and the weights loaded after them it took 37.
 // The weight gradients: a workgroup, one for each compute unit, takes every
 // gridDim-th rows and keeps its columns' sums in registers, so dy and x are
 // read once for dx, dw and db together; the workgroups' sums are added in a
-// fixed order by a second kernel.
+// fixed order by a second kernel.  8192 x 4096 BF16: 42 us, 4.8 TB/s.
 #include "common.h"
 #include "linear.h"
 
@@ -44,6 +44,13 @@ struct Single {
         for (int e = 0; e < 8; ++e)
             f[e] = r.f[e];
     }
+    // makes the value one that the compiler has not seen
+    static __device__ __forceinline__ void renew(Raw &r)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            asm volatile("" : "+v"(r.f[e]));
+    }
     static __device__ __forceinline__ void load8(const float *p, int n, float (&f)[8]) { load8_f32(p, n, f); }
     static __device__ __forceinline__ void store8(float *p, int n, const float (&f)[8]) { store8_f32(p, n, f); }
     static __device__ __forceinline__ float down(float f) { return f; }
@@ -54,6 +61,7 @@ struct Short {
     using Raw = u32x4;
     static __device__ __forceinline__ Raw fetch(const uint16_t *p, int n) { return load8_16(p, n); }
     static __device__ __forceinline__ void open(const Raw &r, float (&f)[8]) { unpack8<Fmt>(r, f); }
+    static __device__ __forceinline__ void renew(Raw &r) { asm volatile("" : "+v"(r)); }
     static __device__ __forceinline__ void load8(const uint16_t *p, int n, float (&f)[8])
     {
         unpack8<Fmt>(load8_16(p, n), f);
@@ -126,16 +134,39 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float *slots)
     }
 }
 
-// WHOLE: N is a multiple of 8, so no access branches on a row's end.
-template <class X, class W, int RT, int V, bool WHOLE>
-__global__ __launch_bounds__(256) void layer_norm_kernel(int M, int N, const typename X::T *__restrict__ x, int ldx,
+// How a row ends.  kCut: the last unit is the row's last eight elements, which
+// two threads then both have: they count in the sums of the first, and both
+// write what they come to.  So no access branches on the row's end (masked
+// loads of single elements made 8192 x 4093 take twice as long as 8192 x 4096).
+// kNarrow: rows shorter than a unit.
+enum RowEnd { kWhole, kCut, kNarrow };
+
+// A unit's column, how many elements from it to load, and how many of those
+// belong to the unit before.
+template <RowEnd END>
+struct Unit {
+    int c, n, shared;
+    __device__ __forceinline__ Unit(int at, int N)
+        : c(END == kCut ? min(at, N - 8) : at), n(END == kNarrow ? N - at : 8), shared(at - c)
+    {
+    }
+    // whether element e is this unit's to count
+    __device__ __forceinline__ bool counts(int e) const
+    {
+        return END == kWhole || (END == kCut ? e >= shared : e < n);
+    }
+};
+
+constexpr int group_threads(int rt) { return rt > 256 ? rt : 256; }
+template <class X, class W, int RT, int V, RowEnd END>
+__global__ __launch_bounds__(group_threads(RT)) void layer_norm_kernel(int M, int N, const typename X::T *__restrict__ x, int ldx,
                                                          const typename W::T *__restrict__ weight,
                                                          const typename W::T *__restrict__ bias, float eps,
                                                          typename X::T *__restrict__ y, int ldy,
                                                          float *__restrict__ mean_out, float *__restrict__ rstd_out)
 {
-    __shared__ float slots[2][4];
-    constexpr int ROWS = 256 / RT;
+    __shared__ float slots[2][RT / 64];
+    constexpr int ROWS = group_threads(RT) / RT;
     const int at = threadIdx.x % RT;
     // a row's two sums use a slot each, with a barrier between any write of a
     // slot and its last readers; with a row a wavefront there is no barrier
@@ -147,40 +178,38 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(int M, int N, const typ
         float v[V][8], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i), n = WHOLE ? 8 : N - c;
-            if (c < N) {
-                xr[i] = X::fetch(x + (size_t)row * ldx + c, n);   // elements past the row are zero
-                if (weight)
-                    wr[i] = W::fetch(weight + c, n);
-                if (bias)
-                    br[i] = W::fetch(bias + c, n);
-            }
+            if (8 * (at + RT * i) >= N)
+                continue;
+            const Unit<END> u(8 * (at + RT * i), N);
+            xr[i] = X::fetch(x + (size_t)row * ldx + u.c, u.n);
+            if (weight)
+                wr[i] = W::fetch(weight + u.c, u.n);
+            if (bias)
+                br[i] = W::fetch(bias + u.c, u.n);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (8 * (at + RT * i) >= N)
                 continue;
+            const Unit<END> u(8 * (at + RT * i), N);
             X::open(xr[i], v[i]);
-            sum += ((v[i][0] + v[i][1]) + (v[i][2] + v[i][3])) + ((v[i][4] + v[i][5]) + (v[i][6] + v[i][7]));
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                t[e] = u.counts(e) ? v[i][e] : 0.f;
+            sum += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
         }
         const float mean = row_sum<RT>(sum, slots[0]) / (float)N;
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i);
+            if (8 * (at + RT * i) >= N)
+                continue;
+            const Unit<END> u(8 * (at + RT * i), N);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 8; ++e) {
                 v[i][e] -= mean;
-            if (WHOLE) {
-                if (c < N)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sq = __builtin_fmaf(v[i][e], v[i][e], sq);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < N)
-                        sq = __builtin_fmaf(v[i][e], v[i][e], sq);
+                sq = u.counts(e) ? __builtin_fmaf(v[i][e], v[i][e], sq) : sq;
             }
         }
         const float rstd = 1.f / sqrtf(row_sum<RT>(sq, slots[1]) / (float)N + eps);
@@ -192,18 +221,18 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(int M, int N, const typ
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i);
-            if (c < N) {
-                float w[8], b[8];
-                if (weight)
-                    W::open(wr[i], w);
-                if (bias)
-                    W::open(br[i], b);
+            if (8 * (at + RT * i) >= N)
+                continue;
+            const Unit<END> u(8 * (at + RT * i), N);
+            float w[8], b[8];
+            if (weight)
+                W::open(wr[i], w);
+            if (bias)
+                W::open(br[i], b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[i][e] = __builtin_fmaf(v[i][e] * rstd, weight ? w[e] : 1.f, bias ? b[e] : 0.f);
-                X::store8(y + (size_t)row * ldy + c, WHOLE ? 8 : N - c, v[i]);
-            }
+            for (int e = 0; e < 8; ++e)
+                v[i][e] = __builtin_fmaf(v[i][e] * rstd, weight ? w[e] : 1.f, bias ? b[e] : 0.f);
+            X::store8(y + (size_t)row * ldy + u.c, u.n, v[i]);
         }
     }
 }
@@ -256,13 +285,14 @@ __global__ __launch_bounds__(256) void layer_norm_long_kernel(int M, int N, cons
     }
 }
 
-// G rows at a time, by RT threads each, 1024 in all (256 with eight
-// units a thread); a workgroup takes rows blockIdx.x G + g, then gridDim.x G
-// further on.  With one unit a thread, the next row's loads are issued before a
-// row is worked on; with more the registers do not hold them.  The groups' sums of dw and db meet in LDS, halves of the groups
-// at a time in a fixed order; they go to sums[block][2][N] or, with one
-// workgroup, straight to dweight and dbias.
-template <class X, class W, int RT, int V, int G, bool WHOLE>
+// G rows at a time, by RT threads each, 1024 in all; a workgroup takes rows
+// blockIdx.x G + g, then gridDim.x G further on.  With one unit a thread, the
+// next row's loads are issued before a row is worked on; with two the
+// registers do not hold them, nor the opened values across the row's sums: a
+// row is opened again behind them.  The groups' sums of dw and db meet in LDS,
+// halves of the groups at a time in a fixed order; they go to
+// sums[block][2][N] or, with one workgroup, straight to dweight and dbias.
+template <class X, class W, int RT, int V, int G, RowEnd END>
 __global__ __launch_bounds__(RT * G) void layer_norm_backward_kernel(
     int M, int N, const typename X::T *__restrict__ dy, int lddy, const typename X::T *__restrict__ x, int ldx,
     const typename W::T *__restrict__ weight, const float *__restrict__ mean, const float *__restrict__ rstd,
@@ -275,12 +305,12 @@ __global__ __launch_bounds__(RT * G) void layer_norm_backward_kernel(
     float dw[V][8], db[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (at + RT * i);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             dw[i][e] = db[i][e] = 0.f;
-        if (weight && c < N)
-            wr[i] = W::fetch(weight + c, WHOLE ? 8 : N - c);
+        const Unit<END> u(8 * (at + RT * i), N);
+        if (weight && 8 * (at + RT * i) < N)
+            wr[i] = W::fetch(weight + u.c, u.n);
     }
     typename X::Raw xr[V], tr[V];
     float mu = 0.f, rs = 0.f;
@@ -291,12 +321,29 @@ __global__ __launch_bounds__(RT * G) void layer_norm_backward_kernel(
         rs = rstd[row];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i), n = WHOLE ? 8 : N - c;
-            if (c < N) {
-                xr[i] = X::fetch(x + (size_t)row * ldx + c, n);
-                tr[i] = X::fetch(dy + (size_t)row * lddy + c, n);   // zero past the row
+            const Unit<END> u(8 * (at + RT * i), N);
+            if (8 * (at + RT * i) < N) {
+                xr[i] = X::fetch(x + (size_t)row * ldx + u.c, u.n);
+                tr[i] = X::fetch(dy + (size_t)row * lddy + u.c, u.n);
             }
         }
+    };
+    // unit i's normalised values, and dy
+    auto open = [&](int i, float (&h)[8], float (&t)[8]) {
+        X::open(xr[i], h);
+        X::open(tr[i], t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[e] = (h[e] - mu) * rs;
+    };
+    auto weigh = [&](int i, float (&t)[8]) {
+        if (!weight)
+            return;
+        float w[8];
+        W::open(wr[i], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            t[e] *= w[e];
     };
     const float inv = 1.f / (float)N;
     const long long step = (long long)gridDim.x * G;
@@ -306,55 +353,59 @@ __global__ __launch_bounds__(RT * G) void layer_norm_backward_kernel(
     // every wavefront of the workgroup runs the same trips
     for (long long first = (long long)blockIdx.x * G; first < M; first += step, turn ^= 1) {
         const long long row = first + group;
-        float h[V][8], t[V][8], a = 0.f, b = 0.f;
+        constexpr int KEPT = V == 1 ? 1 : 0;
+        float hk[KEPT + 1][8], tk[KEPT + 1][8], a = 0.f, b = 0.f;
         if (V > 1)
             fetch(row);
         const float rs_row = rs;
+        if (row < M)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = 8 * (at + RT * i);
-            if (row < M && c < N) {
-                X::open(xr[i], h[i]);
-                X::open(tr[i], t[i]);
+            for (int i = 0; i < V; ++i) {
+                if (8 * (at + RT * i) >= N)
+                    continue;
+                const Unit<END> u(8 * (at + RT * i), N);
+                float h[8], t[8];
+                open(i, h, t);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    h[i][e] = (h[i][e] - mu) * rs;
-            } else {
+                for (int e = 0; e < 8; ++e) {
+                    dw[i][e] = __builtin_fmaf(t[e], h[e], dw[i][e]);
+                    db[i][e] += t[e];
+                }
+                weigh(i, t);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    h[i][e] = t[i][e] = 0.f;
+                for (int e = 0; e < 8; ++e) {
+                    a = u.counts(e) ? a + t[e] : a;
+                    b = u.counts(e) ? __builtin_fmaf(t[e], h[e], b) : b;
+                    if (V == 1)
+                        hk[0][e] = h[e], tk[0][e] = t[e];
+                }
             }
-        }
         if (V == 1)
             fetch(row + step);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float w[8];
-            if (weight)
-                W::open(wr[i], w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dw[i][e] = __builtin_fmaf(t[i][e], h[i][e], dw[i][e]);
-                db[i][e] += t[i][e];
-                if (weight)
-                    t[i][e] = 8 * (at + RT * i) < N ? t[i][e] * w[e] : 0.f;
-                a += t[i][e];
-                b = __builtin_fmaf(t[i][e], h[i][e], b);
-            }
-        }
         row_sum2<RT>(a, b, slots[turn] + RT / 32 * group);
         a *= inv;
         b *= inv;
         if (row < M)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = 8 * (at + RT * i);
-                if (c < N) {
+                if (8 * (at + RT * i) >= N)
+                    continue;
+                const Unit<END> u(8 * (at + RT * i), N);
+                float h[8], t[8];
+                if (V == 1) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        t[i][e] = rs_row * (t[i][e] - a - h[i][e] * b);
-                    X::store8(dx + (size_t)row * lddx + c, WHOLE ? 8 : N - c, t[i]);
+                        h[e] = hk[0][e], t[e] = tk[0][e];
+                } else {
+                    X::renew(xr[i]);   // or the compiler keeps the opened values
+                    X::renew(tr[i]);
+                    open(i, h, t);
+                    weigh(i, t);
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    t[e] = rs_row * (t[e] - a - h[e] * b);
+                X::store8(dx + (size_t)row * lddx + u.c, u.n, t);
             }
     }
     if (!sums && !dweight && !dbias)
@@ -387,18 +438,18 @@ __global__ __launch_bounds__(RT * G) void layer_norm_backward_kernel(
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = 8 * (at + RT * i), n = WHOLE ? 8 : N - c;
-        if (c >= N)
+        if (8 * (at + RT * i) >= N)
             continue;
+        const Unit<END> u(8 * (at + RT * i), N);
         if (sums) {
             float *out = sums + (size_t)blockIdx.x * 2 * N;
-            store8_f32(out + c, n, dw[i]);
-            store8_f32(out + N + c, n, db[i]);
+            store8_f32(out + u.c, u.n, dw[i]);
+            store8_f32(out + N + u.c, u.n, db[i]);
         } else {
             if (dweight)
-                W::store8(dweight + c, n, dw[i]);
+                W::store8(dweight + u.c, u.n, dw[i]);
             if (dbias)
-                W::store8(dbias + c, n, db[i]);
+                W::store8(dbias + u.c, u.n, db[i]);
         }
     }
 }
@@ -531,9 +582,12 @@ unsigned most(long long rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 <
 template <class X, class W, int RT, int V>
 hipError_t forward_as(const NormArgs &a, hipStream_t s)
 {
-    const dim3 grid(most(((long long)a.M + 256 / RT - 1) / (256 / RT)));
-    hipLaunchKernelGGL((a.N % 8 == 0 ? layer_norm_kernel<X, W, RT, V, true> : layer_norm_kernel<X, W, RT, V, false>),
-                       grid, dim3(256), 0, s, a.M, a.N, (const typename X::T *)a.x, a.ldx,
+    constexpr int ROWS = group_threads(RT) / RT;
+    const dim3 grid(most(((long long)a.M + ROWS - 1) / ROWS));
+    const auto kernel = a.N % 8 == 0 ? layer_norm_kernel<X, W, RT, V, kWhole>
+                        : a.N > 8    ? layer_norm_kernel<X, W, RT, V, kCut>
+                                     : layer_norm_kernel<X, W, 64, 1, kNarrow>;   // of the shortest rows' form
+    hipLaunchKernelGGL(kernel, grid, dim3(group_threads(RT)), 0, s, a.M, a.N, (const typename X::T *)a.x, a.ldx,
                        (const typename W::T *)a.weight, (const typename W::T *)a.bias, a.eps,
                        (typename X::T *)a.out, a.ldout, a.mean, a.rstd);
     return hipGetLastError();
@@ -551,9 +605,9 @@ hipError_t forward(const NormArgs &a, hipStream_t s)
     if (a.N <= 4096)
         return forward_as<X, W, 256, 2>(a, s);
     if (a.N <= 8192)
-        return forward_as<X, W, 256, 4>(a, s);
+        return forward_as<X, W, 512, 2>(a, s);
     if (a.N <= kMaxHeld)
-        return forward_as<X, W, 256, 8>(a, s);
+        return forward_as<X, W, 1024, 2>(a, s);
     hipLaunchKernelGGL((layer_norm_long_kernel<X, W>), dim3(most(a.M)), dim3(256), 0, s, a.M, a.N, (const typename X::T *)a.x,
                        a.ldx, (const typename W::T *)a.weight, (const typename W::T *)a.bias, a.eps,
                        (typename X::T *)a.out, a.ldout, a.mean, a.rstd);
@@ -564,9 +618,10 @@ template <class X, class W, int RT, int V, int G>
 hipError_t backward_as(const NormArgs &a, hipStream_t s)
 {
     using WT = typename W::T;
-    hipLaunchKernelGGL((a.N % 8 == 0 ? layer_norm_backward_kernel<X, W, RT, V, G, true>
-                                     : layer_norm_backward_kernel<X, W, RT, V, G, false>),
-                       dim3(a.blocks), dim3(RT * G), 0, s, a.M, a.N, (const typename X::T *)a.dy, a.lddy,
+    const auto kernel = a.N % 8 == 0 ? layer_norm_backward_kernel<X, W, RT, V, G, kWhole>
+                        : a.N > 8    ? layer_norm_backward_kernel<X, W, RT, V, G, kCut>
+                                     : layer_norm_backward_kernel<X, W, 64, 1, 16, kNarrow>;   // of the shortest rows' form
+    hipLaunchKernelGGL(kernel, dim3(a.blocks), dim3(RT * G), 0, s, a.M, a.N, (const typename X::T *)a.dy, a.lddy,
                        (const typename X::T *)a.x, a.ldx, (const WT *)a.weight, a.mean, a.rstd,
                        (typename X::T *)a.out, a.ldout, a.sums, a.sums ? nullptr : (WT *)a.dweight,
                        a.sums ? nullptr : (WT *)a.dbias);
@@ -594,7 +649,7 @@ hipError_t backward(const NormArgs &a, hipStream_t s)
     else if (a.N <= 8192)
         err = backward_as<X, W, 1024, 1, 1>(a, s);
     else if (a.N <= kMaxHeld)
-        err = backward_as<X, W, 256, 8, 1>(a, s);
+        err = backward_as<X, W, 1024, 2, 1>(a, s);
     else {
         hipLaunchKernelGGL((layer_norm_backward_long_kernel<X, W>), dim3(most(a.M)), dim3(256), 0, s, a.M, a.N,
                            (const typename X::T *)a.dy, a.lddy, (const typename X::T *)a.x, a.ldx,
