@@ -15,6 +15,23 @@ namespace {
 
 constexpr int kCols = 256;
 
+// Workgroup `group` of a copy: a unit a thread, read at any alignment, written
+// whole.
+__device__ __forceinline__ void repack(const Repack &r, unsigned group)
+{
+    const unsigned id = group * 256 + threadIdx.x;
+    if (id >= r.units)
+        return;
+    Repack::Job j = r.job[0];
+#pragma unroll
+    for (int i = 1; i < 3; ++i)
+        if (i < r.jobs && id >= r.job[i].first)
+            j = r.job[i];
+    const unsigned per = (unsigned)(j.cols + 7) / 8, u = id - j.first, row = u / per;
+    const int col = 8 * (int)(u - row * per);
+    store8_16(j.to + (size_t)row * j.ld_to + col, 8, load8_16(j.from + (size_t)row * j.ld + col, j.cols - col));
+}
+
 // x to act'(x): one uniform branch on the activation, not one an element.
 __device__ __forceinline__ void slopes(int act, float (&x)[8])
 {
@@ -39,8 +56,13 @@ template <class Fmt, int R>
 __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint16_t *__restrict__ dy, int lddy,
                                                        const uint16_t *__restrict__ z, int ldz,
                                                        uint16_t *__restrict__ dz, int lddz, int act,
-                                                       float *__restrict__ sums, uint16_t *__restrict__ dbias)
+                                                       float *__restrict__ sums, uint16_t *__restrict__ dbias,
+                                                       Repack also, unsigned groups)
 {
+    if (blockIdx.x >= groups) {
+        repack(also, blockIdx.x - groups);
+        return;
+    }
     __shared__ float part[8][kCols + 8];
     const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
     const int strips = (N + kCols - 1) / kCols, strip = blockIdx.x % strips, block = blockIdx.x / strips;
@@ -127,8 +149,12 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
                                                         const uint16_t *__restrict__ g,
                                                         const uint16_t *__restrict__ u, int ldp,
                                                         uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int ldd,
-                                                        int act)
+                                                        int act, Repack also, unsigned groups)
 {
+    if (blockIdx.x >= groups) {
+        repack(also, blockIdx.x - groups);
+        return;
+    }
     // a unit a thread, 32 units x 8 rows a workgroup
     const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
     const int strips = (F + kCols - 1) / kCols;
@@ -171,20 +197,17 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
     store8_16(du + (size_t)row * ldd + col, 8, pack8<Fmt>(b));
 }
 
-// Eight elements a thread: a unit read at any alignment, written whole.
-__global__ __launch_bounds__(256) void repack_kernel(Repack r, unsigned units)
+__global__ __launch_bounds__(256) void repack_kernel(Repack r) { repack(r, blockIdx.x); }
+
+// Counts the jobs' units; returns the workgroups that they take.
+unsigned repack_groups(Repack &r)
 {
-    const unsigned id = blockIdx.x * 256 + threadIdx.x;
-    if (id >= units)
-        return;
-    Repack::Job j = r.job[0];
-#pragma unroll
-    for (int i = 1; i < 3; ++i)
-        if (i < r.jobs && id >= r.job[i].first)
-            j = r.job[i];
-    const unsigned per = (unsigned)(j.cols + 7) / 8, u = id - j.first, row = u / per;
-    const int col = 8 * (int)(u - row * per);
-    store8_16(j.to + (size_t)row * j.ld_to + col, 8, load8_16(j.from + (size_t)row * j.ld + col, j.cols - col));
+    r.units = 0;
+    for (int i = 0; i < r.jobs; ++i) {
+        r.job[i].first = r.units;
+        r.units += (unsigned)r.job[i].rows * (unsigned)((r.job[i].cols + 7) / 8);
+    }
+    return (unsigned)((r.units + 255ULL) / 256);
 }
 
 }  // namespace
@@ -192,27 +215,22 @@ __global__ __launch_bounds__(256) void repack_kernel(Repack r, unsigned units)
 hipError_t launch_repack(const Repack &q, hipStream_t s)
 {
     Repack r = q;
-    unsigned units = 0;
-    for (int i = 0; i < r.jobs; ++i) {
-        r.job[i].first = units;
-        units += (unsigned)r.job[i].rows * (unsigned)((r.job[i].cols + 7) / 8);
-    }
-    if (units)
-        hipLaunchKernelGGL(repack_kernel, dim3((units + 255) / 256), dim3(256), 0, s, r, units);
+    const unsigned groups = repack_groups(r);
+    if (groups)
+        hipLaunchKernelGGL(repack_kernel, dim3(groups), dim3(256), 0, s, r);
     return hipGetLastError();
 }
 
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
-                           int lddz, int act, float *sums, uint16_t *dbias, bool bf16, hipStream_t s)
+                           int lddz, int act, float *sums, uint16_t *dbias, const Repack &q, bool bf16, hipStream_t s)
 {
+    Repack also = q;
     const int rows = grad_rows(M, N);
-    const dim3 grid((unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + rows - 1) / rows));
-    if (rows == 64)
-        hipLaunchKernelGGL((bf16 ? act_grad_kernel<Brain16, 8> : act_grad_kernel<Half16, 8>), grid, dim3(256), 0, s, M,
-                           N, dy, lddy, z, ldz, dz, lddz, act, sums, dbias);
-    else
-        hipLaunchKernelGGL((bf16 ? act_grad_kernel<Brain16, 2> : act_grad_kernel<Half16, 2>), grid, dim3(256), 0, s, M,
-                           N, dy, lddy, z, ldz, dz, lddz, act, sums, dbias);
+    const unsigned groups = (unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + rows - 1) / rows);
+    const auto kernel = rows == 64 ? (bf16 ? act_grad_kernel<Brain16, 8> : act_grad_kernel<Half16, 8>)
+                                   : (bf16 ? act_grad_kernel<Brain16, 2> : act_grad_kernel<Half16, 2>);
+    hipLaunchKernelGGL(kernel, dim3(groups + repack_groups(also)), dim3(256), 0, s, M, N, dy, lddy, z, ldz, dz, lddz,
+                       act, sums, dbias, also, groups);
     return hipGetLastError();
 }
 
@@ -224,11 +242,12 @@ hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out
 }
 
 hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u, int ldp,
-                            uint16_t *dg, uint16_t *du, int ldd, int act, bool bf16, hipStream_t s)
+                            uint16_t *dg, uint16_t *du, int ldd, int act, const Repack &q, bool bf16, hipStream_t s)
 {
-    const dim3 grid((unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + 7) / 8));
-    hipLaunchKernelGGL((bf16 ? gate_grad_kernel<Brain16> : gate_grad_kernel<Half16>), grid, dim3(256), 0, s, M, F, dh,
-                       lddh, g, u, ldp, dg, du, ldd, act);
+    Repack also = q;
+    const unsigned groups = (unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + 7) / 8);
+    hipLaunchKernelGGL((bf16 ? gate_grad_kernel<Brain16> : gate_grad_kernel<Half16>), dim3(groups + repack_groups(also)),
+                       dim3(256), 0, s, M, F, dh, lddh, g, u, ldp, dg, du, ldd, act, also, groups);
     return hipGetLastError();
 }
 

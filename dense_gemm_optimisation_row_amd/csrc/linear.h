@@ -77,6 +77,7 @@ struct Repack {
         int rows, cols, ld, ld_to;
         unsigned first;   // the job's first unit in the launch; filled by the launcher
     } job[3];
+    unsigned units;       // of all jobs; filled by the launcher
 };
 hipError_t launch_repack(const Repack &r, hipStream_t stream);
 
@@ -86,15 +87,17 @@ hipError_t launch_join(const Product &p, hipStream_t stream);
 // with zeros to whole units) and each row block's column sums of the unrounded
 // dZ, rounded to dbias where there is one block, else in FP32 to sums[block][N]
 // (one of them, or neither).  Blocks of 64 rows, 16 where those would leave
-// compute units idle.
+// compute units idle.  The copies `also` ride in the same launch.
 inline int grad_rows(int M, int N) { return (M + 63LL) / 64 * ((N + 255) / 256) >= 1024 ? 64 : 16; }
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
-                           int lddz, int act, float *sums, uint16_t *dbias, bool bf16, hipStream_t stream);
+                           int lddz, int act, float *sums, uint16_t *dbias, const Repack &also, bool bf16,
+                           hipStream_t stream);
 // out[c] = sum over blocks of sums[block][c], in the input format.
 hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out, bool bf16, hipStream_t stream);
 // dG = dH U act'(G), dU = dH act(G), padded likewise.
 hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u,
-                            int ldp, uint16_t *dg, uint16_t *du, int ldd, int act, bool bf16, hipStream_t stream);
+                            int ldp, uint16_t *dg, uint16_t *du, int ldd, int act, const Repack &also, bool bf16,
+                            hipStream_t stream);
 
 // Device check of the C entry points (api.hip): GEMM_OK on gfx950.
 int device_status();

@@ -215,7 +215,7 @@ struct Copies {
         ld = r.job[i].ld_to;
         return i;
     }
-    // Marks copy i (or none) for launch; returns where the operand will be.
+    // Marks copy i (or none); returns where the operand will be.
     const uint16_t *use(int i, const uint16_t *from, uint8_t *ws)
     {
         if (i < 0)
@@ -224,13 +224,13 @@ struct Copies {
         r.job[i].to = (uint16_t *)(ws + at[i]);
         return r.job[i].to;
     }
-    hipError_t launch(hipStream_t s)
+    dgor::Repack marked() const
     {
         dgor::Repack q{};
         for (int i = 0; i < r.jobs; ++i)
             if (r.job[i].from)
                 q.job[q.jobs++] = r.job[i];
-        return q.jobs ? dgor::launch_repack(q, s) : hipSuccess;
+        return q;
     }
 };
 
@@ -353,7 +353,7 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
     p.e.bias = bias;
     p.e.R = R, p.e.ldr = q->ldr;
     p.e.pre = pre, p.e.ldp = q->ldp;
-    const hipError_t err = c.launch(s);
+    const hipError_t err = dgor::launch_repack(c.marked(), s);
     return done(err == hipSuccess ? run_product(p, l, base + c.bytes, s) : err);
 }
 
@@ -429,23 +429,23 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
     const uint16_t *dZ = dY;
     const int blocks = row_blocks(q->M, q->N);
     float *sums = dbias && blocks != 1 ? (float *)(base + l.sums) : nullptr;
-    if (q->M > 0 && q->N > 0 && ((act && (dX || dW)) || dbias)) {
-        uint16_t *out = act && (dX || dW) ? (uint16_t *)(base + l.dz) : nullptr;
-        const hipError_t e = dgor::launch_act_grad(q->M, q->N, dY, q->lddy, act ? pre : nullptr, q->ldp, out, l.lddz,
-                                                   q->activation, sums, blocks == 1 ? dbias : nullptr, bf16, s);
-        if (e != hipSuccess)
-            return GEMM_ERR_LAUNCH;
-        if (out)
-            dZ = out;
-    }
-    // no rows: an empty sum, no workspace
-    if (dbias && blocks != 1 && q->N > 0 &&
-        dgor::launch_sum_blocks(blocks, q->N, sums, dbias, bf16, s) != hipSuccess)
-        return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
     dZ = l.c.use(dX || dW ? l.copy_dy : -1, dZ, base);
     const uint16_t *Xs = l.c.use(dW ? l.copy_x : -1, X, base), *Ws = l.c.use(dX ? l.copy_w : -1, W, base);
-    if (l.c.launch(s) != hipSuccess)
+    hipError_t err;
+    if (q->M > 0 && q->N > 0 && ((act && (dX || dW)) || dbias)) {
+        uint16_t *out = act && (dX || dW) ? (uint16_t *)(base + l.dz) : nullptr;
+        err = dgor::launch_act_grad(q->M, q->N, dY, q->lddy, act ? pre : nullptr, q->ldp, out, l.lddz, q->activation,
+                                    sums, blocks == 1 ? dbias : nullptr, l.c.marked(), bf16, s);
+        if (out)
+            dZ = out;
+    } else {
+        err = dgor::launch_repack(l.c.marked(), s);
+    }
+    // no rows: an empty sum, no workspace
+    if (err == hipSuccess && dbias && blocks != 1 && q->N > 0)
+        err = dgor::launch_sum_blocks(blocks, q->N, sums, dbias, bf16, s);
+    if (err != hipSuccess)
         return GEMM_ERR_LAUNCH;
     if (dX) {
         px.A[0] = px.A[1] = dZ;
@@ -513,7 +513,7 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
     p.B[0] = c.use(copy[1], Wg, base), p.B[1] = c.use(copy[2], Wu, base);
     p.e.Y = H, p.e.ldy = q->ldh;
     p.e.pre = G, p.e.pre2 = U, p.e.ldp = q->ldp;
-    const hipError_t err = c.launch(s);
+    const hipError_t err = dgor::launch_repack(c.marked(), s);
     return done(err == hipSuccess ? run_product(p, l, base + c.bytes, s) : err);
 }
 
@@ -587,14 +587,14 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
     uint16_t *dG = (uint16_t *)(base + l.dg), *dU = (uint16_t *)(base + l.du);
-    if (q->M > 0 && q->F > 0 &&
-        dgor::launch_gate_grad(q->M, q->F, dH, q->lddh, G, U, q->ldp, dG, dU, l.ldd, q->activation, bf16, s) !=
-            hipSuccess)
-        return GEMM_ERR_LAUNCH;
     px.bf16 = pw.bf16 = bf16;
     const uint16_t *Xs = l.c.use(dWg ? l.copy_x : -1, X, base);
     const uint16_t *Gs = l.c.use(dX ? l.copy_wg : -1, Wg, base), *Us = l.c.use(dX ? l.copy_wu : -1, Wu, base);
-    if (l.c.launch(s) != hipSuccess)
+    const hipError_t err = q->M > 0 && q->F > 0
+                               ? dgor::launch_gate_grad(q->M, q->F, dH, q->lddh, G, U, q->ldp, dG, dU, l.ldd,
+                                                        q->activation, l.c.marked(), bf16, s)
+                               : dgor::launch_repack(l.c.marked(), s);
+    if (err != hipSuccess)
         return GEMM_ERR_LAUNCH;
     if (dX) {
         px.A[0] = dG, px.A[1] = dU;

@@ -345,8 +345,9 @@ int gemm_conv2d_f16_f32acc_noalloc(const gemm_conv2d_params *params, const uint1
  * Conventions beyond those above:
  *   - Matrices are row-major with the given row strides (ld..., in elements,
  *     at least the row length); any element alignment, row length and stride
- *     is taken.  16-byte aligned operands whose strides and row lengths are
- *     multiples of 8 take the faster kernels.
+ *     is taken.  Operands whose rows or strides are not multiples of 8 are, as
+ *     a rule, first copied into the workspace; at strides that are, the
+ *     fastest kernels want 16-byte aligned addresses.
  *   - W holds K inputs x N outputs: stored K x N (op_w GEMM_OP_N) or N x K
  *     (GEMM_OP_T); weight gradients come in the storage of their weight.
  *   - Outputs must not overlap inputs or each other, except that Y may be the
