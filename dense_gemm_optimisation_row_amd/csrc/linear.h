@@ -52,6 +52,9 @@ enum RingTile { kRing256, kRing256x128, kRing128, kRing128x64, kRing64 };
 constexpr int ring_tile_m(RingTile t) { return t <= kRing256x128 ? 256 : (t == kRing64 ? 64 : 128); }
 constexpr int ring_tile_n(RingTile t) { return t == kRing256 ? 256 : (t <= kRing128 ? 128 : 64); }
 hipError_t launch_linear_ring(const Product &p, RingTile tile, hipStream_t stream);
+// The two products of a backward pass (the weight's gradient, as K x M by K x N,
+// and the input's) in one launch, on one of the three smaller tiles.
+hipError_t launch_linear_ring_pair(const Product &weight, const Product &input, RingTile tile, hipStream_t stream);
 
 // Few rows (at most kSkinnyRows, A as M x K, one product); each operand at
 // least eight elements from its first to its last.

@@ -79,8 +79,18 @@ __device__ __forceinline__ int range_of(int rows, int cols, int ld)
                : (int)(((uint32_t)(rows - 1) * (uint32_t)ld + ((uint32_t)(cols + 7) & ~7u)) * 2u);
 }
 
+// Stages that a load is ahead of its fragments' stage, and the ring's bytes.
+constexpr int ring_ahead(int bm) { return bm == 64 ? 7 : 3; }
+constexpr int ring_a_bytes(int bm, bool ta)
+{
+    const int d = ring_ahead(bm), stage = 32 * bm * 2;
+    return ta ? (d + 1) * stage : ((d + 1) / 2 + 1) * 2 * stage;
+}
+constexpr int ring_bytes(int bm, int bn, bool ta) { return ring_a_bytes(bm, ta) + (ring_ahead(bm) + 1) * 32 * bn * 2; }
+
+// Tile `bid` (of both batches) and part `part` of a product, by 256 threads.
 template <class Op, int BM, int BN, bool TA, bool TB, bool GATED>
-__global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
+__device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bid, int part)
 {
     constexpr int BK = 32;
     constexpr int HM = BM / 2, HN = BN / 2;        // a wavefront's part of the tile,
@@ -89,18 +99,15 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     constexpr int LPA = BM / 64, LPB = BN / 64;    // a wavefront's loads of each operand and stage
     constexpr int HALF_A = BK * HM * 2, HALF_B = BK * HN * 2, STAGE_A = 2 * HALF_A, STAGE_B = 2 * HALF_B;
     constexpr int PAIR = 2 * STAGE_A;
-    constexpr int D = BM == 64 ? 7 : 3;            // stages that a load is ahead of its fragments' stage
-    constexpr int A_PAIRS = (D + 1) / 2 + 1;
-    constexpr int A_BYTES = TA ? (D + 1) * STAGE_A : A_PAIRS * PAIR;
-    constexpr int LDS_BYTES = A_BYTES + (D + 1) * STAGE_B;
+    constexpr int D = ring_ahead(BM), A_PAIRS = (D + 1) / 2 + 1;
+    constexpr int A_BYTES = ring_a_bytes(BM, TA), LDS_BYTES = ring_bytes(BM, BN, TA);
     constexpr int FT = GATED ? HN : BN;            // output columns of a tile
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS_BYTES];
     const uint32_t ring = lds_address(lds);
 
     const int per = p.tiles_m * p.tiles_n;
-    const int batch = blockIdx.x >= (unsigned)per ? 1 : 0;
+    const int batch = bid >= per ? 1 : 0;
     int tm, tn;
-    dgor_tile_of_block((int)blockIdx.x - batch * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    dgor_tile_of_block(bid - batch * per, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
     const int m0 = tm * BM, n0 = tn * FT;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -108,7 +115,7 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     // stages of 32 k; a segment's are a whole number of pairs
     const int seg_stages = 2 * ((K + 2 * BK - 1) / (2 * BK));
     const int total = p.nseg == 2 ? 2 * seg_stages : (K + BK - 1) / BK;
-    const int s0 = p.splits > 1 ? (int)blockIdx.y * p.chunk * 2 : 0;
+    const int s0 = p.splits > 1 ? part * p.chunk * 2 : 0;
     const int steps = (p.splits > 1 ? min(s0 + p.chunk * 2, total) : total) - s0;
 
     // ---- loads.  Wavefronts 0 and 1 fill half 0 of a stage, 2 and 3 half 1.
@@ -427,13 +434,13 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
         if (p.splits > 1) {
             rows([&](int row, Rows &v, Rows &u) {
                 const int ld = part_stride(p);
-                float *part = p.part + ((size_t)batch * p.splits + blockIdx.y) * part_size(p) + (size_t)row * ld + col;
+                float *to = p.part + ((size_t)batch * p.splits + part) * part_size(p) + (size_t)row * ld + col;
 #pragma unroll
                 for (int q = 0; q < TOGETHER; ++q)
                     if (row + STEP * q < M) {
-                        store8_f32(part + (size_t)(STEP * q) * ld, 8, v[q]);
+                        store8_f32(to + (size_t)(STEP * q) * ld, 8, v[q]);
                         if (GATED)
-                            store8_f32(part + p.splits * part_size(p) + (size_t)(STEP * q) * ld, 8, u[q]);
+                            store8_f32(to + p.splits * part_size(p) + (size_t)(STEP * q) * ld, 8, u[q]);
                     }
             });
         } else if (!whole) {
@@ -462,6 +469,48 @@ __global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
     }
 }
 
+template <class Op, int BM, int BN, bool TA, bool TB, bool GATED>
+__global__ __launch_bounds__(256) void linear_ring_kernel(Product p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[ring_bytes(BM, BN, TA)];
+    ring_tile<Op, BM, BN, TA, TB, GATED>(p, lds, (int)blockIdx.x, (int)blockIdx.y);
+}
+
+// Both products of a backward pass in one launch: first the workgroups of the
+// weight's gradient w, then those of the input's gradient x.
+template <class Op, int BM, int BN, bool TB>
+__global__ __launch_bounds__(256) void linear_ring_pair_kernel(Product w, Product x, int w_groups)
+{
+    constexpr int A = ring_bytes(BM, BN, true), B = ring_bytes(BM, BN, false);
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[A > B ? A : B];
+    const bool first = (int)blockIdx.x < w_groups;
+    const Product &p = first ? w : x;
+    const int id = (int)blockIdx.x - (first ? 0 : w_groups), per = p.tiles_m * p.tiles_n * p.nbatch;
+    if (first)
+        ring_tile<Op, BM, BN, true, false, false>(w, lds, id % per, id / per);
+    else
+        ring_tile<Op, BM, BN, false, TB, false>(x, lds, id % per, id / per);
+}
+
+template <class Op, int BM, int BN>
+hipError_t launch_pair_as(const Product &w, const Product &x, hipStream_t s)
+{
+    const int nw = w.tiles_m * w.tiles_n * w.nbatch * (w.splits > 1 ? w.splits : 1);
+    const int nx = x.tiles_m * x.tiles_n * (x.splits > 1 ? x.splits : 1);
+    const auto kernel =
+        x.trans_b ? linear_ring_pair_kernel<Op, BM, BN, true> : linear_ring_pair_kernel<Op, BM, BN, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(nw + nx)), dim3(256), 0, s, w, x, nw);
+    return hipGetLastError();
+}
+
+void lay_out(Product &p, RingTile tile)
+{
+    const int bm = ring_tile_m(tile), bn = ring_tile_n(tile), ft = p.gated ? bn / 2 : bn;
+    p.tiles_m = (p.M + bm - 1) / bm;
+    p.tiles_n = (p.N + ft - 1) / ft;
+    p.group_m = 4;
+}
+
 template <class Op, int BM, int BN>
 hipError_t launch_ring_as(const Product &p, hipStream_t s)
 {
@@ -488,10 +537,7 @@ hipError_t launch_linear_ring(const Product &q, RingTile tile, hipStream_t s)
     Product p = q;
     if (p.trans_a && p.trans_b)
         return hipErrorInvalidValue;
-    const int bm = ring_tile_m(tile), bn = ring_tile_n(tile), ft = p.gated ? bn / 2 : bn;
-    p.tiles_m = (p.M + bm - 1) / bm;
-    p.tiles_n = (p.N + ft - 1) / ft;
-    p.group_m = 4;
+    lay_out(p, tile);
     switch (tile) {
     case kRing256: return p.bf16 ? launch_ring_as<OpBrain, 256, 256>(p, s) : launch_ring_as<OpHalf, 256, 256>(p, s);
     case kRing256x128:
@@ -501,6 +547,23 @@ hipError_t launch_linear_ring(const Product &q, RingTile tile, hipStream_t s)
     case kRing64: return p.bf16 ? launch_ring_as<OpBrain, 64, 64>(p, s) : launch_ring_as<OpHalf, 64, 64>(p, s);
     }
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_linear_ring_pair(const Product &weight, const Product &input, RingTile tile, hipStream_t s)
+{
+    Product w = weight, x = input;
+    if (!w.trans_a || w.trans_b || x.trans_a || w.gated || x.gated || x.nbatch != 1)
+        return hipErrorInvalidValue;
+    lay_out(w, tile);
+    lay_out(x, tile);
+    switch (tile) {
+    case kRing128:
+        return w.bf16 ? launch_pair_as<OpBrain, 128, 128>(w, x, s) : launch_pair_as<OpHalf, 128, 128>(w, x, s);
+    case kRing128x64:
+        return w.bf16 ? launch_pair_as<OpBrain, 128, 64>(w, x, s) : launch_pair_as<OpHalf, 128, 64>(w, x, s);
+    case kRing64: return w.bf16 ? launch_pair_as<OpBrain, 64, 64>(w, x, s) : launch_pair_as<OpHalf, 64, 64>(w, x, s);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace dgor

@@ -132,3 +132,34 @@ def test_sums_split_over_k(size, dtype):
         x, dz, w = ints(g, K, M, T, -1, 2), ints(g, K, N, T, -1, 2), weight(g, M, N, T, transposed)
         dw = dg.linear_backward(dz, x, w, need_input=False, need_bias=False)[1]
         same(dw, x.double().t() @ dz.double(), "dw")
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["KxN", "NxK"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [(72, 72, 72), (528, 2752, 792), (377, 6424, 256), (264, 96, 4104), (1016, 1008, 1024)],
+                         ids=str)
+def test_both_gradients_of_a_pass(size, dtype, transposed):
+    # small passes run both products in one launch: each tile, one or both
+    # sums split, edges in each direction, and replayed from a graph
+    M, K, N = size
+    T = DTYPES[dtype]
+    say("ring pair", size, dtype, transposed)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x, w, dy = ints(g, M, K, T, -1, 2), weight(g, K, N, T, transposed), ints(g, M, N, T, -1, 2)
+    dx, dw, db = dg.linear_backward(dy, x, w)
+    same(dx, dy.double() @ w.double().t(), "dx")
+    same(dw, x.double().t() @ dy.double(), "dw")
+    same(db, dy.double().sum(0), "dbias")
+    wu, gs, us = weight(g, K, N, T, transposed), ints(g, M, N, T, -1, 2), ints(g, M, N, T, -1, 2)
+    want = gated_grads("relu", *(t.double() for t in (dy, x, w, wu, gs, us)))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = dg.gated_backward(dy, x, w, wu, gs, us, activation="relu")
+    for _ in range(3):
+        for t in got:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, name in zip(got, want, ("dx", "dwg", "dwu")):
+            same(a, b, name)
