@@ -70,8 +70,8 @@ void split(const Product &p, long long parts, Way &w)
 // to 16 to 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N):
 // within 10% of the times measured.  Full rates: 1470, 1280, 1180, 890 and
 // 570 TFLOP/s.  An activation of exponentials adds what its outputs take on the
-// vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs: 236 us, 217
-// without).
+// vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs of 4096: 222 us,
+// 204 without).
 struct RingCost {
     dgor::RingTile tile;
     int share;
@@ -271,7 +271,7 @@ bool whole_units(int cols, int ld) { return ld % 8 == 0 && cols % 8 == 0 && ld <
 // Operands that are copied at the front of the workspace, their rows padded
 // to whole units for the rings: those whose rows or strides are not.  (1000 x
 // 777 by 777 x 1033 on the plain tile, whose loads then fall off dwords: 22
-// us; copied and on the ring: see kRings' figures.)
+// us; copied, 5 us, and on the ring 16 together.)
 struct Copies {
     dgor::Repack r{};
     size_t at[3] = {}, bytes = 0;
@@ -350,7 +350,8 @@ Product weight_gradient_product(int M, int N, int K, int op_w, int ldx, int lddz
 
 // Whether operands off the units are worth a launch that copies them: not for
 // a sum of up to two stages of the plain tile over at most a round of its
-// tiles (100 x 100 by 100 x 100: 9 us against 12).
+// tiles (100 x 100 by 100 x 100: 6.3 us, against 2.9 and 4.6 in two launches,
+// which are 7.5 us and 12.1 as a host issues them one after another).
 bool worth_copies(const Product &p)
 {
     return dgor::product_stages(p) > 2 || tiles(p, dgor::kTile, dgor::kTile) > 512;
