@@ -29,7 +29,7 @@ struct Way {
     Kernel kernel;
     dgor::RingTile tile;
     int splits, chunk;
-    double us;   // on a ring: the time that it was chosen for
+    double us;   // the time that a ring was chosen for, or that few rows take
 };
 
 long long tiles(const Product &p, int tm, int tn)
@@ -87,6 +87,9 @@ constexpr RingCost kRings[] = {
 };
 constexpr int kSplitRows = 40;   // stages of 64 k from which few rows' sums over a K x N matrix are split
 constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
+// Weights that the few-row kernel reads in a microsecond, past 3 us: 33.5 MB
+// 11 us, 134 MB 28 us.
+constexpr double kRowsBytes = 5e6;
 double microseconds(const Product &p, const RingCost &c, int parts)
 {
     const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
@@ -139,6 +142,7 @@ Way choose(const Product &p, bool ring)
             want = want < stages / 8 ? want : stages / 8;
             split(p, want < 32 ? want : 32, w);
         }
+        w.us = 3.0 + 2.0 * p.nseg * p.K * p.N / kRowsBytes + (w.splits > 1 ? kJoinLaunch : 0.0);
         return w;
     }
     if (ring) {
@@ -208,6 +212,9 @@ hipError_t run_product(const Product &q, const Plan &l, void *ws, hipStream_t s)
 // rows take 10% less time on average: 528 rows of 2752 to 791 outputs 25.6 us
 // against 35.2, 3344 rows gated 684 to 640 39.6 against 52.7, 377 rows of 6417
 // to 256 18.6 against 24.0; none takes longer.
+// Of at most 64 rows, where the input's gradient alone is the few-row kernel's:
+// 16 rows of 248 to 640 12.9 against 15.7, 8 rows gated 1344 to 1630 23.2
+// against 25.8.
 struct PairPlan {
     Plan x, w;
     bool together;
@@ -222,8 +229,8 @@ PairPlan plan_pair(const Product &x, const Product &w)
     l.x = plan(x);
     l.w = plan(w);
     l.part = l.x.part > l.w.part ? l.x.part : l.w.part;
-    if (l.x.ring.kernel != Kernel::Ring || l.w.ring.kernel != Kernel::Ring || x.M == 0 || x.N == 0 || w.M == 0 ||
-        w.N == 0)
+    if (!ring_sizes(x) || !ring_sizes(w) || l.x.ring.kernel == Kernel::Tile || l.w.ring.kernel != Kernel::Ring ||
+        x.M == 0 || x.N == 0 || w.M == 0 || w.N == 0)
         return l;
     double best = l.x.ring.us + l.w.ring.us + kLaunch;
     for (const RingCost &c : kRings) {
