@@ -90,24 +90,27 @@ constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's b
 // Weights that the few-row kernel reads in a microsecond, past 3 us: 33.5 MB
 // 11 us, 134 MB 28 us.
 constexpr double kRowsBytes = 5e6;
-double microseconds(const Product &p, const RingCost &c, int parts)
+struct RingTimes {
+    double alone, full, join;   // a round of one tile a unit, a full one, joining the parts
+};
+RingTimes times(const Product &p, const RingCost &c, int parts)
 {
-    const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
     // half lines: B as N x K, and each of two matrices' 32 columns
     const bool halves = p.trans_b || (p.gated && ring_tile_n(c.tile) == 64);
     const double stages = 2.0 * dgor::product_stages(p) / parts * (halves ? c.halves : 1.0);
-    const long long rounds = n / (256LL * c.share), rest = n % (256LL * c.share);
     // an activation's time for a workgroup's outputs
     const double act = p.e.act > GEMM_ACT_RELU && parts == 1
                            ? 9.0 * ring_tile_m(c.tile) * ring_tile_n(c.tile) / (p.gated ? 131072 : 65536)
                            : 0.0;
-    const double alone = c.ends + stages * c.alone + act, full = c.ends_full + stages * c.full + act * c.share;
-    double t = rounds * full;
-    if (rest)
-        t += rest <= 256 ? alone : full;
-    if (parts > 1)
-        t += kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes;
-    return t;
+    return {c.ends + stages * c.alone + act, c.ends_full + stages * c.full + act * c.share,
+            parts > 1 ? kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes : 0.0};
+}
+double microseconds(const Product &p, const RingCost &c, int parts)
+{
+    const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
+    const long long rounds = n / (256LL * c.share), rest = n % (256LL * c.share);
+    const RingTimes t = times(p, c, parts);
+    return rounds * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full) + t.join;
 }
 
 // The best split of a product on a ring's tile.
@@ -206,15 +209,14 @@ hipError_t run_product(const Product &q, const Plan &l, void *ws, hipStream_t s)
     return err == hipSuccess ? join(p, s) : err;
 }
 
-// Both products of a backward pass: each by its own plan, or, where they are
-// small, in one launch on one tile, so that their workgroups run side by side.
-// Of 60 drawn backward passes no longer than 70 us, those with more than 64
-// rows take 10% less time on average: 528 rows of 2752 to 791 outputs 25.6 us
-// against 35.2, 3344 rows gated 684 to 640 39.6 against 52.7, 377 rows of 6417
-// to 256 18.6 against 24.0; none takes longer.
-// Of at most 64 rows, where the input's gradient alone is the few-row kernel's:
-// 16 rows of 248 to 640 12.9 against 15.7, 8 rows gated 1344 to 1630 23.2
-// against 25.8.
+// Both products of a backward pass: each by its own plan, or, where that is
+// estimated shorter, in one launch on one tile, so that their workgroups run
+// side by side, in one round or in rounds that only the last leaves unfilled.
+// In one launch and in two: 528 rows of 2752 to 791 outputs 25.6 us and 35.2,
+// 3344 rows gated 684 to 640 39.6 and 52.7, 2960 rows gated 244 to 5614 100 and
+// 116, 3266 rows of 3512 to 64 30.7 and 38.4; of at most 64 rows, where the
+// input's gradient alone is the few-row kernel's, 16 rows of 248 to 640 12.9
+// and 15.7.  Of 150 drawn passes none takes longer.
 struct PairPlan {
     Plan x, w;
     bool together;
@@ -237,12 +239,20 @@ PairPlan plan_pair(const Product &x, const Product &w)
         if (ring_tile_m(c.tile) == 256)
             continue;
         const Way a = best_on(x, c), b = best_on(w, c);
-        const long long n = tiles(x, ring_tile_m(c.tile), ring_tile_n(c.tile)) * a.splits +
-                            tiles(w, ring_tile_m(c.tile), ring_tile_n(c.tile)) * b.splits;
-        if (n > 256LL * c.share)
-            continue;   // a round of its own each: nothing is gained
-        const double slower = n > 256 ? c.full / c.alone : 1.0;
-        const double t = slower * (a.us > b.us ? a.us : b.us) + (a.splits > 1 && b.splits > 1 ? kLaunch : 0.0);
+        const RingTimes ta = times(x, c, a.splits), tb = times(w, c, b.splits);
+        const double na = (double)tiles(x, ring_tile_m(c.tile), ring_tile_n(c.tile)) * a.splits;
+        const double nb = (double)tiles(w, ring_tile_m(c.tile), ring_tile_n(c.tile)) * b.splits;
+        if (na + nb > (1 << 20))
+            continue;   // a launch holds 2^32 threads
+        double t;
+        if (na + nb <= 256) {
+            t = ta.alone > tb.alone ? ta.alone : tb.alone;
+        } else {
+            const double longer = ta.full > tb.full ? ta.full : tb.full;
+            t = na + nb <= 256.0 * c.share ? longer
+                                           : (na * ta.full + nb * tb.full) / (256.0 * c.share) + 0.5 * longer;
+        }
+        t += ta.join + tb.join;
         if (t < best)
             best = t, l.together = true, l.way_x = a, l.way_w = b;
     }

@@ -137,7 +137,8 @@ def test_sums_split_over_k(size, dtype):
 @pytest.mark.parametrize("transposed", [False, True], ids=["KxN", "NxK"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("size", [(72, 72, 72), (528, 2752, 792), (377, 6424, 256), (264, 96, 4104), (1016, 1008, 1024),
-                                  (1, 64, 8), (3, 1344, 1632), (16, 248, 640), (64, 128, 3520)],
+                                  (1, 64, 8), (3, 1344, 1632), (16, 248, 640), (64, 128, 3520), (3266, 3512, 64),
+                                  (496, 1024, 4288)],
                          ids=str)
 def test_both_gradients_of_a_pass(size, dtype, transposed):
     # small passes run both products in one launch: each tile, one or both
