@@ -99,6 +99,7 @@ _CONV_STEM = {"f32": "gemm_conv2d_f32", "f16": "gemm_conv2d_f16_f32acc", "bf16":
 
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # gemm_activation
+GEMM_ROUND_GRADIENT = 0x100   # flag of a backward pass's activation
 
 
 class LinearParams(ctypes.Structure):

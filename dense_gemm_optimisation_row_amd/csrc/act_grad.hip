@@ -1,11 +1,20 @@
 // The element-wise work around the dense layers' products: copies of operands
 // whose rows are not whole 16-byte units, and of the backward passes the gradient
-// of the pre-activations, rounded to the 16-bit format that the matrix
-// cores take, and the bias gradient's column sums of the unrounded values.
+// of the pre-activations and the bias gradient's column sums of the unrounded
+// values.
 //
-// Bound by memory: each value is read and written once.  A workgroup covers 64
-// (or 16) rows x 256 columns, 32 lanes of eight columns times 8 rows at a time, so a row's accesses are 512 contiguous bytes and the column sums of a
-// workgroup need one pass through LDS.  The sums go out per row block and are
+// The gradient is computed in FP32 and the matrix cores take 16 bits.  It is
+// written as the sum of two bfloat16 terms, so that each product of it is within
+// 2^-17 of that of the FP32 values and has their range: rounded once to
+// bfloat16 it would add as much error to dX and dW as their own rounding does
+// (1.66e-3 in all, 2.35e-3 so), and in binary16 it would overflow past 65504 and
+// vanish below 2^-25.  The caller may ask for the rounding, which halves (binary16:
+// takes a third of) the products' work.
+//
+// Bound by memory: each value is read once and written once, or as two terms.  A
+// workgroup covers 64 (or 16) rows x 256 columns, 32 lanes of eight columns times 8
+// rows at a time, so a row's accesses are 512 contiguous bytes and the column sums
+// of a workgroup need one pass through LDS.  The sums go out per row block and are
 // added in block order by a second kernel, so they do not depend on which
 // workgroup finished first.
 #include "linear.h"
@@ -15,21 +24,44 @@ namespace {
 
 constexpr int kCols = 256;
 
-// Workgroup `group` of a copy: a unit a thread, read at any alignment, written
-// whole.
+// Workgroup `group` of a copy: a unit a thread (further units where there are
+// more than the workgroups take at once), read at any alignment, written whole.
 __device__ __forceinline__ void repack(const Repack &r, unsigned group)
 {
-    const unsigned id = group * 256 + threadIdx.x;
-    if (id >= r.units)
-        return;
-    Repack::Job j = r.job[0];
+    for (unsigned long long id = group * 256ULL + threadIdx.x; id < r.units; id += r.groups * 256ULL) {
+        Repack::Job j = r.job[0];
 #pragma unroll
-    for (int i = 1; i < 3; ++i)
-        if (i < r.jobs && id >= r.job[i].first)
-            j = r.job[i];
-    const unsigned per = (unsigned)(j.cols + 7) / 8, u = id - j.first, row = u / per;
-    const int col = 8 * (int)(u - row * per);
-    store8_16(j.to + (size_t)row * j.ld_to + col, 8, load8_16(j.from + (size_t)row * j.ld + col, j.cols - col));
+        for (int i = 1; i < 3; ++i)
+            if (i < r.jobs && id >= r.job[i].first)
+                j = r.job[i];
+        // a job has fewer than 2^32 units: 2^22 blocks of 128 x 64 elements at most
+        const unsigned per = (unsigned)(j.cols + 7) / 8, u = (unsigned)(id - j.first), row = u / per;
+        const int col = 8 * (int)(u - row * per);
+        u32x4 v = load8_16(j.from + (size_t)row * j.ld + col, j.cols - col);
+        const size_t at = (size_t)row * j.ld_to + col;
+        if (j.lo) {
+            float f[8];
+            u32x4 lo;
+            unpack8<Half16>(v, f);
+            pack8_terms(f, v, lo);
+            store8_16(j.lo + at, 8, lo);
+        }
+        store8_16(j.to + at, 8, v);
+    }
+}
+
+// d in the input format or, where there is a lower term, as two.
+template <class Fmt>
+__device__ __forceinline__ void store_gradient(uint16_t *hi, uint16_t *lo, size_t at, const float (&d)[8])
+{
+    u32x4 v, w;
+    if (lo) {
+        pack8_terms(d, v, w);
+        store8_16(lo + at, 8, w);
+    } else {
+        v = pack8<Fmt>(d);
+    }
+    store8_16(hi + at, 8, v);
 }
 
 // x to act'(x): one uniform branch on the activation, not one an element.
@@ -55,8 +87,8 @@ __device__ __forceinline__ void slopes(int act, float (&x)[8])
 template <class Fmt, int R>
 __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint16_t *__restrict__ dy, int lddy,
                                                        const uint16_t *__restrict__ z, int ldz,
-                                                       uint16_t *__restrict__ dz, int lddz, int act,
-                                                       float *__restrict__ sums, uint16_t *__restrict__ dbias,
+                                                       uint16_t *__restrict__ dz, uint16_t *__restrict__ dz_lo,
+                                                       int lddz, int act, float *__restrict__ sums, uint16_t *__restrict__ dbias,
                                                        Repack also, unsigned groups)
 {
     if (blockIdx.x >= groups) {
@@ -96,7 +128,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(int M, int N, const uint1
                     d[e] *= x[e];
             }
             if (dz)   // past N zeros: its rows are padded to whole units
-                store8_16(dz + (size_t)row * lddz + col, 8, pack8<Fmt>(d));
+                store_gradient<Fmt>(dz, dz_lo, (size_t)row * lddz + col, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 total[e] += d[e];
@@ -148,8 +180,8 @@ template <class Fmt>
 __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint16_t *__restrict__ dh, int lddh,
                                                         const uint16_t *__restrict__ g,
                                                         const uint16_t *__restrict__ u, int ldp,
-                                                        uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int ldd,
-                                                        int act, Repack also, unsigned groups)
+                                                        GateGrads out, int ldd, int act, Repack also,
+                                                        unsigned groups)
 {
     if (blockIdx.x >= groups) {
         repack(also, blockIdx.x - groups);
@@ -193,21 +225,23 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
     case GEMM_ACT_SILU: apply(GEMM_ACT_SILU); break;
     default: apply(GEMM_ACT_NONE);
     }
-    store8_16(dg + (size_t)row * ldd + col, 8, pack8<Fmt>(a));   // past F zeros
-    store8_16(du + (size_t)row * ldd + col, 8, pack8<Fmt>(b));
+    store_gradient<Fmt>(out.g[0], out.g[1], (size_t)row * ldd + col, a);   // past F zeros
+    store_gradient<Fmt>(out.u[0], out.u[1], (size_t)row * ldd + col, b);
 }
 
 __global__ __launch_bounds__(256) void repack_kernel(Repack r) { repack(r, blockIdx.x); }
 
-// Counts the jobs' units; returns the workgroups that they take.
+// Counts the jobs' units; returns the workgroups that take them, a million at
+// most.
 unsigned repack_groups(Repack &r)
 {
     r.units = 0;
     for (int i = 0; i < r.jobs; ++i) {
         r.job[i].first = r.units;
-        r.units += (unsigned)r.job[i].rows * (unsigned)((r.job[i].cols + 7) / 8);
+        r.units += (unsigned long long)r.job[i].rows * ((r.job[i].cols + 7LL) / 8);
     }
-    return (unsigned)((r.units + 255ULL) / 256);
+    const unsigned long long groups = (r.units + 255) / 256;
+    return r.groups = (unsigned)(groups < (1 << 20) ? groups : (1 << 20));
 }
 
 }  // namespace
@@ -222,15 +256,16 @@ hipError_t launch_repack(const Repack &q, hipStream_t s)
 }
 
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
-                           int lddz, int act, float *sums, uint16_t *dbias, const Repack &q, bool bf16, hipStream_t s)
+                           uint16_t *dz_lo, int lddz, int act, float *sums, uint16_t *dbias, const Repack &q, bool bf16,
+                           hipStream_t s)
 {
     Repack also = q;
     const int rows = grad_rows(M, N);
     const unsigned groups = (unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + rows - 1) / rows);
     const auto kernel = rows == 64 ? (bf16 ? act_grad_kernel<Brain16, 8> : act_grad_kernel<Half16, 8>)
                                    : (bf16 ? act_grad_kernel<Brain16, 2> : act_grad_kernel<Half16, 2>);
-    hipLaunchKernelGGL(kernel, dim3(groups + repack_groups(also)), dim3(256), 0, s, M, N, dy, lddy, z, ldz, dz, lddz,
-                       act, sums, dbias, also, groups);
+    hipLaunchKernelGGL(kernel, dim3(groups + repack_groups(also)), dim3(256), 0, s, M, N, dy, lddy, z, ldz, dz,
+                       dz_lo, lddz, act, sums, dbias, also, groups);
     return hipGetLastError();
 }
 
@@ -242,12 +277,12 @@ hipError_t launch_sum_blocks(int blocks, int N, const float *sums, uint16_t *out
 }
 
 hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const uint16_t *g, const uint16_t *u, int ldp,
-                            uint16_t *dg, uint16_t *du, int ldd, int act, const Repack &q, bool bf16, hipStream_t s)
+                            const GateGrads &d, int ldd, int act, const Repack &q, bool bf16, hipStream_t s)
 {
     Repack also = q;
     const unsigned groups = (unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + 7) / 8);
     hipLaunchKernelGGL((bf16 ? gate_grad_kernel<Brain16> : gate_grad_kernel<Half16>), dim3(groups + repack_groups(also)),
-                       dim3(256), 0, s, M, F, dh, lddh, g, u, ldp, dg, du, ldd, act, also, groups);
+                       dim3(256), 0, s, M, F, dh, lddh, g, u, ldp, d, ldd, act, also, groups);
     return hipGetLastError();
 }
 

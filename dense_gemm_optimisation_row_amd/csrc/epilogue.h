@@ -142,6 +142,18 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8])
         v[e] = Fmt::down2(f[2 * e], f[2 * e + 1]);
     return v;
 }
+// f as the sum of two bfloat16 terms, to 2^-17 of it (a binary16 value exactly).
+// What has no finite higher term is that term alone.
+__device__ __forceinline__ void pack8_terms(const float (&f)[8], u32x4 &hi, u32x4 &lo)
+{
+    float r[8];
+    hi = pack8<Brain16>(f);
+    unpack8<Brain16>(hi, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r[e] = __builtin_isfinite(r[e]) ? f[e] - r[e] : 0.f;
+    lo = pack8<Brain16>(r);
+}
 __device__ __forceinline__ void load8_f32(const float *p, int n, float (&f)[8])
 {
     if (n >= 8) {
@@ -253,16 +265,16 @@ __device__ __forceinline__ void activate_slope(int act, float z, float &value, f
     }
 }
 
-// Where a finished tile goes.  Y is M x N in FP32 (y_f32) or the input
-// format; the rest may be null.  Gated products have two sums an element and
-// two saved pre-activations.
+// Where a finished tile goes.  Y is M x N in FP32 (y_f32), binary16 (y_f16, of
+// products on bfloat16 terms) or the input format; the rest may be null.  Gated
+// products have two sums an element and two saved pre-activations.
 struct Epilogue {
     void *Y;
     const uint16_t *bias;
     const void *R;         // residual, in Y's format
     uint16_t *pre, *pre2;
     int ldy, ldr, ldp;
-    int act, y_f32;
+    int act, y_f32, y_f16;
 };
 
 // The bias of eight neighbouring columns, n of them inside the matrix.
@@ -345,6 +357,8 @@ __device__ __forceinline__ void emit_rows(const Epilogue &e, int row, int step, 
             const size_t at = (size_t)(row + i * step) * e.ldy + col;
             if (!GATED && e.y_f32)
                 store8_f32((float *)e.Y + at, n, v[i]);
+            else if (!GATED && e.y_f16)
+                store8_16((uint16_t *)e.Y + at, n, pack8<Half16>(v[i]));
             else
                 store8_16((uint16_t *)e.Y + at, n, pack8<Fmt>(v[i]));
         }

@@ -20,6 +20,8 @@ bool too_large(long long rows, long long cols) { return (rows + 127) / 128 * ((c
 bool ld_ok(int ld, int row) { return ld >= (row > 1 ? row : 1); }
 bool op_ok(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 bool act_ok(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
+// The backward passes' activation carries a flag.
+int act_of(int activation) { return activation & ~GEMM_ROUND_GRADIENT; }
 bool missing(const void *p, long long rows, long long cols) { return rows > 0 && cols > 0 && !p; }
 
 // How a product runs: the kernel, a ring's tile and, where its tiles leave
@@ -40,7 +42,7 @@ long long tiles(const Product &p, int tm, int tn)
 // Whether the few-row kernel takes a product.
 bool few_rows(const Product &p)
 {
-    return !p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows && dgor::spans_a_unit(p);
+    return !p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows && dgor::spans_a_unit(p) && !p.opened;
 }
 
 // Whether sizes and strides let the rings run (the addresses apart).
@@ -51,15 +53,16 @@ bool ring_sizes(const Product &p)
 }
 bool ring_addresses(const Product &p)
 {
-    return (((uintptr_t)p.A[0] | (uintptr_t)p.A[1] | (uintptr_t)p.B[0] | (uintptr_t)p.B[1]) & 15) == 0;
+    const auto all = [](const dgor::Side &s) { return (uintptr_t)s.p | (uintptr_t)s.matrix | (uintptr_t)s.term; };
+    return ((all(p.A) | all(p.B)) & 15) == 0;
 }
 
-void split(const Product &p, long long parts, Way &w)
+void split(int stages, long long parts, Way &w)
 {
     w.splits = 1, w.chunk = 0;
     if (parts > 1) {
-        w.chunk = ceil_div(dgor::product_stages(p), parts);
-        w.splits = ceil_div(dgor::product_stages(p), w.chunk);
+        w.chunk = ceil_div(stages, parts);
+        w.splits = ceil_div(stages, w.chunk);
     }
 }
 
@@ -128,24 +131,24 @@ Way best_on(const Product &p, const RingCost &c)
         if (parts == 1 || t < w.us)
             w.us = t, best = parts;
     }
-    split(p, best, w);
+    split(stages, best, w);
     return w;
 }
 
 Way choose(const Product &p, bool ring)
 {
     Way w{Kernel::Rows, dgor::kRing64, 1, 0, 0};
-    const int stages = dgor::product_stages(p);
     if (few_rows(p)) {
+        const int stages = dgor::row_stages(p);
         // a K x N matrix with a long sum and too few columns for the compute
         // units: parts of at least eight stages, one for each wavefront
         const long long strips = ceil_div(p.N, dgor::skinny_strip(p, true));
         if (!p.trans_b && stages >= kSplitRows && strips < 256) {
             long long want = (256 + strips - 1) / strips;
             want = want < stages / 8 ? want : stages / 8;
-            split(p, want < 32 ? want : 32, w);
+            split(stages, want < 32 ? want : 32, w);
         }
-        w.us = 3.0 + 2.0 * p.nseg * p.K * p.N / kRowsBytes + (w.splits > 1 ? kJoinLaunch : 0.0);
+        w.us = 3.0 + 2.0 * (p.nseg / p.terms) * p.K * p.N / kRowsBytes + (w.splits > 1 ? kJoinLaunch : 0.0);
         return w;
     }
     if (ring) {
@@ -159,11 +162,12 @@ Way choose(const Product &p, bool ring)
     // the plain tile: split until two workgroups a compute unit, keeping at
     // least four stages a part
     w.kernel = Kernel::Tile;
+    const int stages = dgor::product_stages(p);
     const long long n = tiles(p, dgor::kTile, dgor::kTile);
     if (n > 0 && n < 256 && stages >= 8) {
         long long want = 512 / n;
         want = want < stages / 4 ? want : stages / 4;
-        split(p, want < 16 ? want : 16, w);
+        split(stages, want < 16 ? want : 16, w);
     }
     return w;
 }
@@ -285,41 +289,47 @@ hipError_t run_pair(const Product *x, const Product *w, const PairPlan &l, uint8
 // Whether rows are whole units at strides on them.
 bool whole_units(int cols, int ld) { return ld % 8 == 0 && cols % 8 == 0 && ld < (1 << 22); }
 
+// An operand in the workspace or the caller's memory: itself, or its higher
+// term and the lower.
+struct Held {
+    const uint16_t *p, *lo;
+};
+
 // Operands that are copied at the front of the workspace, their rows padded
 // to whole units for the rings: those whose rows or strides are not.  (1000 x
 // 777 by 777 x 1033 on the plain tile, whose loads then fall off dwords: 22
-// us; copied, 5 us, and on the ring 16 together.)
+// us; copied, 5 us, and on the ring 16 together.)  With `open` all, as two
+// bfloat16 terms of a binary16 operand.
 struct Copies {
     dgor::Repack r{};
     size_t at[3] = {}, bytes = 0;
-    bool units = true;   // the operands' rows are whole units, or padded to them
+    bool open = false;
 
     // A stored matrix; returns its index here, -1 where it is used as it is.
     // ld becomes the stride of what the products will read.
     int add(int rows, int cols, int &ld)
     {
-        if (whole_units(cols, ld) || rows == 0 || cols == 0)
+        if ((whole_units(cols, ld) && !open) || rows == 0 || cols == 0)
             return -1;
-        if ((long long)rows * ceil_div(cols, 8) >= (1LL << 30)) {   // a launch's units are counted in 32 bits
-            units = false;
-            return -1;
-        }
         const int i = r.jobs++;
-        r.job[i] = {nullptr, nullptr, rows, cols, ld, (int)round_up((size_t)cols, 8), 0u};
+        r.job[i] = {nullptr, nullptr, nullptr, rows, cols, ld, (int)round_up((size_t)cols, 8), 0};
         at[i] = bytes;
-        bytes += round_up((size_t)rows * r.job[i].ld_to * 2, kWsAlign);
+        bytes += (open ? 2 : 1) * size(i);
         ld = r.job[i].ld_to;
         return i;
     }
     // Marks copy i (or none); returns where the operand will be.
-    const uint16_t *use(int i, const uint16_t *from, uint8_t *ws)
+    Held use(int i, const uint16_t *from, uint8_t *ws)
     {
         if (i < 0)
-            return from;
-        r.job[i].from = from;
-        r.job[i].to = (uint16_t *)(ws + at[i]);
-        return r.job[i].to;
+            return {from, nullptr};
+        dgor::Repack::Job &j = r.job[i];
+        j.from = from;
+        j.to = (uint16_t *)(ws + at[i]);
+        j.lo = open ? (uint16_t *)(ws + at[i] + size(i)) : nullptr;
+        return {j.to, j.lo};
     }
+    size_t size(int i) const { return round_up((size_t)r.job[i].rows * r.job[i].ld_to * 2, kWsAlign); }
     dgor::Repack marked() const
     {
         dgor::Repack q{};
@@ -334,12 +344,12 @@ Product plain_product(int M, int N, int K)
 {
     Product p{};
     p.M = M, p.N = N, p.K = K;
-    p.nseg = p.nbatch = 1;
+    p.nseg = p.nbatch = p.terms = 1;
     return p;
 }
 
 // The three products of a layer with n weights W (1, or 2 for the gated one)
-// of K inputs x N outputs.
+// of K inputs x N outputs; dZ in `terms` (Product).
 Product forward_product(int M, int N, int K, int op_w, int ldx, int ldw, bool gated)
 {
     Product p = plain_product(M, N, K);
@@ -348,21 +358,46 @@ Product forward_product(int M, int N, int K, int op_w, int ldx, int ldw, bool ga
     p.gated = gated;
     return p;
 }
-Product input_gradient_product(int M, int N, int K, int op_w, int lddz, int ldw, int n)   // dX = sum of dZ W^T
+Product input_gradient_product(int M, int N, int K, int op_w, int lddz, int ldw, int n, int terms)   // dX = sum of dZ W^T
 {
     Product p = plain_product(M, K, N);
     p.lda = lddz, p.ldb = ldw;
     p.trans_b = op_w == GEMM_OP_N;
-    p.nseg = n;
+    p.nseg = n * terms;
+    p.terms = terms;
     return p;
 }
-Product weight_gradient_product(int M, int N, int K, int op_w, int ldx, int lddz, int n)   // X^T dZ, or dZ^T X
+Product weight_gradient_product(int M, int N, int K, int op_w, int ldx, int lddz, int n, int terms)   // X^T dZ, or dZ^T X
 {
     Product p = op_w == GEMM_OP_N ? plain_product(K, N, M) : plain_product(N, K, M);
     p.lda = op_w == GEMM_OP_N ? ldx : lddz, p.ldb = op_w == GEMM_OP_N ? lddz : ldx;
     p.trans_a = true;
     p.nbatch = n;
+    p.nseg = p.terms = terms;
     return p;
+}
+
+// One matrix, or two held alike; `low`: which of the pairs takes the lower term.
+dgor::Side side(const Held &a, const Held &b, int low)
+{
+    const auto bytes = [](const uint16_t *from, const uint16_t *to) { return (long long)((uintptr_t)to - (uintptr_t)from); };
+    return {a.p, bytes(a.p, b.p), a.lo ? bytes(a.p, a.lo) : 0, low};
+}
+// The pairs of a backward product: dZ's (A, or B where `swapped`) with the other
+// operand's.
+void set_pairs(Product &p, const dgor::Side &dz, const dgor::Side &other, bool swapped)
+{
+    p.A = swapped ? other : dz;
+    p.B = swapped ? dz : other;
+}
+constexpr int kGradientLow = 1, kOtherLow = 2;   // in Product's order of the terms
+
+// The terms that the gradient of a pre-activation is held in: one where the
+// caller asks for its rounding or it needs none, else two, and the products of
+// binary16 operands, opened into two themselves, have three.
+int gradient_terms(bool bf16, bool exact, int activation)
+{
+    return exact || (activation & GEMM_ROUND_GRADIENT) ? 1 : bf16 ? 2 : 3;
 }
 
 // Whether operands off the units are worth a launch that copies them: not for
@@ -391,7 +426,7 @@ void copy_operands(Product &p, Copies &c, int (&copy)[3])
         int again = ld;
         copy[2] = c.add(rows, cols, again);
     }
-    p.units = c.units;
+    p.units = true;
 }
 
 bool workspace_ok(const void *ws, size_t have, size_t need)
@@ -444,8 +479,9 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
     uint8_t *base = (uint8_t *)ws;
     hipStream_t s = (hipStream_t)stream;
     p.bf16 = bf16;
-    p.A[0] = p.A[1] = c.use(copy[0], X, base);
-    p.B[0] = p.B[1] = c.use(copy[1], W, base);
+    const Held Xs = c.use(copy[0], X, base), Ws = c.use(copy[1], W, base);
+    p.A = side(Xs, Xs, 0);
+    p.B = side(Ws, Ws, 0);
     p.e.Y = Y, p.e.ldy = q->ldy, p.e.y_f32 = q->y_f32 != 0;
     p.e.bias = bias;
     p.e.R = R, p.e.ldr = q->ldr;
@@ -454,19 +490,54 @@ int run_linear(bool bf16, const gemm_linear_params *q, const uint16_t *X, const 
     return done(err == hipSuccess ? run_product(p, l, base + c.bytes, s) : err);
 }
 
-// Workspace of the dense layer's backward pass: copies, dZ, the column sums of
-// each row block, and the partial sums of whichever product is running.
+// Workspace of the dense layer's backward pass: copies, dZ or its two terms, the
+// column sums of each row block, and the partial sums of whichever product is
+// running.
 struct BackwardLayout {
     Copies c;
     PairPlan products;
     int copy_dy, copy_x, copy_w;
-    int lddz;
-    size_t dz, sums, part, bytes;   // offsets, and the whole size
+    int terms, lddz;
+    size_t dz, dz_lo, sums, part, bytes;   // offsets, and the whole size
 };
 
 int row_blocks(int M, int N) { return ceil_div(M, dgor::grad_rows(M, N)); }
 
-int check_linear_backward(const gemm_linear_backward_params *q, Product &px, Product &pw, BackwardLayout &l)
+void lay_out(const gemm_linear_backward_params *q, bool bf16, Product &px, Product &pw, BackwardLayout &l)
+{
+    // slopes of 0 and 1 leave dY's values as they are
+    const int kind = act_of(q->activation);
+    const bool act = kind != GEMM_ACT_NONE, t = q->op_w == GEMM_OP_T;
+    l = BackwardLayout{};
+    l.terms = gradient_terms(bf16, kind <= GEMM_ACT_RELU, q->activation);
+    l.c.open = l.terms == 3;
+    int ldx = q->ldx, ldw = q->ldw;
+    l.lddz = act ? (int)round_up((size_t)q->N, 8) : q->lddy;
+    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1, l.terms);
+    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1, l.terms);
+    const bool for_x = !few_rows(px) && (l.c.open || worth_copies(px)), for_w = l.c.open || worth_copies(pw);
+    l.copy_dy = !act && (for_x || for_w) ? l.c.add(q->M, q->N, l.lddz) : -1;
+    l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
+    l.copy_w = for_x ? l.c.add(t ? q->N : q->K, t ? q->K : q->N, ldw) : -1;
+    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1, l.terms);
+    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1, l.terms);
+    const bool dz_units = act || for_x || for_w || whole_units(q->N, l.lddz);
+    px.opened = l.c.open && for_x;
+    pw.opened = l.c.open;
+    px.units = dz_units && (for_x || (!l.c.open && whole_units(t ? q->K : q->N, ldw)));
+    pw.units = dz_units && (for_w || whole_units(q->K, ldx));
+    const size_t dz_bytes = act ? round_up((size_t)q->M * l.lddz * 2, kWsAlign) : 0;
+    l.dz = l.c.bytes;
+    l.dz_lo = l.dz + dz_bytes;
+    l.sums = l.dz_lo + (l.terms > 1 ? dz_bytes : 0);
+    l.part = l.sums + round_up((size_t)row_blocks(q->M, q->N) * q->N * sizeof(float), kWsAlign);
+    l.products = plan_pair(px, pw);
+    l.bytes = l.part + l.products.part;
+}
+
+// Checks, products and layout of one format, and the workspace's size for either.
+int check_linear_backward(const gemm_linear_backward_params *q, bool bf16, Product &px, Product &pw, BackwardLayout &l,
+                          size_t &bytes)
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
@@ -474,27 +545,15 @@ int check_linear_backward(const gemm_linear_backward_params *q, Product &px, Pro
         return GEMM_ERR_INVALID_DIM;
     if (!op_ok(q->op_w) || !ld_ok(q->lddy, q->N))
         return GEMM_ERR_INVALID_LAYOUT;
-    if (!act_ok(q->activation))
+    if (!act_ok(act_of(q->activation)))
         return GEMM_ERR_INVALID_ACTIVATION;
-    const bool act = q->activation != GEMM_ACT_NONE, t = q->op_w == GEMM_OP_T;
-    int ldx = q->ldx, ldw = q->ldw;
-    l.lddz = act ? (int)round_up((size_t)q->N, 8) : q->lddy;
-    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1);
-    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1);
-    const bool for_x = !few_rows(px) && worth_copies(px), for_w = worth_copies(pw);
-    l.copy_dy = !act && (for_x || for_w) ? l.c.add(q->M, q->N, l.lddz) : -1;
-    l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
-    l.copy_w = for_x ? l.c.add(t ? q->N : q->K, t ? q->K : q->N, ldw) : -1;
-    px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1);
-    pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1);
-    const bool dz_units = act || for_x || for_w || whole_units(q->N, l.lddz);
-    px.units = l.c.units && dz_units && (for_x || whole_units(t ? q->K : q->N, ldw));
-    pw.units = l.c.units && dz_units && (for_w || whole_units(q->K, ldx));
-    l.dz = l.c.bytes;
-    l.sums = l.dz + (act ? round_up((size_t)q->M * l.lddz * 2, kWsAlign) : 0);
-    l.part = l.sums + round_up((size_t)row_blocks(q->M, q->N) * q->N * sizeof(float), kWsAlign);
-    l.products = plan_pair(px, pw);
-    l.bytes = l.part + l.products.part;
+    bytes = 0;
+    if (gradient_terms(false, act_of(q->activation) <= GEMM_ACT_RELU, q->activation) > 1) {   // the formats differ
+        lay_out(q, !bf16, px, pw, l);
+        bytes = l.bytes;
+    }
+    lay_out(q, bf16, px, pw, l);
+    bytes = l.bytes > bytes ? l.bytes : bytes;
     return GEMM_OK;
 }
 
@@ -504,10 +563,12 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
 {
     Product px, pw;
     BackwardLayout l;
-    const int rc = check_linear_backward(q, px, pw, l);
+    size_t need;
+    const int rc = check_linear_backward(q, bf16, px, pw, l, need);
     if (rc != GEMM_OK)
         return rc;
-    const bool act = q->activation != GEMM_ACT_NONE;
+    const int kind = act_of(q->activation);
+    const bool act = kind != GEMM_ACT_NONE;
     const int w_row = q->op_w ? q->K : q->N;
     if ((dX && (!ld_ok(q->ldw, w_row) || !ld_ok(q->lddx, q->K))) ||
         (dW && (!ld_ok(q->ldx, q->K) || !ld_ok(q->lddw, w_row))) || (act && !ld_ok(q->ldp, q->N)))
@@ -515,26 +576,27 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
     if (missing(dY, q->M, q->N) || (act && missing(pre, q->M, q->N)) || (dX && missing(W, q->K, q->N)) ||
         (dW && missing(X, q->M, q->K)))
         return GEMM_ERR_NULL_PTR;
-    if (!workspace_ok(ws, ws_bytes, l.bytes))
+    if (!workspace_ok(ws, ws_bytes, need))
         return GEMM_ERR_WORKSPACE;
     const int dev = dgor::device_status();
     if (dev != GEMM_OK)
         return dev;
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
-    const uint16_t *dZ = dY;
     const int blocks = row_blocks(q->M, q->N);
     float *sums = dbias && blocks != 1 ? (float *)(base + l.sums) : nullptr;
-    px.bf16 = pw.bf16 = bf16;
-    dZ = l.c.use(dX || dW ? l.copy_dy : -1, dZ, base);
-    const uint16_t *Xs = l.c.use(dW ? l.copy_x : -1, X, base), *Ws = l.c.use(dX ? l.copy_w : -1, W, base);
+    px.bf16 = pw.bf16 = bf16 || l.terms > 1;
+    px.e.y_f16 = pw.e.y_f16 = !bf16 && l.terms > 1;
+    Held dZ = l.c.use(dX || dW ? l.copy_dy : -1, dY, base);
+    const Held Xs = l.c.use(dW ? l.copy_x : -1, X, base), Ws = l.c.use(dX ? l.copy_w : -1, W, base);
     hipError_t err;
     if (q->M > 0 && q->N > 0 && ((act && (dX || dW)) || dbias)) {
         uint16_t *out = act && (dX || dW) ? (uint16_t *)(base + l.dz) : nullptr;
-        err = dgor::launch_act_grad(q->M, q->N, dY, q->lddy, act ? pre : nullptr, q->ldp, out, l.lddz, q->activation,
-                                    sums, blocks == 1 ? dbias : nullptr, l.c.marked(), bf16, s);
+        uint16_t *lo = out && l.terms > 1 ? (uint16_t *)(base + l.dz_lo) : nullptr;
+        err = dgor::launch_act_grad(q->M, q->N, dY, q->lddy, act ? pre : nullptr, q->ldp, out, lo, l.lddz, kind, sums,
+                                    blocks == 1 ? dbias : nullptr, l.c.marked(), bf16, s);
         if (out)
-            dZ = out;
+            dZ = {out, lo};
     } else {
         err = dgor::launch_repack(l.c.marked(), s);
     }
@@ -544,14 +606,11 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
     if (err != hipSuccess)
         return GEMM_ERR_LAUNCH;
     if (dX) {
-        px.A[0] = px.A[1] = dZ;
-        px.B[0] = px.B[1] = Ws;
+        set_pairs(px, side(dZ, dZ, kGradientLow), side(Ws, Ws, kOtherLow), false);
         px.e.Y = dX, px.e.ldy = q->lddx;
     }
     if (dW) {
-        const bool t = q->op_w == GEMM_OP_T;
-        pw.A[0] = pw.A[1] = t ? dZ : Xs;
-        pw.B[0] = pw.B[1] = t ? Xs : dZ;
+        set_pairs(pw, side(dZ, dZ, kGradientLow), side(Xs, Xs, kOtherLow), q->op_w == GEMM_OP_N);
         pw.e.Y = dW, pw.e.ldy = q->lddw;
     }
     return done(run_pair(dX ? &px : nullptr, dW ? &pw : nullptr, l.products, base + l.part, s));
@@ -601,25 +660,54 @@ int run_gated(bool bf16, const gemm_gated_params *q, const uint16_t *X, const ui
     uint8_t *base = (uint8_t *)ws;
     hipStream_t s = (hipStream_t)stream;
     p.bf16 = bf16;
-    p.A[0] = p.A[1] = c.use(copy[0], X, base);
-    p.B[0] = c.use(copy[1], Wg, base), p.B[1] = c.use(copy[2], Wu, base);
+    const Held Xs = c.use(copy[0], X, base), Gs = c.use(copy[1], Wg, base), Us = c.use(copy[2], Wu, base);
+    p.A = side(Xs, Xs, 0);
+    p.B = side(Gs, Us, 0);
     p.e.Y = H, p.e.ldy = q->ldh;
     p.e.pre = G, p.e.pre2 = U, p.e.ldp = q->ldp;
     const hipError_t err = dgor::launch_repack(c.marked(), s);
     return done(err == hipSuccess ? run_product(p, l, base + c.bytes, s) : err);
 }
 
-// Workspace of the gated backward pass: copies, dG and dU, then the partial
-// sums of whichever product is running.
+// Workspace of the gated backward pass: copies, dG and dU or their terms, then
+// the partial sums of whichever product is running.
 struct GatedBackwardLayout {
     Copies c;
     PairPlan products;
     int copy_x, copy_wg, copy_wu;
-    int ldd;
-    size_t dg, du, part, bytes;
+    int terms, ldd;
+    size_t d, d_bytes, part, bytes;   // dG, dU and their lower terms, each d_bytes after the one before
 };
 
-int check_gated_backward(const gemm_gated_backward_params *q, Product &px, Product &pw, GatedBackwardLayout &l)
+void lay_out(const gemm_gated_backward_params *q, bool bf16, Product &px, Product &pw, GatedBackwardLayout &l)
+{
+    l = GatedBackwardLayout{};
+    l.terms = gradient_terms(bf16, false, q->activation);
+    l.c.open = l.terms == 3;
+    l.ldd = (int)round_up((size_t)q->F, 8);
+    const bool t = q->op_w == GEMM_OP_T;
+    int ldx = q->ldx, ldw = q->ldw, ldu = q->ldw;
+    px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, ldw, 2, l.terms);
+    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2, l.terms);
+    const bool for_x = !few_rows(px) && (l.c.open || worth_copies(px)), for_w = l.c.open || worth_copies(pw);
+    l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
+    l.copy_wg = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldw) : -1;
+    l.copy_wu = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldu) : -1;
+    px.ldb = ldw;
+    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2, l.terms);
+    px.opened = l.c.open && for_x;
+    pw.opened = l.c.open;
+    px.units = for_x || (!l.c.open && whole_units(t ? q->K : q->F, ldw));
+    pw.units = for_w || whole_units(q->K, ldx);
+    l.d = l.c.bytes;
+    l.d_bytes = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
+    l.part = l.d + (l.terms > 1 ? 4 : 2) * l.d_bytes;
+    l.products = plan_pair(px, pw);
+    l.bytes = l.part + l.products.part;
+}
+
+int check_gated_backward(const gemm_gated_backward_params *q, bool bf16, Product &px, Product &pw,
+                         GatedBackwardLayout &l, size_t &bytes)
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
@@ -627,27 +715,15 @@ int check_gated_backward(const gemm_gated_backward_params *q, Product &px, Produ
         return GEMM_ERR_INVALID_DIM;
     if (!op_ok(q->op_w) || !ld_ok(q->lddh, q->F) || !ld_ok(q->ldp, q->F))
         return GEMM_ERR_INVALID_LAYOUT;
-    if (!act_ok(q->activation))
+    if (!act_ok(act_of(q->activation)))
         return GEMM_ERR_INVALID_ACTIVATION;
-    l.ldd = (int)round_up((size_t)q->F, 8);
-    const bool t = q->op_w == GEMM_OP_T;
-    int ldx = q->ldx, ldw = q->ldw, ldu = q->ldw;
-    px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, ldw, 2);
-    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2);
-    const bool for_x = !few_rows(px) && worth_copies(px), for_w = worth_copies(pw);
-    l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
-    l.copy_wg = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldw) : -1;
-    l.copy_wu = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldu) : -1;
-    px.ldb = ldw;
-    pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2);
-    px.units = l.c.units && (for_x || whole_units(t ? q->K : q->F, ldw));
-    pw.units = l.c.units && (for_w || whole_units(q->K, ldx));
-    const size_t d_bytes = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
-    l.dg = l.c.bytes;
-    l.du = l.dg + d_bytes;
-    l.part = l.du + d_bytes;
-    l.products = plan_pair(px, pw);
-    l.bytes = l.part + l.products.part;
+    bytes = 0;
+    if (gradient_terms(false, false, q->activation) > 1) {   // the formats differ
+        lay_out(q, !bf16, px, pw, l);
+        bytes = l.bytes;
+    }
+    lay_out(q, bf16, px, pw, l);
+    bytes = l.bytes > bytes ? l.bytes : bytes;
     return GEMM_OK;
 }
 
@@ -657,7 +733,8 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
 {
     Product px, pw;
     GatedBackwardLayout l;
-    const int rc = check_gated_backward(q, px, pw, l);
+    size_t need;
+    const int rc = check_gated_backward(q, bf16, px, pw, l, need);
     if (rc != GEMM_OK)
         return rc;
     const int w_row = q->op_w ? q->K : q->F;
@@ -670,32 +747,33 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
         return GEMM_ERR_NULL_PTR;
     if (!dX && !dWg)
         return GEMM_OK;
-    if (!workspace_ok(ws, ws_bytes, l.bytes))
+    if (!workspace_ok(ws, ws_bytes, need))
         return GEMM_ERR_WORKSPACE;
     const int dev = dgor::device_status();
     if (dev != GEMM_OK)
         return dev;
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
-    uint16_t *dG = (uint16_t *)(base + l.dg), *dU = (uint16_t *)(base + l.du);
-    px.bf16 = pw.bf16 = bf16;
-    const uint16_t *Xs = l.c.use(dWg ? l.copy_x : -1, X, base);
-    const uint16_t *Gs = l.c.use(dX ? l.copy_wg : -1, Wg, base), *Us = l.c.use(dX ? l.copy_wu : -1, Wu, base);
+    const auto part = [&](int i) { return (uint16_t *)(base + l.d + i * l.d_bytes); };
+    const bool two = l.terms > 1;
+    const dgor::GateGrads d{{part(0), two ? part(2) : nullptr}, {part(1), two ? part(3) : nullptr}};
+    px.bf16 = pw.bf16 = bf16 || two;
+    px.e.y_f16 = pw.e.y_f16 = !bf16 && two;
+    const Held Xs = l.c.use(dWg ? l.copy_x : -1, X, base);
+    const Held Gs = l.c.use(dX ? l.copy_wg : -1, Wg, base), Us = l.c.use(dX ? l.copy_wu : -1, Wu, base);
     const hipError_t err = q->M > 0 && q->F > 0
-                               ? dgor::launch_gate_grad(q->M, q->F, dH, q->lddh, G, U, q->ldp, dG, dU, l.ldd,
-                                                        q->activation, l.c.marked(), bf16, s)
+                               ? dgor::launch_gate_grad(q->M, q->F, dH, q->lddh, G, U, q->ldp, d, l.ldd,
+                                                        act_of(q->activation), l.c.marked(), bf16, s)
                                : dgor::launch_repack(l.c.marked(), s);
     if (err != hipSuccess)
         return GEMM_ERR_LAUNCH;
+    const dgor::Side dz = side({d.g[0], d.g[1]}, {d.u[0], d.u[1]}, kGradientLow);
     if (dX) {
-        px.A[0] = dG, px.A[1] = dU;
-        px.B[0] = Gs, px.B[1] = Us;
+        set_pairs(px, dz, side(Gs, Us, kOtherLow), false);
         px.e.Y = dX, px.e.ldy = q->lddx;
     }
     if (dWg) {
-        const bool t = q->op_w == GEMM_OP_T;
-        pw.A[0] = t ? dG : Xs, pw.A[1] = t ? dU : Xs;
-        pw.B[0] = t ? Xs : dG, pw.B[1] = t ? Xs : dU;
+        set_pairs(pw, dz, side(Xs, Xs, kOtherLow), q->op_w == GEMM_OP_N);
         pw.e.Y = dWg, pw.Y1 = dWu, pw.e.ldy = q->lddw;
     }
     return done(run_pair(dX ? &px : nullptr, dWg ? &pw : nullptr, l.products, base + l.part, s));
@@ -735,9 +813,10 @@ int gemm_linear_backward_workspace(const gemm_linear_backward_params *params, si
         return GEMM_ERR_NULL_PTR;
     Product px, pw;
     BackwardLayout l;
-    const int rc = check_linear_backward(params, px, pw, l);
+    size_t need;
+    const int rc = check_linear_backward(params, true, px, pw, l, need);
     if (rc == GEMM_OK)
-        *bytes = l.bytes;
+        *bytes = need;
     return rc;
 }
 int gemm_linear_backward_f16(const gemm_linear_backward_params *params, const uint16_t *dY, const uint16_t *X,
@@ -783,9 +862,10 @@ int gemm_gated_backward_workspace(const gemm_gated_backward_params *params, size
         return GEMM_ERR_NULL_PTR;
     Product px, pw;
     GatedBackwardLayout l;
-    const int rc = check_gated_backward(params, px, pw, l);
+    size_t need;
+    const int rc = check_gated_backward(params, true, px, pw, l, need);
     if (rc == GEMM_OK)
-        *bytes = l.bytes;
+        *bytes = need;
     return rc;
 }
 int gemm_gated_backward_f16(const gemm_gated_backward_params *params, const uint16_t *dH, const uint16_t *X,

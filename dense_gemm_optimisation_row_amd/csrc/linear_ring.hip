@@ -112,9 +112,9 @@ __device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bi
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int M = p.M, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;
-    // stages of 32 k; a segment's are a whole number of pairs
+    // stages of 32 k; of several segments each has a whole number of pairs
     const int seg_stages = 2 * ((K + 2 * BK - 1) / (2 * BK));
-    const int total = p.nseg == 2 ? 2 * seg_stages : (K + BK - 1) / BK;
+    const int total = p.nseg > 1 ? p.nseg * seg_stages : (K + BK - 1) / BK;
     const int s0 = p.splits > 1 ? part * p.chunk * 2 : 0;
     const int steps = (p.splits > 1 ? min(s0 + p.chunk * 2, total) : total) - s0;
 
@@ -122,7 +122,9 @@ __device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bi
     const int lhalf = wave >> 1, alid0 = LPA * (wave & 1), blid0 = LPB * (wave & 1);
     const int bcol = GATED ? n0 : n0 + HN * lhalf;            // first column of this wavefront's half of B
     const int b_left = N - bcol;
-    const uint16_t *const B0 = p.B[GATED ? lhalf : batch], *const B1 = p.B[GATED ? lhalf : 1];
+    // the batch's segments, and the one that the sum begins in
+    const int pairs_a = batch * p.nseg, pairs_b = GATED ? lhalf : pairs_a;
+    const int seg0 = p.nseg > 1 ? s0 / seg_stages : 0;
     uint32_t b_off[LPB];
     const int b_kc = 8 * ((lane & 3) ^ (2 * ((lane >> 4) & 1)));
 #pragma unroll
@@ -145,15 +147,17 @@ __device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bi
     // than found anew: a stage's scalar work is between its first MFMAs.
     struct Stream {
         const uint16_t *p;
-        int k_left, until;
+        int k_left, until, seg;
         uint32_t dst;
     };
-    const bool second = p.nseg == 2 && s0 >= seg_stages;
-    const int k_first = BK * (second ? s0 - seg_stages : s0);
-    const int until = p.nseg == 2 && !second ? seg_stages - s0 : 0x7fffffff;
+    const int k_first = BK * (s0 - seg0 * seg_stages);
+    // stages of segment `seg` from its stage `gone` on; the last has no end, its
+    // loads past k read zeros
+    auto stages_of = [&](int seg, int gone) { return seg + 1 < p.nseg ? seg_stages - gone : 0x7fffffff; };
+    const int until = stages_of(seg0, s0 - seg0 * seg_stages);
     const size_t b_row = TB ? (size_t)bcol * ldb : (size_t)bcol;
     const size_t b_step = TB ? 1 : (size_t)ldb;
-    Stream bs{(second ? B1 : B0) + b_row + k_first * b_step, K - k_first, until, 0};
+    Stream bs{p.B.of(pairs_b + seg0, p.terms) + b_row + k_first * b_step, K - k_first, until, seg0, 0};
     auto b_loads = [&]() {
         Loads L;
         L.k_left = bs.k_left;
@@ -167,13 +171,12 @@ __device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bi
         bs.p += BK * b_step;
         bs.k_left -= BK;
         if (--bs.until == 0)
-            bs = Stream{B1 + b_row, K, 0x7fffffff, bs.dst};
+            bs = Stream{p.B.of(pairs_b + bs.seg + 1, p.terms) + b_row, K, stages_of(bs.seg + 1, 0), bs.seg + 1, bs.dst};
         return L;
     };
     auto load_b = [&](const Loads &L, int q) {
         load_to_lds(L.r, L.dst + (uint32_t)(q * 1024), TB && b_kc >= L.k_left ? kOutside : b_off[q]);
     };
-    const uint16_t *const A0 = p.A[batch], *const A1 = p.A[1];
     // A as M x K: a wavefront loads a quarter of the tile's rows, eight a load
     uint32_t a_off[TA ? LPA : 2];
     int a_kc[2] = {0, 0};
@@ -197,7 +200,7 @@ __device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bi
     constexpr int A_DEEP = TA ? BK : 2 * BK;
     const size_t a_row = TA ? (size_t)arow : (size_t)m0 * lda;
     const size_t a_step = TA ? (size_t)lda : 1;
-    Stream as{(second ? A1 : A0) + a_row + k_first * a_step, K - k_first, until, 0};
+    Stream as{p.A.of(pairs_a + seg0, p.terms) + a_row + k_first * a_step, K - k_first, until, seg0, 0};
     auto a_loads = [&]() {
         Loads L;
         L.k_left = as.k_left;
@@ -215,7 +218,7 @@ __device__ __forceinline__ void ring_tile(const Product &p, uint8_t *lds, int bi
         as.k_left -= A_DEEP;
         as.until -= A_DEEP / BK;
         if (as.until == 0)
-            as = Stream{A1 + a_row, K, 0x7fffffff, as.dst};
+            as = Stream{p.A.of(pairs_a + as.seg + 1, p.terms) + a_row, K, stages_of(as.seg + 1, 0), as.seg + 1, as.dst};
         return L;
     };
     auto load_a = [&](const Loads &L, int j) {

@@ -85,9 +85,9 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
     };
     u32x4 ra[UNITS], rb[UNITS];
     auto load_stage = [&](int t) {
-        const int seg = t >= per_seg ? 1 : 0;
+        const int seg = p.nseg > 1 ? t / per_seg : 0, pair = batch * p.nseg + seg;
         const int k0 = (t - seg * per_seg) * BK;
-        const uint16_t *A = p.A[seg | batch];
+        const uint16_t *A = p.A.of(pair, p.terms);
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             const int u = tid + 256 * i;
@@ -98,10 +98,10 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Product p)
             int which;
             if (TB) {
                 const int n = b_col(u / 8, which);
-                rb[i] = load_unit(p.B[GATED ? which : seg | batch], p.ldb, n, N, k0 + 8 * (u % 8), K);
+                rb[i] = load_unit(p.B.of(GATED ? which : pair, p.terms), p.ldb, n, N, k0 + 8 * (u % 8), K);
             } else {
                 const int n = b_col(8 * (u % W), which);
-                rb[i] = load_unit(p.B[GATED ? which : seg | batch], p.ldb, k0 + u / W, K, n, N);
+                rb[i] = load_unit(p.B.of(GATED ? which : pair, p.terms), p.ldb, k0 + u / W, K, n, N);
             }
         }
     };

@@ -24,8 +24,8 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import (ACTIVATIONS, GEMM_OK, GEMM_OP_N, GEMM_OP_T, GatedBackwardParams, GatedParams, GemmError,
-                      LayerNormParams, LinearBackwardParams, LinearParams)
+from .binding import (ACTIVATIONS, GEMM_OK, GEMM_OP_N, GEMM_OP_T, GEMM_ROUND_GRADIENT, GatedBackwardParams, GatedParams,
+                      GemmError, LayerNormParams, LinearBackwardParams, LinearParams)
 
 _KIND = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}
 _functions = {}
@@ -80,6 +80,11 @@ def _activation(name):
         return ACTIVATIONS[name]
     except KeyError:
         raise ValueError(f"unknown activation {name!r}: one of {sorted(ACTIVATIONS)}") from None
+
+
+def _rounded(act, round_gradient):
+    """The activation of a backward pass, flagged where its gradient is rounded."""
+    return act | (GEMM_ROUND_GRADIENT if round_gradient else 0)
 
 
 def _kind16(t, name):
@@ -297,18 +302,25 @@ def _linear_form(x, w, bias, residual, activation, save_pre, out_dtype, y, pre):
 
 
 def linear_backward(dy, x, w, pre=None, activation="none", need_input=True, need_weight=True, need_bias=True,
-                    dx=None, dw=None, dbias=None, workspace=None, stream=None):
+                    dx=None, dw=None, dbias=None, workspace=None, stream=None, round_gradient=False):
     """Gradients ``(dx, dw, dbias)`` of ``linear`` from that of its output (in
     x's type) and its saved ``pre`` (not needed without an activation); None
     for those not needed.  The residual's gradient is dy.  dw has w's shape and
-    storage."""
+    storage.
+
+    The gradient of the pre-activation is held to 2^-17 of its values and with the
+    range of FP32, as two terms, which takes two products' work for dx and dw
+    each, three in float16.  With ``round_gradient`` it is rounded to x's type and
+    takes one: dx and dw are off by about 1.4 times their own rounding, and in
+    float16 a gradient past 65504 becomes infinite, one below 2^-25 zero.  (none
+    and relu need no rounding.)"""
     need_input, need_weight, need_bias = (bool(need_input) or dx is not None, bool(need_weight) or dw is not None,
                                           bool(need_bias) or dbias is not None)
     key = ("linear_backward", dy.shape, dy.stride(), dy.dtype, dy.device, x.shape, x.stride(), x.dtype, x.device,
            w.shape, w.stride(), w.dtype, w.device, _sig(pre), activation, need_input, need_weight, need_bias,
-           _sig(dx), _sig(dw), _sig(dbias))
+           _sig(dx), _sig(dw), _sig(dbias), bool(round_gradient))
     form = _FORMS.get(key) or _keep(key, _linear_backward_form(dy, x, w, pre, activation, need_input, need_weight,
-                                                               need_bias, dx, dw, dbias))
+                                                               need_bias, dx, dw, dbias, round_gradient))
 
     def go(handle):
         dys, xs, pres = dy, x, pre
@@ -324,7 +336,8 @@ def linear_backward(dy, x, w, pre=None, activation="none", need_input=True, need
     return _run(form, stream, (dy, x, w, pre, dx, dw, dbias, workspace), go)
 
 
-def _linear_backward_form(dy, x, w, pre, activation, need_input, need_weight, need_bias, dx, dw, dbias):
+def _linear_backward_form(dy, x, w, pre, activation, need_input, need_weight, need_bias, dx, dw, dbias,
+                          round_gradient):
     _gpu(dy, "dy")
     kind = _kind16(dy, "dy")
     op, ldw = _weight(w, "w", dy)
@@ -340,7 +353,7 @@ def _linear_backward_form(dy, x, w, pre, activation, need_input, need_weight, ne
     lddx = _out(dx, tuple(x.shape), x, "dx") if need_input else 0
     lddw = _grad_stride(w, op, dw, "dw") if need_weight else 0
     _vector(dbias, N, "dbias", dy)
-    params = LinearBackwardParams(M, N, K, op, lddy, ldx, ldw, ldp, lddx, lddw, act)
+    params = LinearBackwardParams(M, N, K, op, lddy, ldx, ldw, ldp, lddx, lddw, _rounded(act, round_gradient))
     copies = [n for n, c in (("dy", copy_dy), ("x", copy_x), ("pre", copy_p)) if c]
     return _Form(dy, "gemm_linear_backward", kind, params, copies=copies, extra=op)
 
@@ -394,17 +407,19 @@ def _gate_weights(wg, wu, like):
 
 
 def gated_backward(dh, x, wg, wu, g, u, activation="silu", need_input=True, need_weight=True, dx=None, dwg=None,
-                   dwu=None, workspace=None, stream=None):
+                   dwu=None, workspace=None, stream=None, round_gradient=False):
     """Gradients ``(dx, dwg, dwu)`` of ``gated`` from that of its output and
-    its saved products g and u; None for those not needed."""
+    its saved products g and u; None for those not needed.  The gradients of g
+    and u are held as ``linear_backward`` holds that of its pre-activation (here
+    under every activation), or rounded with ``round_gradient``."""
     if (dwg is None) != (dwu is None):
         raise ValueError("dwg and dwu are given together or not at all")
     need_input, need_weight = bool(need_input) or dx is not None, bool(need_weight) or dwg is not None
     key = ("gated_backward", dh.shape, dh.stride(), dh.dtype, dh.device, x.shape, x.stride(), x.dtype, x.device,
            wg.shape, wg.stride(), wg.dtype, wg.device, wu.shape, wu.stride(), wu.dtype, wu.device, _sig(g), _sig(u),
-           activation, need_input, need_weight, _sig(dx), _sig(dwg), _sig(dwu))
+           activation, need_input, need_weight, _sig(dx), _sig(dwg), _sig(dwu), bool(round_gradient))
     form = _FORMS.get(key) or _keep(key, _gated_backward_form(dh, x, wg, wu, g, u, activation, need_input,
-                                                              need_weight, dx, dwg, dwu))
+                                                              need_weight, dx, dwg, dwu, round_gradient))
 
     def go(handle):
         dhs, xs, gs, us = dh, x, g, u
@@ -419,7 +434,7 @@ def gated_backward(dh, x, wg, wu, g, u, activation="silu", need_input=True, need
     return _run(form, stream, (dh, x, wg, wu, g, u, dx, dwg, dwu, workspace), go)
 
 
-def _gated_backward_form(dh, x, wg, wu, g, u, activation, need_input, need_weight, dx, dwg, dwu):
+def _gated_backward_form(dh, x, wg, wu, g, u, activation, need_input, need_weight, dx, dwg, dwu, round_gradient):
     _gpu(dh, "dh")
     kind = _kind16(dh, "dh")
     op, ldw = _gate_weights(wg, wu, dh)
@@ -437,7 +452,7 @@ def _gated_backward_form(dh, x, wg, wu, g, u, activation, need_input, need_weigh
         lddw = _grad_stride(wg, op, dwg, "dwg")
         if _grad_stride(wu, op, dwu, "dwu") != lddw:
             raise ValueError("dwg and dwu must have one stride")
-    params = GatedBackwardParams(M, F, K, op, lddh, ldx, ldw, ldp, lddx, lddw, act)
+    params = GatedBackwardParams(M, F, K, op, lddh, ldx, ldw, ldp, lddx, lddw, _rounded(act, round_gradient))
     copies = [n for n, c in (("dh", copy_dh), ("x", copy_x), ("g", copy_g), ("u", copy_u)) if c]
     return _Form(dh, "gemm_gated_backward", kind, params, copies=copies, extra=op)
 

@@ -373,6 +373,18 @@ typedef enum {
     GEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
 } gemm_activation;
 
+/* May be added to the activation of a backward pass.  The gradients dZ (dG, dU)
+ * of the pre-activations are computed in FP32 and enter the products with dX
+ * and dW as sums of two bfloat16 terms: to 2^-17 of each value and with the
+ * range of FP32, at two products' work each, three in binary16 (none and relu,
+ * whose dZ are dY's values or zero, take one).  (An infinite operand or gradient
+ * may there come out as NaN.)  With this flag they are rounded once to the input
+ * format instead, and each product runs once: the relative error of dX and dW
+ * grows by about 1.4 times their own rounding's, and in binary16 a dZ past
+ * 65504 becomes infinite and one below 2^-25 zero, whatever the products would
+ * come to.  dbias is summed from FP32 either way. */
+#define GEMM_ROUND_GRADIENT 0x100
+
 /* Dense layer: Z = X W + bias, Y = act(Z) + R.  X is M x K, W K x N, Y and R
  * M x N; bias (N), R and pre may be NULL.  Y and R are FP32 (y_f32 nonzero)
  * or in X's format; pre, when given, receives Z in X's format, which the
@@ -393,13 +405,13 @@ int gemm_linear_bf16(const gemm_linear_params *params, const uint16_t *X, const 
 /* Its backward pass: dZ = dY act'(Z), dX = dZ W^T, dW = X^T dZ, dbias = the
  * column sums of dZ (R's gradient is dY itself).  Each of dX, dW and dbias
  * may be NULL: it is then not computed.  pre is the forward pass's Z (not
- * read without an activation).  dZ is rounded to the input format for the
- * two products, not for dbias.  W is read for dX only, X for dW only. */
+ * read without an activation).  W is read for dX only, X for dW only.  The
+ * workspace's size serves either format and any of the three outputs. */
 typedef struct {
     int M, N, K;
     int op_w;
     int lddy, ldx, ldw, ldp, lddx, lddw;
-    int activation;
+    int activation;   /* a gemm_activation, with or without GEMM_ROUND_GRADIENT */
 } gemm_linear_backward_params;
 int gemm_linear_backward_workspace(const gemm_linear_backward_params *params, size_t *bytes);
 int gemm_linear_backward_f16(const gemm_linear_backward_params *params, const uint16_t *dY, const uint16_t *X,
@@ -427,12 +439,13 @@ int gemm_gated_bf16(const gemm_gated_params *params, const uint16_t *X, const ui
                     uint16_t *H, uint16_t *G, uint16_t *U, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Its backward pass: dG = dH U act'(G), dU = dH act(G), dX = dG Wg^T + dU
- * Wu^T, dWg = X^T dG, dWu = X^T dU.  dX may be NULL, and dWg and dWu both. */
+ * Wu^T, dWg = X^T dG, dWu = X^T dU.  dX may be NULL, and dWg and dWu both.  dG
+ * and dU are held for the products as dZ is, under every activation. */
 typedef struct {
     int M, F, K;
     int op_w;
     int lddh, ldx, ldw, ldp, lddx, lddw;
-    int activation;
+    int activation;   /* as gemm_linear_backward_params */
 } gemm_gated_backward_params;
 int gemm_gated_backward_workspace(const gemm_gated_backward_params *params, size_t *bytes);
 int gemm_gated_backward_f16(const gemm_gated_backward_params *params, const uint16_t *dH, const uint16_t *X,

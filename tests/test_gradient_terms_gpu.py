@@ -1,0 +1,228 @@
+"""The backward passes' products of a pre-activation's gradient, which is
+computed in FP32 and held as two 16-bit terms: against the formulas in 64 bits,
+with nothing added to the results' own rounding beyond
+
+* 2^-17 of each product's magnitude: a value's two bfloat16 terms leave 2^-9 of
+  2^-9 of it, the product of both lower terms (binary16) is as small and left out;
+* the gradient's own error in FP32 (a slope's 2e-6, and half steps);
+* the sum's, 2^-24 of the magnitudes an addition, `terms` of them a product.
+
+Rounded once to 16 bits, as it is where the caller asks for that, the gradient
+errs by half a step of its type instead.
+"""
+import pytest
+import torch
+
+import dense_gemm_optimisation_row_amd as dg
+from dense_gemm_optimisation_row_amd import binding, build, layers
+from helpers import say
+from layer_reference import act_slope, act_value, gated_grads, linear_grads
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+STEP = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
+ULP = 2.0 ** -24
+TERMS = {torch.float16: 3, torch.bfloat16: 2}
+# rows, outputs, inputs: the few-row kernel (16 to 64 rows, whole and split
+# sums, cut strips), rings of every size, both products in one launch and not
+SHAPES = [(1, 264, 1032), (3, 7, 5), (5, 4096, 72), (30, 2600, 100), (48, 4104, 136), (60, 4096, 200), (64, 520, 256),
+          (77, 131, 520), (520, 264, 1000), (300, 2056, 1000), (1000, 1096, 1032), (2048, 2048, 4096)]
+
+
+@pytest.fixture(scope="module", params=["product", "poisoned"], autouse=True)
+def library(request):
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU (run the CPU suite with -m 'not gpu')")
+    if request.param == "product":
+        yield request.param
+        return
+    lib, load, kept = binding.load(build.POISON_LIB), binding.load, dict(layers._functions)
+    layers._functions.clear()
+    layers._FORMS.clear()
+    binding.load = lambda *a: lib
+    yield request.param
+    binding.load = load
+    layers._functions.clear()
+    layers._FORMS.clear()
+    layers._functions.update(kept)
+
+
+class Make:
+    def __init__(self, seed, dtype):
+        self.g, self.dtype = torch.Generator(device="cuda").manual_seed(seed), dtype
+
+    def normal(self, rows, cols, scale=1.0):
+        return (torch.randn(rows, cols, generator=self.g, device="cuda") * scale).to(self.dtype)
+
+    def ints(self, rows, cols, most):
+        return torch.randint(-most, most + 1, (rows, cols), generator=self.g, device="cuda").to(self.dtype)
+
+    def weight(self, rows, cols, transposed, of=None):
+        of = of or (lambda r, c: self.normal(r, c, rows ** -0.5))
+        return of(cols, rows).t() if transposed else of(rows, cols)
+
+
+def within(got, ref, err, what):
+    tol = err + (ref.abs() + err) * STEP[got.dtype] + TINY[got.dtype]
+    off = (got.double() - ref).abs()
+    assert bool(torch.isfinite(got).all()), f"{what}: not finite"
+    assert bool((off <= tol).all()), f"{what}: worst {float((off / tol).max()):.3g} of the bound"
+
+
+def same(got, ref, what):
+    want = ref.to(got.dtype)
+    assert bool((got == want).all()), f"{what}: {int((got != want).sum())} of {got.numel()} differ"
+
+
+def product_bound(d, e, w, terms):
+    """Of d w summed in FP32, d off by e and then held as terms."""
+    return (e + (d + e) * 2.0 ** -17) @ w + terms * d.shape[1] * ULP * ((d + e) @ w)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["KxN", "NxK"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear_gradients_add_no_rounding(shape, dtype, transposed):
+    M, N, K = shape
+    T = DTYPES[dtype]
+    for act in ("gelu_tanh", "silu"):
+        say("terms linear", shape, dtype, transposed, act)
+        mk = Make(71, T)
+        x, w = mk.normal(M, K), mk.weight(K, N, transposed)
+        dy, pre = mk.normal(M, N), mk.normal(M, N, 3.0)
+        dx, dw, db = dg.linear_backward(dy, x, w, pre=pre, activation=act)
+        X, W, D, Z = x.double(), w.double(), dy.double(), pre.double()
+        want = linear_grads(act, D, X, W, Z)
+        dz = (D * act_slope(act, Z)).abs()
+        e = D.abs() * 2e-6 + 2 * ULP * dz + 2.0 ** -126
+        within(dx, want[0], product_bound(dz, e, W.abs().t(), TERMS[T]), "dx")
+        within(dw, want[1], product_bound(dz.t(), e.t(), X.abs(), TERMS[T]).t(), "dw")
+        within(db, want[2], e.sum(0) + M * ULP * dz.sum(0), "dbias")
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["KxF", "FxK"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_gated_gradients_add_no_rounding(shape, dtype, transposed):
+    M, F, K = shape
+    T = DTYPES[dtype]
+    act = "silu"
+    say("terms gated", shape, dtype, transposed)
+    mk = Make(72, T)
+    x, wg, wu = mk.normal(M, K), mk.weight(K, F, transposed), mk.weight(K, F, transposed)
+    dh, g, u = mk.normal(M, F), mk.normal(M, F), mk.normal(M, F)
+    dx, dwg, dwu = dg.gated_backward(dh, x, wg, wu, g, u, activation=act)
+    X, A, B, D, G, U = (t.double() for t in (x, wg, wu, dh, g, u))
+    want = gated_grads(act, D, X, A, B, G, U)
+    d1, d2 = (D * U * act_slope(act, G)).abs(), (D * act_value(act, G)).abs()
+    e1 = (D * U).abs() * 2e-6 + 3 * ULP * d1 + 2.0 ** -126
+    e2 = D.abs() * 4e-7 * G.abs() + 3 * ULP * d2 + 2.0 ** -126
+    n = TERMS[T]
+    within(dx, want[0], product_bound(torch.cat((d1, d2), 1), torch.cat((e1, e2), 1),
+                                      torch.cat((A.abs().t(), B.abs().t())), n), "dx")
+    within(dwg, want[1], product_bound(d1.t(), e1.t(), X.abs(), n).t(), "dwg")
+    within(dwu, want[2], product_bound(d2.t(), e2.t(), X.abs(), n).t(), "dwu")
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["KxF", "FxK"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_every_pair_of_terms_is_summed(shape, dtype, transposed):
+    """Integers of more bits than a term has on one side, of a term's on the
+    other: no product of two lower terms, so the sums are exact bit for bit."""
+    M, F, K = shape
+    T = DTYPES[dtype]
+    # gradients of 9 to 12 bits, then (binary16) the other operands' 11 bits
+    for wide in ("gradient",) + (("others",) if dtype == "f16" else ()):
+        say("terms exact", shape, dtype, transposed, wide)
+        mk = Make(73, T)
+        if wide == "gradient":
+            dh, g, u = mk.ints(M, F, 40), mk.ints(M, F, 40), mk.ints(M, F, 40)
+            small = 1
+        else:
+            dh, g, u = mk.ints(M, F, 1), mk.ints(M, F, 1), mk.ints(M, F, 1)
+            small = 2000
+        # few nonzero weights and inputs keep the sums below 2^24
+        def sparse(r, c):
+            keep = torch.rand(r, c, generator=mk.g, device="cuda") < 0.25
+            return mk.ints(r, c, small) * keep
+        x, wg, wu = sparse(M, K), mk.weight(K, F, transposed, sparse), mk.weight(K, F, transposed, sparse)
+        want = gated_grads("none", *(t.double() for t in (dh, x, wg, wu, g, u)))
+        got = dg.gated_backward(dh, x, wg, wu, g, u, activation="none")
+        for t, ref, name in zip(got, want, ("dx", "dwg", "dwu")):
+            assert float(ref.abs().max()) < 2 ** 24
+            ok = ref.abs() <= torch.finfo(T).max          # binary16 overflows beyond
+            same(torch.where(ok, t.double(), 0.0).to(T), torch.where(ok, ref, 0.0), name)
+            assert bool((torch.isinf(t) | ok | (ref.abs() < 65520)).all()), name
+
+
+def test_binary16_gradients_keep_the_range_of_their_products():
+    """Gradients past 65504 and far below binary16's smallest, whose products
+    are ordinary values."""
+    T = torch.float16
+    for M, F, K in ((2, 264, 136), (300, 264, 136), (700, 520, 1032)):
+        for size, other in ((2.0 ** 10, 2.0 ** -14), (2.0 ** -14, 2.0 ** 9)):
+            say("range", M, F, K, size)
+            mk = Make(74, T)
+            x, wg, wu = mk.normal(M, K, other), mk.normal(K, F, other), mk.normal(K, F, other)
+            dh, g, u = mk.normal(M, F, size), mk.normal(M, F, 1.0), mk.normal(M, F, size)
+            X, A, B, D, G, U = (t.double() for t in (x, wg, wu, dh, g, u))
+            want = gated_grads("silu", D, X, A, B, G, U)
+            d1, d2 = (D * U * act_slope("silu", G)).abs(), (D * act_value("silu", G)).abs()
+            assert float(d1.max()) > 65504 if size > 1 else float(d1.median()) < 2.0 ** -25
+            e1, e2 = (D * U).abs() * 2e-6 + 3 * ULP * d1, D.abs() * 4e-7 * G.abs() + 3 * ULP * d2
+            got = dg.gated_backward(dh, x, wg, wu, g, u)
+            within(got[0], want[0], product_bound(torch.cat((d1, d2), 1), torch.cat((e1, e2), 1),
+                                                  torch.cat((A.abs().t(), B.abs().t())), 3), "dx")
+            within(got[1], want[1], product_bound(d1.t(), e1.t(), X.abs(), 3).t(), "dwg")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_rounding_the_gradient_is_the_callers_choice(dtype):
+    T = DTYPES[dtype]
+    for M, N, K in ((1, 264, 1032), (48, 520, 264), (520, 264, 1000)):
+        say("rounded", M, N, K, dtype)
+        mk = Make(75, T)
+        x, w, dy, pre = mk.normal(M, K), mk.normal(K, N, K ** -0.5), mk.normal(M, N), mk.normal(M, N, 3.0)
+        X, W, D, Z = x.double(), w.double(), dy.double(), pre.double()
+        want = linear_grads("silu", D, X, W, Z)
+        got = dg.linear_backward(dy, x, w, pre=pre, activation="silu", round_gradient=True)
+        dz = (D * act_slope("silu", Z)).abs()
+        e = D.abs() * 2e-6 + 2 * ULP * dz
+        r = e + (dz + e) * STEP[T] + TINY[T]
+        within(got[0], want[0], r @ W.abs().t() + N * ULP * ((dz + r) @ W.abs().t()), "dx")
+        within(got[1], want[1], X.abs().t() @ r + M * ULP * (X.abs().t() @ (dz + r)), "dw")
+        within(got[2], want[2], e.sum(0) + M * ULP * dz.sum(0), "dbias")
+        # where it needs no rounding both are one
+        for act in ("none", "relu"):
+            a = dg.linear_backward(dy, x, w, pre=pre, activation=act)
+            b = dg.linear_backward(dy, x, w, pre=pre, activation=act, round_gradient=True)
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+        wu, g, u = mk.normal(K, N, K ** -0.5), mk.ints(M, N, 3), mk.ints(M, N, 3)
+        xi, wi, di = mk.ints(M, K, 2), mk.ints(K, N, 2), mk.ints(M, N, 3)
+        got = dg.gated_backward(di, xi, wi, wi, g, u, activation="relu", round_gradient=True)
+        for t, ref in zip(got, gated_grads("relu", *(v.double() for v in (di, xi, wi, wi, g, u)))):
+            same(t, ref, "gated")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_terms_in_a_graph_replay_as_they_run(dtype):
+    T = DTYPES[dtype]
+    mk = Make(76, T)
+    M, F, K = 200, 264, 136
+    x, wg, wu, dh, g, u = (mk.normal(*s) for s in ((M, K), (K, F), (K, F), (M, F), (M, F), (M, F)))
+    dg.gated_backward(dh, x, wg, wu, g, u)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dg.gated_backward(dh, x, wg, wu, g, u)
+    for _ in range(3):
+        for t in (x, wg, wu, dh, g, u):
+            t.copy_(mk.normal(*t.shape))
+        eager = dg.gated_backward(dh, x, wg, wu, g, u)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))
