@@ -88,7 +88,26 @@ class GemmError(RuntimeError):
         super().__init__(f"{where}: {status_string(status)} (status {status})")
 
 
-class ConvParams(ctypes.Structure):
+_MAX_INT = 2 ** 31 - 1
+
+
+def _in_range(**sizes):
+    """Refuses sizes that a C int does not hold: ctypes would cut them off."""
+    for name, v in sizes.items():
+        if not -_MAX_INT <= v <= _MAX_INT:
+            raise ValueError(f"{name} is {v}: sizes and strides are at most 2^31 - 1")
+
+
+class _Params(ctypes.Structure):
+    """A parameter struct of the C ABI, its sizes and strides checked to fit."""
+
+    def __init__(self, *values, **named):
+        given = {**dict(zip((f[0] for f in self._fields_), values)), **named}
+        _in_range(**{f[0]: given[f[0]] for f in self._fields_ if f[1] is ctypes.c_int and f[0] in given})
+        super().__init__(*values, **named)
+
+
+class ConvParams(_Params):
     """gemm_conv2d_params of include/gemm.h."""
     _fields_ = [(n, ctypes.c_int) for n in (
         "N", "C", "H", "W", "K", "R", "S", "stride_h", "stride_w", "pad_h", "pad_w",
@@ -102,31 +121,31 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # g
 GEMM_ROUND_GRADIENT = 0x100   # flag of a backward pass's activation
 
 
-class LinearParams(ctypes.Structure):
+class LinearParams(_Params):
     """gemm_linear_params of include/gemm.h."""
     _fields_ = [(n, ctypes.c_int) for n in (
         "M", "N", "K", "op_w", "ldx", "ldw", "ldy", "ldr", "ldp", "activation", "y_f32")]
 
 
-class LinearBackwardParams(ctypes.Structure):
+class LinearBackwardParams(_Params):
     """gemm_linear_backward_params."""
     _fields_ = [(n, ctypes.c_int) for n in (
         "M", "N", "K", "op_w", "lddy", "ldx", "ldw", "ldp", "lddx", "lddw", "activation")]
 
 
-class GatedParams(ctypes.Structure):
+class GatedParams(_Params):
     """gemm_gated_params."""
     _fields_ = [(n, ctypes.c_int) for n in (
         "M", "F", "K", "op_w", "ldx", "ldw", "ldh", "ldp", "activation")]
 
 
-class GatedBackwardParams(ctypes.Structure):
+class GatedBackwardParams(_Params):
     """gemm_gated_backward_params."""
     _fields_ = [(n, ctypes.c_int) for n in (
         "M", "F", "K", "op_w", "lddh", "ldx", "ldw", "ldp", "lddx", "lddw", "activation")]
 
 
-class LayerNormParams(ctypes.Structure):
+class LayerNormParams(_Params):
     """gemm_layer_norm_params."""
     _fields_ = [(n, ctypes.c_int) for n in ("M", "N", "ldx", "ldy", "lddx", "weight_f32")] + [("eps", ctypes.c_float)]
 
@@ -232,6 +251,7 @@ def raw_gemm(kind, variant: int | None, M: int, N: int, K: int,
     ``kind`` is the input format ("f32", "f16", "bf16", or a bool for f16)."""
     lib = load()
     stem = _STEM[kind_of(kind)]
+    _in_range(M=M, N=N, K=K)
     if variant is None:
         return int(getattr(lib, stem)(M, N, K, A, B, C, stream))
     return int(getattr(lib, stem + "_variant")(variant, M, N, K, A, B, C, stream))
@@ -242,6 +262,7 @@ def raw_gemm_ex(kind, op_a: int, op_b: int, M: int, N: int, K: int, alpha: float
                 C: int | None, ldc: int, stream: int | None) -> int:
     """``gemm_*_ex`` with plain integers; returns the status code."""
     f = getattr(load(), _STEM[kind_of(kind)] + "_ex")
+    _in_range(M=M, N=N, K=K, lda=lda, ldb=ldb, ldc=ldc)
     return int(f(op_a, op_b, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, stream))
 
 
@@ -253,6 +274,7 @@ def plan(kind, M: int, N: int, K: int, variant: int = AUTO,
     """
     lib = load()
     out = Plan()
+    _in_range(M=M, N=N, K=K)
     f = getattr(lib, _STEM[kind_of(kind)] + "_plan")
     rc = f(variant, M, N, K, A or None, B or None, C or None, ctypes.byref(out))
     if rc != GEMM_OK:
@@ -275,6 +297,8 @@ def _check(A, B, C, in_dtype, out_dtype=None):
         raise ValueError("A and B must be contiguous (row-major)")
     M, K = A.shape
     N = B.shape[1]
+    if max(M, N, K) > _MAX_INT:
+        _in_range(M=M, N=N, K=K)
     if C is None:
         C = torch.empty((M, N), dtype=out_dtype, device=A.device)
     elif (tuple(C.shape) != (M, N) or C.dtype != out_dtype or not C.is_contiguous()
@@ -400,17 +424,19 @@ def _call_ex(kind, A, B, C, alpha, beta, stream):
         raise ValueError("A and B must be GPU tensors on one device")
     M, K = A.shape
     N = B.shape[1]
+    op_a, lda = _layout(A, "A")
+    op_b, ldb = _layout(B, "B")
+    _in_range(M=M, N=N, K=K, lda=lda, ldb=ldb)
     if C is None:
         if beta != 0:
             raise ValueError("beta != 0 needs an input C")
         C = torch.empty((M, N), dtype=torch.float32, device=A.device)
     elif tuple(C.shape) != (M, N) or C.dtype != torch.float32 or C.device != A.device:
         raise ValueError("C must be a float32 M x N tensor on A's device")
-    op_a, lda = _layout(A, "A")
-    op_b, ldb = _layout(B, "B")
     op_c, ldc = _layout(C, "C")
     if op_c != GEMM_OP_N:
         raise ValueError("C must have contiguous rows")
+    _in_range(ldc=ldc)
     with torch.cuda.device(A.device):
         rc = raw_gemm_ex(kind, op_a, op_b, M, N, K, float(alpha), _ptr(A), lda, _ptr(B), ldb,
                          float(beta), _ptr(C), ldc, _stream_handle(A.device, stream))
