@@ -562,6 +562,8 @@ __global__ __launch_bounds__(256) void layer_norm_join_kernel(int blocks, int N,
 }
 
 constexpr int kMaxHeld = 16384;   // longest row that a workgroup holds
+// Longest row: a column a step of the long kernels (2048) past it is still an int.
+constexpr int kMaxColumns = 0x7fffffff - 4095;
 constexpr int kUnits = 256;       // compute units
 
 struct NormArgs {
@@ -658,7 +660,7 @@ hipError_t backward(const NormArgs &a, hipStream_t s)
         if (err == hipSuccess && a.sums) {
             hipLaunchKernelGGL((layer_norm_sums_kernel<X>), dim3((a.N + 2047) / 2048, a.blocks), dim3(256), 0, s, a.M,
                                a.N, (const typename X::T *)a.dy, a.lddy, (const typename X::T *)a.x, a.ldx, a.mean,
-                               a.rstd, (a.M + a.blocks - 1) / a.blocks, a.sums);
+                               a.rstd, a.M / a.blocks + (a.M % a.blocks != 0), a.sums);
             err = hipGetLastError();
         }
     }
@@ -685,7 +687,7 @@ int check(const gemm_layer_norm_params *p)
 {
     if (!p)
         return GEMM_ERR_NULL_PTR;
-    if (p->M < 0 || p->N < 0 || !(p->eps >= 0.f))
+    if (p->M < 0 || p->N < 0 || p->N > kMaxColumns || !(p->eps >= 0.f))
         return GEMM_ERR_INVALID_DIM;
     const int least = p->N > 1 ? p->N : 1;
     if (p->ldx < least || p->ldy < least)

@@ -462,7 +462,7 @@ int gemm_gated_backward_bf16(const gemm_gated_backward_params *params, const uin
  *   y = (x - mean) rstd weight + bias.
  * weight and bias (N elements; NULL: ones, zeros) are in x's format, or FP32
  * (weight_f32 nonzero).  mean and rstd (M FP32 values) may be NULL. eps
- * negative or NaN -> GEMM_ERR_INVALID_DIM. */
+ * negative or NaN, or N past 2^31 - 4096 -> GEMM_ERR_INVALID_DIM. */
 typedef struct {
     int M, N;
     int ldx, ldy;       /* rows of x; rows of y, or of dy in the backward pass */

@@ -76,3 +76,19 @@ def test_sizes_past_an_int_are_refused(name):
 def test_the_largest_sizes_of_an_int_still_have_parameters():
     p = binding.LayerNormParams(2 ** 31 - 1, 2, 2, 2, 2, 0, 1e-5)
     assert p.M == 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("stem", ["gemm_layer_norm", "gemm_layer_norm_backward"])
+def test_layer_norm_rows_that_overflow_a_column_are_refused(stem):
+    """The long rows' kernels step 2048 columns past a row's end; the sizes
+    that stay an int are taken (an empty batch launches nothing)."""
+    address, most = 0x1000, 2 ** 31 - 4096
+
+    def call(M, N):
+        params = binding.LayerNormParams(M, N, N, N, N, 0, 1e-5)
+        pointers = [address] * 6 + [None] if stem == "gemm_layer_norm" else \
+            [address] * 6 + [None, None, address, 2 ** 40, None]
+        return binding.raw_layer(stem, "bf16", params, *pointers)
+    for N in (most + 1, 2 ** 31 - 2048, 2 ** 31 - 1):
+        assert call(1, N) == binding.GEMM_ERR_INVALID_DIM
+    assert call(0, most) == 0
