@@ -22,7 +22,7 @@
 namespace dgor {
 namespace {
 
-constexpr int kCols = 256;
+constexpr int kCols = kGradCols;
 
 // Workgroup `group` of a copy: a unit a thread (further units where there are
 // more than the workgroups take at once), read at any alignment, written whole.
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
                                                         const uint16_t *__restrict__ g,
                                                         const uint16_t *__restrict__ u, int ldp,
                                                         GateGrads out, int ldd, int act, Repack also,
-                                                        unsigned groups)
+                                                        unsigned groups, unsigned blocks)
 {
     if (blockIdx.x >= groups) {
         repack(also, blockIdx.x - groups);
@@ -189,44 +189,46 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(int M, int F, const uint
     }
     // a unit a thread, 32 units x 8 rows a workgroup
     const int lane = threadIdx.x & 31, r8 = threadIdx.x >> 5;
-    const int strips = (F + kCols - 1) / kCols;
-    const int col = (int)(blockIdx.x % strips) * kCols + 8 * lane, n = F - col;
-    const int row = (int)(blockIdx.x / strips) * 8 + r8;
-    if (n <= 0 || row >= M)
-        return;
-    u32x4 dv, gv, uv;
-    const size_t at = (size_t)row * ldp + col;
-    if (n >= 8) {
-        dv = load8_16(dh + (size_t)row * lddh + col, 8);
-        gv = load8_16(g + at, 8);
-        uv = load8_16(u + at, 8);
-    } else {
-        dv = load8_16(dh + (size_t)row * lddh + col, n);
-        gv = load8_16(g + at, n);
-        uv = load8_16(u + at, n);
-    }
-    float d[8], x[8], y[8], a[8], b[8];
-    unpack8<Fmt>(dv, d);
-    unpack8<Fmt>(gv, x);
-    unpack8<Fmt>(uv, y);
-    auto apply = [&](int which) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float value, slope;
-            activate_slope(which, x[e], value, slope);
-            a[e] = d[e] * y[e] * slope;
-            b[e] = d[e] * value;
+    const unsigned strips = (unsigned)(F + kCols - 1) / kCols;
+    for (unsigned block = blockIdx.x; block < blocks; block += groups) {
+        const int col = (int)(block % strips) * kCols + 8 * lane, n = F - col;
+        const int row = (int)(block / strips) * 8 + r8;
+        if (n <= 0 || row >= M)
+            continue;
+        u32x4 dv, gv, uv;
+        const size_t at = (size_t)row * ldp + col;
+        if (n >= 8) {
+            dv = load8_16(dh + (size_t)row * lddh + col, 8);
+            gv = load8_16(g + at, 8);
+            uv = load8_16(u + at, 8);
+        } else {
+            dv = load8_16(dh + (size_t)row * lddh + col, n);
+            gv = load8_16(g + at, n);
+            uv = load8_16(u + at, n);
         }
-    };
-    switch (act) {
-    case GEMM_ACT_RELU: apply(GEMM_ACT_RELU); break;
-    case GEMM_ACT_GELU: apply(GEMM_ACT_GELU); break;
-    case GEMM_ACT_GELU_TANH: apply(GEMM_ACT_GELU_TANH); break;
-    case GEMM_ACT_SILU: apply(GEMM_ACT_SILU); break;
-    default: apply(GEMM_ACT_NONE);
+        float d[8], x[8], y[8], a[8], b[8];
+        unpack8<Fmt>(dv, d);
+        unpack8<Fmt>(gv, x);
+        unpack8<Fmt>(uv, y);
+        auto apply = [&](int which) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float value, slope;
+                activate_slope(which, x[e], value, slope);
+                a[e] = d[e] * y[e] * slope;
+                b[e] = d[e] * value;
+            }
+        };
+        switch (act) {
+        case GEMM_ACT_RELU: apply(GEMM_ACT_RELU); break;
+        case GEMM_ACT_GELU: apply(GEMM_ACT_GELU); break;
+        case GEMM_ACT_GELU_TANH: apply(GEMM_ACT_GELU_TANH); break;
+        case GEMM_ACT_SILU: apply(GEMM_ACT_SILU); break;
+        default: apply(GEMM_ACT_NONE);
+        }
+        store_gradient<Fmt>(out.g[0], out.g[1], (size_t)row * ldd + col, a);   // past F zeros
+        store_gradient<Fmt>(out.u[0], out.u[1], (size_t)row * ldd + col, b);
     }
-    store_gradient<Fmt>(out.g[0], out.g[1], (size_t)row * ldd + col, a);   // past F zeros
-    store_gradient<Fmt>(out.u[0], out.u[1], (size_t)row * ldd + col, b);
 }
 
 __global__ __launch_bounds__(256) void repack_kernel(Repack r) { repack(r, blockIdx.x); }
@@ -260,9 +262,8 @@ hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uin
                            hipStream_t s)
 {
     Repack also = q;
-    const int rows = grad_rows(M, N);
-    const unsigned groups = (unsigned)((N + kCols - 1) / kCols) * (unsigned)((M + rows - 1) / rows);
-    const auto kernel = rows == 64 ? (bf16 ? act_grad_kernel<Brain16, 8> : act_grad_kernel<Half16, 8>)
+    const unsigned groups = grad_groups(M, N);
+    const auto kernel = grad_rows(M, N) == 64 ? (bf16 ? act_grad_kernel<Brain16, 8> : act_grad_kernel<Half16, 8>)
                                    : (bf16 ? act_grad_kernel<Brain16, 2> : act_grad_kernel<Half16, 2>);
     hipLaunchKernelGGL(kernel, dim3(groups + repack_groups(also)), dim3(256), 0, s, M, N, dy, lddy, z, ldz, dz,
                        dz_lo, lddz, act, sums, dbias, also, groups);
@@ -280,9 +281,10 @@ hipError_t launch_gate_grad(int M, int F, const uint16_t *dh, int lddh, const ui
                             const GateGrads &d, int ldd, int act, const Repack &q, bool bf16, hipStream_t s)
 {
     Repack also = q;
-    const unsigned groups = (unsigned)((F + kCols - 1) / kCols) * (unsigned)((M + 7) / 8);
+    const unsigned groups = gate_groups(M, F);
     hipLaunchKernelGGL((bf16 ? gate_grad_kernel<Brain16> : gate_grad_kernel<Half16>), dim3(groups + repack_groups(also)),
-                       dim3(256), 0, s, M, F, dh, lddh, g, u, ldp, d, ldd, act, also, groups);
+                       dim3(256), 0, s, M, F, dh, lddh, g, u, ldp, d, ldd, act, also, groups,
+                       gate_blocks(M, F));
     return hipGetLastError();
 }
 

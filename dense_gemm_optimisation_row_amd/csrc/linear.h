@@ -120,6 +120,15 @@ hipError_t launch_join(const Product &p, hipStream_t stream);
 // compute units idle.  dZ is rounded to the input format or, with dz_lo, held
 // as two bfloat16 terms.  The copies `also` ride in the same launch.
 inline int grad_rows(int M, int N) { return (M + 63LL) / 64 * ((N + 255) / 256) >= 1024 ? 64 : 16; }
+constexpr int kGradCols = 256;   // of a workgroup
+inline unsigned grad_groups(int M, int N)
+{
+    return (unsigned)((N + kGradCols - 1LL) / kGradCols) * (unsigned)((M + grad_rows(M, N) - 1LL) / grad_rows(M, N));
+}
+// Workgroups of launch_gate_grad, which take blocks of eight rows: four million
+// at most, and as many turns as the blocks need.
+inline unsigned gate_blocks(int M, int F) { return (unsigned)((F + kGradCols - 1LL) / kGradCols) * (unsigned)((M + 7LL) / 8); }
+inline unsigned gate_groups(int M, int F) { return gate_blocks(M, F) < (1u << 22) ? gate_blocks(M, F) : 1u << 22; }
 hipError_t launch_act_grad(int M, int N, const uint16_t *dy, int lddy, const uint16_t *z, int ldz, uint16_t *dz,
                            uint16_t *dz_lo, int lddz, int act, float *sums, uint16_t *dbias, const Repack &also, bool bf16,
                            hipStream_t stream);

@@ -15,8 +15,12 @@ constexpr size_t kWsAlign = 256;
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// A launch holds 2^32 threads: at most 2^22 tiles of 128 x 64, twice.
-bool too_large(long long rows, long long cols) { return (rows + 127) / 128 * ((cols + 63) / 64) > (1LL << 22); }
+// A launch holds fewer than 2^32 threads.  With fewer than 2^22 blocks of 128 x
+// 64 the smallest tiles, 64 x 32 (gated) or two of 64 x 64 (both weights'
+// gradients), are fewer than 2^24 of 256 threads; kernels that would need more
+// are not chosen.
+constexpr long long kThreads = 1LL << 32;
+bool too_large(long long rows, long long cols) { return (rows + 127) / 128 * ((cols + 63) / 64) >= (1LL << 22); }
 bool ld_ok(int ld, int row) { return ld >= (row > 1 ? row : 1); }
 bool op_ok(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 bool act_ok(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
@@ -42,7 +46,8 @@ long long tiles(const Product &p, int tm, int tn)
 // Whether the few-row kernel takes a product.
 bool few_rows(const Product &p)
 {
-    return !p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows && dgor::spans_a_unit(p) && !p.opened;
+    return !p.trans_a && p.nbatch == 1 && p.M <= dgor::kSkinnyRows && dgor::spans_a_unit(p) && !p.opened &&
+           512LL * ceil_div(p.N, dgor::skinny_strip(p, false)) < kThreads;
 }
 
 // Whether sizes and strides let the rings run (the addresses apart).

@@ -541,23 +541,28 @@ __global__ __launch_bounds__(256) void layer_norm_join_kernel(int blocks, int N,
 {
     __shared__ float part[8][32];
     const int lane = threadIdx.x & 31, b8 = threadIdx.x >> 5;
-    const long long c = (long long)blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (c < 2LL * N)
+    // every thread of the workgroup makes the same turns: more than one where the
+    // grid is at its most
+    for (long long first = (long long)blockIdx.x * 32; first < 2LL * N; first += (long long)gridDim.x * 32) {
+        const long long c = first + lane;
+        float s = 0.f;
+        if (c < 2LL * N)
 #pragma unroll 4
-        for (int b = b8; b < blocks; b += 8)
-            s += sums[(size_t)b * 2 * N + c];
-    part[b8][lane] = s;
-    __syncthreads();
-    if (b8 || c >= 2LL * N)
-        return;
-    s = ((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])) +
-        ((part[4][lane] + part[5][lane]) + (part[6][lane] + part[7][lane]));
-    if (c < N) {
-        if (dweight)
-            dweight[c] = W::down(s);
-    } else if (dbias) {
-        dbias[c - N] = W::down(s);
+            for (int b = b8; b < blocks; b += 8)
+                s += sums[(size_t)b * 2 * N + c];
+        part[b8][lane] = s;
+        __syncthreads();
+        if (b8 == 0 && c < 2LL * N) {
+            s = ((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])) +
+                ((part[4][lane] + part[5][lane]) + (part[6][lane] + part[7][lane]));
+            if (c < N) {
+                if (dweight)
+                    dweight[c] = W::down(s);
+            } else if (dbias) {
+                dbias[c - N] = W::down(s);
+            }
+        }
+        __syncthreads();   // the sums' readers are done
     }
 }
 
@@ -577,9 +582,9 @@ struct NormArgs {
     void *dweight, *dbias;
 };
 
-// A grid's workgroups: one for each row (or four rows) up to a million, whose
-// loops then take the rest.
-unsigned most(long long rows) { return (unsigned)(rows < (1 << 20) ? rows : (1 << 20)); }
+// A grid's workgroups: one for each row (or four rows, or 32 columns) up to a
+// million, whose loops then take the rest.
+unsigned most(long long want) { return (unsigned)(want < (1 << 20) ? want : (1 << 20)); }
 
 template <class X, class W, int RT, int V>
 hipError_t forward_as(const NormArgs &a, hipStream_t s)
@@ -666,8 +671,8 @@ hipError_t backward(const NormArgs &a, hipStream_t s)
     }
     if (err != hipSuccess || !a.sums)
         return err;
-    hipLaunchKernelGGL((layer_norm_join_kernel<W>), dim3((unsigned)((2LL * a.N + 31) / 32)), dim3(256), 0, s, a.blocks,
-                       a.N, a.sums, (typename W::T *)a.dweight, (typename W::T *)a.dbias);
+    hipLaunchKernelGGL((layer_norm_join_kernel<W>), dim3(most((2LL * a.N + 31) / 32)), dim3(256), 0, s, a.blocks, a.N,
+                       a.sums, (typename W::T *)a.dweight, (typename W::T *)a.dbias);
     return hipGetLastError();
 }
 
@@ -763,8 +768,8 @@ int run_backward(Type t, const gemm_layer_norm_params *p, const void *dy, const 
     const hipError_t err = dispatch(t, p->weight_f32 != 0, [&](auto X, auto W) {
         using WT = typename decltype(W)::T;
         if (empty) {
-            hipLaunchKernelGGL((layer_norm_join_kernel<decltype(W)>), dim3((unsigned)((2LL * a.N + 31) / 32)),
-                               dim3(256), 0, (hipStream_t)stream, 0, a.N, a.sums, (WT *)dweight, (WT *)dbias);
+            hipLaunchKernelGGL((layer_norm_join_kernel<decltype(W)>), dim3(most((2LL * a.N + 31) / 32)), dim3(256), 0,
+                               (hipStream_t)stream, 0, a.N, a.sums, (WT *)dweight, (WT *)dbias);
             return hipGetLastError();
         }
         return backward<decltype(X), decltype(W)>(a, (hipStream_t)stream);

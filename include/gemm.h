@@ -358,9 +358,9 @@ int gemm_conv2d_f16_f32acc_noalloc(const gemm_conv2d_params *params, const uint1
  *     call's work completes.
  *   - Results do not depend on timing: sums are added in a fixed order.
  *   - Errors: NULL params or a NULL required pointer of nonzero extent ->
- *     GEMM_ERR_NULL_PTR; a negative size, or a matrix of more than 2^22
- *     blocks of 128 x 64 -> GEMM_ERR_INVALID_DIM; an op flag or stride outside its range
- *     -> GEMM_ERR_INVALID_LAYOUT; an unknown activation ->
+ *     GEMM_ERR_NULL_PTR; a negative size, or a matrix of 2^22 blocks of 128 x
+ *     64 and more -> GEMM_ERR_INVALID_DIM; an op flag or stride outside its
+ *     range -> GEMM_ERR_INVALID_LAYOUT; an unknown activation ->
  *     GEMM_ERR_INVALID_ACTIVATION; a workspace that is missing, misaligned or
  *     too small -> GEMM_ERR_WORKSPACE; otherwise as gemm_f32.  A size of zero
  *     writes what an empty sum gives: nothing, or zeros.
