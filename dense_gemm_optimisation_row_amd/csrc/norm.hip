@@ -688,11 +688,12 @@ hipError_t dispatch(Type t, bool weight_f32, F f)
     return weight_f32 ? f(Short<Brain16>{}, Single{}) : f(Short<Brain16>{}, Short<Brain16>{});
 }
 
+// (eps is the forward pass's)
 int check(const gemm_layer_norm_params *p)
 {
     if (!p)
         return GEMM_ERR_NULL_PTR;
-    if (p->M < 0 || p->N < 0 || p->N > kMaxColumns || !(p->eps >= 0.f))
+    if (p->M < 0 || p->N < 0 || p->N > kMaxColumns)
         return GEMM_ERR_INVALID_DIM;
     const int least = p->N > 1 ? p->N : 1;
     if (p->ldx < least || p->ldy < least)
@@ -720,6 +721,8 @@ int run_forward(Type t, const gemm_layer_norm_params *p, const void *x, const vo
     const int rc = check(p);
     if (rc != GEMM_OK)
         return rc;
+    if (!(p->eps >= 0.f))
+        return GEMM_ERR_INVALID_DIM;
     if (p->M == 0 || p->N == 0)
         return GEMM_OK;
     if (!x || !y)
