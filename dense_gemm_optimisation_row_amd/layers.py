@@ -11,6 +11,11 @@ library itself allocates nothing.  A status other than GEMM_OK raises
 ``GemmError``, a tensor of the wrong shape, type or layout ``ValueError`` or
 ``TypeError`` before anything is launched.
 
+The functions are the passes themselves and record nothing for autograd: a
+tensor that requires grad is refused (``ValueError``) where torch records
+gradients, since theirs would be lost.  Call them under ``torch.no_grad()``, in
+the two halves of an autograd function, or on detached tensors.
+
 A call's checks, C parameters and workspace size depend on its arguments'
 shapes, strides, types and devices only, so they are made once for each such
 form and kept (``_FORMS``, nothing of the tensors themselves): a repeated call
@@ -73,6 +78,15 @@ def _keep(key, form):
 
 def _sig(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _no_grad(*tensors):
+    """Refuses tensors whose gradients the caller expects torch to record."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("a tensor requires grad, which these functions do not record: call them under "
+                                 "torch.no_grad() or on detached tensors, and use the _backward functions")
 
 
 def _activation(name):
@@ -259,6 +273,7 @@ def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, ou
     sums before the activation, in x's type, for ``linear_backward``.  ``y``
     may be the residual itself."""
     save_pre = bool(save_pre) or pre is not None
+    _no_grad(x, w, bias, residual, y, pre)
     key = ("linear", x.shape, x.stride(), x.dtype, x.device, w.shape, w.stride(), w.dtype, w.device, _sig(bias),
            _sig(residual), activation, save_pre, out_dtype, _sig(y), _sig(pre))
     form = _FORMS.get(key) or _keep(key, _linear_form(x, w, bias, residual, activation, save_pre, out_dtype, y, pre))
@@ -314,6 +329,7 @@ def linear_backward(dy, x, w, pre=None, activation="none", need_input=True, need
     takes one: dx and dw are off by about 1.4 times their own rounding, and in
     float16 a gradient past 65504 becomes infinite, one below 2^-25 zero.  (none
     and relu need no rounding.)"""
+    _no_grad(dy, x, w, pre, dx, dw, dbias)
     need_input, need_weight, need_bias = (bool(need_input) or dx is not None, bool(need_weight) or dw is not None,
                                           bool(need_bias) or dbias is not None)
     key = ("linear_backward", dy.shape, dy.stride(), dy.dtype, dy.device, x.shape, x.stride(), x.dtype, x.device,
@@ -366,6 +382,7 @@ def gated(x, wg, wu, activation="silu", save_pre=False, h=None, workspace=None, 
     K x 2F matrix will do), both products in one kernel.  With ``save_pre``
     returns ``(h, g, u)``, the products for ``gated_backward``."""
     save_pre = bool(save_pre)
+    _no_grad(x, wg, wu, h)
     key = ("gated", x.shape, x.stride(), x.dtype, x.device, wg.shape, wg.stride(), wg.dtype, wg.device, wu.shape,
            wu.stride(), wu.dtype, wu.device, activation, save_pre, _sig(h))
     form = _FORMS.get(key) or _keep(key, _gated_form(x, wg, wu, activation, h))
@@ -414,6 +431,7 @@ def gated_backward(dh, x, wg, wu, g, u, activation="silu", need_input=True, need
     under every activation), or rounded with ``round_gradient``."""
     if (dwg is None) != (dwu is None):
         raise ValueError("dwg and dwu are given together or not at all")
+    _no_grad(dh, x, wg, wu, g, u, dx, dwg, dwu)
     need_input, need_weight = bool(need_input) or dx is not None, bool(need_weight) or dwg is not None
     key = ("gated_backward", dh.shape, dh.stride(), dh.dtype, dh.device, x.shape, x.stride(), x.dtype, x.device,
            wg.shape, wg.stride(), wg.dtype, wg.device, wu.shape, wu.stride(), wu.dtype, wu.device, _sig(g), _sig(u),
@@ -474,6 +492,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save_stats=False, y=None, st
     tensor; weight and bias in x's type or float32.  With ``save_stats``
     returns ``(y, mean, rstd)``, the statistics of each row in float32 for
     ``layer_norm_backward``."""
+    _no_grad(x, weight, bias, y)
     key = ("layer_norm", x.shape, x.stride(), x.dtype, x.device, _sig(weight), _sig(bias), eps, _sig(y))
     form = _FORMS.get(key) or _keep(key, _layer_norm_form(x, weight, bias, eps, y))
 
@@ -512,6 +531,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_weight=True, dx=None, dw
     output and its saved statistics; the last two in weight's type (float32
     without one), None unless ``need_weight``."""
     need_weight = bool(need_weight)
+    _no_grad(dy, x, weight, mean, rstd, dx, dweight, dbias)
     key = ("layer_norm_backward", dy.shape, dy.stride(), dy.dtype, dy.device, x.shape, x.stride(), x.dtype, x.device,
            _sig(weight), _sig(mean), _sig(rstd), need_weight, _sig(dx), _sig(dweight), _sig(dbias))
     form = _FORMS.get(key) or _keep(key, _layer_norm_backward_form(dy, x, weight, mean, rstd, need_weight, dx, dweight,
