@@ -1,8 +1,9 @@
 """The dense layers' choice of kernels, on the CPU: what it launches at the
-largest sizes."""
+largest sizes, and that the forms which the GPU tests run are all there are."""
 import pytest
 
 import linear_plan as plan
+from linear_cases import FORMS, line
 from dense_gemm_optimisation_row_amd import binding as b
 
 pytestmark = pytest.mark.skipif(plan.hipcc() is None, reason="needs hipcc")
@@ -47,3 +48,40 @@ def test_launches_hold_fewer_than_2_to_32_threads(rows, cols, over):
         assert status == 0 or (status == b.GEMM_ERR_INVALID_DIM and not launches), (line, status)
         for launch in launches:
             assert 0 <= launch.get("threads", 0) < 2 ** 32, (line, launch)
+
+
+RING = ["256x256", "256x128", "128x128", "128x64", "64x64"]
+
+
+def forms(lines):
+    """(kernel, tile, layout, whether split, matrices summed, terms, batches) of
+    every product that these calls launch."""
+    found = set()
+    for status, _, launches in plan.launches(lines):
+        assert status == 0
+        found |= {(v["kind"], v["tile"], v["layout"], v["splits"] > 1, v["segments"] // v["terms"], v["terms"],
+                   v["batches"]) for v in launches if v["kind"] in ("ring", "pair", "tile")}
+    return found
+
+
+def every_form():
+    for kind, tiles in (("ring", RING), ("pair", RING[2:]), ("tile", ["64x64"])):
+        for tile in tiles:
+            for split in (False, True):
+                if kind != "pair":
+                    for layout in ("gated_KxN", "gated_NxK"):
+                        yield kind, tile, layout, split, 1, 1, 1
+                for terms in (1, 2, 3):
+                    for n in (1, 2):
+                        yield kind, tile, "KxM", split, 1, terms, n
+                        for layout in ("KxN", "NxK"):
+                            yield kind, tile, layout, split, n, terms, 1
+
+
+def test_the_tested_forms_are_all_that_calls_take():
+    # 256 x 128 loads half lines of weights as N x K, and is slower than 256 x 256
+    # or 128 x 128 at every size; the plain tile gets no operands opened into
+    # terms, which are copies at 16 bytes
+    taken = {f for f in every_form() if not (f[1] == "256x128" and f[2].endswith("NxK")) and not
+             (f[0] == "tile" and f[5] == 3)}
+    assert forms([line(c) for c in FORMS]) == taken
