@@ -45,3 +45,27 @@ def layer_norm_grads(dy, x, w, mean, rstd):
     t = dy if w is None else dy * w
     dx = rstd[:, None] * (t - t.mean(1, keepdim=True) - h * (t * h).mean(1, keepdim=True))
     return dx, (dy * h).sum(0), dy.sum(0)
+
+
+# ------------------------------------------------ gradients by differences --
+
+def derivative_bounds(act):
+    """The largest magnitude of an activation's second and third derivatives."""
+    z = torch.linspace(-12, 12, 200001, dtype=torch.float64, requires_grad=True)
+    d, found = act_value(act, z).sum(), []
+    for _ in range(3):
+        d, = torch.autograd.grad(d.sum(), z, create_graph=True)
+        found.append(float(d.detach().abs().max()))
+    return found[1], found[2]
+
+
+def difference_bound(act, dy, z, q, h, sums, step):
+    """How far <gradient, v> may be from the central difference of <dy, act(z)>
+    with the step h, where z moves by q along v: the third derivative's h^2 / 6
+    q^3; the errors of two evaluations, `sums` each and 4e-7 |act(z)| with the
+    activation's, over 2 h; and the slope at z rounded to 16 bits, half a step
+    `step` of it."""
+    second, third = derivative_bounds(act)
+    wide = z.abs() + h * q.abs()
+    each = h * h / 6 * third * q.abs() ** 3 + (1.13 * sums + 4e-7 * wide) / h + second * step * z.abs() * q.abs()
+    return float((dy.abs() * each).sum())
