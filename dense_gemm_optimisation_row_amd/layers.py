@@ -80,13 +80,11 @@ def _sig(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
 
 
-def _no_grad(*tensors):
-    """Refuses tensors whose gradients the caller expects torch to record."""
+def _grad_unless_off():
+    """Refuses a call on tensors that require grad, where torch would record it."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("a tensor requires grad, which these functions do not record: call them under "
-                                 "torch.no_grad() or on detached tensors, and use the _backward functions")
+        raise ValueError("a tensor requires grad, which these functions do not record: call them under "
+                         "torch.no_grad() or on detached tensors, and use the _backward functions")
 
 
 def _activation(name):
@@ -233,7 +231,7 @@ def _on(device, stream, tensors):
 
 def _run(form, stream, tensors, go):
     """go(handle of the call's stream), with the device and stream current."""
-    if stream is None and form.index == torch.cuda.current_device():
+    if stream is None and form.index == torch._C._cuda_getDevice():   # (there are GPU tensors: torch has its GPU)
         return go(torch._C._cuda_getCurrentRawStream(form.index))
     with _on(form.device, stream, tensors) as handle:
         return go(handle)
@@ -273,7 +271,9 @@ def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, ou
     sums before the activation, in x's type, for ``linear_backward``.  ``y``
     may be the residual itself."""
     save_pre = bool(save_pre) or pre is not None
-    _no_grad(x, w, bias, residual, y, pre)
+    if x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or \
+            (residual is not None and residual.requires_grad):
+        _grad_unless_off()
     key = ("linear", x.shape, x.stride(), x.dtype, x.device, w.shape, w.stride(), w.dtype, w.device, _sig(bias),
            _sig(residual), activation, save_pre, out_dtype, _sig(y), _sig(pre))
     form = _FORMS.get(key) or _keep(key, _linear_form(x, w, bias, residual, activation, save_pre, out_dtype, y, pre))
@@ -329,7 +329,8 @@ def linear_backward(dy, x, w, pre=None, activation="none", need_input=True, need
     takes one: dx and dw are off by about 1.4 times their own rounding, and in
     float16 a gradient past 65504 becomes infinite, one below 2^-25 zero.  (none
     and relu need no rounding.)"""
-    _no_grad(dy, x, w, pre, dx, dw, dbias)
+    if dy.requires_grad or x.requires_grad or w.requires_grad or (pre is not None and pre.requires_grad):
+        _grad_unless_off()
     need_input, need_weight, need_bias = (bool(need_input) or dx is not None, bool(need_weight) or dw is not None,
                                           bool(need_bias) or dbias is not None)
     key = ("linear_backward", dy.shape, dy.stride(), dy.dtype, dy.device, x.shape, x.stride(), x.dtype, x.device,
@@ -382,7 +383,8 @@ def gated(x, wg, wu, activation="silu", save_pre=False, h=None, workspace=None, 
     K x 2F matrix will do), both products in one kernel.  With ``save_pre``
     returns ``(h, g, u)``, the products for ``gated_backward``."""
     save_pre = bool(save_pre)
-    _no_grad(x, wg, wu, h)
+    if x.requires_grad or wg.requires_grad or wu.requires_grad:
+        _grad_unless_off()
     key = ("gated", x.shape, x.stride(), x.dtype, x.device, wg.shape, wg.stride(), wg.dtype, wg.device, wu.shape,
            wu.stride(), wu.dtype, wu.device, activation, save_pre, _sig(h))
     form = _FORMS.get(key) or _keep(key, _gated_form(x, wg, wu, activation, h))
@@ -431,7 +433,9 @@ def gated_backward(dh, x, wg, wu, g, u, activation="silu", need_input=True, need
     under every activation), or rounded with ``round_gradient``."""
     if (dwg is None) != (dwu is None):
         raise ValueError("dwg and dwu are given together or not at all")
-    _no_grad(dh, x, wg, wu, g, u, dx, dwg, dwu)
+    if dh.requires_grad or x.requires_grad or wg.requires_grad or wu.requires_grad or g.requires_grad or \
+            u.requires_grad:
+        _grad_unless_off()
     need_input, need_weight = bool(need_input) or dx is not None, bool(need_weight) or dwg is not None
     key = ("gated_backward", dh.shape, dh.stride(), dh.dtype, dh.device, x.shape, x.stride(), x.dtype, x.device,
            wg.shape, wg.stride(), wg.dtype, wg.device, wu.shape, wu.stride(), wu.dtype, wu.device, _sig(g), _sig(u),
@@ -492,7 +496,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save_stats=False, y=None, st
     tensor; weight and bias in x's type or float32.  With ``save_stats``
     returns ``(y, mean, rstd)``, the statistics of each row in float32 for
     ``layer_norm_backward``."""
-    _no_grad(x, weight, bias, y)
+    if x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad):
+        _grad_unless_off()
     key = ("layer_norm", x.shape, x.stride(), x.dtype, x.device, _sig(weight), _sig(bias), eps, _sig(y))
     form = _FORMS.get(key) or _keep(key, _layer_norm_form(x, weight, bias, eps, y))
 
@@ -531,7 +536,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_weight=True, dx=None, dw
     output and its saved statistics; the last two in weight's type (float32
     without one), None unless ``need_weight``."""
     need_weight = bool(need_weight)
-    _no_grad(dy, x, weight, mean, rstd, dx, dweight, dbias)
+    if dy.requires_grad or x.requires_grad or (weight is not None and weight.requires_grad) or mean.requires_grad or \
+            rstd.requires_grad:
+        _grad_unless_off()
     key = ("layer_norm_backward", dy.shape, dy.stride(), dy.dtype, dy.device, x.shape, x.stride(), x.dtype, x.device,
            _sig(weight), _sig(mean), _sig(rstd), need_weight, _sig(dx), _sig(dweight), _sig(dbias))
     form = _FORMS.get(key) or _keep(key, _layer_norm_backward_form(dy, x, weight, mean, rstd, need_weight, dx, dweight,
