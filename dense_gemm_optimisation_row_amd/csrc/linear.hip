@@ -93,6 +93,7 @@ constexpr RingCost kRings[] = {
     {dgor::kRing128x64, 2, 4.8, 0.243, 6.2, 0.33, 1.12},
     {dgor::kRing64, 2, 4.0, 0.158, 4.2, 0.243, 1.08},
 };
+constexpr int kRingTiles = sizeof(kRings) / sizeof(kRings[0]);
 constexpr int kSplitRows = 40;   // stages of 64 k from which few rows' sums over a K x N matrix are split
 constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
 // Weights that the few-row kernel reads in a microsecond, past 3 us: 33.5 MB
@@ -113,10 +114,10 @@ RingTimes times(const Product &p, const RingCost &c, int parts)
     return {c.ends + stages * c.alone + act, c.ends_full + stages * c.full + act * c.share,
             parts > 1 ? kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes : 0.0};
 }
-double microseconds(const Product &p, const RingCost &c, int parts)
+double microseconds(const Product &p, const RingCost &c, long long n, int parts)   // n tiles
 {
-    const long long n = tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile)) * parts;
-    const long long rounds = n / (256LL * c.share), rest = n % (256LL * c.share);
+    const unsigned long long groups = (unsigned long long)n * parts;
+    const unsigned long long rounds = groups / (256u * c.share), rest = groups % (256u * c.share);
     const RingTimes t = times(p, c, parts);
     return rounds * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full) + t.join;
 }
@@ -132,7 +133,7 @@ Way best_on(const Product &p, const RingCost &c)
     for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
         if (parts > 1 && (2 * parts > stages || n * parts > 512 * c.share))
             break;
-        const double t = microseconds(p, c, parts);
+        const double t = microseconds(p, c, n, parts);
         if (parts == 1 || t < w.us)
             w.us = t, best = parts;
     }
@@ -140,7 +141,13 @@ Way best_on(const Product &p, const RingCost &c)
     return w;
 }
 
-Way choose(const Product &p, bool ring)
+// The best on each tile, of kRings' order; found once a plan.
+struct RingWays {
+    Way on[kRingTiles];
+};
+
+// `ways`: a product's on the rings, null off them.
+Way choose(const Product &p, const RingWays *ways)
 {
     Way w{Kernel::Rows, dgor::kRing64, 1, 0, 0};
     if (few_rows(p)) {
@@ -156,12 +163,10 @@ Way choose(const Product &p, bool ring)
         w.us = 3.0 + 2.0 * (p.nseg / p.terms) * p.K * p.N / kRowsBytes + (w.splits > 1 ? kJoinLaunch : 0.0);
         return w;
     }
-    if (ring) {
-        for (const RingCost &c : kRings) {
-            const Way v = best_on(p, c);
+    if (ways) {
+        for (const Way &v : ways->on)
             if (w.kernel != Kernel::Ring || v.us < w.us)
                 w = v;
-        }
         return w;
     }
     // the plain tile: split until two workgroups a compute unit, keeping at
@@ -183,16 +188,31 @@ struct Plan {
     Way off, ring;
     size_t part;
 };
-Plan plan(const Product &p)
+RingWays ring_ways(const Product &p)
+{
+    RingWays w;
+    for (int i = 0; i < kRingTiles; ++i)
+        w.on[i] = best_on(p, kRings[i]);
+    return w;
+}
+Plan plan(const Product &p, const RingWays *ways)   // null: its strides are not the rings'
 {
     const auto bytes = [&](const Way &w) {
         return w.splits <= 1 ? 0 : (size_t)(p.gated ? 2 : p.nbatch) * w.splits * dgor::part_size(p) * sizeof(float);
     };
     Plan l;
-    l.off = choose(p, false);
-    l.ring = ring_sizes(p) ? choose(p, true) : l.off;
+    l.off = choose(p, nullptr);
+    l.ring = ways ? choose(p, ways) : l.off;
     l.part = round_up(bytes(l.off) > bytes(l.ring) ? bytes(l.off) : bytes(l.ring), kWsAlign);
     return l;
+}
+
+Plan plan(const Product &p)
+{
+    if (!ring_sizes(p) || few_rows(p))
+        return plan(p, nullptr);
+    const RingWays w = ring_ways(p);
+    return plan(p, &w);
 }
 
 hipError_t join(const Product &p, hipStream_t s) { return p.splits > 1 ? dgor::launch_join(p, s) : hipSuccess; }
@@ -237,17 +257,20 @@ constexpr double kLaunch = 3.0;   // a launch: its gap on the GPU, or the host's
 PairPlan plan_pair(const Product &x, const Product &w)
 {
     PairPlan l{};
-    l.x = plan(x);
-    l.w = plan(w);
+    const bool rings_x = ring_sizes(x), rings_w = ring_sizes(w);
+    const RingWays wx = rings_x ? ring_ways(x) : RingWays{}, ww = rings_w ? ring_ways(w) : RingWays{};
+    l.x = plan(x, rings_x ? &wx : nullptr);
+    l.w = plan(w, rings_w ? &ww : nullptr);
     l.part = l.x.part > l.w.part ? l.x.part : l.w.part;
-    if (!ring_sizes(x) || !ring_sizes(w) || l.x.ring.kernel == Kernel::Tile || l.w.ring.kernel != Kernel::Ring ||
+    if (!rings_x || !rings_w || l.x.ring.kernel == Kernel::Tile || l.w.ring.kernel != Kernel::Ring ||
         x.M == 0 || x.N == 0 || w.M == 0 || w.N == 0)
         return l;
     double best = l.x.ring.us + l.w.ring.us + kLaunch;
-    for (const RingCost &c : kRings) {
+    for (int i = 0; i < kRingTiles; ++i) {
+        const RingCost &c = kRings[i];
         if (ring_tile_m(c.tile) == 256)
             continue;
-        const Way a = best_on(x, c), b = best_on(w, c);
+        const Way &a = wx.on[i], &b = ww.on[i];
         const RingTimes ta = times(x, c, a.splits), tb = times(w, c, b.splits);
         const double na = (double)tiles(x, ring_tile_m(c.tile), ring_tile_n(c.tile)) * a.splits;
         const double nb = (double)tiles(w, ring_tile_m(c.tile), ring_tile_n(c.tile)) * b.splits;
