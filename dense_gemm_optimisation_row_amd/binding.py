@@ -118,7 +118,9 @@ _CONV_STEM = {"f32": "gemm_conv2d_f32", "f16": "gemm_conv2d_f16_f32acc", "bf16":
 
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # gemm_activation
-GEMM_ROUND_GRADIENT = 0x100   # flag of a backward pass's activation
+# flags of a backward pass's activation
+GEMM_ROUND_GRADIENT, GEMM_ONLY_F16, GEMM_ONLY_BF16 = 0x100, 0x200, 0x400
+GEMM_NO_INPUT_GRADIENT, GEMM_NO_WEIGHT_GRADIENT = 0x800, 0x1000
 
 
 class LinearParams(_Params):

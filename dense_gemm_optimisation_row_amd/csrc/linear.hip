@@ -24,8 +24,12 @@ bool too_large(long long rows, long long cols) { return (rows + 127) / 128 * ((c
 bool ld_ok(int ld, int row) { return ld >= (row > 1 ? row : 1); }
 bool op_ok(int op) { return op == GEMM_OP_N || op == GEMM_OP_T; }
 bool act_ok(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
-// The backward passes' activation carries a flag.
-int act_of(int activation) { return activation & ~GEMM_ROUND_GRADIENT; }
+// The backward passes' activation carries flags.
+constexpr int kFlags = GEMM_ROUND_GRADIENT | GEMM_ONLY_F16 | GEMM_ONLY_BF16 | GEMM_NO_INPUT_GRADIENT | GEMM_NO_WEIGHT_GRADIENT;
+int act_of(int activation) { return activation & ~kFlags; }
+bool wants_input(int activation) { return !(activation & GEMM_NO_INPUT_GRADIENT); }
+bool wants_weight(int activation) { return !(activation & GEMM_NO_WEIGHT_GRADIENT); }
+bool takes(bool bf16, int activation) { return !(activation & (bf16 ? GEMM_ONLY_F16 : GEMM_ONLY_BF16)); }
 bool missing(const void *p, long long rows, long long cols) { return rows > 0 && cols > 0 && !p; }
 
 // How a product runs: the kernel, a ring's tile and, where its tiles leave
@@ -254,9 +258,17 @@ struct PairPlan {
 };
 constexpr double kLaunch = 3.0;   // a launch: its gap on the GPU, or the host's time for it
 
-PairPlan plan_pair(const Product &x, const Product &w)
+PairPlan plan_pair(const Product &x, const Product &w, bool want_x, bool want_w)
 {
     PairPlan l{};
+    if (!want_x || !want_w) {
+        if (want_x)
+            l.x = plan(x);
+        if (want_w)
+            l.w = plan(w);
+        l.part = want_x ? l.x.part : (want_w ? l.w.part : 0);
+        return l;
+    }
     const bool rings_x = ring_sizes(x), rings_w = ring_sizes(w);
     const RingWays wx = rings_x ? ring_ways(x) : RingWays{}, ww = rings_w ? ring_ways(w) : RingWays{};
     l.x = plan(x, rings_x ? &wx : nullptr);
@@ -536,6 +548,7 @@ void lay_out(const gemm_linear_backward_params *q, bool bf16, Product &px, Produ
     // slopes of 0 and 1 leave dY's values as they are
     const int kind = act_of(q->activation);
     const bool act = kind != GEMM_ACT_NONE, t = q->op_w == GEMM_OP_T;
+    const bool want_x = wants_input(q->activation), want_w = wants_weight(q->activation);
     l = BackwardLayout{};
     l.terms = gradient_terms(bf16, kind <= GEMM_ACT_RELU, q->activation);
     l.c.open = l.terms == 3;
@@ -543,7 +556,8 @@ void lay_out(const gemm_linear_backward_params *q, bool bf16, Product &px, Produ
     l.lddz = act ? (int)round_up((size_t)q->N, 8) : q->lddy;
     px = input_gradient_product(q->M, q->N, q->K, q->op_w, l.lddz, ldw, 1, l.terms);
     pw = weight_gradient_product(q->M, q->N, q->K, q->op_w, ldx, l.lddz, 1, l.terms);
-    const bool for_x = !few_rows(px) && (l.c.open || worth_copies(px)), for_w = l.c.open || worth_copies(pw);
+    const bool for_x = want_x && !few_rows(px) && (l.c.open || worth_copies(px));
+    const bool for_w = want_w && (l.c.open || worth_copies(pw));
     l.copy_dy = !act && (for_x || for_w) ? l.c.add(q->M, q->N, l.lddz) : -1;
     l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
     l.copy_w = for_x ? l.c.add(t ? q->N : q->K, t ? q->K : q->N, ldw) : -1;
@@ -554,16 +568,17 @@ void lay_out(const gemm_linear_backward_params *q, bool bf16, Product &px, Produ
     pw.opened = l.c.open;
     px.units = dz_units && (for_x || (!l.c.open && whole_units(t ? q->K : q->N, ldw)));
     pw.units = dz_units && (for_w || whole_units(q->K, ldx));
-    const size_t dz_bytes = act ? round_up((size_t)q->M * l.lddz * 2, kWsAlign) : 0;
+    const size_t dz_bytes = act && (want_x || want_w) ? round_up((size_t)q->M * l.lddz * 2, kWsAlign) : 0;
     l.dz = l.c.bytes;
     l.dz_lo = l.dz + dz_bytes;
     l.sums = l.dz_lo + (l.terms > 1 ? dz_bytes : 0);
     l.part = l.sums + round_up((size_t)row_blocks(q->M, q->N) * q->N * sizeof(float), kWsAlign);
-    l.products = plan_pair(px, pw);
+    l.products = plan_pair(px, pw, want_x, want_w);
     l.bytes = l.part + l.products.part;
 }
 
-// Checks, products and layout of one format, and the workspace's size for either.
+// Checks, products and layout of one format, and the workspace's size for
+// either, or for the one that the flags name.
 int check_linear_backward(const gemm_linear_backward_params *q, bool bf16, Product &px, Product &pw, BackwardLayout &l,
                           size_t &bytes)
 {
@@ -576,7 +591,8 @@ int check_linear_backward(const gemm_linear_backward_params *q, bool bf16, Produ
     if (!act_ok(act_of(q->activation)))
         return GEMM_ERR_INVALID_ACTIVATION;
     bytes = 0;
-    if (gradient_terms(false, act_of(q->activation) <= GEMM_ACT_RELU, q->activation) > 1) {   // the formats differ
+    // where the formats differ
+    if (takes(!bf16, q->activation) && gradient_terms(false, act_of(q->activation) <= GEMM_ACT_RELU, q->activation) > 1) {
         lay_out(q, !bf16, px, pw, l);
         bytes = l.bytes;
     }
@@ -595,6 +611,8 @@ int run_linear_backward(bool bf16, const gemm_linear_backward_params *q, const u
     const int rc = check_linear_backward(q, bf16, px, pw, l, need);
     if (rc != GEMM_OK)
         return rc;
+    if (!takes(bf16, q->activation) || (dX && !wants_input(q->activation)) || (dW && !wants_weight(q->activation)))
+        return GEMM_ERR_INVALID_ACTIVATION;
     const int kind = act_of(q->activation);
     const bool act = kind != GEMM_ACT_NONE;
     const int w_row = q->op_w ? q->K : q->N;
@@ -714,10 +732,12 @@ void lay_out(const gemm_gated_backward_params *q, bool bf16, Product &px, Produc
     l.c.open = l.terms == 3;
     l.ldd = (int)round_up((size_t)q->F, 8);
     const bool t = q->op_w == GEMM_OP_T;
+    const bool want_x = wants_input(q->activation), want_w = wants_weight(q->activation);
     int ldx = q->ldx, ldw = q->ldw, ldu = q->ldw;
     px = input_gradient_product(q->M, q->F, q->K, q->op_w, l.ldd, ldw, 2, l.terms);
     pw = weight_gradient_product(q->M, q->F, q->K, q->op_w, ldx, l.ldd, 2, l.terms);
-    const bool for_x = !few_rows(px) && (l.c.open || worth_copies(px)), for_w = l.c.open || worth_copies(pw);
+    const bool for_x = want_x && !few_rows(px) && (l.c.open || worth_copies(px));
+    const bool for_w = want_w && (l.c.open || worth_copies(pw));
     l.copy_x = for_w ? l.c.add(q->M, q->K, ldx) : -1;
     l.copy_wg = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldw) : -1;
     l.copy_wu = for_x ? l.c.add(t ? q->F : q->K, t ? q->K : q->F, ldu) : -1;
@@ -730,8 +750,8 @@ void lay_out(const gemm_gated_backward_params *q, bool bf16, Product &px, Produc
     l.d = l.c.bytes;
     l.d_bytes = round_up((size_t)q->M * l.ldd * 2, kWsAlign);
     l.part = l.d + (l.terms > 1 ? 4 : 2) * l.d_bytes;
-    l.products = plan_pair(px, pw);
-    l.bytes = l.part + l.products.part;
+    l.products = plan_pair(px, pw, want_x, want_w);
+    l.bytes = want_x || want_w ? l.part + l.products.part : 0;
 }
 
 int check_gated_backward(const gemm_gated_backward_params *q, bool bf16, Product &px, Product &pw,
@@ -746,7 +766,7 @@ int check_gated_backward(const gemm_gated_backward_params *q, bool bf16, Product
     if (!act_ok(act_of(q->activation)))
         return GEMM_ERR_INVALID_ACTIVATION;
     bytes = 0;
-    if (gradient_terms(false, false, q->activation) > 1) {   // the formats differ
+    if (takes(!bf16, q->activation) && gradient_terms(false, false, q->activation) > 1) {   // the formats differ
         lay_out(q, !bf16, px, pw, l);
         bytes = l.bytes;
     }
@@ -765,6 +785,8 @@ int run_gated_backward(bool bf16, const gemm_gated_backward_params *q, const uin
     const int rc = check_gated_backward(q, bf16, px, pw, l, need);
     if (rc != GEMM_OK)
         return rc;
+    if (!takes(bf16, q->activation) || (dX && !wants_input(q->activation)) || (dWg && !wants_weight(q->activation)))
+        return GEMM_ERR_INVALID_ACTIVATION;
     const int w_row = q->op_w ? q->K : q->F;
     if ((dX && (!ld_ok(q->ldw, w_row) || !ld_ok(q->lddx, q->K))) ||
         (dWg && (!ld_ok(q->ldx, q->K) || !ld_ok(q->lddw, w_row))))
@@ -842,7 +864,7 @@ int gemm_linear_backward_workspace(const gemm_linear_backward_params *params, si
     Product px, pw;
     BackwardLayout l;
     size_t need;
-    const int rc = check_linear_backward(params, true, px, pw, l, need);
+    const int rc = check_linear_backward(params, !params || takes(true, params->activation), px, pw, l, need);
     if (rc == GEMM_OK)
         *bytes = need;
     return rc;
@@ -891,7 +913,7 @@ int gemm_gated_backward_workspace(const gemm_gated_backward_params *params, size
     Product px, pw;
     GatedBackwardLayout l;
     size_t need;
-    const int rc = check_gated_backward(params, true, px, pw, l, need);
+    const int rc = check_gated_backward(params, !params || takes(true, params->activation), px, pw, l, need);
     if (rc == GEMM_OK)
         *bytes = need;
     return rc;

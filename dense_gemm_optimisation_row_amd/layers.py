@@ -29,7 +29,8 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import (ACTIVATIONS, GEMM_OK, GEMM_OP_N, GEMM_OP_T, GEMM_ROUND_GRADIENT, GatedBackwardParams, GatedParams,
+from .binding import (ACTIVATIONS, GEMM_OK, GEMM_NO_INPUT_GRADIENT, GEMM_NO_WEIGHT_GRADIENT, GEMM_ONLY_BF16,
+                      GEMM_ONLY_F16, GEMM_OP_N, GEMM_OP_T, GEMM_ROUND_GRADIENT, GatedBackwardParams, GatedParams,
                       GemmError, LayerNormParams, LinearBackwardParams, LinearParams)
 
 _KIND = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}
@@ -94,9 +95,10 @@ def _activation(name):
         raise ValueError(f"unknown activation {name!r}: one of {sorted(ACTIVATIONS)}") from None
 
 
-def _rounded(act, round_gradient):
-    """The activation of a backward pass, flagged where its gradient is rounded."""
-    return act | (GEMM_ROUND_GRADIENT if round_gradient else 0)
+def _flagged(act, kind, need_input, need_weight, round_gradient):
+    """The activation of a backward pass with what the call will be."""
+    return (act | (GEMM_ROUND_GRADIENT if round_gradient else 0) | (GEMM_ONLY_F16 if kind == "f16" else GEMM_ONLY_BF16)
+            | (0 if need_input else GEMM_NO_INPUT_GRADIENT) | (0 if need_weight else GEMM_NO_WEIGHT_GRADIENT))
 
 
 def _kind16(t, name):
@@ -370,7 +372,8 @@ def _linear_backward_form(dy, x, w, pre, activation, need_input, need_weight, ne
     lddx = _out(dx, tuple(x.shape), x, "dx") if need_input else 0
     lddw = _grad_stride(w, op, dw, "dw") if need_weight else 0
     _vector(dbias, N, "dbias", dy)
-    params = LinearBackwardParams(M, N, K, op, lddy, ldx, ldw, ldp, lddx, lddw, _rounded(act, round_gradient))
+    params = LinearBackwardParams(M, N, K, op, lddy, ldx, ldw, ldp, lddx, lddw,
+                                  _flagged(act, kind, need_input, need_weight, round_gradient))
     copies = [n for n, c in (("dy", copy_dy), ("x", copy_x), ("pre", copy_p)) if c]
     return _Form(dy, "gemm_linear_backward", kind, params, copies=copies, extra=op)
 
@@ -474,7 +477,8 @@ def _gated_backward_form(dh, x, wg, wu, g, u, activation, need_input, need_weigh
         lddw = _grad_stride(wg, op, dwg, "dwg")
         if _grad_stride(wu, op, dwu, "dwu") != lddw:
             raise ValueError("dwg and dwu must have one stride")
-    params = GatedBackwardParams(M, F, K, op, lddh, ldx, ldw, ldp, lddx, lddw, _rounded(act, round_gradient))
+    params = GatedBackwardParams(M, F, K, op, lddh, ldx, ldw, ldp, lddx, lddw,
+                                 _flagged(act, kind, need_input, need_weight, round_gradient))
     copies = [n for n, c in (("dh", copy_dh), ("x", copy_x), ("g", copy_g), ("u", copy_u)) if c]
     return _Form(dh, "gemm_gated_backward", kind, params, copies=copies, extra=op)
 

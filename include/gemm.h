@@ -373,8 +373,9 @@ typedef enum {
     GEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
 } gemm_activation;
 
-/* May be added to the activation of a backward pass.  The gradients dZ (dG, dU)
- * of the pre-activations are computed in FP32 and enter the products with dX
+/* Flags that may be added to the activation of a backward pass.
+ *
+ * GEMM_ROUND_GRADIENT: the gradients dZ (dG, dU) of the pre-activations are computed in FP32 and enter the products with dX
  * and dW as sums of two bfloat16 terms: to 2^-17 of each value and with the
  * range of FP32, at two products' work each, three in binary16 (none and relu,
  * whose dZ are dY's values or zero, take one).  (An infinite operand or gradient
@@ -382,8 +383,17 @@ typedef enum {
  * format instead, and each product runs once: the relative error of dX and dW
  * grows by about 1.4 times their own rounding's, and in binary16 a dZ past
  * 65504 becomes infinite and one below 2^-25 zero, whatever the products would
- * come to.  dbias is summed from FP32 either way. */
+ * come to.  dbias is summed from FP32 either way.
+ *
+ * What the call will be, so that its workspace holds no more than that needs
+ * (without them it serves either format and all outputs): the entry point of
+ * one format, no dX, no dW (dWg and dWu).  A call that is another ->
+ * GEMM_ERR_INVALID_ACTIVATION. */
 #define GEMM_ROUND_GRADIENT 0x100
+#define GEMM_ONLY_F16 0x200
+#define GEMM_ONLY_BF16 0x400
+#define GEMM_NO_INPUT_GRADIENT 0x800
+#define GEMM_NO_WEIGHT_GRADIENT 0x1000
 
 /* Dense layer: Z = X W + bias, Y = act(Z) + R.  X is M x K, W K x N, Y and R
  * M x N; bias (N), R and pre may be NULL.  Y and R are FP32 (y_f32 nonzero)
@@ -405,13 +415,12 @@ int gemm_linear_bf16(const gemm_linear_params *params, const uint16_t *X, const 
 /* Its backward pass: dZ = dY act'(Z), dX = dZ W^T, dW = X^T dZ, dbias = the
  * column sums of dZ (R's gradient is dY itself).  Each of dX, dW and dbias
  * may be NULL: it is then not computed.  pre is the forward pass's Z (not
- * read without an activation).  W is read for dX only, X for dW only.  The
- * workspace's size serves either format and any of the three outputs. */
+ * read without an activation).  W is read for dX only, X for dW only. */
 typedef struct {
     int M, N, K;
     int op_w;
     int lddy, ldx, ldw, ldp, lddx, lddw;
-    int activation;   /* a gemm_activation, with or without GEMM_ROUND_GRADIENT */
+    int activation;   /* a gemm_activation and flags */
 } gemm_linear_backward_params;
 int gemm_linear_backward_workspace(const gemm_linear_backward_params *params, size_t *bytes);
 int gemm_linear_backward_f16(const gemm_linear_backward_params *params, const uint16_t *dY, const uint16_t *X,

@@ -17,3 +17,52 @@ def test_the_backward_pass_of_layer_norm_does_not_read_eps(eps):
     assert b.raw_layer("gemm_layer_norm_backward", "bf16", p, None, *[P] * 5, None, None, P, 0, None) \
         == b.GEMM_ERR_NULL_PTR
     assert b.raw_layer("gemm_layer_norm", "bf16", p, *[P] * 6, None) == b.GEMM_ERR_INVALID_DIM
+
+
+def _linear(activation):
+    return b.LinearBackwardParams(4096, 8192, 4096, 0, 8192, 4096, 8192, 8192, 4096, 8192, activation)
+
+
+def _gated(activation):
+    return b.GatedBackwardParams(4096, 4096, 2048, 0, 4096, 2048, 4096, 4096, 2048, 4096, activation)
+
+
+BACKWARD = {"gemm_linear_backward": (_linear, 7, 4, 5), "gemm_gated_backward": (_gated, 9, 6, 7)}   # pointers; dX's, dW's
+SILU = b.ACTIVATIONS["silu"]
+
+
+@pytest.mark.parametrize("stem", BACKWARD)
+def test_a_backward_pass_has_workspace_for_what_it_is(stem):
+    make = BACKWARD[stem][0]
+
+    def size(flags):
+        return b.layer_workspace(stem, make(SILU | flags))
+    assert size(0) == max(size(b.GEMM_ONLY_F16), size(b.GEMM_ONLY_BF16))
+    # bfloat16 opens no operand: the terms of the gradients, partial sums, and
+    # the bias gradient's row blocks
+    assert size(b.GEMM_ONLY_BF16) < size(b.GEMM_ONLY_F16)
+    assert size(b.GEMM_ONLY_BF16 | b.GEMM_ROUND_GRADIENT) < size(b.GEMM_ONLY_BF16)
+    for one in (b.GEMM_NO_INPUT_GRADIENT, b.GEMM_NO_WEIGHT_GRADIENT):
+        assert 0 < size(b.GEMM_ONLY_F16 | one) < size(b.GEMM_ONLY_F16)
+        assert 0 < size(b.GEMM_ONLY_BF16 | one) <= size(b.GEMM_ONLY_BF16)
+    # neither gradient: the row blocks' sums of the bias gradient, if any
+    none = size(b.GEMM_NO_INPUT_GRADIENT | b.GEMM_NO_WEIGHT_GRADIENT)
+    assert none == (4096 // 64 * 8192 * 4 if stem == "gemm_linear_backward" else 0)
+
+
+@pytest.mark.parametrize("stem", BACKWARD)
+def test_a_backward_pass_that_is_not_what_its_flags_say_is_refused(stem):
+    make, pointers, dx, dw = BACKWARD[stem]
+
+    def call(kind, flags, leave=()):
+        p = [None if i in leave else P for i in range(pointers)]
+        return b.raw_layer(stem, kind, make(SILU | flags), *p, None, 0, None)   # no workspace: never launched
+    weights = (dw,) if stem == "gemm_linear_backward" else (dw, dw + 1)
+    bad, short = b.GEMM_ERR_INVALID_ACTIVATION, b.GEMM_ERR_WORKSPACE
+    assert call("f16", b.GEMM_ONLY_BF16) == bad and call("bf16", b.GEMM_ONLY_F16) == bad
+    assert call("f16", b.GEMM_ONLY_F16) == short and call("bf16", b.GEMM_ONLY_BF16) == short
+    assert call("bf16", b.GEMM_NO_INPUT_GRADIENT) == bad
+    assert call("bf16", b.GEMM_NO_INPUT_GRADIENT, (dx,)) == short
+    assert call("bf16", b.GEMM_NO_WEIGHT_GRADIENT) == bad
+    assert call("bf16", b.GEMM_NO_WEIGHT_GRADIENT, weights) == short
+    assert call("bf16", 0x2000) == bad and call("bf16", 0x80) == bad
