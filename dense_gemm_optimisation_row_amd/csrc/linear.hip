@@ -79,9 +79,11 @@ void split(int stages, long long parts, Way &w)
 // workgroups of the tile run on a compute unit at once.  A round of at most one
 // a unit takes ends + alone for each 32 k, a full one ends_full + full each.
 // Parts are written in FP32 and joined by another launch.  Microseconds, fitted
-// to 16 to 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N):
-// within 10% of the times measured.  Full rates: 1470, 1280, 1180, 890 and
-// 570 TFLOP/s.  An activation of exponentials adds what its outputs take on the
+// to 16 to 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N).
+// Over 184 products of every tile, layout and split they are 0.89 to 1.20 of the
+// times measured for four in five, 0.60 to 1.70 for all (short gated sums take less
+// than estimated, long ones of few columns more); which is chosen hangs on
+// their order alone.  Full rates of the fit: 1470, 1280, 1180, 890 and 570 TFLOP/s.  An activation of exponentials adds what its outputs take on the
 // vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs of 4096: 222 us,
 // 204 without).
 struct RingCost {
@@ -98,7 +100,10 @@ constexpr RingCost kRings[] = {
     {dgor::kRing64, 2, 4.0, 0.158, 4.2, 0.243, 1.08},
 };
 constexpr int kRingTiles = sizeof(kRings) / sizeof(kRings[0]);
-constexpr int kSplitRows = 40;   // stages of 64 k from which few rows' sums over a K x N matrix are split
+// Stages of 64 k from which few rows' sums over a K x N matrix are split.  At 40
+// whole and split take 9.4 and 8.1 us (1 row, 512 outputs), 14.0 and 11.8 (4096), 17.7
+// and 15.1 (48 rows); at 24 6.8 and 8.3, 9.9 and 10.7, 12.7 and 13.1; at 32 they are level.
+constexpr int kSplitRows = 40;
 constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
 // Weights that the few-row kernel reads in a microsecond, past 3 us: 33.5 MB
 // 11 us, 134 MB 28 us.
@@ -245,11 +250,10 @@ hipError_t run_product(const Product &q, const Plan &l, void *ws, hipStream_t s)
 // Both products of a backward pass: each by its own plan, or, where that is
 // estimated shorter, in one launch on one tile, so that their workgroups run
 // side by side, in one round or in rounds that only the last leaves unfilled.
-// In one launch and in two: 528 rows of 2752 to 791 outputs 25.6 us and 35.2,
-// 3344 rows gated 684 to 640 39.6 and 52.7, 2960 rows gated 244 to 5614 100 and
-// 116, 3266 rows of 3512 to 64 30.7 and 38.4; of at most 64 rows, where the
-// input's gradient alone is the few-row kernel's, 16 rows of 248 to 640 12.9
-// and 15.7.  Of 150 drawn passes none takes longer.
+// In one launch and in two: 1144 rows gated 256 to 3816 (f16) 47.2 and 70.3, 104
+// rows gated 88 to 2072 10.1 and 15.3; of at most 64 rows, where the input's
+// gradient alone is the few-row kernel's, 24 rows of 224 to 1192 9.6 and 14.3.
+// Of 72 drawn passes none takes longer, and the median gains 1.21 times.
 struct PairPlan {
     Plan x, w;
     bool together;

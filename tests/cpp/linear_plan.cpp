@@ -21,10 +21,14 @@ static const char *layout(const Product &p)
 static void product(const char *kernel, const Product &p, int tm, int tn, long long threads)
 {
     const long long tiles = (long long)((p.M + tm - 1) / tm) * ((p.N + (p.gated ? tn / 2 : tn) - 1) / (p.gated ? tn / 2 : tn));
+    double us = 0;   // what a ring was chosen for, its join included; printed in tenths
+    for (const RingCost &c : kRings)
+        if (threads == 256 && ring_tile_m(c.tile) == tm && ring_tile_n(c.tile) == tn)
+            us = microseconds(p, c, tiles * p.nbatch, p.splits > 1 ? p.splits : 1);
     printf("%s tile=%dx%d layout=%s M=%d N=%d K=%d segments=%d terms=%d batches=%d splits=%d chunk=%d stages=%d "
-           "threads=%lld\n",
+           "threads=%lld estimate=%d\n",
            kernel, tm, tn, layout(p), p.M, p.N, p.K, p.nseg, p.terms, p.nbatch, p.splits > 1 ? p.splits : 1, p.chunk,
-           product_stages(p), tiles * p.nbatch * threads);
+           product_stages(p), tiles * p.nbatch * threads, (int)(10 * us + 0.5));
 }
 
 int device_status() { return GEMM_OK; }
