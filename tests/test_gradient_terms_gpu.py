@@ -226,3 +226,47 @@ def test_terms_in_a_graph_replay_as_they_run(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, eager))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_terms_of_nothing(dtype):
+    T = DTYPES[dtype]
+
+    def e(*shape):
+        return torch.ones(*shape, dtype=T, device="cuda")
+    for M, N, K in ((0, 16, 24), (5, 0, 24), (100, 0, 24), (5, 16, 0), (100, 16, 0), (0, 0, 0)):
+        say("nothing", M, N, K, dtype)
+        dx, dw, db = dg.linear_backward(e(M, N), e(M, K), e(K, N), pre=e(M, N), activation="silu")
+        assert dx.shape == (M, K) and dw.shape == (K, N) and db.shape == (N,)
+        if not M:
+            assert bool((dw == 0).all()) and bool((db == 0).all())
+        if not N:
+            assert bool((dx == 0).all())
+        dx, dwg, dwu = dg.gated_backward(e(M, N), e(M, K), e(K, N), e(K, N), e(M, N), e(M, N))
+        assert dx.shape == (M, K) and dwg.shape == dwu.shape == (K, N)
+        if not M:
+            assert bool((dwg == 0).all()) and bool((dwu == 0).all())
+        if not N:
+            assert bool((dx == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", [(5, 264, 136), (200, 264, 136), (600, 520, 264)], ids=str)
+def test_nonfinite_gradients_stay_in_their_row(shape, dtype):
+    """A row's infinities and NaN reach that row of dX only, and of the weights'
+    gradients the columns that they are in."""
+    M, N, K = shape
+    T = DTYPES[dtype]
+    mk = Make(77, T)
+    x, w, dy, pre = mk.normal(M, K), mk.normal(K, N, K ** -0.5), mk.normal(M, N), mk.normal(M, N)
+    clean = dg.linear_backward(dy, x, w, pre=pre, activation="silu")
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        say("nonfinite", shape, dtype, bad)
+        d = dy.clone()
+        d[M - 2, N - 1] = bad
+        dx, dw, db = dg.linear_backward(d, x, w, pre=pre, activation="silu")
+        keep = [i for i in range(M) if i != M - 2]
+        assert torch.equal(dx[keep], clean[0][keep])
+        assert not bool(torch.isfinite(dx[M - 2]).any())
+        assert torch.equal(dw[:, :N - 1], clean[1][:, :N - 1]) and not bool(torch.isfinite(dw[:, N - 1]).any())
+        assert torch.equal(db[:N - 1], clean[2][:N - 1]) and not bool(torch.isfinite(db[N - 1]))
