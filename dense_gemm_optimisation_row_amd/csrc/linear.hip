@@ -5,15 +5,22 @@
 #include <stdint.h>
 
 #include "linear.h"
+#include "ring_plan.h"
 
 namespace {
 
 using dgor::Epilogue;
 using dgor::Product;
+using dgor::RingCost;
+using dgor::RingTimes;
+using dgor::ceil_div;
+using dgor::kJoinLaunch;
+using dgor::kRings;
+using dgor::kRingTiles;
+using dgor::tiles;
 
 constexpr size_t kWsAlign = 256;
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // A launch holds fewer than 2^32 threads.  With fewer than 2^22 blocks of 128 x
 // 64 the smallest tiles, 64 x 32 (gated) or two of 64 x 64 (both weights'
@@ -41,11 +48,6 @@ struct Way {
     int splits, chunk;
     double us;   // the time that a ring was chosen for, or that few rows take
 };
-
-long long tiles(const Product &p, int tm, int tn)
-{
-    return (long long)ceil_div(p.M, tm) * ceil_div(p.N, p.gated ? tn / 2 : tn) * p.nbatch;
-}
 
 // Whether the few-row kernel takes a product.
 bool few_rows(const Product &p)
@@ -75,62 +77,13 @@ void split(int stages, long long parts, Way &w)
     }
 }
 
-// Time of a product on a ring's tile with its sum in `parts`.  Up to `share`
-// workgroups of the tile run on a compute unit at once.  A round of at most one
-// a unit takes ends + alone for each 32 k, a full one ends_full + full each.
-// Parts are written in FP32 and joined by another launch.  Microseconds, fitted
-// to 16 to 4096 workgroups of each tile and sums of 256 to 4096 (BF16, K x N).
-// Over 184 products of every tile, layout and split they are 0.89 to 1.20 of the
-// times measured for four in five, 0.60 to 1.70 for all (short gated sums take less
-// than estimated, long ones of few columns more); which is chosen hangs on
-// their order alone.  Full rates of the fit: 1470, 1280, 1180, 890 and 570 TFLOP/s.  An activation of exponentials adds what its outputs take on the
-// vector ALUs: 9 us for 256 x 256 (GELU, 4096 x 8192 outputs of 4096: 222 us,
-// 204 without).
-struct RingCost {
-    dgor::RingTile tile;
-    int share;
-    double ends, alone, ends_full, full;
-    double halves;   // times as long a stage whose loads take half lines
-};
-constexpr RingCost kRings[] = {
-    {dgor::kRing256, 1, 14.5, 0.73, 14.5, 0.73, 1.0},
-    {dgor::kRing256x128, 1, 9.8, 0.42, 9.8, 0.42, 1.3},
-    {dgor::kRing128, 2, 6.8, 0.295, 7.5, 0.455, 1.17},
-    {dgor::kRing128x64, 2, 4.8, 0.243, 6.2, 0.33, 1.12},
-    {dgor::kRing64, 2, 4.0, 0.158, 4.2, 0.243, 1.08},
-};
-constexpr int kRingTiles = sizeof(kRings) / sizeof(kRings[0]);
 // Stages of 64 k from which few rows' sums over a K x N matrix are split.  At 40
 // whole and split take 9.4 and 8.1 us (1 row, 512 outputs), 14.0 and 11.8 (4096), 17.7
 // and 15.1 (48 rows); at 24 6.8 and 8.3, 9.9 and 10.7, 12.7 and 13.1; at 32 they are level.
 constexpr int kSplitRows = 40;
-constexpr double kJoinLaunch = 4.5, kJoinBytes = 8e6;   // and a microsecond's bytes
 // Weights that the few-row kernel reads in a microsecond, past 3 us: 33.5 MB
 // 11 us, 134 MB 28 us.
 constexpr double kRowsBytes = 5e6;
-struct RingTimes {
-    double alone, full, join;   // a round of one tile a unit, a full one, joining the parts
-};
-RingTimes times(const Product &p, const RingCost &c, int parts)
-{
-    // half lines: B as N x K, and each of two matrices' 32 columns
-    const bool halves = p.trans_b || (p.gated && ring_tile_n(c.tile) == 64);
-    const double stages = 2.0 * dgor::product_stages(p) / parts * (halves ? c.halves : 1.0);
-    // an activation's time for a workgroup's outputs
-    const double act = p.e.act > GEMM_ACT_RELU && parts == 1
-                           ? 9.0 * ring_tile_m(c.tile) * ring_tile_n(c.tile) / (p.gated ? 131072 : 65536)
-                           : 0.0;
-    return {c.ends + stages * c.alone + act, c.ends_full + stages * c.full + act * c.share,
-            parts > 1 ? kJoinLaunch + 8.0 * parts * (p.gated ? 2 : p.nbatch) * p.M * p.N / kJoinBytes : 0.0};
-}
-double microseconds(const Product &p, const RingCost &c, long long n, int parts)   // n tiles
-{
-    const unsigned long long groups = (unsigned long long)n * parts;
-    const unsigned long long rounds = groups / (256u * c.share), rest = groups % (256u * c.share);
-    const RingTimes t = times(p, c, parts);
-    return rounds * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full) + t.join;
-}
-
 // The best split of a product on a ring's tile.
 Way best_on(const Product &p, const RingCost &c)
 {
