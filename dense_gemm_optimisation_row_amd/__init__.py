@@ -20,7 +20,8 @@ from .binding import (  # noqa: F401
 
 def __getattr__(name):
     # the layers import torch, which the host-only uses of this package do not need
-    if name in ("gated", "gated_backward", "layer_norm", "layer_norm_backward", "linear", "linear_backward"):
+    if name in ("gated", "gated_backward", "gated_i8", "layer_norm", "layer_norm_backward", "linear", "linear_backward",
+                "linear_i8", "orthogonalize", "quantize_i8"):
         from . import layers
         globals()[name] = getattr(layers, name)
         return globals()[name]

@@ -36,6 +36,7 @@ GEMM_ERR_INVALID_LAYOUT = -7
 GEMM_ERR_WORKSPACE = -8
 GEMM_ERR_SCRATCH_LIMIT = -9
 GEMM_ERR_INVALID_ACTIVATION = -10
+GEMM_ERR_INVALID_COEFFICIENTS = -11
 GEMM_OP_N, GEMM_OP_T = 0, 1
 
 AUTO = -1
@@ -63,6 +64,11 @@ EXPORTS = ("gemm_f32", "gemm_f16_f32acc", "gemm_bf16_f32acc",
            "gemm_layer_norm_f32", "gemm_layer_norm_f16", "gemm_layer_norm_bf16",
            "gemm_layer_norm_backward_workspace", "gemm_layer_norm_backward_f32",
            "gemm_layer_norm_backward_f16", "gemm_layer_norm_backward_bf16",
+           "gemm_quantize_i8_f32", "gemm_quantize_i8_f16", "gemm_quantize_i8_bf16",
+           "gemm_linear_i8_workspace", "gemm_linear_i8_f32", "gemm_linear_i8_f16", "gemm_linear_i8_bf16",
+           "gemm_gated_i8_workspace", "gemm_gated_i8_f32", "gemm_gated_i8_f16", "gemm_gated_i8_bf16",
+           "gemm_orthogonalize_workspace", "gemm_orthogonalize_f32", "gemm_orthogonalize_f16",
+           "gemm_orthogonalize_bf16",
            "gemm_status_string", "gemm_variant_name")
 
 # Entry-point name stem per input format.
@@ -152,6 +158,34 @@ class LayerNormParams(_Params):
     _fields_ = [(n, ctypes.c_int) for n in ("M", "N", "ldx", "ldy", "lddx", "weight_f32")] + [("eps", ctypes.c_float)]
 
 
+class QuantizeParams(_Params):
+    """gemm_quantize_i8_params."""
+    _fields_ = [(n, ctypes.c_int) for n in ("M", "K", "ldx", "ldq")]
+
+
+class LinearI8Params(_Params):
+    """gemm_linear_i8_params."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "M", "N", "K", "op_w", "ldx", "ldw", "ldy", "ldr", "activation", "unaligned")]
+
+
+class GatedI8Params(_Params):
+    """gemm_gated_i8_params."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "M", "F", "K", "op_w", "ldx", "ldw", "ldh", "activation", "unaligned")]
+
+
+GEMM_MAX_STEPS = 32
+
+
+class OrthogonalizeParams(_Params):
+    """gemm_orthogonalize_params; ``coefficients`` a, b, c of each step."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("batch", "M", "N", "op_g", "op_o", "ldg", "ldo", "steps")]
+                + [(n, ctypes.c_longlong) for n in ("stride_g", "stride_o")]
+                + [(n, ctypes.c_double) for n in ("eps", "scale")]
+                + [("coefficients", ctypes.c_double * (3 * GEMM_MAX_STEPS))])
+
+
 # Parameter struct, pointer arguments (workspace apart), workspace or not, and
 # element formats of the layer entry points.
 _LAYERS = {"gemm_linear": (LinearParams, 6, True, ("f16", "bf16")),
@@ -159,7 +193,11 @@ _LAYERS = {"gemm_linear": (LinearParams, 6, True, ("f16", "bf16")),
            "gemm_gated": (GatedParams, 6, True, ("f16", "bf16")),
            "gemm_gated_backward": (GatedBackwardParams, 9, True, ("f16", "bf16")),
            "gemm_layer_norm": (LayerNormParams, 6, False, ("f32", "f16", "bf16")),
-           "gemm_layer_norm_backward": (LayerNormParams, 8, True, ("f32", "f16", "bf16"))}
+           "gemm_layer_norm_backward": (LayerNormParams, 8, True, ("f32", "f16", "bf16")),
+           "gemm_quantize_i8": (QuantizeParams, 3, False, ("f32", "f16", "bf16")),
+           "gemm_linear_i8": (LinearI8Params, 7, True, ("f32", "f16", "bf16")),
+           "gemm_gated_i8": (GatedI8Params, 7, True, ("f32", "f16", "bf16")),
+           "gemm_orthogonalize": (OrthogonalizeParams, 2, True, ("f32", "f16", "bf16"))}
 
 
 class Plan(ctypes.Structure):

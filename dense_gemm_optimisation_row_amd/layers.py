@@ -1,6 +1,8 @@
 """The layers around the products, for torch tensors on the GPU: the dense
 layer with bias, activation and residual, the gated up-projection and layer
-norm, each with its backward pass.  Argument checks and marshalling only: the
+norm, each with its backward pass; the first two on 8-bit codes with a scale for
+each token and channel, and what makes such codes; and the orthogonalised update
+of a weight from its gradient.  Argument checks and marshalling only: the
 arithmetic is in the HIP kernels behind the C ABI of ``include/gemm.h``.
 
 Rows may have any stride; weights are ``K x N`` views whose storage is
@@ -30,8 +32,9 @@ import torch
 
 from . import binding
 from .binding import (ACTIVATIONS, GEMM_OK, GEMM_NO_INPUT_GRADIENT, GEMM_NO_WEIGHT_GRADIENT, GEMM_ONLY_BF16,
-                      GEMM_ONLY_F16, GEMM_OP_N, GEMM_OP_T, GEMM_ROUND_GRADIENT, GatedBackwardParams, GatedParams,
-                      GemmError, LayerNormParams, LinearBackwardParams, LinearParams)
+                      GEMM_ONLY_F16, GEMM_OP_N, GEMM_OP_T, GEMM_MAX_STEPS, GEMM_ROUND_GRADIENT, GatedBackwardParams,
+                      GatedI8Params, GatedParams, GemmError, LayerNormParams, LinearBackwardParams, LinearI8Params,
+                      LinearParams, OrthogonalizeParams, QuantizeParams)
 
 _KIND = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}
 _functions = {}
@@ -579,3 +582,267 @@ def _layer_norm_backward_form(dy, x, weight, mean, rstd, need_weight, dx, dweigh
     params = LayerNormParams(M, N, ldx, lddy, lddx, wt == torch.float32, 0.0)
     copies = [n for n, c in (("dy", copy_dy), ("x", copy_x)) if c]
     return _Form(dy, "gemm_layer_norm_backward", _KIND[dy.dtype], params, dtype=wt, copies=copies)
+
+
+# ---------------------------------------------------- 8-bit dense layers --
+
+def _kind_of(dtype, name):
+    if dtype not in _KIND:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, not {dtype}")
+    return _KIND[dtype]
+
+
+def _scales(t, n, name, like):
+    """Scales of n rows or columns: n float32 values one after another."""
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on the GPU of the first argument")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, not {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values, not {tuple(t.shape)}")
+
+
+def quantize_i8(x, q=None, scale=None, stream=None):
+    """``(q, scale)``: the rows of a float32, float16 or bfloat16 x (..., K) as
+    int8 codes of x's shape and one float32 scale each, of shape (...): the
+    largest |x| of the row times float32(1 / 127), at least 2^-126, and x / scale to the
+    nearest whole number, ties to even.  A row that holds a NaN or an infinity gets the
+    scale NaN and zeros.  Weights are quantised as outputs by inputs:
+    ``q, s = quantize_i8(weight)``, and ``q.t()`` with ``s`` goes into
+    ``linear_i8``."""
+    if x.requires_grad:
+        _grad_unless_off()
+    key = ("quantize_i8", x.shape, x.stride(), x.dtype, x.device, _sig(q), _sig(scale))
+    form = _FORMS.get(key) or _keep(key, _quantize_form(x, q, scale))
+
+    def go(handle):
+        xs = _in(x, "x", form) if form.copies else x
+        codes = x.new_empty(x.shape, dtype=torch.int8) if q is None else q
+        steps = x.new_empty(form.shape, dtype=torch.float32) if scale is None else scale
+        _done(form.entry(form.ref, xs.data_ptr(), codes.data_ptr(), steps.data_ptr(), handle), form)
+        return codes, steps
+    return _run(form, stream, (x, q, scale), go)
+
+
+def _quantize_form(x, q, scale):
+    _gpu(x, "x")
+    kind = _kind_of(x.dtype, "x")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    K = x.shape[-1]
+    M, ldx, copy_x = _rows(x, K, "x", x)
+    ldq = _out(q, tuple(x.shape), x, "q", torch.int8)
+    shape = tuple(x.shape[:-1])
+    if scale is not None:
+        if tuple(scale.shape) != shape:
+            raise ValueError(f"scale is {tuple(scale.shape)}, expected {shape}")
+        _scales(scale, M, "scale", x)
+    return _Form(x, "gemm_quantize_i8", kind, QuantizeParams(M, K, ldx, ldq), shape, copies=["x"] if copy_x else ())
+
+
+def _off_units(*tensors):
+    return any(t.data_ptr() & 15 for t in tensors)
+
+
+def _codes(x, name):
+    _gpu(x, name)
+    if x.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8, not {x.dtype}")
+
+
+def linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, activation="none", out_dtype=None, y=None,
+              workspace=None, stream=None):
+    """``act(x_scale w_scale (x w) + bias) + residual`` for int8 x (..., K) with
+    a float32 scale for each of its rows and int8 w (K x N) with one for each of
+    its columns (``quantize_i8``).  The sums are exact (K up to 131071), the rest
+    is float32; ``bias`` is float32, the residual and the result ``out_dtype``:
+    float32, float16 or bfloat16; by default y's or the residual's type, else
+    bfloat16.  w is fastest stored outputs by inputs (a transposed view) with K a multiple of 16:
+    other weights are copied into that form in each call.  ``y`` may be the
+    residual itself."""
+    if (bias is not None and bias.requires_grad) or (residual is not None and residual.requires_grad) or \
+            x_scale.requires_grad or w_scale.requires_grad:
+        _grad_unless_off()
+    off = _off_units(x, w)
+    key = ("linear_i8", x.shape, x.stride(), x.dtype, x.device, _sig(x_scale), w.shape, w.stride(), w.dtype, w.device,
+           _sig(w_scale), _sig(bias), _sig(residual), activation, out_dtype, _sig(y), off)
+    form = _FORMS.get(key) or _keep(key, _linear_i8_form(x, x_scale, w, w_scale, bias, residual, activation, out_dtype,
+                                                         y, off))
+
+    def go(handle):
+        xs, rs = (_in(x, "x", form), _in(residual, "residual", form)) if form.copies else (x, residual)
+        out = x.new_empty(form.shape, dtype=form.dtype) if y is None else y
+        ws = _workspace(form, workspace, x)
+        _done(form.entry(form.ref, xs.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
+                         _ptr(rs), out.data_ptr(), _ptr(ws), _size(ws), handle), form)
+        return out
+    return _run(form, stream, (x, x_scale, w, w_scale, bias, residual, y, workspace), go)
+
+
+def _linear_i8_form(x, x_scale, w, w_scale, bias, residual, activation, out_dtype, y, off):
+    _codes(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    op, ldw = _weight(w, "w", x)
+    K, N = w.shape
+    M, ldx, copy_x = _rows(x, K, "x", x)
+    _scales(x_scale, M, "x_scale", x)
+    _scales(w_scale, N, "w_scale", x)
+    act = _activation(activation)
+    if out_dtype is None:
+        out_dtype = next((t.dtype for t in (y, residual) if t is not None), torch.bfloat16)
+    kind = _kind_of(out_dtype, "out_dtype")
+    shape = tuple(x.shape[:-1]) + (N,)
+    _vector(bias, N, "bias", x, torch.float32)
+    ldr, copy_r = 0, False
+    if residual is not None:
+        if tuple(residual.shape) != shape:
+            raise ValueError(f"residual is {tuple(residual.shape)}, expected {shape}")
+        _, ldr, copy_r = _rows(residual, N, "residual", x, M, out_dtype)
+    ldy = _out(y, shape, x, "y", out_dtype)
+    # (a copy of x is on 16 bytes; that it is then copied once more costs little beside it)
+    params = LinearI8Params(M, N, K, op, ldx, ldw, ldy, ldr, act, off)
+    copies = [n for n, c in (("x", copy_x), ("residual", copy_r)) if c]
+    return _Form(x, "gemm_linear_i8", kind, params, shape, out_dtype, copies)
+
+
+def gated_i8(x, x_scale, wg, wg_scale, wu, wu_scale, activation="silu", out_dtype=None, h=None, workspace=None,
+             stream=None):
+    """``act(x wg) * (x wu)`` for int8 x (..., K) and K x F weights (of one
+    storage and stride), each product scaled as in ``linear_i8``; the result is
+    ``out_dtype``: float32, float16 or bfloat16, by default h's type or
+    bfloat16."""
+    if x_scale.requires_grad or wg_scale.requires_grad or wu_scale.requires_grad:
+        _grad_unless_off()
+    off = _off_units(x, wg, wu)
+    key = ("gated_i8", x.shape, x.stride(), x.dtype, x.device, _sig(x_scale), wg.shape, wg.stride(), wg.dtype,
+           wg.device, _sig(wg_scale), _sig(wu), _sig(wu_scale), activation, out_dtype, _sig(h), off)
+    form = _FORMS.get(key) or _keep(key, _gated_i8_form(x, x_scale, wg, wg_scale, wu, wu_scale, activation, out_dtype,
+                                                        h, off))
+
+    def go(handle):
+        xs = _in(x, "x", form) if form.copies else x
+        out = x.new_empty(form.shape, dtype=form.dtype) if h is None else h
+        ws = _workspace(form, workspace, x)
+        _done(form.entry(form.ref, xs.data_ptr(), x_scale.data_ptr(), wg.data_ptr(), wg_scale.data_ptr(),
+                         wu.data_ptr(), wu_scale.data_ptr(), out.data_ptr(), _ptr(ws), _size(ws), handle), form)
+        return out
+    return _run(form, stream, (x, x_scale, wg, wg_scale, wu, wu_scale, h, workspace), go)
+
+
+def _gated_i8_form(x, x_scale, wg, wg_scale, wu, wu_scale, activation, out_dtype, h, off):
+    _codes(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    op, ldw = _gate_weights(wg, wu, x)
+    K, F = wg.shape
+    M, ldx, copy_x = _rows(x, K, "x", x)
+    _scales(x_scale, M, "x_scale", x)
+    _scales(wg_scale, F, "wg_scale", x)
+    _scales(wu_scale, F, "wu_scale", x)
+    act = _activation(activation)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if h is None else h.dtype
+    kind = _kind_of(out_dtype, "out_dtype")
+    shape = tuple(x.shape[:-1]) + (F,)
+    ldh = _out(h, shape, x, "h", out_dtype)
+    return _Form(x, "gemm_gated_i8", kind, GatedI8Params(M, F, K, op, ldx, ldw, ldh, act, off), shape, out_dtype,
+                 copies=["x"] if copy_x else ())
+
+
+# --------------------------------------------------- orthogonalised update --
+
+def _matrices(t, name):
+    """(batch, op, row stride, stride between matrices) of a matrix or a stack
+    of them (..., M, N), each stored by rows or by columns."""
+    rows, cols = t.shape[-2:]
+    batch = _count(t.shape[:-2])
+    lead = t.shape[:-2]
+    stride = 0
+    if batch > 1:
+        # the leading dimensions must be one stride apart: last to first
+        expect = None
+        for n, s in zip(reversed(lead), reversed(t.stride()[:-2])):
+            if n == 1:
+                continue
+            if expect is None:
+                stride = s
+            elif s != expect:
+                raise ValueError(f"{name}'s leading dimensions must be one stride apart (strides {t.stride()})")
+            expect = s * n
+    s0, s1 = t.stride()[-2:]
+    if s1 == 1 or cols <= 1:
+        op, ld = GEMM_OP_N, s0 if rows > 1 else max(cols, 1)
+    elif s0 == 1 or rows <= 1:
+        op, ld = GEMM_OP_T, s1 if cols > 1 else max(rows, 1)
+    else:
+        raise ValueError(f"{name} needs a unit stride in one dimension (strides {t.stride()})")
+    if ld > _MAX_INT:
+        raise ValueError(f"{name}'s stride {ld} is out of range")
+    if ld < (rows if op == GEMM_OP_T else cols):
+        raise ValueError(f"{name}'s rows overlap (strides {t.stride()})")
+    return batch, op, ld, stride
+
+
+def _step_coefficients(coefficients, steps):
+    """a, b, c of every step, one after another."""
+    triples = list(coefficients)
+    if triples and not hasattr(triples[0], "__len__"):
+        triples = [tuple(triples)] * steps
+    if len(triples) != steps or any(len(t) != 3 for t in triples):
+        raise ValueError(f"coefficients are a, b, c, or {steps} such triples")
+    return tuple(float(v) for t in triples for v in t)
+
+
+def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, out=None, workspace=None,
+                  stream=None):
+    """The orthogonalised update of a gradient g (M x N) or of each of a stack
+    (..., M, N), float32, float16 or bfloat16: with X = g / (|g| + eps), |g| the
+    root of its sum of squares, ``steps`` Newton-Schulz steps
+    X = a X + (b A + c A A) X, A = X X^T, then ``scale`` X, in g's type and
+    storage.  ``coefficients`` are a, b, c, or such a triple for each step; they must not let
+    a singular value of at most 1, nor what multiplies it, grow past 256.
+    Products are computed from two float16 terms of each operand, to 2^-23 of
+    its values.  g may be a transposed view (a weight gradient of
+    ``linear_backward``); ``out`` may be g itself."""
+    if g.requires_grad:
+        _grad_unless_off()
+    values = _step_coefficients(coefficients, steps)
+    key = ("orthogonalize", g.shape, g.stride(), g.dtype, g.device, steps, values, eps, scale, _sig(out))
+    form = _FORMS.get(key) or _keep(key, _orthogonalize_form(g, steps, values, eps, scale, out))
+
+    def go(handle):
+        o = out
+        if o is None:
+            o = g.new_empty(form.shape)
+            if form.extra:
+                o = o.mT
+        ws = _workspace(form, workspace, g)
+        _done(form.entry(form.ref, g.data_ptr(), o.data_ptr(), _ptr(ws), _size(ws), handle), form)
+        return o
+    return _run(form, stream, (g, out, workspace), go)
+
+
+def _orthogonalize_form(g, steps, values, eps, scale, out):
+    _gpu(g, "g")
+    kind = _kind_of(g.dtype, "g")
+    if g.dim() < 2:
+        raise ValueError("g must be a matrix or a stack of them")
+    if not 1 <= steps <= GEMM_MAX_STEPS:
+        raise ValueError(f"steps must be 1 to {GEMM_MAX_STEPS}, not {steps}")
+    M, N = g.shape[-2:]
+    batch, op_g, ldg, stride_g = _matrices(g, "g")
+    if out is None:
+        op_o, ldo, stride_o = op_g, max(M if op_g == GEMM_OP_T else N, 1), M * N
+    else:
+        if out.shape != g.shape or out.dtype != g.dtype or out.device != g.device:
+            raise ValueError("out must match g")
+        _, op_o, ldo, stride_o = _matrices(out, "out")
+        extent = (N - 1) * ldo + M if op_o == GEMM_OP_T else (M - 1) * ldo + N
+        if batch > 1 and M and N and stride_o < extent:
+            raise ValueError(f"out's matrices overlap (strides {out.stride()})")
+    params = OrthogonalizeParams(batch, M, N, op_g, op_o, ldg, ldo, steps, stride_g, stride_o, eps, scale)
+    params.coefficients[:len(values)] = values
+    turned = op_g == GEMM_OP_T
+    shape = tuple(g.shape[:-2]) + ((N, M) if turned else (M, N))
+    return _Form(g, "gemm_orthogonalize", kind, params, shape, extra=turned and out is None)

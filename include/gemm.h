@@ -52,7 +52,8 @@ typedef enum {
     GEMM_ERR_INVALID_LAYOUT = -7,
     GEMM_ERR_WORKSPACE = -8,
     GEMM_ERR_SCRATCH_LIMIT = -9,
-    GEMM_ERR_INVALID_ACTIVATION = -10
+    GEMM_ERR_INVALID_ACTIVATION = -10,
+    GEMM_ERR_INVALID_COEFFICIENTS = -11
 } gemm_status;
 
 /*
@@ -502,6 +503,113 @@ int gemm_layer_norm_backward_f16(const gemm_layer_norm_params *params, const uin
 int gemm_layer_norm_backward_bf16(const gemm_layer_norm_params *params, const uint16_t *dy, const uint16_t *x,
                                   const void *weight, const float *mean, const float *rstd, uint16_t *dx,
                                   void *dweight, void *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A dense layer's weights beyond its forward and backward pass: products on 8-bit
+ * operands with a scale for each token and channel, the quantisation that makes
+ * such operands, and the update that orthogonalises a gradient.  Conventions as
+ * for the feed-forward operators above, and:
+ *   - Scales and bias are FP32 and contiguous.
+ *   - 8-bit operands are used where they are if their rows run along K, are
+ *     whole multiples of 16 bytes at strides that are, and begin on 16 bytes;
+ *     otherwise they are first copied into the workspace, K x N weights
+ *     transposed.  `unaligned` nonzero says that X or W may begin anywhere (both
+ *     are then copied); without it a call on such an operand ->
+ *     GEMM_ERR_INVALID_LAYOUT.
+ */
+
+/* Quantisation of each of M rows of K elements:
+ *   scale = max(max |x| times the FP32 nearest 1 / 127, 2^-126), rounded to FP32,
+ *   q = x / scale to the nearest whole number, ties to even, of the exact
+ * quotient.  A row that holds a NaN or an infinity gets the scale NaN and codes
+ * of zero.  K past 2^31 - 65537 -> GEMM_ERR_INVALID_DIM.  No workspace. */
+typedef struct {
+    int M, K;
+    int ldx, ldq;
+} gemm_quantize_i8_params;
+int gemm_quantize_i8_f32(const gemm_quantize_i8_params *params, const float *x, int8_t *q, float *scale,
+                         void *stream);
+int gemm_quantize_i8_f16(const gemm_quantize_i8_params *params, const uint16_t *x, int8_t *q, float *scale,
+                         void *stream);
+int gemm_quantize_i8_bf16(const gemm_quantize_i8_params *params, const uint16_t *x, int8_t *q, float *scale,
+                          void *stream);
+
+/* 8-bit dense layer: Z[m][n] = x_scale[m] w_scale[n] (sum over k of X[m][k]
+ * W[k][n]) + bias[n], Y = act(Z) + R.  The sums are exact, in INT32 (K past
+ * 131071 -> GEMM_ERR_INVALID_DIM), the rest is FP32; Y and R (Y may be R itself)
+ * are in the entry point's format, to which Y is rounded once.  bias and R may be
+ * NULL. */
+typedef struct {
+    int M, N, K;
+    int op_w;
+    int ldx, ldw, ldy, ldr;
+    int activation;
+    int unaligned;
+} gemm_linear_i8_params;
+int gemm_linear_i8_workspace(const gemm_linear_i8_params *params, size_t *bytes);
+int gemm_linear_i8_f32(const gemm_linear_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *W,
+                       const float *w_scale, const float *bias, const float *R, float *Y, void *workspace,
+                       size_t workspace_bytes, void *stream);
+int gemm_linear_i8_f16(const gemm_linear_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *W,
+                       const float *w_scale, const float *bias, const uint16_t *R, uint16_t *Y, void *workspace,
+                       size_t workspace_bytes, void *stream);
+int gemm_linear_i8_bf16(const gemm_linear_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *W,
+                        const float *w_scale, const float *bias, const uint16_t *R, uint16_t *Y, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* 8-bit gated up-projection: H = act(G) U with G and U the products of X with Wg
+ * and Wu (both K x F, of one storage and stride), scaled as above. */
+typedef struct {
+    int M, F, K;
+    int op_w;
+    int ldx, ldw, ldh;
+    int activation;
+    int unaligned;
+} gemm_gated_i8_params;
+int gemm_gated_i8_workspace(const gemm_gated_i8_params *params, size_t *bytes);
+int gemm_gated_i8_f32(const gemm_gated_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *Wg,
+                      const float *wg_scale, const int8_t *Wu, const float *wu_scale, float *H, void *workspace,
+                      size_t workspace_bytes, void *stream);
+int gemm_gated_i8_f16(const gemm_gated_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *Wg,
+                      const float *wg_scale, const int8_t *Wu, const float *wu_scale, uint16_t *H, void *workspace,
+                      size_t workspace_bytes, void *stream);
+int gemm_gated_i8_bf16(const gemm_gated_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *Wg,
+                       const float *wg_scale, const int8_t *Wu, const float *wu_scale, uint16_t *H, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* Orthogonalised update of each of `batch` matrices G, M x N, by Newton-Schulz
+ * steps:
+ *   X = G / (|G| + eps), |G| the root of the sum of squares,
+ *   `steps` times: X = a X + (b A + c A A) X, A = X X^T (X^T from the other side
+ *   where M > N), with the step's own a, b, c,
+ *   O = scale X.
+ * The operands of the products are held as two binary16 terms each at a power of
+ * two that the coefficients give, to 2^-23 of a value and 2^-37 of the largest;
+ * a step's sums, A and c A A + b A are computed in FP32, |G| in FP64.
+ * G and O are stored M x N (op GEMM_OP_N) or N x M (GEMM_OP_T), stride_g and
+ * stride_o elements from a matrix to the next (read only where batch > 1).  O may
+ * be G itself (same pointer, op and strides).  A matrix of zeros gives zeros; one
+ * with a NaN or an infinity NaN.  steps outside [1, GEMM_MAX_STEPS] or eps
+ * negative or NaN -> GEMM_ERR_INVALID_DIM; coefficients that are not finite, or
+ * whose steps let a singular value of at most 1, or what multiplies it, grow past
+ * 256 -> GEMM_ERR_INVALID_COEFFICIENTS. */
+#define GEMM_MAX_STEPS 32
+typedef struct {
+    int batch, M, N;
+    int op_g, op_o;
+    int ldg, ldo;
+    int steps;
+    long long stride_g, stride_o;
+    double eps, scale;
+    double coefficients[3 * GEMM_MAX_STEPS];   /* a, b, c of each step */
+} gemm_orthogonalize_params;
+int gemm_orthogonalize_workspace(const gemm_orthogonalize_params *params, size_t *bytes);
+int gemm_orthogonalize_f32(const gemm_orthogonalize_params *params, const float *G, float *O, void *workspace,
+                           size_t workspace_bytes, void *stream);
+int gemm_orthogonalize_f16(const gemm_orthogonalize_params *params, const uint16_t *G, uint16_t *O, void *workspace,
+                           size_t workspace_bytes, void *stream);
+int gemm_orthogonalize_bf16(const gemm_orthogonalize_params *params, const uint16_t *G, uint16_t *O, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 /* Static, NUL-terminated descriptions; never NULL ("unknown ..." for values
  * outside the enums). */

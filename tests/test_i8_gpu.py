@@ -1,0 +1,363 @@
+"""Rows as 8-bit codes with a scale, and the dense layer and gated up-projection
+on such codes, against their formulas in 64 bits.
+
+Codes and scales have to be equal: both are defined exactly.  Products of small
+codes under scales that are powers of two, with no activation or relu, are exact
+in FP32, so they have to be the rounded exact result bit for bit, whatever kernel,
+split, edge or copy a size takes.  Others are held to a bound: the sum is an exact
+integer, its conversion and the two scales round by 2^-24 each, the bias by 2^-24
+of the result; an activation and the rounding of the result as in the tests of the
+16-bit layers (4e-7 |z| beyond 1.13 times its argument's error)."""
+import pytest
+import torch
+
+import dense_gemm_optimisation_row_amd as dg
+from helpers import say
+from layer_reference import act_value
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+STEP = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126, torch.float32: 2.0 ** -126}
+ULP = 2.0 ** -24
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+@pytest.fixture(autouse=True, scope="module")
+def need_gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU (run the CPU suite with -m 'not gpu')")
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def padded(v, pad, shift=0):
+    """v's values as a view of rows that are `pad` longer, `shift` elements into a buffer."""
+    rows, cols = v.shape
+    flat = torch.full((rows * (cols + pad) + shift,), 77, dtype=v.dtype, device=v.device)
+    view = flat[shift:].view(rows, cols + pad)[:, :cols]
+    view.copy_(v)
+    return view
+
+
+def held(rows, cols, dtype, pad, shift):
+    """An output view in a buffer of a mark, and a check that nothing around it was written."""
+    flat = torch.full((rows * (cols + pad) + shift + 16,), 7, dtype=dtype, device="cuda")
+    view = flat[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+
+    def intact():
+        rest = flat.clone()
+        rest[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols] = 7
+        return bool((rest == 7).all())
+    return view, intact
+
+
+# ------------------------------------------------------------ quantisation --
+
+def quantized(x):
+    """(codes, scales) by the definition, in 64 bits."""
+    x = x.double()
+    top = x.abs().amax(-1) if x.shape[-1] else torch.zeros(x.shape[:-1], dtype=torch.float64, device=x.device)
+    bad = ~torch.isfinite(x).all(-1)
+    # fl(top fl(1 / 127)): the product of two FP32 values is exact in 64 bits
+    scale = (top * torch.tensor(1 / 127, dtype=torch.float32).double().item()).float().clamp_min(2.0 ** -126)
+    scale = torch.where(bad, torch.full_like(scale, float("nan")), scale)
+    q = torch.round(x / scale.double()[..., None])
+    return torch.where(bad[..., None], torch.zeros_like(q), q).to(torch.int8), scale
+
+
+def check_codes(x, what, q=None, scale=None):
+    got, s = dg.quantize_i8(x, q=q, scale=scale)
+    want, t = quantized(x)
+    assert got.dtype == torch.int8 and got.shape == x.shape and s.dtype == torch.float32 and s.shape == x.shape[:-1]
+    assert torch.equal(torch.nan_to_num(s, nan=-1.0), torch.nan_to_num(t, nan=-1.0)), f"{what}: scales"
+    assert torch.equal(got, want), f"{what}: {int((got != want).sum())} codes of {got.numel()}"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [1, 2, 7, 8, 63, 64, 100, 511, 512, 513, 777, 2048, 4095, 4096, 4097, 8200, 16384, 16385,
+                               40000, 65536, 65537, 140001])
+def test_codes(K, dtype):
+    for M in (1, 3, 66) + ((1030,) if K <= 4097 else ()):
+        for pad, shift in ((0, 0), (5, 3)):
+            say("quantize", M, K, dtype, pad, shift)
+            x = torch.randn(M, K, generator=gen(K + M), device="cuda") * torch.exp(
+                3 * torch.randn(M, 1, generator=gen(K), device="cuda"))
+            x = padded(x.to(DTYPES[dtype]), pad, shift)
+            q, intact = held(M, K, torch.int8, pad, shift)
+            check_codes(x, f"{M} x {K} {dtype} {pad}", q=q if pad else None)
+            assert intact()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_codes_at_the_borders_between_two(dtype):
+    T = DTYPES[dtype]
+    halves = torch.arange(-254, 255, device="cuda").double() / 2      # the largest is 127: a scale of 1, ties
+    rows = [halves, halves * 2.0 ** -20, halves * 0.75, halves * 1.1]
+    x = torch.stack(rows).to(T)
+    check_codes(x, "ties")
+    # values next to the borders of arbitrary scales, as near as the type comes
+    for seed in range(4):
+        top = (torch.rand(64, 1, generator=gen(seed), device="cuda") * 100 + 0.01).to(T)
+        scale = (top.double() * torch.tensor(1 / 127, dtype=torch.float32).double().item()).float().double()
+        near = (scale * (halves[None] + (0.5 if seed % 2 else 0.0))).to(T)
+        near = torch.where(near.abs() <= top, near, top.expand_as(near))
+        near[:, 0] = top[:, 0]
+        check_codes(near, f"near borders {seed}")
+        bits = near.view(torch.int32 if dtype == "f32" else torch.int16)
+        for d in (-1, 1):
+            moved = (bits + d).view(T)
+            check_codes(torch.where(torch.isfinite(moved), moved, near), f"next to borders {seed} {d}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_codes_of_unusual_rows(dtype):
+    T = DTYPES[dtype]
+    info = torch.finfo(T)
+    x = torch.randn(12, 300, generator=gen(5), device="cuda").to(T)
+    x[0] = 0
+    x[1] = -0.0
+    x[2, 7] = float("nan")
+    x[3, 299] = float("inf")
+    x[4, 0] = float("-inf")
+    x[5] = info.max
+    x[6] = info.min
+    x[7] *= info.smallest_normal
+    x[8] = info.smallest_normal
+    x[9] = 2.0 ** -133 if dtype != "f16" else 2.0 ** -24    # below the normal numbers
+    x[10, 3] = info.max
+    x[11, 1:] = 0
+    check_codes(x, f"unusual {dtype}")
+    check_codes(x[:, :0], "no columns")
+    check_codes(x[:0], "no rows")
+    check_codes(x.view(3, 4, 300), "stack")
+    check_codes(x.view(3, 4, 300).transpose(0, 1), "stack of strided rows")
+    check_codes(x[0], "one row")
+
+
+def test_codes_of_more_rows_than_a_launch_takes():
+    x = torch.randn((1 << 21) + 5, 3, generator=gen(1), device="cuda")
+    check_codes(x, "many rows")
+
+
+# ---------------------------------------------------------------- products --
+
+def codes(g, rows, cols, low=-3, high=4, pad=0, shift=0):
+    return padded(torch.randint(low, high, (rows, cols), generator=g, device="cuda", dtype=torch.int8), pad, shift)
+
+
+def weight(g, K, N, stored, **how):
+    return codes(g, N, K, **how).t() if stored == "NK" else codes(g, K, N, **how)
+
+
+def powers(g, n):
+    return 2.0 ** torch.randint(-3, 3, (n,), generator=g, device="cuda").float()
+
+
+def product(x, w):
+    """x w in 64 bits, exactly."""
+    return x.double() @ w.double()
+
+
+def same(got, want, what):
+    want = want.to(got.dtype)
+    assert got.shape == want.shape and bool((got == want).all()), \
+        f"{what}: {int((got != want).sum())} of {got.numel()} differ"
+
+
+def within(got, ref, err, what):
+    tol = err + (ref.abs() + err) * STEP[got.dtype] + TINY[got.dtype]
+    off = (got.double() - ref).abs()
+    assert bool(torch.isfinite(got).all()), f"{what}: not finite"
+    assert bool((off <= tol).all()), f"{what}: worst {float((off / tol).max()):.3g} of the bound"
+
+
+# rows, outputs, inputs: single elements, odd sizes, few rows of each block count,
+# every ring's tiles whole and ragged, sums shorter than a stage and split ones
+SHAPES = [(1, 1, 1), (1, 17, 16), (3, 5, 7), (1, 4096, 4096), (2, 264, 1040), (16, 128, 512), (17, 40, 4099), (33, 100, 72),
+          (48, 130, 2048), (64, 257, 144), (65, 72, 4096), (66, 65, 16), (129, 130, 131), (200, 1024, 1040),
+          (257, 300, 264), (520, 520, 136), (100, 64, 16000), (1000, 1033, 777)]
+LARGE = [(2056, 2176, 208), (4096, 2048, 80), (1537, 4100, 512)]
+
+
+@pytest.mark.parametrize("stored", ["NK", "KN"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES + LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_linear_of_small_codes(shape, dtype, stored):
+    M, N, K = shape
+    T = DTYPES[dtype]
+    for pad, shift in ((0, 0), (16, 0), (3, 5)):
+        say("linear_i8", shape, dtype, stored, pad, shift)
+        g = gen(M * 7 + N * 3 + K + pad)
+        x, w = codes(g, M, K, pad=pad, shift=shift), weight(g, K, N, stored, pad=pad, shift=shift)
+        sx, sw, b = powers(g, M), powers(g, N), torch.randint(-5, 6, (N,), generator=g, device="cuda").float()
+        r = padded(torch.randint(-3, 4, (M, N), generator=g, device="cuda").to(T), pad)
+        z = product(x, w) * sx.double()[:, None] * sw.double()
+        same(dg.linear_i8(x, sx, w, sw, out_dtype=T), z, "plain")
+        y, intact = held(M, N, T, pad, shift)
+        out = dg.linear_i8(x, sx, w, sw, bias=b, residual=r, activation="relu", y=y)
+        assert out is y
+        # relu's value is exact in FP32, the residual's sum rounds once to it and once to the type
+        same(y, ((z + b.double()).clamp(min=0) + r.double()).float(), "bias, relu, residual")
+        assert intact()
+
+
+@pytest.mark.parametrize("stored", ["NK", "KN"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES + LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_gated_of_small_codes(shape, dtype, stored):
+    M, F, K = shape
+    T = DTYPES[dtype]
+    for pad, shift in ((0, 0), (5, 3)):
+        say("gated_i8", shape, dtype, stored, pad, shift)
+        g = gen(M * 5 + F * 3 + K + pad)
+        x = codes(g, M, K, low=-1, high=2, pad=pad, shift=shift)
+        wg, wu = (weight(g, K, F, stored, low=-1, high=2, pad=pad, shift=shift) for _ in range(2))
+        sx, sg, su = powers(g, M), powers(g, F), powers(g, F)
+        G, U = (product(x, w) * sx.double()[:, None] * s.double() for w, s in ((wg, sg), (wu, su)))
+        h, intact = held(M, F, T, pad, shift)
+        dg.gated_i8(x, sx, wg, sg, wu, su, activation="relu", h=h)
+        # (the product of two exact values rounds once to FP32, and that to the type)
+        same(h, (G.clamp(min=0) * U).float(), "relu")
+        assert intact()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1, 100, 300), (40, 513, 1024), (300, 264, 2000), (1100, 1200, 640)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_values(shape, dtype, act):
+    M, N, K = shape
+    T = DTYPES[dtype]
+    g = gen(M + N + K)
+    x, sx = dg.quantize_i8(torch.randn(M, K, generator=g, device="cuda"))
+    (wq, sw), (uq, su) = (dg.quantize_i8(torch.randn(N, K, generator=g, device="cuda") * K ** -0.5) for _ in range(2))
+    b = torch.randn(N, generator=g, device="cuda")
+    r = torch.randn(M, N, generator=g, device="cuda").to(T)
+    G, U = (product(x, w.t()) * sx.double()[:, None] * s.double() for w, s in ((wq, sw), (uq, su)))
+    z = G + b.double()
+    dz = 3 * ULP * G.abs() + 2 * ULP * z.abs()
+
+    def act_err(z, dz):
+        return dz if act == "none" else 1.13 * dz + 4e-7 * z.abs()
+    v = act_value(act, z)
+    within(dg.linear_i8(x, sx, wq.t(), sw, bias=b, activation=act, out_dtype=T), v, act_err(z, dz), "linear")
+    ref = v + r.double()
+    within(dg.linear_i8(x, sx, wq.t(), sw, bias=b, residual=r, activation=act), ref,
+           act_err(z, dz) + ULP * ref.abs(), "linear with a residual")
+    dG, dU = (4 * ULP * t.abs() for t in (G, U))
+    a, da = act_value(act, G), act_err(G, dG)
+    ref = a * U
+    within(dg.gated_i8(x, sx, wq.t(), sw, uq.t(), su, activation=act, out_dtype=T), ref,
+           da * U.abs() + a.abs() * dU + da * dU + 2 * ULP * ref.abs(), "gated")
+
+
+def test_the_longest_sum_of_the_largest_codes():
+    K = 131071
+    for M in (1, 70):
+        x = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+        w = torch.full((24, K), -128, dtype=torch.int8, device="cuda")
+        w[1] = 127
+        one = torch.ones
+        y = dg.linear_i8(x, one(M, device="cuda"), w.t(), one(24, device="cuda"), out_dtype=torch.float32)
+        same(y, product(x, w.t()).float(), f"{M} rows")
+    with pytest.raises(dg.GemmError):
+        x = torch.zeros(1, K + 1, dtype=torch.int8, device="cuda")
+        dg.linear_i8(x, one(1, device="cuda"), x.t(), one(1, device="cuda"))
+
+
+def test_sizes_of_zero():
+    z = torch.zeros
+    for M, N, K in ((0, 8, 16), (8, 0, 16), (8, 24, 0), (70, 24, 0), (0, 0, 0)):
+        x, w = z(M, K, dtype=torch.int8, device="cuda"), z(N, K, dtype=torch.int8, device="cuda").t()
+        sx, sw = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+        b = torch.arange(N, device="cuda").float()
+        y = dg.linear_i8(x, sx, w, sw, bias=b, out_dtype=torch.float32)
+        same(y, b.double().expand(M, N), "bias alone")
+        assert dg.gated_i8(x, sx, w, sw, w, sw).shape == (M, N)
+
+
+def test_leading_dimensions_and_defaults():
+    g = gen(3)
+    x = codes(g, 24, 64).view(2, 3, 4, 64)
+    w, sw = codes(g, 40, 64).t(), powers(g, 40)
+    sx = powers(g, 24).view(2, 3, 4)
+    flat = product(x.reshape(24, 64), w) * sx.double().view(24, 1) * sw.double()
+    y = dg.linear_i8(x, sx, w, sw)
+    assert y.dtype == torch.bfloat16 and y.shape == (2, 3, 4, 40)
+    same(y.view(24, 40), flat, "stack")
+    turned = x.transpose(0, 2)
+    y = dg.linear_i8(turned, sx.transpose(0, 2).contiguous(), w, sw, out_dtype=torch.float32)
+    same(y.transpose(0, 2).reshape(24, 40), flat, "strided stack")
+    r = torch.ones(2, 3, 4, 40, dtype=torch.float16, device="cuda")
+    y = dg.linear_i8(x, sx, w, sw, residual=r, y=r)      # in place
+    assert y is r and y.dtype == torch.float16
+    same(y.view(24, 40), flat + 1, "in place")
+    # the halves of one matrix as the gate's and the up projection's weights
+    both, s = codes(g, 80, 64), powers(g, 80)
+    h = dg.gated_i8(x, sx, both[:40].t(), s[:40], both[40:].t(), s[40:], activation="none", out_dtype=torch.float32)
+    G = product(x.reshape(24, 64), both.t()) * sx.double().view(24, 1) * s.double()
+    same(h.view(24, 40), (G[:, :40] * G[:, 40:]).float(), "halves")
+
+
+def test_scales_of_nan_reach_their_row_and_column_only():
+    g = gen(9)
+    for M in (3, 100):
+        x, w, sx, sw = codes(g, M, 96), codes(g, 50, 96).t(), powers(g, M), powers(g, 50)
+        sx[1], sw[7] = float("nan"), float("inf")
+        y = dg.linear_i8(x, sx, w, sw, out_dtype=torch.float32)
+        ref = (product(x, w).float() * sx[:, None]) * sw
+        assert torch.equal(torch.nan_to_num(y, nan=1e9, posinf=2e9, neginf=-2e9),
+                           torch.nan_to_num(ref, nan=1e9, posinf=2e9, neginf=-2e9))
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_a_served_block_in_a_graph_and_on_another_stream(M):
+    """Norm, codes, gated projections, codes, down projection: as one step, captured and
+    replayed on new inputs, and on a stream of its own."""
+    g = gen(21)
+    D, F = 256, 720
+    norm = torch.rand(D, generator=g, device="cuda").to(torch.bfloat16)
+    (wg, sg), (wu, su) = (dg.quantize_i8(torch.randn(F, D, generator=g, device="cuda") / 16) for _ in range(2))
+    wd, sd = dg.quantize_i8(torch.randn(D, F, generator=g, device="cuda") / 27)
+
+    def step(x, stream=None):
+        n = dg.layer_norm(x, norm, stream=stream)
+        q, s = dg.quantize_i8(n, stream=stream)
+        h = dg.gated_i8(q, s, wg.t(), sg, wu.t(), su, stream=stream)
+        p, t = dg.quantize_i8(h, stream=stream)
+        return n, q, s, h, p, t, dg.linear_i8(p, t, wd.t(), sd, residual=x, stream=stream)
+
+    def check(x, out, what):
+        n, q, s, h, p, t, y = out
+        for a, codes_, scales in ((n, q, s), (h, p, t)):
+            want, steps = quantized(a)
+            assert torch.equal(codes_, want) and torch.equal(scales, steps), what
+        G, U = (product(q, w.t()) * s.double()[:, None] * v.double() for w, v in ((wg, sg), (wu, su)))
+        a = act_value("silu", G)
+        da = 1.13 * 4 * ULP * G.abs() + 4e-7 * G.abs()
+        within(h, a * U, da * U.abs() + 7 * ULP * (a * U).abs() + 4 * ULP * da * U.abs(), what + ": gated")
+        z = product(p, wd.t()) * t.double()[:, None] * sd.double()
+        within(y, z + x.double(), 3 * ULP * z.abs() + 3 * ULP * (z + x.double()).abs(), what + ": down")
+
+    def inputs(seed):
+        return torch.randn(M, D, generator=gen(seed), device="cuda").to(torch.bfloat16)
+    x = inputs(1)
+    check(x, step(x), "eager")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = step(x, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    check(x, out, "stream")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x)
+    for seed in range(2, 6):
+        x.copy_(inputs(seed))
+        step(inputs(seed + 10))            # eager work between the replays
+        graph.replay()
+        torch.cuda.synchronize()
+        check(x, out, f"replay {seed}")
