@@ -22,7 +22,6 @@
 #include <stdint.h>
 
 #include "ring.h"
-#include "ring_plan.h"
 
 namespace dgor {
 namespace {
@@ -55,32 +54,42 @@ __device__ __forceinline__ void store8_of(int fmt, void *p, size_t at, int n, co
         store8_16((uint16_t *)p + at, n, fmt == kF16 ? pack8<Half16>(f) : pack8<Brain16>(f));
 }
 
-// Matrices in two terms: rows padded with zeros to whole units.
+// Matrices in two terms.  A row is groups of 32 columns, each 64 bytes of higher
+// terms and then 64 of lower ones, so that what a 32-deep stage takes of a row is
+// one whole line of 128 bytes: a compute unit takes about as many pieces a
+// microsecond whatever their size, and from two matrices, 64 bytes at a time, the
+// 64 x 64 tile took 17 us for 777 x 1033 by its transpose.  Rows are padded
+// with zeros to whole units of eight.
 struct Pair {
-    uint16_t *hi;
-    long long term, matrix;   // elements from a value's higher term to its lower, and to the next matrix
+    uint16_t *p;
+    long long matrix;   // elements from a matrix to the next
     int ld;
+    __host__ __device__ static int stride(int cols) { return 2 * ((cols + 31) / 32 * 32); }
+    __device__ __forceinline__ uint16_t *at(long long m, int row, int col) const
+    {
+        return p + m * matrix + (size_t)row * ld + 2 * (col & ~31) + (col & 31);
+    }
     __device__ __forceinline__ void load8(long long m, int row, int col, float (&f)[8]) const
     {
-        const uint16_t *p = hi + m * matrix + (size_t)row * ld + col;
+        const uint16_t *q = at(m, row, col);
         float lo[8];
-        unpack8<Half16>(*reinterpret_cast<const u32x4 *>(p), f);
-        unpack8<Half16>(*reinterpret_cast<const u32x4 *>(p + term), lo);
+        unpack8<Half16>(*reinterpret_cast<const u32x4 *>(q), f);
+        unpack8<Half16>(*reinterpret_cast<const u32x4 *>(q + 32), lo);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             f[e] += lo[e];
     }
     __device__ __forceinline__ void store8(long long m, int row, int col, const float (&f)[8]) const
     {
-        uint16_t *p = hi + m * matrix + (size_t)row * ld + col;
+        uint16_t *q = at(m, row, col);
         const u32x4 h = pack8<Half16>(f);
         float r[8];
         unpack8<Half16>(h, r);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             r[e] = f[e] - r[e];
-        *reinterpret_cast<u32x4 *>(p) = h;
-        *reinterpret_cast<u32x4 *>(p + term) = pack8<Half16>(r);
+        *reinterpret_cast<u32x4 *>(q) = h;
+        *reinterpret_cast<u32x4 *>(q + 32) = pack8<Half16>(r);
     }
 };
 
@@ -140,7 +149,10 @@ __global__ __launch_bounds__(256) void start_kernel(Source g, Pair x, const doub
     __shared__ float tile[64][65];
     const long long m = blockIdx.x / per;
     const int id = (int)(blockIdx.x - m * per), r0 = 64 * (id / across), c0 = 64 * (id % across);
-    const double v = block_sum((int)threadIdx.x < blocks ? sums[m * blocks + threadIdx.x] : 0.0, lds);
+    double v = 0;
+    for (int i = threadIdx.x; i < blocks; i += 256)
+        v += sums[m * blocks + i];
+    v = block_sum(v, lds);
     const double factor = by / (sqrt(v) + eps);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -190,25 +202,18 @@ struct Finish {
     int out_ld, fmt;
     bool turned;
 
-    __device__ __forceinline__ void value(long long m, int row, int col, float (&v)[8]) const
+    // Eight neighbouring elements of a row: their value from the sums v and, of the
+    // polynomial, A's elements a (of the symmetric results a column's are a row's).
+    __device__ __forceinline__ void value(int row, int col, float (&v)[8], const float (&a)[8]) const
     {
-        if (polynomial) {
-            float a[8];
-            with.load8(m, row, col, a);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = __builtin_fmaf(alpha, v[e], beta * a[e]) + (row == col + e ? diagonal : 0.f);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] *= alpha;
-        }
+        for (int e = 0; e < 8; ++e)
+            v[e] = polynomial ? __builtin_fmaf(alpha, v[e], beta * a[e]) + (row == col + e ? diagonal : 0.f)
+                              : alpha * v[e];
     }
-    // Eight neighbouring elements of a row of the result, n of them inside it.  (Of
-    // the symmetric results also the ones of a column: they are the same.)
-    __device__ __forceinline__ void put(long long m, int row, int col, int n, float (&v)[8]) const
+    // n of them inside the result
+    __device__ __forceinline__ void store(long long m, int row, int col, int n, const float (&v)[8]) const
     {
-        value(m, row, col, v);
         if (out)
             store8_of(fmt, out, m * out_matrix + (size_t)row * out_ld + col, n, v);
         else
@@ -216,138 +221,634 @@ struct Finish {
     }
 };
 
-// The tile of a symmetric result that workgroup `id` of `all` computes: row by row
-// of the lower triangle, those of one XCD (id % 8) next to each other.
-__device__ __forceinline__ void triangle_tile(int id, int all, int &tm, int &tn)
-{
-    const int per = all >> 3, rem = all & 7, xcd = id & 7;
-    const int l = xcd * per + min(xcd, rem) + (id >> 3);
-    int r = (int)((sqrtf(8.f * (float)l + 1.f) - 1.f) * 0.5f);
-    while ((long long)(r + 1) * (r + 2) / 2 <= l)
-        ++r;
-    while ((long long)r * (r + 1) / 2 > l)
-        --r;
-    tm = r;
-    tn = l - r * (r + 1) / 2;
-}
+// The three products of a step.
+enum Which { kGram, kPolynomial, kUpdate };
 
-struct Batch {
-    long long a, b;   // elements from a matrix's operands to the next one's
-    int per;          // tiles of a matrix
+// One product of matrices in two terms: A, M x K, by B, N x K (TB) or K x N.
+struct Operands {
+    int M, N, K;
+    Pair a, b;
 };
 
-template <int BM, int BN, bool TB, bool SYM>
-__global__ __launch_bounds__(256) void newton_schulz_kernel(Product p, Batch batch, Finish f)
-{
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[ring_bytes(BM, BN, false)];
-    constexpr int HM = BM / 2, HN = BN / 2, FA = HM / 16, FB = HN / 16;
-    const int m = (int)blockIdx.x / batch.per, id = (int)blockIdx.x - m * batch.per, part = (int)blockIdx.y;
-    int tm, tn;
-    if (SYM)
-        triangle_tile(id, batch.per, tm, tn);
-    else
-        dgor_tile_of_block(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    p.A.p += m * batch.a;
-    p.B.p += m * batch.b;
-    floatx4 acc[FA][FB];
-    ring_sum<OpHalf, BM, BN, false, TB, false>(p, lds, tm, tn, 0, part, acc);
+// The 32-deep stages of all tiles of all matrices, dealt to the workgroups: the
+// first `whole` tiles a tile at a time, in full rounds, in which the workgroups of an
+// XCD read the same panels at the same time; the others' stages in runs of `run`,
+// one run a workgroup.  A tile in several runs is left in FP32 in their slabs, two a
+// workgroup (the tile that its run begins in, and the one that it ends in), and
+// joined by another launch.
+struct Work {
+    int tiles, per, stages;   // tiles of all matrices and of one; stages of a tile
+    int tiles_m, tiles_n;     // of one matrix's result
+    int groups, whole, run;
+    float *slabs;
+    // slab of a tile that begins at stage `begin` of the runs' stages, in run w
+    __device__ __forceinline__ size_t slab(int w, long long begin, int size) const
+    {
+        return (size_t)(2 * w + (begin >= (long long)w * run ? 1 : 0)) * size;
+    }
+};
 
-    // 32 rows at a time through the wavefront's own part of LDS
-    constexpr int ROW = HN + 4, LANES = HN / 8, STEP = 64 / LANES;
-    static_assert(4 * 32 * ROW * 4 <= ring_bytes(BM, BN, false), "the epilogue uses the ring's LDS");
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    float *w = reinterpret_cast<float *>(lds) + wave * 32 * ROW;
-    const int first = tm * BM + (wave >> 1) * HM, left = tn * BN + (wave & 1) * HN;
-    const bool along = p.splits > 1 || !f.turned, across = p.splits <= 1 && (f.turned || (SYM && tm != tn));
-#pragma unroll 1
-    for (int round = 0; round < FA / 2; ++round) {
-        stage_rows(acc, round, w, ROW, lane);
-        const int top = first + 32 * round;
-        if (along) {
-            const int c = 8 * (lane % LANES), col = left + c;
-#pragma unroll 1
-            for (int r = lane / LANES; r < 32; r += STEP) {
-                const int row = top + r;
-                if (row >= p.M || col >= p.N)
-                    break;
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = w[r * ROW + c + e];
-                if (p.splits > 1)
-                    store8_f32(p.part + ((long long)m * p.splits + part) * part_size(p) +
-                                   (size_t)row * part_stride(p) + col, 8, v);
-                else
-                    f.put(m, row, col, p.N - col, v);
-            }
-        }
-        if (across) {   // four lanes a column: 64 bytes of 16-bit results
-            const int r = 8 * (lane & 3), row = top + r;
-#pragma unroll 1
-            for (int c = lane >> 2; c < HN; c += 16) {
-                const int col = left + c;
-                if (row >= p.M || col >= p.N)
-                    break;
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = w[(r + e) * ROW + c];
-                f.put(m, col, row, p.M - row, v);
-            }
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+// Tile `id` of a matrix: all of them, or (symmetric) those on and below the
+// diagonal, row by row.
+template <bool SYM>
+__device__ __forceinline__ void tile_of(const Work &w, int id, int &tm, int &tn)
+{
+    if (SYM) {
+        int r = (int)((sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
+        while ((long long)(r + 1) * (r + 2) / 2 <= id)
+            ++r;
+        while ((long long)r * (r + 1) / 2 > id)
+            --r;
+        tm = r;
+        tn = id - (int)((long long)r * (r + 1) / 2);
+    } else {
+        // groups of four tile rows, column by column: neighbours share panels
+        const int span = 4 * w.tiles_n, group = id / span, in = id - group * span, first = 4 * group;
+        const int rows = min(w.tiles_m - first, 4);
+        tm = first + in % rows;
+        tn = in / rows;
     }
 }
 
-// Adds the parts of split sums: a 64 x 64 block a workgroup.
-template <bool SYM>
-__global__ __launch_bounds__(256) void newton_schulz_join_kernel(Product p, Batch batch, Finish f)
+// The tile's main loop: 32-deep stages of both terms of both operands, loaded
+// straight into a ring of NB LDS buffers, the fragments of the next stage read
+// and the loads of the stage NB further issued between the MFMAs.  A block of 16 x
+// 16 outputs takes three MFMAs from four fragments, where a loop over the three
+// products would read six and load each operand's higher term twice.
+//
+// A stage buffer: A, then B.  Rows along k (A, and B as N x K): eight units of 16
+// bytes a row, higher terms and then lower ones, unit c of row r at 8 r + (c ^
+// ((r >> 1) & 7)).  B as K x N: two halves of the tile's columns, each 32 k rows of
+// W = HN / 4 units, unit u of row k at W k + (u ^ x(k)), x as in ring.h.
+//
+// Before stage t: this wavefront's loads of stage t + 1 and its reads of stage t
+// have returned, then a barrier.  So all of stage t + 1 has landed, and nobody
+// still reads stage t's buffer, which the loads of stage t + NB refill.
+template <int BM, int BN>
+constexpr int stage_bytes() { return (BM + BN) * 32 * 2 * 2; }
+
+// `steps` stages from s0, those from `stop` on zeros, by the four wavefronts of
+// one of the workgroup's groups; `lds` is the group's.
+template <int BM, int BN, int NB, bool TB>
+__device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
+                                         int stop, int steps, floatx4 (&acc)[BM / 32][BN / 32])
 {
-    __shared__ float tile[64][68];
-    const int m = (int)blockIdx.x / batch.per, id = (int)blockIdx.x - m * batch.per;
-    int tm, tn;
-    if (SYM)
-        triangle_tile(id, batch.per, tm, tn);
-    else
-        dgor_tile_of_block(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    const bool across = f.turned || (SYM && tm != tn);
-    const int r0 = 64 * tm, c0 = 64 * tn;
+    constexpr int BK = 32, HM = BM / 2, HN = BN / 2, FA = HM / 16, FB = HN / 16, W = HN / 4;
+    constexpr int LPA = BM / 32, LPB = BN / 32, LOADS = LPA + LPB;   // a wavefront's, of a stage
+    constexpr int HALF_B = HN * 128, B_AT = BM * 128, STAGE = stage_bytes<BM, BN>();
+    const uint32_t ring = lds_address(lds);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) & 3);
+    const int lda = p.a.ld, ldb = p.b.ld;
+    const int a_left = p.M - m0, end = min(p.K, BK * stop);   // what is past `end` reads as zero
+
+    // ---- loads.  Of rows along k eight a load: unit (lane % 8) of row lane / 8,
+    // which holds k's unit `unit` & 3 of the term unit / 4
+    const int lhalf = wave >> 1;
+    uint32_t a_off[2], b_off[TB ? 2 : LPB];
+    int kc[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int r = (int)(threadIdx.x >> 3) + 32 * t, c = 8 * (int)(threadIdx.x & 7);
+    for (int q = 0; q < 2; ++q) {
+        const int unit = (lane & 7) ^ ((4 * q + (lane >> 4)) & 7);
+        kc[q] = 8 * (unit & 3);
+        a_off[q] = (uint32_t)((8 * (LPA * wave + q) + (lane >> 3)) * lda + 8 * unit) * 2u;
+        if (TB)
+            b_off[q] = (uint32_t)((8 * (LPB * wave + q) + (lane >> 3)) * ldb + 8 * unit) * 2u;
+    }
+    const uint32_t a_rows = (uint32_t)(16 * lda) * 2u, b_rows = (uint32_t)(16 * ldb) * 2u;
+    const int bcol = TB ? n0 : n0 + HN * lhalf, b_left = p.N - bcol;
+    if (!TB)
+#pragma unroll
+        for (int q = 0; q < LPB; ++q) {
+            const int k = (64 / W) * (LPB * (wave & 1) + q) + lane / W, u = (lane % W) ^ row_swizzle<W>(k);
+            b_off[TB ? 0 : q] = 32 * (u >> 3) + 8 * (u & 3) < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
+        }
+    const size_t b_step = TB ? 2 : (size_t)ldb;   // elements from a k to the next
+    const uint16_t *ap = p.a.p + m * p.a.matrix + (size_t)m0 * lda + (size_t)(2 * BK) * s0;
+    const uint16_t *bp = p.b.p + m * p.b.matrix + (TB ? (size_t)bcol * ldb : (size_t)(2 * bcol)) + BK * s0 * b_step;
+    int k_left = end - BK * s0;
+    uint32_t to = ring;   // the buffer that the next loads fill
+    const uint32_t at_a = (uint32_t)(LPA * wave * 1024);
+    const uint32_t at_b = (uint32_t)(B_AT + (TB ? LPB * wave * 1024 : lhalf * HALF_B + LPB * (wave & 1) * 1024));
+    struct Loads {
+        intx4 a, b;
+        int k_left;
+        uint32_t to;
+    };
+    auto loads = [&]() {   // of the next stage
+        Loads L;
+        L.k_left = k_left;
+        L.to = to;
+        L.a = rsrc_words(ap, 0);
+        L.b = rsrc_words(bp, 0);
+        L.a.z = k_left <= 0 ? 0 : (a_left >= BM ? 0x7fffffff : (a_left - 1) * lda * 2 + 128);
+        if (TB)
+            L.b.z = k_left <= 0 ? 0 : (b_left >= BN ? 0x7fffffff : (b_left - 1) * ldb * 2 + 128);
+        else
+            L.b.z = k_left >= BK || b_left <= 0 ? 0x7fffffff
+                                                : (k_left <= 0 ? 0 : (k_left - 1) * ldb * 2 + 4 * ((b_left + 31) & ~31));
+        ap += 2 * BK;
+        bp += BK * b_step;
+        k_left -= BK;
+        to = to == ring + (uint32_t)((NB - 1) * STAGE) ? ring : to + STAGE;
+        return L;
+    };
+    auto load = [&](const Loads &L, int i) {   // load i of the stage
+        if (i < LPA)
+            load_to_lds(L.a, L.to + at_a + (uint32_t)(i * 1024),
+                        kc[i & 1] >= L.k_left ? kOutside : a_off[i & 1] + (uint32_t)(i >> 1) * a_rows);
+        else if (TB)
+            load_to_lds(L.b, L.to + at_b + (uint32_t)((i - LPA) * 1024),
+                        kc[i & 1] >= L.k_left ? kOutside : b_off[(i - LPA) & 1] + (uint32_t)((i - LPA) >> 1) * b_rows);
+        else
+            load_to_lds(L.b, L.to + at_b + (uint32_t)((i - LPA) * 1024), b_off[TB ? 0 : i - LPA]);
+    };
+    static_assert(LPA % 2 == 0 && LPB % 2 == 0, "");
+
+    // ---- fragments.  Lane (g, s) = (lane / 16, lane % 16): k 8 g .. 8 g + 7 of
+    // row s of A's block and column s of B's
+    const int s16 = lane & 15, g = lane >> 4;
+    const uint32_t row_lane = (uint32_t)(s16 * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
+    const uint32_t a_lane = row_lane + (uint32_t)((wave >> 1) * HM * 128);
+    const int kr = 8 * g + (s16 >> 2);
+    const uint32_t b_lane = (uint32_t)B_AT + (TB ? row_lane + (uint32_t)((wave & 1) * HN * 128)
+                                                 : (uint32_t)(kr * (W * 16) + 8 * (s16 & 1) + (wave & 1) * HALF_B));
+    uint32_t b_unit[TB ? 1 : FB];   // of the higher terms; the lower ones are four units on
+    if (!TB)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+            b_unit[TB ? 0 : j] = (uint32_t)(((8 * (j >> 1) + 2 * (j & 1) + ((s16 & 3) >> 1)) ^ row_swizzle<W>(kr)) * 16);
+    auto read_b = [&](uint32_t at, int j, int term) -> halfx8 {
+        if (TB)
+            return *reinterpret_cast<const halfx8 *>(lds + at + ((b_lane ^ (uint32_t)(64 * term)) + (uint32_t)(j * 2048)));
+        const uint8_t *q = lds + at + b_lane + (b_unit[TB ? 0 : j] ^ (uint32_t)(64 * term));
+        const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
+        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * (W * 16)));
+        return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    struct Fragments {
+        halfx8 a[2][FA], b[2][FB];
+    };
+    constexpr int READS = 2 * (FA + FB);
+    auto read = [&](uint32_t at, int r, Fragments &f) {   // read r of the stage in the buffer at `at`
+        if (r < 2 * FA)
+            f.a[r / FA][r % FA] = *reinterpret_cast<const halfx8 *>(
+                lds + at + ((a_lane ^ (uint32_t)(64 * (r / FA))) + (uint32_t)((r % FA) * 2048)));
+        else
+            f.b[(r - 2 * FA) / FB][(r - 2 * FA) % FB] = read_b(at, (r - 2 * FA) % FB, (r - 2 * FA) / FB);
+    };
+
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                asm("v_accvgpr_write_b32 %0, 0" : "=a"(acc[i][j][r]));   // keeps the array in the accumulators
+
+    auto stage = [&](uint32_t next, const Fragments &c, Fragments &n) {
+        constexpr int MFMAS = 3 * FA * FB;
+        constexpr int FIRST = MFMAS - READS >= LOADS ? READS : 2, EVERY = (MFMAS - FIRST) / LOADS;
+        static_assert(EVERY > 0 && READS <= MFMAS, "all issued");
+        Loads L;
+#pragma unroll
+        for (int x = 0; x < MFMAS; ++x) {
+            const int i = x / (3 * FB), t = x / FB % 3, j = x % FB;   // hi hi, lo hi, hi lo
+            acc[i][j] = OpHalf::mfma(c.a[t == 1][i], c.b[t == 2][j], acc[i][j]);
+            if (x < READS)
+                read(next, x, n);
+            if (x == 0)
+                L = loads();
+            if (x >= FIRST && (x - FIRST) % EVERY == EVERY - 1 && (x - FIRST) / EVERY < LOADS)
+                load(L, (x - FIRST) / EVERY);
+            // keep this order: the compiler would otherwise cluster the reads and
+            // loads, and move MFMAs across the barrier
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    Fragments f0, f1;
+#pragma unroll
+    for (int st = 0; st < NB; ++st) {
+        const Loads L = loads();
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            load(L, i);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt((NB - 1) * LOADS));
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int r = 0; r < READS; ++r)
+        read(0, r, f0);
+    uint32_t at = 0;   // the buffer of the stage whose fragments are in use
+    auto begin = [&]() {
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0((NB - 2) * LOADS));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        at = at == (uint32_t)((NB - 1) * STAGE) ? 0u : at + STAGE;
+    };
+    for (int t = 0; t < steps; t += 2) {
+        begin();
+        stage(at, f0, f1);
+        if (t + 1 < steps) {
+            begin();
+            stage(at, f1, f0);
+        }
+    }
+    // no load may still be writing LDS, nor a wavefront reading the ring
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
+    __builtin_amdgcn_s_barrier();
+    dgor_acc_hazard_wait();
+}
+
+// The same on a tile of 256 x 256, 128 x 128 a wavefront, whose 32 fragments a stage
+// leave no registers for the next stage's: two buffers, and the stage in four
+// quadrants of 48 MFMAs, in an order in which a half of the fragments is last
+// used long before the next stage wants it.  With A's halves 0 and 1 and B's, f the
+// one that the stage begins with and o the other, the quadrants are (0, f), (0, o),
+// (1, o), (1, f), and the next stage begins with o.  Meanwhile are read: B's o and
+// A's 1 of this stage, then A's 0 and B's o of the next.  Half way through the stage
+// nobody reads its buffer any more: the loads of the stage after the next go there in
+// the two quadrants that follow, and have the two after that to land.
+//
+// Why this tile: LDS serves 128 bytes a cycle, of which a stage moves 192 KB here in
+// its 3072 cycles of MFMAs, and 96 KB on 128 x 128 in 768, which is then bound by it.
+template <bool TB>
+__device__ __forceinline__ void quad_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
+                                         int steps, floatx4 (&acc)[8][8])
+{
+    constexpr int BK = 32, SIDE = 256, HALF = 128, LP = SIDE / 32;
+    constexpr int HALF_B = HALF * 128, B_AT = SIDE * 128, STAGE = stage_bytes<SIDE, SIDE>();
+    const uint32_t ring = lds_address(lds);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lda = p.a.ld, ldb = p.b.ld;
+    const int a_left = p.M - m0, end = min(p.K, BK * (s0 + steps));
+
+    // ---- loads, as in pair_sum
+    const int lhalf = wave >> 1;
+    uint32_t a_off[2], b_off[TB ? 2 : LP];
+    int kc[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int unit = (lane & 7) ^ ((4 * q + (lane >> 4)) & 7), row = 8 * (LP * wave + q) + (lane >> 3);
+        kc[q] = 8 * (unit & 3);
+        a_off[q] = (uint32_t)(row * lda + 8 * unit) * 2u;
+        if (TB)
+            b_off[q] = (uint32_t)(row * ldb + 8 * unit) * 2u;
+    }
+    const uint32_t a_rows = (uint32_t)(16 * lda) * 2u, b_rows = (uint32_t)(16 * ldb) * 2u;
+    const int bcol = TB ? n0 : n0 + HALF * lhalf, b_left = p.N - bcol;
+    if (!TB)
+#pragma unroll
+        for (int q = 0; q < LP; ++q) {
+            const int k = 2 * (LP * (wave & 1) + q) + (lane >> 5), u = (lane & 31) ^ row_swizzle<16>(k);
+            b_off[TB ? 0 : q] = 32 * (u >> 3) + 8 * (u & 3) < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
+        }
+    const size_t b_step = TB ? 2 : (size_t)ldb;
+    const uint16_t *ap = p.a.p + m * p.a.matrix + (size_t)m0 * lda + (size_t)(2 * BK) * s0;
+    const uint16_t *bp = p.b.p + m * p.b.matrix + (TB ? (size_t)bcol * ldb : (size_t)(2 * bcol)) + BK * s0 * b_step;
+    int k_left = end - BK * s0;
+    const uint32_t at_a = ring + (uint32_t)(LP * wave * 1024);
+    const uint32_t at_b = ring + (uint32_t)(B_AT + (TB ? LP * wave * 1024 : lhalf * HALF_B + LP * (wave & 1) * 1024));
+    struct Loads {
+        intx4 a, b;
+        int k_left;
+    };
+    auto loads = [&]() {
+        Loads L;
+        L.k_left = k_left;
+        L.a = rsrc_words(ap, 0);
+        L.b = rsrc_words(bp, 0);
+        L.a.z = k_left <= 0 ? 0 : (a_left >= SIDE ? 0x7fffffff : (a_left - 1) * lda * 2 + 128);
+        if (TB)
+            L.b.z = k_left <= 0 ? 0 : (b_left >= SIDE ? 0x7fffffff : (b_left - 1) * ldb * 2 + 128);
+        else
+            L.b.z = k_left >= BK || b_left <= 0 ? 0x7fffffff
+                                                : (k_left <= 0 ? 0 : (k_left - 1) * ldb * 2 + 4 * ((b_left + 31) & ~31));
+        ap += 2 * BK;
+        bp += BK * b_step;
+        k_left -= BK;
+        return L;
+    };
+    auto load = [&](const Loads &L, int buffer, int i) {
+        const uint32_t to = (uint32_t)(buffer * STAGE + (i % LP) * 1024);
+        if (i < LP)
+            load_to_lds(L.a, at_a + to, kc[i & 1] >= L.k_left ? kOutside : a_off[i & 1] + (uint32_t)(i >> 1) * a_rows);
+        else if (TB)
+            load_to_lds(L.b, at_b + to,
+                        kc[i & 1] >= L.k_left ? kOutside : b_off[i & 1] + (uint32_t)((i - LP) >> 1) * b_rows);
+        else
+            load_to_lds(L.b, at_b + to, b_off[TB ? 0 : i - LP]);
+    };
+
+    // ---- fragments, as in pair_sum; half h of A's and B's blocks is four
+    const int s16 = lane & 15, g = lane >> 4;
+    const uint32_t row_lane = (uint32_t)(s16 * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
+    const uint32_t a_lane = row_lane + (uint32_t)((wave >> 1) * HALF * 128);
+    const int kr = 8 * g + (s16 >> 2);
+    const uint32_t b_lane = (uint32_t)B_AT + (TB ? row_lane + (uint32_t)((wave & 1) * HALF * 128)
+                                                 : (uint32_t)(kr * 512 + 8 * (s16 & 1) + (wave & 1) * HALF_B));
+    uint32_t b_unit[TB ? 1 : 4];   // of blocks 0 to 3; 4 to 7 are sixteen units on
+    if (!TB)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b_unit[TB ? 0 : j] = (uint32_t)(((8 * (j >> 1) + 2 * (j & 1) + ((s16 & 3) >> 1)) ^ row_swizzle<16>(kr)) * 16);
+    halfx8 fa[2][8], fb[2][8];
+    auto read_a = [&](int buffer, int h, int r) {   // read r of 8 of A's half h
+        const int t = r >> 2, i = 4 * h + (r & 3);
+        fa[t][i] = *reinterpret_cast<const halfx8 *>(
+            lds + ((a_lane ^ (uint32_t)(64 * t)) + (uint32_t)(buffer * STAGE + i * 2048)));
+    };
+    auto read_b = [&](int buffer, int h, int r) {
+        const int t = r >> 2, j = 4 * h + (r & 3);
+        if (TB) {
+            fb[t][j] = *reinterpret_cast<const halfx8 *>(
+                lds + ((b_lane ^ (uint32_t)(64 * t)) + (uint32_t)(buffer * STAGE + j * 2048)));
+            return;
+        }
+        const uint8_t *q = lds + (b_lane + (b_unit[TB ? 0 : j & 3] ^ (uint32_t)(64 * t)) + (uint32_t)(buffer * STAGE + (j >> 2) * 256));
+        const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
+        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * 512));
+        fb[t][j] = __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                asm("v_accvgpr_write_b32 %0, 0" : "=a"(acc[i][j][r]));   // keeps the array in the accumulators
+
+    // A quadrant: its MFMAs, eight reads between the first of them, and (with
+    // loads) the given eight loads between all
+    auto quadrant = [&](int ih, int jh, auto reads, auto issue) {
+#pragma unroll
+        for (int x = 0; x < 48; ++x) {
+            const int i = 4 * ih + x / 12, t = x / 4 % 3, j = 4 * jh + x % 4;   // hi hi, lo hi, hi lo
+            acc[i][j] = OpHalf::mfma(fa[t == 1][i], fb[t == 2][j], acc[i][j]);
+            if (x % 3 == 0 && x / 3 < 8)
+                reads(x / 3);
+            if (x % 6 == 5)
+                issue(x / 6);
+            __builtin_amdgcn_sched_barrier(0);   // keep this order
+        }
+    };
+    auto none = [](int) {};
+    auto stage = [&](int parity) {   // of the stage: its buffer, and the half of B that it begins with
+        const int f = parity, o = 1 - parity;
+        quadrant(0, f, [&](int r) { read_b(parity, o, r); }, none);
+        quadrant(0, o, [&](int r) { read_a(parity, 1, r); }, none);
+        // this stage's reads have returned and the next stage's loads landed,
+        // everyone's
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
+        __builtin_amdgcn_s_barrier();
+        const Loads L = loads();
+        __builtin_amdgcn_sched_barrier(0);
+        quadrant(1, o, [&](int r) { read_a(o, 0, r); }, [&](int l) { load(L, parity, l); });
+        quadrant(1, f, [&](int r) { read_b(o, o, r); }, [&](int l) { load(L, parity, 8 + l); });
+    };
+
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+        const Loads L = loads();
+#pragma unroll
+        for (int i = 0; i < 2 * LP; ++i)
+            load(L, st, i);
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * LP));
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        read_a(0, 0, r);
+        read_b(0, 0, r);
+    }
+    for (int t = 0; t < steps; t += 2) {
+        stage(0);
+        if (t + 1 < steps)
+            stage(1);
+    }
+    // no load may still be writing LDS, nor a wavefront reading the buffers
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
+    __builtin_amdgcn_s_barrier();
+    dgor_acc_hazard_wait();
+}
+
+// GROUPS: groups of four wavefronts, which take halves of a tile's stages on rings
+// of their own and add their sums in LDS.  Two on the 64 x 64 tile, whose stages are
+// too short for one wavefront a SIMD to cover its own waits.
+template <int SIDE, int NB, int GROUPS, Which WHICH>
+__global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p, Work work, Finish f)
+{
+    constexpr bool SYM = WHICH != kUpdate, TB = SYM;
+    constexpr int HALF = SIDE / 2, F = HALF / 16;
+    constexpr int ROW = HALF + 4, LANES = HALF / 8, STEP = 64 / LANES;
+    constexpr int ROWS = 32 / GROUPS;                                // of a round, a group's
+    constexpr int BATCH = SIDE == 128 ? 4 : ROWS / STEP < 2 ? 1 : 2;   // rows of a lane at once
+    constexpr int RING = NB * stage_bytes<SIDE, SIDE>(), REGION = 32 * ROW;
+    static_assert(GROUPS == 1 || F == 2, "a group's sums are one round");
+    static_assert(4 * REGION * 4 <= RING && GROUPS * RING <= 160 * 1024, "the epilogue uses the ring's LDS");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[GROUPS * RING];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) & 3);
+    const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 8));
+    float *const w = reinterpret_cast<float *>(lds) + wave * REGION;                            // group 0's sums
+    float *const own = reinterpret_cast<float *>(lds + group * RING) + wave * REGION;
+    // the sum of an element of the wavefront's part of the tile
+    auto sum = [&](int at) { return GROUPS == 1 ? w[at] : w[at] + w[RING / 4 + at]; };
+
+    // workgroup ids go round the XCDs: the ones of an XCD take neighbouring tiles
+    const int per = work.groups >> 3, rem = work.groups & 7, xcd = (int)blockIdx.x & 7;
+    const int me = xcd * per + min(xcd, rem) + ((int)blockIdx.x >> 3);
+    const long long all = (long long)(work.tiles - work.whole) * work.stages;
+    const long long last = min((long long)(me + 1) * work.run, all);
+    long long unit = (long long)me * work.run;
+    for (int tile = me;;) {
+        int s0 = 0, steps = work.stages;
+        long long begin = 0;
+        const bool alone = tile < work.whole;
+        if (!alone) {
+            if (unit >= last)
+                break;
+            const int t = (int)(unit / work.stages);
+            begin = (long long)t * work.stages;
+            tile = work.whole + t;
+            s0 = (int)(unit - begin);
+            steps = (int)min(last - unit, (long long)(work.stages - s0));
+            unit += steps;
+        }
+        const int m = tile / work.per;
+        int tm, tn;
+        tile_of<SYM>(work, tile - m * work.per, tm, tn);
+        floatx4 acc[F][F];
+        if constexpr (SIDE == 256) {
+            quad_sum<TB>(p, m, lds, tm * SIDE, tn * SIDE, s0, steps, acc);
+        } else {
+            const int each = (steps + GROUPS - 1) / GROUPS;
+            pair_sum<SIDE, SIDE, NB, TB>(p, m, lds + group * RING, tm * SIDE, tn * SIDE, s0 + group * each,
+                                         min(s0 + steps, s0 + (group + 1) * each), each, acc);
+        }
+
+        // 32 rows at a time through the wavefront's own part of LDS: a lane has
+        // eight columns of every STEP-th row, and then, of what is also written
+        // across, eight rows of a column.  A's elements are loaded a batch ahead and
+        // before the batch's stores, whose returns they would else wait for (a row
+        // at a time a 128 x 128 tile took 12 us more).
+        const bool part = steps < work.stages;
+        const bool mirrored = SYM && !part && tn < tm, turned = WHICH == kUpdate && !part && f.turned;
+        float *slab = work.slabs + (part ? work.slab(me, begin, SIDE * SIDE) : 0);
+        const int r0 = ROWS * group + lane / LANES, c = 8 * (lane % LANES);
+        const int in = (wave >> 1) * HALF, left = (wave & 1) * HALF;   // in the tile
+        const int top = tm * SIDE + in, col = tn * SIDE + left + c;
+        const bool polynomial = WHICH == kPolynomial && !part;
+        u32x4 with[BATCH][2];
+        auto load_with = [&](int first) {   // of the lane's rows from `first` on
+#pragma unroll
+            for (int q = 0; q < BATCH; ++q) {
+                const uint16_t *at = f.with.at(m, min(top + first + r0 + STEP * q, p.M - 1), min(col, p.N - 1) & ~7);
+                with[q][0] = *reinterpret_cast<const u32x4 *>(at);
+                with[q][1] = *reinterpret_cast<const u32x4 *>(at + 32);
+            }
+        };
+        if (polynomial)
+            load_with(0);
+#pragma unroll 1
+        for (int round = 0; round < F / 2; ++round) {
+            stage_rows(acc, round, own, ROW, lane);
+            if (GROUPS > 1)
+                __syncthreads();
+            const int row0 = top + 32 * round;
+            if (polynomial) {
+#pragma unroll 1
+                for (int b = 0; b < ROWS; b += BATCH * STEP) {
+                    float v[BATCH][8];
+#pragma unroll
+                    for (int q = 0; q < BATCH; ++q) {
+                        const int r = b + r0 + STEP * q;
+                        float a[8], lo[8];
+                        unpack8<Half16>(with[q][0], a);
+                        unpack8<Half16>(with[q][1], lo);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            a[e] += lo[e];
+                            v[q][e] = sum(r * ROW + c + e);
+                        }
+                        f.value(row0 + r, col, v[q], a);
+                        if (mirrored)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                w[r * ROW + c + e] = v[q][e];
+                    }
+                    if (GROUPS == 1 && 32 * round + b + BATCH * STEP < HALF)
+                        load_with(32 * round + b + BATCH * STEP);
+#pragma unroll
+                    for (int q = 0; q < BATCH; ++q)
+                        if (row0 + b + r0 + STEP * q < p.M && col < p.N)
+                            f.store(m, row0 + b + r0 + STEP * q, col, p.N - col, v[q]);
+                }
+            } else if (!turned) {
+#pragma unroll 1
+                for (int r = r0; r < ROWS * (group + 1); r += STEP) {
+                    if (row0 + r >= p.M || col >= p.N)
+                        break;
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = sum(r * ROW + c + e) * (part ? 1.f : f.alpha);
+                    if (part)
+                        store8_f32(slab + (in + 32 * round + r) * SIDE + left + c, 8, v);
+                    else
+                        f.store(m, row0 + r, col, p.N - col, v);
+                }
+            }
+            if (mirrored || turned) {   // four lanes a column: 64 bytes of 16-bit results
+                if (polynomial) {
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                    if (GROUPS > 1)
+                        __syncthreads();   // (both groups' rows)
+                }
+                const int r = 8 * (lane & 3), row = row0 + r;
+#pragma unroll 1
+                for (int x = (lane >> 2) + 16 * group; x < HALF; x += 16 * GROUPS) {
+                    const int at = tn * SIDE + left + x;
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = polynomial ? w[(r + e) * ROW + x] : f.alpha * sum((r + e) * ROW + x);
+                    if (row < p.M && at < p.N)
+                        f.store(m, at, row, p.M - row, v);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        if (alone)
+            tile += work.groups;
+        // the next tile's loads count in order only after these stores, and fill
+        // LDS that other wavefronts may still read
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
+        __builtin_amdgcn_s_barrier();
+    }
+}
+
+// Adds the slabs of the tiles in several runs, in their order: a block of 64 x 64
+// a workgroup.
+template <int SIDE, bool SYM>
+__global__ __launch_bounds__(256) void newton_schulz_join_kernel(Operands p, Work work, Finish f)
+{
+    constexpr int ACROSS = SIDE / 64, BLOCKS = ACROSS * ACROSS;
+    __shared__ float block[64][68];
+    const int t = (int)blockIdx.x / BLOCKS, id = (int)blockIdx.x - t * BLOCKS;
+    const long long begin = (long long)t * work.stages, end = begin + work.stages;
+    const int w0 = (int)(begin / work.run), w1 = (int)((end - 1) / work.run);
+    if (w0 == w1)
+        return;   // a tile in one run
+    const int tile = work.whole + t, m = tile / work.per;
+    int tm, tn;
+    tile_of<SYM>(work, tile - m * work.per, tm, tn);
+    const bool across = f.turned || (SYM && tn < tm);
+    const int in = 64 * (id / ACROSS), left = 64 * (id % ACROSS), r0 = tm * SIDE + in, c0 = tn * SIDE + left;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = (int)(threadIdx.x >> 3) + 32 * q, c = 8 * (int)(threadIdx.x & 7);
         float v[8] = {};
         if (r0 + r < p.M && c0 + c < p.N) {
-            const float *from = p.part + (long long)m * p.splits * part_size(p) + (size_t)(r0 + r) * part_stride(p) + c0 + c;
-            load8_f32(from, 8, v);
-            for (int s = 1; s < p.splits; ++s) {
+            const int at = (in + r) * SIDE + left + c;
+            load8_f32(work.slabs + work.slab(w0, begin, SIDE * SIDE) + at, 8, v);
+            for (int s = w0 + 1; s <= w1; ++s) {
                 float u[8];
-                load8_f32(from + s * part_size(p), 8, u);
+                load8_f32(work.slabs + work.slab(s, begin, SIDE * SIDE) + at, 8, u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[e] += u[e];
             }
         }
+        const bool inside = r0 + r < p.M && c0 + c < p.N;
+        float a[8] = {};
+        if (f.polynomial && inside)
+            f.with.load8(m, r0 + r, c0 + c, a);
+        f.value(r0 + r, c0 + c, v, a);
         if (across)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                tile[r][c + e] = v[e];
-        if (!f.turned && r0 + r < p.M && c0 + c < p.N)
-            f.put(m, r0 + r, c0 + c, p.N - c0 - c, v);
+                block[r][c + e] = v[e];
+        if (!f.turned && inside)
+            f.store(m, r0 + r, c0 + c, p.N - c0 - c, v);
     }
     if (!across)
         return;
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int c = (int)(threadIdx.x >> 3) + 32 * t, r = 8 * (int)(threadIdx.x & 7);
+    for (int q = 0; q < 2; ++q) {
+        const int c = (int)(threadIdx.x >> 3) + 32 * q, r = 8 * (int)(threadIdx.x & 7);
         if (r0 + r < p.M && c0 + c < p.N) {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] = tile[r + e][c];
-            f.put(m, c0 + c, r0 + r, p.M - r0 - r, v);
+                v[e] = block[r + e][c];
+            f.store(m, c0 + c, r0 + r, p.M - r0 - r, v);
         }
     }
 }
@@ -356,66 +857,78 @@ __global__ __launch_bounds__(256) void newton_schulz_join_kernel(Product p, Batc
 
 constexpr size_t kWsAlign = 256;
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-// A launch holds fewer than 2^32 threads.
-constexpr long long kMostGroups = 1 << 24;
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+// A launch holds fewer than 2^32 threads; a tile has up to sixteen blocks to join.
+constexpr long long kMostGroups = 1 << 20;
 
-// The three products of a step.
-enum Which { kGram, kPolynomial, kUpdate };
+// How a product runs.
+enum Tile { kTile256, kTile128, kTile64 };
+constexpr int side_of(Tile t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : 64; }
+
+int results_cols(Which which, int m, int n) { return which == kUpdate ? n : m; }
+
+long long tiles_of(Which which, int m, int n, Tile t)
+{
+    const long long down = ceil_div(m, side_of(t));
+    return which == kUpdate ? down * ceil_div(n, side_of(t)) : down * (down + 1) / 2;
+}
+
 struct Way {
-    RingTile tile;
-    int splits, chunk;
+    Tile tile;
+    int groups, whole, run;   // of Work
+    bool joined;
+    size_t slabs;             // bytes
 };
 
-long long tiles_of(Which which, int m, int n, int bm, int bn)
-{
-    const long long down = ceil_div(m, bm);
-    return which == kUpdate ? down * ceil_div(n, bn) : down * (down + 1) / 2;
-}
+// Microseconds of a tile: its ends (with A's part in the polynomial's), and each
+// stage, where few compute units work and where all do.  From 1 to 2080 tiles and
+// sums of 256 to 4096 (128 x 256 to 4096 x 4096, batches of 1 to 8); over those what
+// is chosen takes at most 1.15 times the shortest of the three tiles, with and
+// without runs.
+struct TileCost {
+    Tile tile;
+    double ends, polynomial, few, all;
+};
+constexpr TileCost kTiles[] = {{kTile256, 16.0, 10.0, 1.58, 2.3}, {kTile128, 7.0, 3.0, 0.58, 0.75},
+                               {kTile64, 4.0, 0.5, 0.206, 0.24}};
+constexpr int kUnits = 256;                       // compute units
+constexpr double kJoin = 5.0, kSlabBytes = 3e6;   // a join's launch; a microsecond's bytes of slabs
 
-Product product_of(Which which, int m, int n)
+// The tile and the way its stages are dealt.
+bool choose(Which which, int m, int n, int batch, Way &best)
 {
-    Product p{};
-    p.M = m, p.N = which == kUpdate ? n : m, p.K = which == kGram ? n : m;
-    p.trans_b = which != kUpdate;
-    p.units = true;
-    p.nseg = p.terms = 3;
-    p.nbatch = p.splits = 1;
-    p.A.low = 1, p.B.low = 2;
-    p.group_m = 4;
-    return p;
-}
-
-// The tile and the split of the sum by the rings' times (ring_plan.h).
-Way choose(Which which, int m, int n, int batch)
-{
-    const Product p = product_of(which, m, n);
-    const int stages = product_stages(p);
-    Way w{kRing64, 1, 0};
-    double best = 0;
+    const int stages = ceil_div(which == kGram ? n : m, 32);
+    double least = 0;
     bool any = false;
-    for (const RingCost &c : kRings) {
-        const int bm = ring_tile_m(c.tile), bn = ring_tile_n(c.tile);
-        if (which != kUpdate && bm != bn)
+    for (const TileCost &c : kTiles) {
+        const long long tiles = batch * tiles_of(which, m, n, c.tile);
+        if (tiles >= kMostGroups)
             continue;
-        const long long groups = batch * tiles_of(which, m, n, bm, bn);
-        for (int parts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-            if (parts > 1 && (2 * parts > stages || groups * parts > 512 * c.share))
-                break;
-            if (groups * parts >= kMostGroups)
-                break;
-            const RingTimes t = times(p, c, parts);
-            const long long all = groups * parts, rounds = all / (256 * c.share), rest = all % (256 * c.share);
-            double us = rounds * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full);
-            if (parts > 1)
-                us += kJoinLaunch + (which == kUpdate ? 8.0 : 4.0) * parts * batch * p.M * p.N / kJoinBytes;
-            if (!any || us < best) {
-                any = true, best = us, w.tile = c.tile;
-                w.chunk = parts > 1 ? ceil_div(stages, parts) : 0;
-                w.splits = parts > 1 ? ceil_div(stages, w.chunk) : 1;
+        const double ends = c.ends + (which == kPolynomial ? c.polynomial : 0.0);
+        const auto stage = [&](long long groups) { return groups < kUnits * 3 / 4 ? c.few : c.all; };
+        const long long rounds = (tiles + kUnits - 1) / kUnits;
+        const double whole = rounds * (ends + stages * stage(tiles));
+        if (!any || whole < least) {
+            any = true, least = whole;
+            best = {c.tile, (int)(tiles < kUnits ? tiles : kUnits), (int)tiles, 1, false, 0};
+        }
+        // whole tiles in full rounds, the rest's stages in runs of at least four
+        const long long rest = tiles % kUnits;
+        for (int groups : {kUnits, kUnits * 3 / 4, kUnits / 2, kUnits / 4}) {
+            const long long run = (rest * stages + groups - 1) / groups;
+            if (rest == 0 || run < 4 || run >= stages || (tiles > kUnits && groups < kUnits))
+                continue;
+            const size_t bytes = (size_t)2 * groups * side_of(c.tile) * side_of(c.tile) * sizeof(float);
+            // (a run is of up to two tiles, at an end of each)
+            const double us = (double)(tiles / kUnits) * (ends + stages * c.all) + 2.0 * c.ends + run * stage(groups) +
+                              kJoin + bytes / kSlabBytes;
+            if (us < least) {
+                least = us;
+                best = {c.tile, groups, (int)(tiles - rest), (int)run, true, bytes};
             }
         }
     }
-    return w;
+    return any;
 }
 
 // Bounds of a step: of X's singular values, and of the polynomial on X X^T's
@@ -478,7 +991,7 @@ int lay_out(const gemm_orthogonalize_params *q, Layout &l)
 {
     if (!q)
         return GEMM_ERR_NULL_PTR;
-    constexpr int LONGEST = (1 << 22) - 8;   // the rings' strides
+    constexpr int LONGEST = (1 << 21) - 32;   // offsets in a tile's 256 rows stay below 2^31 bytes
     if (q->batch < 0 || q->M < 0 || q->N < 0 || q->M > LONGEST || q->N > LONGEST || q->steps < 1 ||
         q->steps > GEMM_MAX_STEPS || !(q->eps >= 0))
         return GEMM_ERR_INVALID_DIM;
@@ -503,18 +1016,16 @@ int lay_out(const gemm_orthogonalize_params *q, Layout &l)
     const bool tall = q->M > q->N;
     l.m = tall ? q->N : q->M, l.n = tall ? q->M : q->N;
     l.turned_in = tall != (q->op_g == GEMM_OP_T), l.turned_out = tall != (q->op_o == GEMM_OP_T);
-    l.ldx = (int)round_up((size_t)l.n, 8), l.lda = (int)round_up((size_t)l.m, 8);
-    for (int i = 0; i < 3; ++i) {
-        l.way[i] = choose((Which)i, l.m, l.n, q->batch);
-        const Way &w = l.way[i];
-        if (q->batch * tiles_of((Which)i, l.m, l.n, ring_tile_m(w.tile), ring_tile_n(w.tile)) * w.splits >= kMostGroups)
+    l.ldx = Pair::stride(l.n), l.lda = Pair::stride(l.m);
+    for (int i = 0; i < 3; ++i)
+        if (!choose((Which)i, l.m, l.n, q->batch, l.way[i]))
             return GEMM_ERR_INVALID_DIM;
-    }
     if (q->batch * (long long)ceil_div(l.m, 64) * ceil_div(l.n, 64) >= kMostGroups)
         return GEMM_ERR_INVALID_DIM;
-    // parts of at least 8192 elements, at most 256 (start_kernel's threads)
-    const long long parts = ((long long)l.m * l.n + 8191) / 8192;
-    l.blocks = (int)(parts < 256 ? parts : 256);
+    // parts of at least 2048 elements, a unit of eight a thread; at most 1024, four
+    // a thread of start_kernel
+    const long long parts = ((long long)l.m * l.n + 2047) / 2048;
+    l.blocks = (int)(parts < 1024 ? parts : 1024);
     if (q->batch * (long long)l.blocks >= kMostGroups)
         return GEMM_ERR_INVALID_DIM;
     const int cols = l.turned_in ? l.m : l.n;
@@ -525,56 +1036,54 @@ int lay_out(const gemm_orthogonalize_params *q, Layout &l)
         l.bytes += round_up(bytes, kWsAlign);
         return at;
     };
-    const size_t b = (size_t)q->batch, x = 4 * b * l.m * l.ldx, a = 4 * b * l.m * l.lda;   // two terms of two bytes
+    const size_t b = (size_t)q->batch, x = 2 * b * l.m * l.ldx, a = 2 * b * l.m * l.lda;
     l.sums = take(sizeof(double) * b * l.blocks);
     l.x[0] = take(x);
     l.x[1] = q->steps > 1 ? take(x) : l.x[0];
     l.gram = take(a);
     l.poly = take(a);
     size_t part = 0;
-    for (int i = 0; i < 3; ++i)
-        if (l.way[i].splits > 1) {
-            const size_t v = sizeof(float) * b * l.way[i].splits * part_size(product_of((Which)i, l.m, l.n));
-            part = v > part ? v : part;
-        }
+    for (const Way &w : l.way)
+        part = w.slabs > part ? w.slabs : part;
     l.part = take(part);
     return GEMM_OK;
 }
 
-template <int BM, int BN>
-void launch_as(Which which, const Product &p, const Batch &b, const Finish &f, const dim3 &grid, hipStream_t s)
+template <int SIDE, int NB, int GROUPS>
+hipError_t launch_as(Which which, const Operands &p, const Work &w, bool joined, const Finish &f, hipStream_t s)
 {
+    const dim3 grid((unsigned)w.groups), blocks((unsigned)((w.tiles - w.whole) * (SIDE / 64) * (SIDE / 64)));
+    const dim3 threads(256 * GROUPS);
     if (which == kUpdate)
-        hipLaunchKernelGGL((newton_schulz_kernel<BM, BN, false, false>), grid, dim3(256), 0, s, p, b, f);
-    else if constexpr (BM == BN)
-        hipLaunchKernelGGL((newton_schulz_kernel<BM, BN, true, true>), grid, dim3(256), 0, s, p, b, f);
+        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, kUpdate>), grid, threads, 0, s, p, w, f);
+    else if (which == kPolynomial)
+        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, kPolynomial>), grid, threads, 0, s, p, w, f);
+    else
+        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, kGram>), grid, threads, 0, s, p, w, f);
+    if (joined && which == kUpdate)
+        hipLaunchKernelGGL((newton_schulz_join_kernel<SIDE, false>), blocks, dim3(256), 0, s, p, w, f);
+    else if (joined)
+        hipLaunchKernelGGL((newton_schulz_join_kernel<SIDE, true>), blocks, dim3(256), 0, s, p, w, f);
+    return hipGetLastError();
 }
 
-hipError_t launch(Which which, Product p, const Way &w, Batch b, const Finish &f, int batch, hipStream_t s)
+hipError_t launch(Which which, const Pair &a, const Pair &b, int m, int n, int batch, const Way &way, float *slabs,
+                  const Finish &f, hipStream_t s)
 {
-    const int bm = ring_tile_m(w.tile), bn = ring_tile_n(w.tile);
-    p.splits = w.splits, p.chunk = w.chunk;
-    p.tiles_m = ceil_div(p.M, bm), p.tiles_n = ceil_div(p.N, bn);
-    b.per = (int)tiles_of(which, p.M, p.N, bm, bn);
-    const dim3 grid((unsigned)(batch * b.per), (unsigned)w.splits);
-    switch (w.tile) {
-    case kRing256: launch_as<256, 256>(which, p, b, f, grid, s); break;
-    case kRing256x128: launch_as<256, 128>(which, p, b, f, grid, s); break;
-    case kRing128: launch_as<128, 128>(which, p, b, f, grid, s); break;
-    case kRing128x64: launch_as<128, 64>(which, p, b, f, grid, s); break;
-    case kRing64: launch_as<64, 64>(which, p, b, f, grid, s); break;
+    Operands p{m, results_cols(which, m, n), which == kGram ? n : m, a, b};
+    Work w;
+    w.per = (int)tiles_of(which, m, n, way.tile);
+    w.tiles = batch * w.per;
+    w.stages = ceil_div(p.K, 32);
+    w.tiles_m = ceil_div(p.M, side_of(way.tile)), w.tiles_n = ceil_div(p.N, side_of(way.tile));
+    w.groups = way.groups, w.whole = way.whole, w.run = way.run;
+    w.slabs = slabs;
+    switch (way.tile) {
+    case kTile256: return launch_as<256, 2, 1>(which, p, w, way.joined, f, s);
+    case kTile128: return launch_as<128, 4, 1>(which, p, w, way.joined, f, s);
+    case kTile64: return launch_as<64, 4, 2>(which, p, w, way.joined, f, s);
     }
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess || w.splits <= 1)
-        return err;
-    p.tiles_m = ceil_div(p.M, 64), p.tiles_n = ceil_div(p.N, 64);
-    b.per = (int)tiles_of(which, p.M, p.N, 64, 64);
-    const dim3 blocks((unsigned)(batch * b.per));
-    if (which == kUpdate)
-        hipLaunchKernelGGL((newton_schulz_join_kernel<false>), blocks, dim3(256), 0, s, p, b, f);
-    else
-        hipLaunchKernelGGL((newton_schulz_join_kernel<true>), blocks, dim3(256), 0, s, p, b, f);
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, void *ws, size_t ws_bytes, void *stream)
@@ -596,8 +1105,7 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
     uint8_t *base = (uint8_t *)ws;
     const int batch = q->batch;
     const auto pair = [&](size_t at, int ld) {
-        const long long size = (long long)l.m * ld;
-        return Pair{(uint16_t *)(base + at), batch * size, size, ld};
+        return Pair{(uint16_t *)(base + at), (long long)l.m * ld, ld};
     };
     const Pair x[2] = {pair(l.x[0], l.ldx), pair(l.x[1], l.ldx)}, gram = pair(l.gram, l.lda), poly = pair(l.poly, l.lda);
 
@@ -610,13 +1118,8 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
                        std::ldexp(1.0, l.step[0].x), across, per, l.turned_in);
     hipError_t err = hipGetLastError();
 
-    const auto of = [&](Which which, const Pair &a, const Pair &b) {
-        Product p = product_of(which, l.m, l.n);
-        p.A = {a.hi, 0, 2 * a.term, 1};
-        p.B = {b.hi, 0, 2 * b.term, 2};
-        p.lda = a.ld, p.ldb = b.ld;
-        p.part = (float *)(base + l.part);
-        return p;
+    const auto product = [&](Which which, const Pair &a, const Pair &b, const Finish &f) {
+        return launch(which, a, b, l.m, l.n, batch, l.way[which], (float *)(base + l.part), f, s);
     };
     for (int i = 0; i < q->steps && err == hipSuccess; ++i) {
         const Step &k = l.step[i];
@@ -624,7 +1127,7 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
         Finish f{};
         f.alpha = (float)std::ldexp(1.0, k.gram - 2 * k.x);
         f.to = gram;
-        err = launch(kGram, of(kGram, now, now), l.way[kGram], {now.matrix, now.matrix, 0}, f, batch, s);
+        err = product(kGram, now, now, f);
         if (err != hipSuccess)
             break;
         f.polynomial = true;
@@ -632,7 +1135,7 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
         f.beta = (float)std::ldexp(k.b, k.poly - k.gram);
         f.diagonal = (float)std::ldexp(k.a, k.poly);
         f.with = gram, f.to = poly;
-        err = launch(kPolynomial, of(kPolynomial, gram, gram), l.way[kPolynomial], {gram.matrix, gram.matrix, 0}, f, batch, s);
+        err = product(kPolynomial, gram, gram, f);
         if (err != hipSuccess)
             break;
         f = Finish{};
@@ -644,7 +1147,7 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
             f.out = O, f.out_ld = q->ldo, f.out_matrix = batch > 1 ? q->stride_o : 0;
             f.fmt = fmt, f.turned = l.turned_out;
         }
-        err = launch(kUpdate, of(kUpdate, poly, now), l.way[kUpdate], {poly.matrix, now.matrix, 0}, f, batch, s);
+        err = product(kUpdate, poly, now, f);
     }
     return err == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
