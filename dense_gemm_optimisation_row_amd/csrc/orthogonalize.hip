@@ -194,7 +194,10 @@ __global__ __launch_bounds__(256) void start_kernel(Source g, Pair x, const doub
 // its transpose where `turned`.
 struct Finish {
     bool polynomial;
-    float alpha, beta, diagonal;
+    // [1]: what is left of the coefficient after its rounding to FP32.  Where the
+    // singular values are near 1, a + b + c is far below a and b, and so are P's
+    // entries: their terms' roundings would weigh 5 to 7 times as much in them.
+    float alpha[2], beta[2], diagonal[2];
     Pair with;             // A, symmetric
     Pair to;
     void *out;             // null: to `to`
@@ -208,8 +211,14 @@ struct Finish {
     {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[e] = polynomial ? __builtin_fmaf(alpha, v[e], beta * a[e]) + (row == col + e ? diagonal : 0.f)
-                              : alpha * v[e];
+            if (polynomial) {
+                // the large terms cancel first, in the FMAs, which round once
+                const bool on = row == col + e;
+                const float rest = __builtin_fmaf(alpha[1], v[e], __builtin_fmaf(beta[1], a[e], on ? diagonal[1] : 0.f));
+                v[e] = __builtin_fmaf(alpha[0], v[e], __builtin_fmaf(beta[0], a[e], on ? diagonal[0] : 0.f)) + rest;
+            } else {
+                v[e] *= alpha[0];
+            }
     }
     // n of them inside the result
     __device__ __forceinline__ void store(long long m, int row, int col, int n, const float (&v)[8]) const
@@ -288,10 +297,15 @@ template <int BM, int BN>
 constexpr int stage_bytes() { return (BM + BN) * 32 * 2 * 2; }
 
 // `steps` stages from s0, those from `stop` on zeros, by the four wavefronts of
-// one of the workgroup's groups; `lds` is the group's.
-template <int BM, int BN, int NB, bool TB>
+// one of the workgroup's groups; `lds` is the group's.  LOW: the cross products
+// have sums of their own, `low`.  Each MFMA rounds its sum four times, and the higher
+// terms' sum is then rounded by a third as many, which halves the error of short
+// sums (47 x 16: 1.4e-6 and 1.0e-6, FP32 products 0.8e-6; 78 x 1067: 1.6e-6, 1.2e-6
+// and 1.3e-6).  Long ones, on the larger tiles, are far below FP32's without it.
+template <int BM, int BN, int NB, bool TB, bool LOW>
 __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
-                                         int stop, int steps, floatx4 (&acc)[BM / 32][BN / 32])
+                                         int stop, int steps, floatx4 (&acc)[BM / 32][BN / 32],
+                                         floatx4 (&low)[LOW ? BM / 32 : 1][LOW ? BN / 32 : 1])
 {
     constexpr int BK = 32, HM = BM / 2, HN = BN / 2, FA = HM / 16, FB = HN / 16, W = HN / 4;
     constexpr int LPA = BM / 32, LPB = BN / 32, LOADS = LPA + LPB;   // a wavefront's, of a stage
@@ -403,8 +417,11 @@ __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t
 #pragma unroll
         for (int j = 0; j < FB; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                asm("v_accvgpr_write_b32 %0, 0" : "=a"(acc[i][j][r]));   // keeps the array in the accumulators
+            for (int r = 0; r < 4; ++r) {
+                asm("v_accvgpr_write_b32 %0, 0" : "=a"(acc[i][j][r]));   // keeps the arrays in the accumulators
+                if (LOW)
+                    asm("v_accvgpr_write_b32 %0, 0" : "=a"(low[LOW ? i : 0][LOW ? j : 0][r]));
+            }
 
     auto stage = [&](uint32_t next, const Fragments &c, Fragments &n) {
         constexpr int MFMAS = 3 * FA * FB;
@@ -414,7 +431,8 @@ __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t
 #pragma unroll
         for (int x = 0; x < MFMAS; ++x) {
             const int i = x / (3 * FB), t = x / FB % 3, j = x % FB;   // hi hi, lo hi, hi lo
-            acc[i][j] = OpHalf::mfma(c.a[t == 1][i], c.b[t == 2][j], acc[i][j]);
+            floatx4 &sum = !LOW || t == 0 ? acc[i][j] : low[LOW ? i : 0][LOW ? j : 0];
+            sum = OpHalf::mfma(c.a[t == 1][i], c.b[t == 2][j], sum);
             if (x < READS)
                 read(next, x, n);
             if (x == 0)
@@ -635,6 +653,28 @@ __device__ __forceinline__ void quad_sum(const Operands &p, long long m, uint8_t
     dgor_acc_hazard_wait();
 }
 
+// stage_rows of the sum of two sums.
+template <int F>
+__device__ __forceinline__ void stage_sums(const floatx4 (&acc)[F][F], const floatx4 (&low)[F][F], int round, float *w,
+                                           int row, int lane)
+{
+    const int s16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int k = 0; k < F / 2; ++k)
+        if (round == k) {
+#pragma unroll
+            for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+                for (int j = 0; j < F; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        w[(16 * ii + 4 * g + r) * row + 16 * j + s16] =
+                            dgor_acc_read(acc[2 * k + ii][j][r]) + dgor_acc_read(low[2 * k + ii][j][r]);
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // GROUPS: groups of four wavefronts, which take halves of a tile's stages on rings
 // of their own and add their sums in LDS.  Two on the 64 x 64 tile, whose stages are
 // too short for one wavefront a SIMD to cover its own waits.
@@ -681,13 +721,14 @@ __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p,
         const int m = tile / work.per;
         int tm, tn;
         tile_of<SYM>(work, tile - m * work.per, tm, tn);
-        floatx4 acc[F][F];
+        constexpr bool LOW = SIDE == 64;
+        floatx4 acc[F][F], low[LOW ? F : 1][LOW ? F : 1];
         if constexpr (SIDE == 256) {
             quad_sum<TB>(p, m, lds, tm * SIDE, tn * SIDE, s0, steps, acc);
         } else {
             const int each = (steps + GROUPS - 1) / GROUPS;
-            pair_sum<SIDE, SIDE, NB, TB>(p, m, lds + group * RING, tm * SIDE, tn * SIDE, s0 + group * each,
-                                         min(s0 + steps, s0 + (group + 1) * each), each, acc);
+            pair_sum<SIDE, SIDE, NB, TB, LOW>(p, m, lds + group * RING, tm * SIDE, tn * SIDE, s0 + group * each,
+                                         min(s0 + steps, s0 + (group + 1) * each), each, acc, low);
         }
 
         // 32 rows at a time through the wavefront's own part of LDS: a lane has
@@ -715,7 +756,10 @@ __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p,
             load_with(0);
 #pragma unroll 1
         for (int round = 0; round < F / 2; ++round) {
-            stage_rows(acc, round, own, ROW, lane);
+            if constexpr (LOW)
+                stage_sums(acc, low, round, own, ROW, lane);
+            else
+                stage_rows(acc, round, own, ROW, lane);
             if (GROUPS > 1)
                 __syncthreads();
             const int row0 = top + 32 * round;
@@ -755,7 +799,7 @@ __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p,
                     float v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[e] = sum(r * ROW + c + e) * (part ? 1.f : f.alpha);
+                        v[e] = sum(r * ROW + c + e) * (part ? 1.f : f.alpha[0]);
                     if (part)
                         store8_f32(slab + (in + 32 * round + r) * SIDE + left + c, 8, v);
                     else
@@ -776,7 +820,7 @@ __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p,
                     float v[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[e] = polynomial ? w[(r + e) * ROW + x] : f.alpha * sum((r + e) * ROW + x);
+                        v[e] = polynomial ? w[(r + e) * ROW + x] : f.alpha[0] * sum((r + e) * ROW + x);
                     if (row < p.M && at < p.N)
                         f.store(m, at, row, p.M - row, v);
                 }
@@ -1121,29 +1165,33 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
     const auto product = [&](Which which, const Pair &a, const Pair &b, const Finish &f) {
         return launch(which, a, b, l.m, l.n, batch, l.way[which], (float *)(base + l.part), f, s);
     };
+    const auto hold = [](float (&to)[2], double v) {
+        to[0] = (float)v;
+        to[1] = (float)(v - to[0]);
+    };
     for (int i = 0; i < q->steps && err == hipSuccess; ++i) {
         const Step &k = l.step[i];
         const Pair &now = x[i & 1], &next = x[(i + 1) & 1];
         Finish f{};
-        f.alpha = (float)std::ldexp(1.0, k.gram - 2 * k.x);
+        f.alpha[0] = (float)std::ldexp(1.0, k.gram - 2 * k.x);
         f.to = gram;
         err = product(kGram, now, now, f);
         if (err != hipSuccess)
             break;
         f.polynomial = true;
-        f.alpha = (float)std::ldexp(k.c, k.poly - 2 * k.gram);
-        f.beta = (float)std::ldexp(k.b, k.poly - k.gram);
-        f.diagonal = (float)std::ldexp(k.a, k.poly);
+        hold(f.alpha, std::ldexp(k.c, k.poly - 2 * k.gram));
+        hold(f.beta, std::ldexp(k.b, k.poly - k.gram));
+        hold(f.diagonal, std::ldexp(k.a, k.poly));
         f.with = gram, f.to = poly;
         err = product(kPolynomial, gram, gram, f);
         if (err != hipSuccess)
             break;
         f = Finish{};
         if (i + 1 < q->steps) {
-            f.alpha = (float)std::ldexp(1.0, l.step[i + 1].x - k.poly - k.x);
+            f.alpha[0] = (float)std::ldexp(1.0, l.step[i + 1].x - k.poly - k.x);
             f.to = next;
         } else {
-            f.alpha = (float)std::ldexp(q->scale, -k.poly - k.x);
+            f.alpha[0] = (float)std::ldexp(q->scale, -k.poly - k.x);
             f.out = O, f.out_ld = q->ldo, f.out_matrix = batch > 1 ? q->stride_o : 0;
             f.fmt = fmt, f.turned = l.turned_out;
         }
