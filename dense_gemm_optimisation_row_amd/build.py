@@ -1,7 +1,8 @@
 """Build the HIP libraries in-tree, beside this file: ``libdgor_gemm.so`` (the
 product), ``libdgor_calibrate.so`` (the benchmark's matrix-core calibration
 kernel) and ``libdgor_gemm_poison.so`` (the product built with LDS poisoning,
-for the race tests).
+for the race tests); and ``_marshal.so``, the extension module through which
+short calls of the layers reach the product (host code, against torch).
 
 Every source in ``csrc/`` is compiled for gfx950 with hipcc (in parallel),
 then linked into one shared library that exports the C ABI of
@@ -37,6 +38,7 @@ CAL_LIB = os.path.join(PKG, "libdgor_calibrate.so")
 # runs ahead of the barrier retiring a buffer sees NaN (a debug build for the
 # race tests; the product loads LIB).
 POISON_LIB = os.path.join(PKG, "libdgor_gemm_poison.so")
+MARSHAL_LIB = os.path.join(PKG, "_marshal.so")
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
@@ -79,20 +81,41 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
+def _marshal() -> None:
+    """Compile the extension module against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL_LIB + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in include_paths()), f"-I{sysconfig.get_paths()['include']}",
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, f"-L{lib}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_LIB)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile all sources, link the GEMM library and the calibration
-    library; return the GEMM library's path."""
+    """Compile all sources, link the GEMM library, the calibration library and
+    the extension module; return the GEMM library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     jobs_list = [(src, False) for src in SOURCES + CAL_SOURCES] + [(src, True) for src in SOURCES]
     jobs = min(len(jobs_list), max(1, min(8, os.cpu_count() or 1)))
     with ThreadPoolExecutor(jobs) as ex:
+        marshal = ex.submit(_marshal)
         objs = list(ex.map(lambda j: _compile(*j), jobs_list))
+        marshal.result()
     n = len(SOURCES)
     _link(objs[:n], LIB)
     _link(objs[n:n + len(CAL_SOURCES)], CAL_LIB)
     _link(objs[n + len(CAL_SOURCES):], POISON_LIB)
     if verbose:
-        print(f"built {LIB}, {CAL_LIB} and {POISON_LIB}")
+        print(f"built {LIB}, {CAL_LIB}, {POISON_LIB} and {MARSHAL_LIB}")
     return LIB
 
 

@@ -902,8 +902,9 @@ __global__ __launch_bounds__(256) void newton_schulz_join_kernel(Operands p, Wor
 constexpr size_t kWsAlign = 256;
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
-// A launch holds fewer than 2^32 threads; a tile has up to sixteen blocks to join.
-constexpr long long kMostGroups = 1 << 20;
+// A launch holds fewer than 2^32 threads; the products' tiles are dealt to at most
+// 256 workgroups, and counted in ints.
+constexpr long long kMostGroups = 1 << 24, kMostTiles = 1 << 30;
 
 // How a product runs.
 enum Tile { kTile256, kTile128, kTile64 };
@@ -946,7 +947,7 @@ bool choose(Which which, int m, int n, int batch, Way &best)
     bool any = false;
     for (const TileCost &c : kTiles) {
         const long long tiles = batch * tiles_of(which, m, n, c.tile);
-        if (tiles >= kMostGroups)
+        if (tiles >= kMostTiles)
             continue;
         const double ends = c.ends + (which == kPolynomial ? c.polynomial : 0.0);
         const auto stage = [&](long long groups) { return groups < kUnits * 3 / 4 ? c.few : c.all; };

@@ -56,7 +56,8 @@ def _function(stem, kind):
 
 class _Form:
     """What a call of one form needs besides its tensors."""
-    __slots__ = ("device", "index", "entry", "stem", "params", "ref", "workspace", "shape", "dtype", "copies", "extra")
+    __slots__ = ("device", "index", "entry", "stem", "params", "ref", "workspace", "sized", "shape", "dtype", "copies",
+                 "extra")
 
     def __init__(self, like, stem, kind, params, shape=(), dtype=None, copies=(), extra=None):
         self.device, self.index, self.stem = like.device, like.device.index, stem
@@ -64,7 +65,7 @@ class _Form:
         self.params, self.ref = params, ctypes.byref(params)
         self.shape, self.dtype, self.extra = shape, dtype, extra
         self.copies = copies      # the tensors whose leading dimensions do not fold into rows
-        self.workspace = 0
+        self.workspace, self.sized = 0, size_of is not None
         if size_of is not None:
             need = _NEED()
             rc = size_of(self.ref, ctypes.byref(need))
@@ -584,6 +585,46 @@ def _layer_norm_backward_form(dy, x, weight, mean, rstd, need_weight, dx, dweigh
     return _Form(dy, "gemm_layer_norm_backward", _KIND[dy.dtype], params, dtype=wt, copies=copies)
 
 
+# --------------------------------------------- calls of forms seen before --
+#
+# The kernels of a few rows on 8-bit operands take 3 to 5 us, less than a call's
+# checks, allocations and marshalling in Python (8 to 9 us with the launch): the
+# extension module does these for a form that a call in Python has made and kept.
+
+_marshal = None
+_QUANTIZE_I8, _LINEAR_I8, _GATED_I8 = range(3)
+_TYPES = {None: 0, torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
+
+
+def _again(op, stem, tensors, extra):
+    """The result of a call whose form is known to the extension module; None
+    where it is not, or where the call is not one on the current device."""
+    if not tensors[0].is_cuda or -1 in extra:
+        return None
+    global _marshal
+    if _marshal is None:
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("the extension module _marshal.so is missing or of another torch: build it with "
+                               "`python -m dense_gemm_optimisation_row_amd.build`") from e
+        _marshal = module
+    index = torch._C._cuda_getDevice()
+    out = _marshal.run(op, tensors, extra, index, torch._C._cuda_getCurrentRawStream(index))
+    if type(out) is int:
+        raise GemmError(out, stem)
+    return out
+
+
+def _remember(op, tensors, extra, form, slots, outputs):
+    """Makes a form known to the extension module.  slots: the entry point's
+    pointers, each the index of a tensor or -1 - that of an output; outputs: the
+    index of a given tensor, or (shape, dtype)."""
+    if not form.copies and -1 not in extra and form.index == torch._C._cuda_getDevice():
+        _marshal.keep(op, tensors, extra, form.index, ctypes.cast(form.entry, ctypes.c_void_p).value,
+                      bytes(form.params), slots, outputs, form.workspace if form.sized else -1)
+
+
 # ---------------------------------------------------- 8-bit dense layers --
 
 def _kind_of(dtype, name):
@@ -610,6 +651,11 @@ def quantize_i8(x, q=None, scale=None, stream=None):
     scale NaN and zeros.  Weights are quantised as outputs by inputs:
     ``q, s = quantize_i8(weight)``, and ``q.t()`` with ``s`` goes into
     ``linear_i8``."""
+    tensors = (x, q, scale)
+    if stream is None:
+        done = _again(_QUANTIZE_I8, "gemm_quantize_i8", tensors, ())
+        if done is not None:
+            return done
     if x.requires_grad:
         _grad_unless_off()
     key = ("quantize_i8", x.shape, x.stride(), x.dtype, x.device, _sig(q), _sig(scale))
@@ -621,7 +667,12 @@ def quantize_i8(x, q=None, scale=None, stream=None):
         steps = x.new_empty(form.shape, dtype=torch.float32) if scale is None else scale
         _done(form.entry(form.ref, xs.data_ptr(), codes.data_ptr(), steps.data_ptr(), handle), form)
         return codes, steps
-    return _run(form, stream, (x, q, scale), go)
+    done = _run(form, stream, tensors, go)
+    if stream is None:
+        _remember(_QUANTIZE_I8, tensors, (), form, (0, -1, -2),
+                  ((tuple(x.shape), torch.int8) if q is None else 1,
+                   (form.shape, torch.float32) if scale is None else 2))
+    return done
 
 
 def _quantize_form(x, q, scale):
@@ -660,6 +711,12 @@ def linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, activation="none
     bfloat16.  w is fastest stored outputs by inputs (a transposed view) with K a multiple of 16:
     other weights are copied into that form in each call.  ``y`` may be the
     residual itself."""
+    tensors = (x, x_scale, w, w_scale, bias, residual, y)
+    extra = (ACTIVATIONS.get(activation, -1), _TYPES.get(out_dtype, -1))
+    if stream is None and workspace is None:
+        done = _again(_LINEAR_I8, "gemm_linear_i8", tensors, extra)
+        if done is not None:
+            return done
     if (bias is not None and bias.requires_grad) or (residual is not None and residual.requires_grad) or \
             x_scale.requires_grad or w_scale.requires_grad:
         _grad_unless_off()
@@ -676,7 +733,11 @@ def linear_i8(x, x_scale, w, w_scale, bias=None, residual=None, activation="none
         _done(form.entry(form.ref, xs.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
                          _ptr(rs), out.data_ptr(), _ptr(ws), _size(ws), handle), form)
         return out
-    return _run(form, stream, (x, x_scale, w, w_scale, bias, residual, y, workspace), go)
+    done = _run(form, stream, tensors + (workspace,), go)
+    if stream is None and workspace is None:
+        _remember(_LINEAR_I8, tensors, extra, form, (0, 1, 2, 3, 4, 5, -1),
+                  ((form.shape, form.dtype) if y is None else 6,))
+    return done
 
 
 def _linear_i8_form(x, x_scale, w, w_scale, bias, residual, activation, out_dtype, y, off):
@@ -712,6 +773,12 @@ def gated_i8(x, x_scale, wg, wg_scale, wu, wu_scale, activation="silu", out_dtyp
     storage and stride), each product scaled as in ``linear_i8``; the result is
     ``out_dtype``: float32, float16 or bfloat16, by default h's type or
     bfloat16."""
+    tensors = (x, x_scale, wg, wg_scale, wu, wu_scale, h)
+    extra = (ACTIVATIONS.get(activation, -1), _TYPES.get(out_dtype, -1))
+    if stream is None and workspace is None:
+        done = _again(_GATED_I8, "gemm_gated_i8", tensors, extra)
+        if done is not None:
+            return done
     if x_scale.requires_grad or wg_scale.requires_grad or wu_scale.requires_grad:
         _grad_unless_off()
     off = _off_units(x, wg, wu)
@@ -727,7 +794,11 @@ def gated_i8(x, x_scale, wg, wg_scale, wu, wu_scale, activation="silu", out_dtyp
         _done(form.entry(form.ref, xs.data_ptr(), x_scale.data_ptr(), wg.data_ptr(), wg_scale.data_ptr(),
                          wu.data_ptr(), wu_scale.data_ptr(), out.data_ptr(), _ptr(ws), _size(ws), handle), form)
         return out
-    return _run(form, stream, (x, x_scale, wg, wg_scale, wu, wu_scale, h, workspace), go)
+    done = _run(form, stream, tensors + (workspace,), go)
+    if stream is None and workspace is None:
+        _remember(_GATED_I8, tensors, extra, form, (0, 1, 2, 3, 4, 5, -1),
+                  ((form.shape, form.dtype) if h is None else 6,))
+    return done
 
 
 def _gated_i8_form(x, x_scale, wg, wg_scale, wu, wu_scale, activation, out_dtype, h, off):
