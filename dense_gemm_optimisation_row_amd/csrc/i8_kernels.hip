@@ -384,34 +384,46 @@ hipError_t launch_blocks(const Product &p, const I8Epilogue &e, hipStream_t s)
 
 // ----------------------------------------------------------------- copies --
 //
-// A workgroup copies 16 KB.  Rows: 16 bytes a thread and turn, read at any
-// address.  Transposed: blocks of 128 x 128 through LDS; a thread takes four k of
-// four columns as dwords and turns them round in registers.
+// A workgroup copies 4 KB: a unit of 16 bytes a thread, or a block of 64 x 64 that is
+// transposed through LDS, where a thread turns four k of four columns round in
+// registers.  Loads are at any address and none is in a branch: one that would
+// leave the matrix takes the matrix's last bytes and is shifted.  (Blocks of 16 KB
+// and bytes one by one at the edges: 8 us for 1000 x 777 and 777 x 1033.)
 
 __device__ __forceinline__ void pack_rows(const I8Pack::Job &j, unsigned block)
 {
-    const long long units = j.ld_to / 16, all = units * j.rows;
+    const long long units = j.ld_to / 16, id = (long long)block * 256 + threadIdx.x, row = id / units;
+    if (row >= j.rows)
+        return;
+    const int c = 16 * (int)(id - row * units), n = j.cols - c;   // n bytes of the row, at least one
+    const int8_t *from = j.from + row * j.ld;
+    u32x4 v;
+    if (j.cols >= 16) {
+        v = *reinterpret_cast<const u32x4_at1 *>(from + min(c, j.cols - 16));
+        if (n < 16) {
+            const int s = 8 * (16 - n);
+            uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+            lo = s < 64 ? lo >> s | hi << (64 - s) : hi >> (s - 64);
+            hi = s < 64 ? hi >> s : 0;
+            v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
+    } else {
+        uint32_t b[16];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const long long id = (long long)block * 1024 + t * 256 + threadIdx.x;
-        if (id >= all)
-            return;
-        const long long row = id / units;
-        const int c = 16 * (int)(id - row * units), n = j.cols - c;
-        const int8_t *from = j.from + row * j.ld + c;
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (n >= 16)
-            v = *reinterpret_cast<const u32x4_at1 *>(from);
-        else
+        for (int e = 0; e < 16; ++e)
+            b[e] = (uint8_t)from[min(e, n - 1)];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e < n)
-                    v[e >> 2] |= (uint32_t)(uint8_t)from[e] << (8 * (e & 3));
-        *reinterpret_cast<u32x4 *>(j.to + row * j.ld_to + c) = v;
+        for (int e = 0; e < 4; ++e) {
+            v[e] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[e] |= 4 * e + i < n ? b[4 * e + i] << (8 * i) : 0u;
+        }
     }
+    *reinterpret_cast<u32x4 *>(j.to + row * j.ld_to + c) = v;
 }
 
-constexpr int kTurned = 128;   // a side of a transposed block
+constexpr int kTurned = 64;   // a side of a transposed block
 
 __device__ __forceinline__ void pack_turned(const I8Pack::Job &j, unsigned block, uint32_t *lds)
 {
@@ -419,40 +431,38 @@ __device__ __forceinline__ void pack_turned(const I8Pack::Job &j, unsigned block
     constexpr int PITCH = kTurned / 4 + 1;   // dwords of a column's k
     const int across = (j.rows + kTurned - 1) / kTurned;
     const int n0 = kTurned * (int)(block % across), k0 = kTurned * (int)(block / across);
+    const int c = 4 * (int)(threadIdx.x & 15), k = 4 * (int)(threadIdx.x >> 4);   // of the block
+    uint32_t r[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int id = t * 256 + threadIdx.x, c = 4 * (id & 31), k = 4 * (id >> 5);   // of the block
-        uint32_t r[4], v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int kk = k0 + k + i, n = j.rows - n0 - c;
-            const int8_t *from = j.from + (long long)kk * j.ld + n0 + c;
+    for (int i = 0; i < 4; ++i) {
+        const int kk = k0 + k + i, at = n0 + c;
+        const int8_t *from = j.from + (long long)min(kk, j.cols - 1) * j.ld;
+        if (j.rows >= 4) {
+            const int first = min(at, j.rows - 4);
+            const uint32_t v = *reinterpret_cast<const u32_at1 *>(from + first);
+            r[i] = kk < j.cols && at - first < 4 ? v >> (8 * (at - first)) : 0u;
+        } else {
             r[i] = 0;
-            if (kk < j.cols && n >= 4)
-                r[i] = *reinterpret_cast<const u32_at1 *>(from);
-            else if (kk < j.cols)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < n)
-                        r[i] |= (uint32_t)(uint8_t)from[e] << (8 * e);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[e] |= ((r[i] >> (8 * e)) & 0xffu) << (8 * i);
-            lds[(c + e) * PITCH + (id >> 5)] = v[e];
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b = (uint8_t)from[min(at + e, j.rows - 1)];
+                r[i] |= kk < j.cols && at + e < j.rows ? b << (8 * e) : 0u;
+            }
         }
     }
-    __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int id = t * 256 + threadIdx.x, n = id >> 3, u = id & 7;   // eight units a column
-        if (n0 + n < j.rows && k0 + 16 * u < j.ld_to) {
-            const uint32_t *q = lds + n * PITCH + 4 * u;
-            *reinterpret_cast<u32x4 *>(j.to + (long long)(n0 + n) * j.ld_to + k0 + 16 * u) = u32x4{q[0], q[1], q[2], q[3]};
-        }
+    for (int e = 0; e < 4; ++e) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v |= ((r[i] >> (8 * e)) & 0xffu) << (8 * i);
+        lds[(c + e) * PITCH + (threadIdx.x >> 4)] = v;
+    }
+    __syncthreads();
+    const int n = (int)(threadIdx.x >> 2), u = (int)(threadIdx.x & 3);   // four units a column
+    if (n0 + n < j.rows && k0 + 16 * u < j.ld_to) {
+        const uint32_t *q = lds + n * PITCH + 4 * u;
+        *reinterpret_cast<u32x4 *>(j.to + (long long)(n0 + n) * j.ld_to + k0 + 16 * u) = u32x4{q[0], q[1], q[2], q[3]};
     }
 }
 
@@ -517,7 +527,7 @@ hipError_t launch_i8_pack(const I8Pack &q, hipStream_t s)
         I8Pack::Job &j = r.job[i];
         j.first = (unsigned)blocks;
         blocks += j.transpose ? ((j.rows + kTurned - 1LL) / kTurned) * ((j.cols + kTurned - 1LL) / kTurned)
-                              : ((long long)(j.ld_to / 16) * j.rows + 1023) / 1024;
+                              : ((long long)(j.ld_to / 16) * j.rows + 255) / 256;
     }
     if (blocks == 0)
         return hipSuccess;
