@@ -19,6 +19,7 @@
 //
 // Bound by the matrix cores where the tiles fill the compute units.
 #include <cmath>
+#include <cstddef>
 #include <stdint.h>
 
 #include "ring.h"
@@ -298,10 +299,9 @@ constexpr int stage_bytes() { return (BM + BN) * 32 * 2 * 2; }
 
 // `steps` stages from s0, those from `stop` on zeros, by the four wavefronts of
 // one of the workgroup's groups; `lds` is the group's.  LOW: the cross products
-// have sums of their own, `low`.  Each MFMA rounds its sum four times, and the higher
-// terms' sum is then rounded by a third as many, which halves the error of short
-// sums (47 x 16: 1.4e-6 and 1.0e-6, FP32 products 0.8e-6; 78 x 1067: 1.6e-6, 1.2e-6
-// and 1.3e-6).  Long ones, on the larger tiles, are far below FP32's without it.
+// have sums of their own, `low`, to which the lower terms' products belong too.  Each
+// MFMA rounds its sum four times, and the higher terms' sum is then rounded by a
+// third as many.
 template <int BM, int BN, int NB, bool TB, bool LOW>
 __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
                                          int stop, int steps, floatx4 (&acc)[BM / 32][BN / 32],
@@ -424,15 +424,15 @@ __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t
             }
 
     auto stage = [&](uint32_t next, const Fragments &c, Fragments &n) {
-        constexpr int MFMAS = 3 * FA * FB;
+        constexpr int TERMS = LOW ? 4 : 3, MFMAS = TERMS * FA * FB;
         constexpr int FIRST = MFMAS - READS >= LOADS ? READS : 2, EVERY = (MFMAS - FIRST) / LOADS;
         static_assert(EVERY > 0 && READS <= MFMAS, "all issued");
         Loads L;
 #pragma unroll
         for (int x = 0; x < MFMAS; ++x) {
-            const int i = x / (3 * FB), t = x / FB % 3, j = x % FB;   // hi hi, lo hi, hi lo
+            const int i = x / (TERMS * FB), t = x / FB % TERMS, j = x % FB;   // hi hi, lo hi, hi lo, lo lo
             floatx4 &sum = !LOW || t == 0 ? acc[i][j] : low[LOW ? i : 0][LOW ? j : 0];
-            sum = OpHalf::mfma(c.a[t == 1][i], c.b[t == 2][j], sum);
+            sum = OpHalf::mfma(c.a[t & 1][i], c.b[t >> 1][j], sum);
             if (x < READS)
                 read(next, x, n);
             if (x == 0)
@@ -678,7 +678,8 @@ __device__ __forceinline__ void stage_sums(const floatx4 (&acc)[F][F], const flo
 // GROUPS: groups of four wavefronts, which take halves of a tile's stages on rings
 // of their own and add their sums in LDS.  Two on the 64 x 64 tile, whose stages are
 // too short for one wavefront a SIMD to cover its own waits.
-template <int SIDE, int NB, int GROUPS, Which WHICH>
+// LOW: as pair_sum's.
+template <int SIDE, int NB, int GROUPS, bool LOW, Which WHICH>
 __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p, Work work, Finish f)
 {
     constexpr bool SYM = WHICH != kUpdate, TB = SYM;
@@ -721,7 +722,6 @@ __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p,
         const int m = tile / work.per;
         int tm, tn;
         tile_of<SYM>(work, tile - m * work.per, tm, tn);
-        constexpr bool LOW = SIDE == 64;
         floatx4 acc[F][F], low[LOW ? F : 1][LOW ? F : 1];
         if constexpr (SIDE == 256) {
             quad_sum<TB>(p, m, lds, tm * SIDE, tn * SIDE, s0, steps, acc);
@@ -897,6 +897,224 @@ __global__ __launch_bounds__(256) void newton_schulz_join_kernel(Operands p, Wor
     }
 }
 
+// --------------------------------------------------------- small matrices --
+//
+// A matrix that fits LDS in two terms next to its A: all steps in one launch, a
+// workgroup of 16 wavefronts a matrix.  Bound by the latency of a product's chain,
+// LDS to MFMA to LDS and a barrier, where the launches of the kernels above, three a
+// step, take 5 us each (64 x 64: 76 us).
+//
+// X is planes of 32 columns, A and P after it likewise: row r of a plane 128 bytes,
+// higher terms and then lower ones, unit c at 8 r + (c ^ ((r >> 1) & 7)).  Rows and
+// columns up to multiples of 32 are zeros.
+constexpr int kSmallWaves = 16, kSmallBytes = 159 * 1024;
+constexpr int kSmallUnits = 6;     // units of eight of G a thread loads
+constexpr int kSmallBlocks = 10;   // 16 x 16 blocks of X a wavefront computes
+struct SmallStep {
+    float gram, alpha[2], beta[2], diagonal[2], next;   // Finish's; of A's, P's and the next X's sums
+};
+struct Small {
+    Source g;
+    int m, n, mp, np;   // mp, np: padded to multiples of 32
+    bool turned_in, turned_out;
+    double eps, by;
+    int steps;
+    void *out;
+    int out_ld, fmt;
+    long long out_matrix;
+    SmallStep step[GEMM_MAX_STEPS];
+};
+
+__global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(Small p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kSmallBytes];
+    __shared__ double sums[kSmallWaves];
+    const int lane = threadIdx.x & 63;
+    int s16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const long long matrix = blockIdx.x;
+    const int mp = p.mp, plane = mp * 128, nb = (p.n + 15) / 16;
+    int mb = (p.m + 15) / 16;
+    uint8_t *const xs = lds, *const as = lds + p.np / 32 * plane;
+
+    // G, its norm, X
+    for (int i = threadIdx.x; i < (p.np + mp) / 32 * plane / 16; i += 64 * kSmallWaves)
+        *reinterpret_cast<u32x4 *>(lds + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+    const int across = (p.g.cols + 7) / 8, units = across * p.g.rows;
+    float f[kSmallUnits][8];
+    double v = 0;
+#pragma unroll
+    for (int t = 0; t < kSmallUnits; ++t) {
+        const int id = (int)threadIdx.x + 64 * kSmallWaves * t;
+        if (id < units) {
+            p.g.load8(matrix, id / across, 8 * (id % across), f[t]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v += (double)f[t][e] * (double)f[t][e];
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        v += __shfl_xor(v, o, 64);
+    if (lane == 0)
+        sums[wave] = v;
+    __syncthreads();   // and LDS is zero
+    v = sums[0];
+#pragma unroll
+    for (int i = 1; i < kSmallWaves; ++i)
+        v += sums[i];
+    const double factor = p.by / (sqrt(v) + p.eps);
+    // element (r, c) of planes at `base`; its lower term is 64 bytes on, by an XOR
+    auto place = [&](uint8_t *base, int r, int c) {
+        return base + (c >> 5) * plane + r * 128 + ((((c & 31) >> 3) ^ ((r >> 1) & 7)) * 16) + 2 * (c & 7);
+    };
+    auto lower = [&](uint8_t *q) { return lds + ((uint32_t)(q - lds) ^ 64u); };
+    auto put = [&](uint8_t *base, int r, int c, float y) {
+        uint8_t *q = place(base, r, c);
+        const _Float16 hi = (_Float16)y;
+        *reinterpret_cast<_Float16 *>(q) = hi;
+        *reinterpret_cast<_Float16 *>(lower(q)) = (_Float16)(y - (float)hi);
+    };
+#pragma unroll
+    for (int t = 0; t < kSmallUnits; ++t) {
+        const int id = (int)threadIdx.x + 64 * kSmallWaves * t;
+        if (id < units) {
+            const int r = id / across, c = 8 * (id % across);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < p.g.cols)
+                    put(xs, p.turned_in ? c + e : r, p.turned_in ? r : c + e, (float)(f[t][e] * factor));
+        }
+    }
+    __syncthreads();
+
+    // fragments: rows 16 b .. of planes at base, k 32 t ..; and columns 16 b ..
+    auto along = [&](const uint8_t *base, int b, int t, int term) {
+        const uint32_t at = (uint32_t)(base - lds) + (uint32_t)(t * plane + (16 * b + s16) * 128 + ((g ^ ((s16 >> 1) & 7)) * 16));
+        return *reinterpret_cast<const halfx8 *>(lds + (at ^ (uint32_t)(64 * term)));
+    };
+    auto across_x = [&](int b, int t, int term) {
+        shortx4 part[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = 32 * t + 8 * g + 4 * h + (s16 >> 2), u = 4 * term + 2 * (b & 1) + ((s16 & 3) >> 1);
+            const uint8_t *q = xs + (b >> 1) * plane + k * 128 + ((u ^ ((k >> 1) & 7)) * 16) + 8 * (s16 & 1);
+            part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
+        }
+        return __builtin_bit_cast(halfx8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    // the sum over `stages` of a block: all four products, the cross ones apart, and
+    // two halves of the others, for fewer roundings of each
+    auto block = [&](int stages, auto a_of, auto b_of) {
+        floatx4 sum = {0.f, 0.f, 0.f, 0.f}, other = sum, low = sum;
+        auto add = [&](int t, floatx4 &to) {
+            const halfx8 a0 = a_of(t, 0), b0 = b_of(t, 0), a1 = a_of(t, 1), b1 = b_of(t, 1);
+            to = OpHalf::mfma(a0, b0, to);
+            low = OpHalf::mfma(a1, b1, low);   // (counts in sums of few products)
+            low = OpHalf::mfma(a1, b0, low);
+            low = OpHalf::mfma(a0, b1, low);
+        };
+        const int half = (stages + 1) / 2;
+        for (int t = 0; t < half; ++t) {
+            add(t, sum);
+            if (half + t < stages)
+                add(half + t, other);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            sum[r] = sum[r] + other[r] + low[r];
+        return sum;
+    };
+
+    constexpr int SQUARES = 4;   // blocks of A a wavefront computes, of mp = 128
+#pragma unroll 1
+    for (int i = 0; i < p.steps; ++i) {
+        // (else every block's addresses are found once, kept, and spilled)
+        asm volatile("" : "+v"(s16), "+v"(g), "+s"(mb));
+        const int squares = mb * mb;
+        // read where the argument lies: an index into it that is not a constant
+        // puts a copy of it into scratch memory
+        typedef const __attribute__((address_space(4))) char ArgumentByte;
+        typedef const __attribute__((address_space(4))) float ArgumentFloat;
+        ArgumentFloat *at = (ArgumentFloat *)((ArgumentByte *)__builtin_amdgcn_kernarg_segment_ptr() +
+                                              offsetof(Small, step) + i * sizeof(SmallStep));
+        static_assert(sizeof(SmallStep) == 8 * sizeof(float), "");
+        const SmallStep k = {at[0], {at[1], at[2]}, {at[3], at[4]}, {at[5], at[6]}, at[7]};
+        for (int id = wave; id < squares; id += kSmallWaves) {
+            const int bi = id / mb, bj = id % mb;
+            const floatx4 v4 = block(p.np / 32, [&](int t, int term) { return along(xs, bi, t, term); },
+                                     [&](int t, int term) { return along(xs, bj, t, term); });
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                put(as, 16 * bi + 4 * g + r, 16 * bj + s16, k.gram * v4[r]);
+        }
+        __syncthreads();
+        floatx4 held[kSmallBlocks];
+#pragma unroll
+        for (int b = 0; b < SQUARES; ++b) {
+            const int id = wave + kSmallWaves * b, bi = id / mb, bj = id % mb;
+            if (id < squares) {
+                held[b] = block(mp / 32, [&](int t, int term) { return along(as, bi, t, term); },
+                                [&](int t, int term) { return along(as, bj, t, term); });
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * bi + 4 * g + r, col = 16 * bj + s16;
+                    uint8_t *q = place(as, row, col);
+                    const float a = (float)*reinterpret_cast<_Float16 *>(q) + (float)*reinterpret_cast<_Float16 *>(lower(q));
+                    const bool on = row == col;
+                    const float rest = __builtin_fmaf(k.alpha[1], held[b][r], __builtin_fmaf(k.beta[1], a, on ? k.diagonal[1] : 0.f));
+                    held[b][r] = __builtin_fmaf(k.alpha[0], held[b][r], __builtin_fmaf(k.beta[0], a, on ? k.diagonal[0] : 0.f)) + rest;
+                }
+            }
+        }
+        __syncthreads();   // A has been read
+#pragma unroll
+        for (int b = 0; b < SQUARES; ++b) {
+            const int id = wave + kSmallWaves * b, bi = id / mb, bj = id % mb;
+            if (id < squares) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    put(as, 16 * bi + 4 * g + r, 16 * bj + s16, held[b][r]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kSmallBlocks; ++b) {
+            const int id = wave + kSmallWaves * b, bi = id % mb, bj = id / mb;
+            if (id < mb * nb) {
+                held[b] = block(mp / 32, [&](int t, int term) { return along(as, bi, t, term); },
+                                [&](int t, int term) { return across_x(bj, t, term); });
+            }
+        }
+        __syncthreads();   // X has been read
+#pragma unroll
+        for (int b = 0; b < kSmallBlocks; ++b) {
+            const int id = wave + kSmallWaves * b, bi = id % mb, bj = id / mb;
+            if (id < mb * nb) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * bi + 4 * g + r, col = 16 * bj + s16;
+                    const float y = k.next * held[b][r];
+                    if (i + 1 < p.steps)
+                        put(xs, row, col, y);
+                    else if (row < p.m && col < p.n)   // the result, as it is stored
+                        reinterpret_cast<float *>(xs)[p.turned_out ? col * p.m + row : row * p.n + col] = y;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    const int cols = p.turned_out ? p.m : p.n, rows = p.turned_out ? p.n : p.m, wide = (cols + 7) / 8;
+    for (int id = threadIdx.x; id < wide * rows; id += 64 * kSmallWaves) {
+        const int r = id / wide, c = 8 * (id % wide);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = reinterpret_cast<const float *>(xs)[r * cols + min(c + e, cols - 1)];
+        store8_of(p.fmt, p.out, matrix * p.out_matrix + (size_t)r * p.out_ld + c, cols - c, y);
+    }
+}
+
 // ------------------------------------------------------------------- host --
 
 constexpr size_t kWsAlign = 256;
@@ -1022,6 +1240,7 @@ struct Step {
 };
 
 struct Layout {
+    bool small;              // all steps in one launch
     int m, n, ldx, lda;
     bool turned_in, turned_out;
     int blocks, lg;          // of the sums of squares
@@ -1029,6 +1248,16 @@ struct Layout {
     Step step[GEMM_MAX_STEPS];
     size_t sums, x[2], gram, poly, part, bytes;   // offsets, and the whole size
 };
+
+// A step of the small kernel takes about 2 us and 0.26 for each of these, of the
+// others 15 us and more: 64 x 64 28 us against 77, 16 x 1000 48 and 75, 96 x 300 (63
+// stages) 97 and 95.
+constexpr int kSmallStages = 44;
+long long small_stages(int m, int n)
+{
+    const int mb = ceil_div(m, 16), nb = ceil_div(n, 16), mt = ceil_div(m, 32), nt = ceil_div(n, 32);
+    return (long long)ceil_div(mb * mb, kSmallWaves) * (nt + mt) + (long long)ceil_div(mb * nb, kSmallWaves) * mt;
+}
 
 bool ld_ok(int ld, int row) { return ld >= (row > 1 ? row : 1); }
 
@@ -1061,6 +1290,15 @@ int lay_out(const gemm_orthogonalize_params *q, Layout &l)
     const bool tall = q->M > q->N;
     l.m = tall ? q->N : q->M, l.n = tall ? q->M : q->N;
     l.turned_in = tall != (q->op_g == GEMM_OP_T), l.turned_out = tall != (q->op_o == GEMM_OP_T);
+    // LDS holds X and A, 16 x 16 blocks and G's units are no more than the registers
+    // take, and a wavefront's 32-deep block products a step at most kSmallStages
+    const long long mp = (l.m + 31LL) / 32 * 32, np = (l.n + 31LL) / 32 * 32;
+    const int cols = l.turned_in ? l.m : l.n, rows = l.turned_in ? l.n : l.m;
+    l.small = mp <= 128 && 4 * mp * (mp + np) <= kSmallBytes &&
+              ceil_div(l.m, 16) * ceil_div(l.n, 16) <= kSmallWaves * kSmallBlocks &&
+              (long long)rows * ceil_div(cols, 8) <= 64 * kSmallWaves * kSmallUnits && q->batch < kMostGroups / 4 && small_stages(l.m, l.n) <= kSmallStages;
+    if (l.small)
+        return GEMM_OK;
     l.ldx = Pair::stride(l.n), l.lda = Pair::stride(l.m);
     for (int i = 0; i < 3; ++i)
         if (!choose((Which)i, l.m, l.n, q->batch, l.way[i]))
@@ -1073,7 +1311,6 @@ int lay_out(const gemm_orthogonalize_params *q, Layout &l)
     l.blocks = (int)(parts < 1024 ? parts : 1024);
     if (q->batch * (long long)l.blocks >= kMostGroups)
         return GEMM_ERR_INVALID_DIM;
-    const int cols = l.turned_in ? l.m : l.n;
     while (l.lg < 8 && (8 << l.lg) < cols)
         ++l.lg;
     const auto take = [&](size_t bytes) {
@@ -1094,23 +1331,29 @@ int lay_out(const gemm_orthogonalize_params *q, Layout &l)
     return GEMM_OK;
 }
 
-template <int SIDE, int NB, int GROUPS>
+template <int SIDE, int NB, int GROUPS, bool LOW = false>
 hipError_t launch_as(Which which, const Operands &p, const Work &w, bool joined, const Finish &f, hipStream_t s)
 {
     const dim3 grid((unsigned)w.groups), blocks((unsigned)((w.tiles - w.whole) * (SIDE / 64) * (SIDE / 64)));
     const dim3 threads(256 * GROUPS);
     if (which == kUpdate)
-        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, kUpdate>), grid, threads, 0, s, p, w, f);
+        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, LOW, kUpdate>), grid, threads, 0, s, p, w, f);
     else if (which == kPolynomial)
-        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, kPolynomial>), grid, threads, 0, s, p, w, f);
+        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, LOW, kPolynomial>), grid, threads, 0, s, p, w, f);
     else
-        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, kGram>), grid, threads, 0, s, p, w, f);
+        hipLaunchKernelGGL((newton_schulz_kernel<SIDE, NB, GROUPS, LOW, kGram>), grid, threads, 0, s, p, w, f);
     if (joined && which == kUpdate)
         hipLaunchKernelGGL((newton_schulz_join_kernel<SIDE, false>), blocks, dim3(256), 0, s, p, w, f);
     else if (joined)
         hipLaunchKernelGGL((newton_schulz_join_kernel<SIDE, true>), blocks, dim3(256), 0, s, p, w, f);
     return hipGetLastError();
 }
+
+// Up to this many rows the sums are short enough for their few products' rounding to
+// show: 20 x 1587 errs by 1.5e-6, and with LOW, at 10% of the time, by 1.0e-6 (FP32
+// products: 1.0e-6).  Past it FP32's own sums err more (777 x 1033: 2.8e-6 and 1.7e-6
+// without).
+constexpr int kFewRows = 128;
 
 hipError_t launch(Which which, const Pair &a, const Pair &b, int m, int n, int batch, const Way &way, float *slabs,
                   const Finish &f, hipStream_t s)
@@ -1126,7 +1369,9 @@ hipError_t launch(Which which, const Pair &a, const Pair &b, int m, int n, int b
     switch (way.tile) {
     case kTile256: return launch_as<256, 2, 1>(which, p, w, way.joined, f, s);
     case kTile128: return launch_as<128, 4, 1>(which, p, w, way.joined, f, s);
-    case kTile64: return launch_as<64, 4, 2>(which, p, w, way.joined, f, s);
+    case kTile64:
+        return m <= kFewRows ? launch_as<64, 4, 2, true>(which, p, w, way.joined, f, s)
+                             : launch_as<64, 4, 2>(which, p, w, way.joined, f, s);
     }
     return hipErrorInvalidValue;
 }
@@ -1141,7 +1386,7 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
         return GEMM_OK;
     if (!G || !O)
         return GEMM_ERR_NULL_PTR;
-    if (!ws || ws_bytes < l.bytes || ((uintptr_t)ws & (kWsAlign - 1)) != 0)
+    if (l.bytes && (!ws || ws_bytes < l.bytes || ((uintptr_t)ws & (kWsAlign - 1)) != 0))
         return GEMM_ERR_WORKSPACE;
     const int dev = device_status();
     if (dev != GEMM_OK)
@@ -1149,13 +1394,44 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
     hipStream_t s = (hipStream_t)stream;
     uint8_t *base = (uint8_t *)ws;
     const int batch = q->batch;
+    const auto hold = [](float (&to)[2], double v) {
+        to[0] = (float)v;
+        to[1] = (float)(v - to[0]);
+    };
+    // what the sums of step i's products are multiplied by
+    const auto gram_of = [&](int i) { return (float)std::ldexp(1.0, l.step[i].gram - 2 * l.step[i].x); };
+    const auto next_of = [&](int i) {
+        const int from = l.step[i].poly + l.step[i].x;
+        return i + 1 < q->steps ? (float)std::ldexp(1.0, l.step[i + 1].x - from) : (float)std::ldexp(q->scale, -from);
+    };
+    const auto polynomial_of = [&](int i, auto &f) {
+        const Step &k = l.step[i];
+        hold(f.alpha, std::ldexp(k.c, k.poly - 2 * k.gram));
+        hold(f.beta, std::ldexp(k.b, k.poly - k.gram));
+        hold(f.diagonal, std::ldexp(k.a, k.poly));
+    };
+    const bool t = q->op_g == GEMM_OP_T;
+    const Source g{G, t ? q->N : q->M, t ? q->M : q->N, q->ldg, batch > 1 ? q->stride_g : 0, fmt};
+    if (l.small) {
+        Small p{};
+        p.g = g;
+        p.m = l.m, p.n = l.n, p.mp = (l.m + 31) / 32 * 32, p.np = (l.n + 31) / 32 * 32;
+        p.turned_in = l.turned_in, p.turned_out = l.turned_out;
+        p.eps = q->eps, p.by = std::ldexp(1.0, l.step[0].x);
+        p.steps = q->steps;
+        p.out = O, p.out_ld = q->ldo, p.out_matrix = batch > 1 ? q->stride_o : 0, p.fmt = fmt;
+        for (int i = 0; i < q->steps; ++i) {
+            polynomial_of(i, p.step[i]);
+            p.step[i].gram = gram_of(i), p.step[i].next = next_of(i);
+        }
+        hipLaunchKernelGGL(newton_schulz_small_kernel, dim3((unsigned)batch), dim3(64 * kSmallWaves), 0, s, p);
+        return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    }
     const auto pair = [&](size_t at, int ld) {
         return Pair{(uint16_t *)(base + at), (long long)l.m * ld, ld};
     };
     const Pair x[2] = {pair(l.x[0], l.ldx), pair(l.x[1], l.ldx)}, gram = pair(l.gram, l.lda), poly = pair(l.poly, l.lda);
 
-    const bool t = q->op_g == GEMM_OP_T;
-    const Source g{G, t ? q->N : q->M, t ? q->M : q->N, q->ldg, batch > 1 ? q->stride_g : 0, fmt};
     double *sums = (double *)(base + l.sums);
     hipLaunchKernelGGL(squares_kernel, dim3((unsigned)(batch * l.blocks)), dim3(256), 0, s, g, l.blocks, l.lg, sums);
     const int across = ceil_div(g.cols, 64), per = across * ceil_div(g.rows, 64);
@@ -1166,33 +1442,24 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
     const auto product = [&](Which which, const Pair &a, const Pair &b, const Finish &f) {
         return launch(which, a, b, l.m, l.n, batch, l.way[which], (float *)(base + l.part), f, s);
     };
-    const auto hold = [](float (&to)[2], double v) {
-        to[0] = (float)v;
-        to[1] = (float)(v - to[0]);
-    };
     for (int i = 0; i < q->steps && err == hipSuccess; ++i) {
-        const Step &k = l.step[i];
         const Pair &now = x[i & 1], &next = x[(i + 1) & 1];
         Finish f{};
-        f.alpha[0] = (float)std::ldexp(1.0, k.gram - 2 * k.x);
+        f.alpha[0] = gram_of(i);
         f.to = gram;
         err = product(kGram, now, now, f);
         if (err != hipSuccess)
             break;
         f.polynomial = true;
-        hold(f.alpha, std::ldexp(k.c, k.poly - 2 * k.gram));
-        hold(f.beta, std::ldexp(k.b, k.poly - k.gram));
-        hold(f.diagonal, std::ldexp(k.a, k.poly));
+        polynomial_of(i, f);
         f.with = gram, f.to = poly;
         err = product(kPolynomial, gram, gram, f);
         if (err != hipSuccess)
             break;
         f = Finish{};
-        if (i + 1 < q->steps) {
-            f.alpha[0] = (float)std::ldexp(1.0, l.step[i + 1].x - k.poly - k.x);
-            f.to = next;
-        } else {
-            f.alpha[0] = (float)std::ldexp(q->scale, -k.poly - k.x);
+        f.alpha[0] = next_of(i);
+        f.to = next;
+        if (i + 1 == q->steps) {
             f.out = O, f.out_ld = q->ldo, f.out_matrix = batch > 1 ? q->stride_o : 0;
             f.fmt = fmt, f.turned = l.turned_out;
         }

@@ -97,13 +97,16 @@ def test_orthogonalize_refusals(kind):
     # not finite; a singular value of 1 becomes 300; one below 1 grows past 256 within the steps
     for c in ((nan, 0, 0), (1, inf, 0), (300, 0, 0), (4, 0, 0), (0, 0, 300), (1e308, 1e308, 1e308)):
         assert call(ortho(coefficients=c)) == b.GEMM_ERR_INVALID_COEFFICIENTS
-    need = b.layer_workspace("gemm_orthogonalize", ortho())
-    assert call(ortho(), None) == call(ortho(), P, None) == b.GEMM_ERR_NULL_PTR
-    assert call(ortho()) == call(ortho(), work=P, size=need - 1) == call(ortho(), work=P + 128, size=need) \
+    large = ortho(M=300, N=200)
+    need = b.layer_workspace("gemm_orthogonalize", large)
+    assert call(ortho(), None) == call(large, P, None) == b.GEMM_ERR_NULL_PTR
+    assert call(large) == call(large, work=P, size=need - 1) == call(large, work=P + 128, size=need) \
         == b.GEMM_ERR_WORKSPACE
     assert call(ortho(batch=0), None, None) == call(ortho(M=0), None, None) == b.GEMM_OK
     for c in ((1.5, -0.5, 0), (2, -1.5, 0.5), (1.875, -1.25, 0.375), (1, 0, 0), (0, 0, 0)):
-        assert b.layer_workspace("gemm_orthogonalize", ortho(coefficients=c)) > 0
+        assert b.layer_workspace("gemm_orthogonalize", ortho(M=300, N=200, coefficients=c)) > 0
+    # what LDS holds needs none
+    assert b.layer_workspace("gemm_orthogonalize", ortho()) == 0
 
 
 def test_workspaces_do_not_overflow():
