@@ -18,15 +18,16 @@
 // rounding, 2^-24 of the largest eigenvalue, is a singular value of 2^-12.
 //
 // Bound by the matrix cores where the tiles fill the compute units.
-#include <cmath>
 #include <cstddef>
 #include <stdint.h>
 
+#include "orthogonalize.h"
 #include "ring.h"
 
 namespace dgor {
 namespace {
 
+using namespace newton_schulz;
 using namespace ring;
 
 struct OpHalf : Half16 {
@@ -65,7 +66,6 @@ struct Pair {
     uint16_t *p;
     long long matrix;   // elements from a matrix to the next
     int ld;
-    __host__ __device__ static int stride(int cols) { return 2 * ((cols + 31) / 32 * 32); }
     __device__ __forceinline__ uint16_t *at(long long m, int row, int col) const
     {
         return p + m * matrix + (size_t)row * ld + 2 * (col & ~31) + (col & 31);
@@ -230,9 +230,6 @@ struct Finish {
             to.store8(m, row, col, v);
     }
 };
-
-// The three products of a step.
-enum Which { kGram, kPolynomial, kUpdate };
 
 // One product of matrices in two terms: A, M x K, by B, N x K (TB) or K x N.
 struct Operands {
@@ -907,9 +904,6 @@ __global__ __launch_bounds__(256) void newton_schulz_join_kernel(Operands p, Wor
 // X is planes of 32 columns, A and P after it likewise: row r of a plane 128 bytes,
 // higher terms and then lower ones, unit c at 8 r + (c ^ ((r >> 1) & 7)).  Rows and
 // columns up to multiples of 32 are zeros.
-constexpr int kSmallWaves = 16, kSmallBytes = 159 * 1024;
-constexpr int kSmallUnits = 6;     // units of eight of G a thread loads
-constexpr int kSmallBlocks = 10;   // 16 x 16 blocks of X a wavefront computes
 struct SmallStep {
     float gram, alpha[2], beta[2], diagonal[2], next;   // Finish's; of A's, P's and the next X's sums
 };
@@ -1117,220 +1111,6 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
 
 // ------------------------------------------------------------------- host --
 
-constexpr size_t kWsAlign = 256;
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
-// A launch holds fewer than 2^32 threads; the products' tiles are dealt to at most
-// 256 workgroups, and counted in ints.
-constexpr long long kMostGroups = 1 << 24, kMostTiles = 1 << 30;
-
-// How a product runs.
-enum Tile { kTile256, kTile128, kTile64 };
-constexpr int side_of(Tile t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : 64; }
-
-int results_cols(Which which, int m, int n) { return which == kUpdate ? n : m; }
-
-long long tiles_of(Which which, int m, int n, Tile t)
-{
-    const long long down = ceil_div(m, side_of(t));
-    return which == kUpdate ? down * ceil_div(n, side_of(t)) : down * (down + 1) / 2;
-}
-
-struct Way {
-    Tile tile;
-    int groups, whole, run;   // of Work
-    bool joined;
-    size_t slabs;             // bytes
-};
-
-// Microseconds of a tile: its ends (with A's part in the polynomial's), and each
-// stage, where few compute units work and where all do.  From 1 to 2080 tiles and
-// sums of 256 to 4096 (128 x 256 to 4096 x 4096, batches of 1 to 8); over those what
-// is chosen takes at most 1.15 times the shortest of the three tiles, with and
-// without runs.
-struct TileCost {
-    Tile tile;
-    double ends, polynomial, few, all;
-};
-constexpr TileCost kTiles[] = {{kTile256, 16.0, 10.0, 1.58, 2.3}, {kTile128, 7.0, 3.0, 0.58, 0.75},
-                               {kTile64, 4.0, 0.5, 0.206, 0.24}};
-constexpr int kUnits = 256;                       // compute units
-constexpr double kJoin = 5.0, kSlabBytes = 3e6;   // a join's launch; a microsecond's bytes of slabs
-
-// The tile and the way its stages are dealt.
-bool choose(Which which, int m, int n, int batch, Way &best)
-{
-    const int stages = ceil_div(which == kGram ? n : m, 32);
-    double least = 0;
-    bool any = false;
-    for (const TileCost &c : kTiles) {
-        const long long tiles = batch * tiles_of(which, m, n, c.tile);
-        if (tiles >= kMostTiles)
-            continue;
-        const double ends = c.ends + (which == kPolynomial ? c.polynomial : 0.0);
-        const auto stage = [&](long long groups) { return groups < kUnits * 3 / 4 ? c.few : c.all; };
-        const long long rounds = (tiles + kUnits - 1) / kUnits;
-        const double whole = rounds * (ends + stages * stage(tiles));
-        if (!any || whole < least) {
-            any = true, least = whole;
-            best = {c.tile, (int)(tiles < kUnits ? tiles : kUnits), (int)tiles, 1, false, 0};
-        }
-        // whole tiles in full rounds, the rest's stages in runs of at least four
-        const long long rest = tiles % kUnits;
-        for (int groups : {kUnits, kUnits * 3 / 4, kUnits / 2, kUnits / 4}) {
-            const long long run = (rest * stages + groups - 1) / groups;
-            if (rest == 0 || run < 4 || run >= stages || (tiles > kUnits && groups < kUnits))
-                continue;
-            const size_t bytes = (size_t)2 * groups * side_of(c.tile) * side_of(c.tile) * sizeof(float);
-            // (a run is of up to two tiles, at an end of each)
-            const double us = (double)(tiles / kUnits) * (ends + stages * c.all) + 2.0 * c.ends + run * stage(groups) +
-                              kJoin + bytes / kSlabBytes;
-            if (us < least) {
-                least = us;
-                best = {c.tile, groups, (int)(tiles - rest), (int)run, true, bytes};
-            }
-        }
-    }
-    return any;
-}
-
-// Bounds of a step: of X's singular values, and of the polynomial on X X^T's
-// eigenvalues.  |a s + b s^3 + c s^5| and |a + b t + c t^2| over [0, r] and [0,
-// r^2]: at the ends and where the derivative is zero.
-double grown(double a, double b, double c, double r)
-{
-    const auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
-    double most = f(r);
-    const auto at = [&](double t) {   // a zero of a + 3 b t + 5 c t^2, t = s^2
-        if (t > 0 && t < r * r)
-            most = std::fmax(most, f(std::sqrt(t)));
-    };
-    if (c != 0) {
-        const double d = 9 * b * b - 20 * a * c;
-        if (d >= 0) {
-            at((-3 * b + std::sqrt(d)) / (10 * c));
-            at((-3 * b - std::sqrt(d)) / (10 * c));
-        }
-    } else if (b != 0) {
-        at(-a / (3 * b));
-    }
-    return most;
-}
-double multiplied(double a, double b, double c, double r)
-{
-    const double t = r * r;
-    const auto f = [&](double v) { return std::fabs(a + v * (b + v * c)); };
-    double most = std::fmax(f(0), f(t));
-    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < t)
-        most = std::fmax(most, f(-b / (2 * c)));
-    return most;
-}
-// The power of two at which values of at most `most` stay binary16: the rounding
-// of the sums is far below what 60000 leaves to 65504.
-int exponent_for(double most)
-{
-    int e = 0;
-    std::frexp(60000.0 / std::fmax(most, 1.0), &e);   // 60000 / most in [2^(e - 1), 2^e)
-    return e - 1;
-}
-
-struct Step {
-    double a, b, c;
-    int x, gram, poly;   // exponents of X, A and P
-};
-
-struct Layout {
-    bool small;              // all steps in one launch
-    int m, n, ldx, lda;
-    bool turned_in, turned_out;
-    int blocks, lg;          // of the sums of squares
-    Way way[3];
-    Step step[GEMM_MAX_STEPS];
-    size_t sums, x[2], gram, poly, part, bytes;   // offsets, and the whole size
-};
-
-// A step of the small kernel takes about 2 us and 0.26 for each of these, of the
-// others 15 us and more: 64 x 64 28 us against 77, 16 x 1000 48 and 75, 96 x 300 (63
-// stages) 97 and 95.
-constexpr int kSmallStages = 44;
-long long small_stages(int m, int n)
-{
-    const int mb = ceil_div(m, 16), nb = ceil_div(n, 16), mt = ceil_div(m, 32), nt = ceil_div(n, 32);
-    return (long long)ceil_div(mb * mb, kSmallWaves) * (nt + mt) + (long long)ceil_div(mb * nb, kSmallWaves) * mt;
-}
-
-bool ld_ok(int ld, int row) { return ld >= (row > 1 ? row : 1); }
-
-int lay_out(const gemm_orthogonalize_params *q, Layout &l)
-{
-    if (!q)
-        return GEMM_ERR_NULL_PTR;
-    constexpr int LONGEST = (1 << 21) - 32;   // offsets in a tile's 256 rows stay below 2^31 bytes
-    if (q->batch < 0 || q->M < 0 || q->N < 0 || q->M > LONGEST || q->N > LONGEST || q->steps < 1 ||
-        q->steps > GEMM_MAX_STEPS || !(q->eps >= 0))
-        return GEMM_ERR_INVALID_DIM;
-    if ((q->op_g != GEMM_OP_N && q->op_g != GEMM_OP_T) || (q->op_o != GEMM_OP_N && q->op_o != GEMM_OP_T) ||
-        !ld_ok(q->ldg, q->op_g ? q->M : q->N) || !ld_ok(q->ldo, q->op_o ? q->M : q->N))
-        return GEMM_ERR_INVALID_LAYOUT;
-    l = Layout{};
-    double r = 1;
-    for (int i = 0; i < q->steps; ++i) {
-        Step &s = l.step[i];
-        s.a = q->coefficients[3 * i], s.b = q->coefficients[3 * i + 1], s.c = q->coefficients[3 * i + 2];
-        if (!std::isfinite(s.a) || !std::isfinite(s.b) || !std::isfinite(s.c))
-            return GEMM_ERR_INVALID_COEFFICIENTS;
-        const double p = multiplied(s.a, s.b, s.c, r), next = grown(s.a, s.b, s.c, r);
-        if (!(p <= 256) || !(next <= 256))
-            return GEMM_ERR_INVALID_COEFFICIENTS;
-        s.x = exponent_for(r), s.gram = exponent_for(r * r), s.poly = exponent_for(p);
-        r = next;
-    }
-    if (q->batch == 0 || q->M == 0 || q->N == 0)
-        return GEMM_OK;
-    const bool tall = q->M > q->N;
-    l.m = tall ? q->N : q->M, l.n = tall ? q->M : q->N;
-    l.turned_in = tall != (q->op_g == GEMM_OP_T), l.turned_out = tall != (q->op_o == GEMM_OP_T);
-    // LDS holds X and A, 16 x 16 blocks and G's units are no more than the registers
-    // take, and a wavefront's 32-deep block products a step at most kSmallStages
-    const long long mp = (l.m + 31LL) / 32 * 32, np = (l.n + 31LL) / 32 * 32;
-    const int cols = l.turned_in ? l.m : l.n, rows = l.turned_in ? l.n : l.m;
-    l.small = mp <= 128 && 4 * mp * (mp + np) <= kSmallBytes &&
-              ceil_div(l.m, 16) * ceil_div(l.n, 16) <= kSmallWaves * kSmallBlocks &&
-              (long long)rows * ceil_div(cols, 8) <= 64 * kSmallWaves * kSmallUnits && q->batch < kMostGroups / 4 && small_stages(l.m, l.n) <= kSmallStages;
-    if (l.small)
-        return GEMM_OK;
-    l.ldx = Pair::stride(l.n), l.lda = Pair::stride(l.m);
-    for (int i = 0; i < 3; ++i)
-        if (!choose((Which)i, l.m, l.n, q->batch, l.way[i]))
-            return GEMM_ERR_INVALID_DIM;
-    if (q->batch * (long long)ceil_div(l.m, 64) * ceil_div(l.n, 64) >= kMostGroups)
-        return GEMM_ERR_INVALID_DIM;
-    // parts of at least 2048 elements, a unit of eight a thread; at most 1024, four
-    // a thread of start_kernel
-    const long long parts = ((long long)l.m * l.n + 2047) / 2048;
-    l.blocks = (int)(parts < 1024 ? parts : 1024);
-    if (q->batch * (long long)l.blocks >= kMostGroups)
-        return GEMM_ERR_INVALID_DIM;
-    while (l.lg < 8 && (8 << l.lg) < cols)
-        ++l.lg;
-    const auto take = [&](size_t bytes) {
-        const size_t at = l.bytes;
-        l.bytes += round_up(bytes, kWsAlign);
-        return at;
-    };
-    const size_t b = (size_t)q->batch, x = 2 * b * l.m * l.ldx, a = 2 * b * l.m * l.lda;
-    l.sums = take(sizeof(double) * b * l.blocks);
-    l.x[0] = take(x);
-    l.x[1] = q->steps > 1 ? take(x) : l.x[0];
-    l.gram = take(a);
-    l.poly = take(a);
-    size_t part = 0;
-    for (const Way &w : l.way)
-        part = w.slabs > part ? w.slabs : part;
-    l.part = take(part);
-    return GEMM_OK;
-}
-
 template <int SIDE, int NB, int GROUPS, bool LOW = false>
 hipError_t launch_as(Which which, const Operands &p, const Work &w, bool joined, const Finish &f, hipStream_t s)
 {
@@ -1477,8 +1257,8 @@ int gemm_orthogonalize_workspace(const gemm_orthogonalize_params *params, size_t
 {
     if (!bytes)
         return GEMM_ERR_NULL_PTR;
-    dgor::Layout l;
-    const int rc = dgor::lay_out(params, l);
+    dgor::newton_schulz::Layout l;
+    const int rc = dgor::newton_schulz::lay_out(params, l);
     if (rc == GEMM_OK)
         *bytes = l.bytes;
     return rc;

@@ -584,7 +584,7 @@ int gemm_gated_i8_bf16(const gemm_gated_i8_params *params, const int8_t *X, cons
  *   where M > N), with the step's own a, b, c,
  *   O = scale X.
  * The operands of the products are held as two binary16 terms each at a power of
- * two that the coefficients give, to 2^-23 of a value and 2^-37 of the largest;
+ * two that the coefficients give, to 2^-23 of a value and 2^-39 of the largest;
  * a step's sums, A and c A A + b A are computed in FP32, |G| in FP64.
  * G and O are stored M x N (op GEMM_OP_N) or N x M (GEMM_OP_T), stride_g and
  * stride_o elements from a matrix to the next (read only where batch > 1).  O may

@@ -114,7 +114,8 @@ def signs(M, N, k, seed, batch=1):
 
 EXACT = [(1, 1, 0), (1, 5, 1), (4, 1, 1), (8, 8, 2), (16, 33, 3), (33, 16, 3), (64, 64, 3), (65, 64, 4), (72, 200, 4),
          (128, 256, 4), (129, 130, 4), (257, 100, 4), (300, 77, 4), (256, 512, 4), (520, 264, 5), (777, 1033, 5),
-         (1033, 777, 5), (64, 4096, 4), (2000, 40, 4), (1024, 1024, 5), (2049, 1500, 5)]
+         (1033, 777, 5), (64, 4096, 4), (2000, 40, 4), (1024, 1024, 5), (2049, 1500, 5), (128, 4100, 4), (96, 96, 3), (40, 300, 4),
+         (3000, 3000, 5), (2200, 4400, 5), (4400, 2300, 5), (4100, 4096, 5), (4070, 4200, 5)]
 
 
 @pytest.mark.parametrize("stored", ["rows", "columns"])
