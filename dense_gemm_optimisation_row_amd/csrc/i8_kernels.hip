@@ -490,12 +490,11 @@ hipError_t launch_i8_ring(const Product &q, const I8Epilogue &e, RingTile tile, 
     p.group_m = 4;
     switch (tile) {
     case kRing256: return launch_ring_as<256, 256>(p, e, s);
-    case kRing256x128: return launch_ring_as<256, 128>(p, e, s);
     case kRing128: return launch_ring_as<128, 128>(p, e, s);
     case kRing128x64: return launch_ring_as<128, 64>(p, e, s);
     case kRing64: return launch_ring_as<64, 64>(p, e, s);
+    default: return hipErrorInvalidValue;   // 256 x 128 is never the shortest on rows along k
     }
-    return hipErrorInvalidValue;
 }
 
 hipError_t launch_i8_rows(const Product &q, const I8Epilogue &e, hipStream_t s)

@@ -76,6 +76,8 @@ void choose_ring(Plan &l)
     double best = 0;
     bool any = false;
     for (const dgor::RingCost &c : dgor::kRings) {
+        if (c.tile == dgor::kRing256x128)   // never the shortest with its half lines
+            continue;
         const long long n = dgor::tiles(p, ring_tile_m(c.tile), ring_tile_n(c.tile));
         for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
             if (parts > 1 && (2 * parts > stages || n * parts > 512 * c.share))

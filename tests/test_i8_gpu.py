@@ -180,7 +180,7 @@ def within(got, ref, err, what):
 SHAPES = [(1, 1, 1), (1, 17, 16), (3, 5, 7), (1, 4096, 4096), (2, 264, 1040), (16, 128, 512), (17, 40, 4099), (33, 100, 72),
           (48, 130, 2048), (64, 257, 144), (65, 72, 4096), (66, 65, 16), (129, 130, 131), (200, 1024, 1040),
           (257, 300, 264), (520, 520, 136), (100, 64, 16000), (1000, 1033, 777)]
-LARGE = [(2056, 2176, 208), (4096, 2048, 80), (1537, 4100, 512)]
+LARGE = [(2056, 2176, 208), (4096, 2048, 80), (1537, 4100, 512), (1000, 2100, 1040), (4090, 4090, 528), (4090, 2040, 528)]
 
 
 @pytest.mark.parametrize("stored", ["NK", "KN"])
