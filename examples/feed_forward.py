@@ -1,6 +1,7 @@
 """A transformer's feed-forward sublayer on the layer functions: a training
-step (forward and backward) over a batch of sequences and a decoding step for
-one token, y = x + down(silu(norm(x) Wg) * (norm(x) Wu)).
+step (forward and backward) over a batch of sequences, the orthogonalised update of
+its matrices, and a decoding step for one token, in bfloat16 and with the weights
+and activations in 8 bits, y = x + down(silu(norm(x) Wg) * (norm(x) Wu)).
 
 Run as ``python examples/feed_forward.py [--features 1024 --inner 2816 --tokens 4096]``.
 """
@@ -45,6 +46,32 @@ class FeedForward:
         dx, dweight, dbias = dg.layer_norm_backward(dn, x, self.norm_weight, mean, rstd)
         return dx.add_(dy), dweight, dbias, dgate, dup, ddown
 
+    def update(self, grads, rate=0.02):
+        """Gate, up and down moved against their orthogonalised gradients (of the
+        same sizes: gate and up in one call)."""
+        dgate, dup, ddown = grads
+        rows, cols = self.gate.shape
+        scale = rate * max(1.0, cols / rows) ** 0.5
+        step = dg.orthogonalize(torch.stack((dgate, dup)), scale=scale)
+        self.gate -= step[0]
+        self.up -= step[1]
+        self.down -= dg.orthogonalize(ddown, scale=scale)
+
+
+class ServedFeedForward:
+    """The sublayer with its weights as 8-bit codes, outputs by inputs, and a scale for
+    each output; the activations' codes are made as they come."""
+
+    def __init__(self, block):
+        self.norm_weight, self.norm_bias = block.norm_weight, block.norm_bias
+        self.gate, self.up, self.down = (dg.quantize_i8(w.t().contiguous()) for w in (block.gate, block.up, block.down))
+
+    def __call__(self, x):
+        n, n_scale = dg.quantize_i8(dg.layer_norm(x, self.norm_weight, self.norm_bias))
+        (wg, sg), (wu, su), (wd, sd) = self.gate, self.up, self.down
+        h, h_scale = dg.quantize_i8(dg.gated_i8(n, n_scale, wg.t(), sg, wu.t(), su))
+        return dg.linear_i8(h, h_scale, wd.t(), sd, residual=x)
+
 
 def plain(block, x, dy):
     """The same in 64-bit torch operations: y and the gradients of x and down."""
@@ -87,8 +114,14 @@ def main(argv=None):
     train = milliseconds(lambda: block.backward(dy, block.forward(x)[1]))
     flops = 18 * a.tokens * a.features * a.inner
     print(f"  {train:.3f} ms, {flops / train / 1e9:.0f} TFLOP/s")
+    block.update(grads[3:])
+    print(f"update: {milliseconds(lambda: block.update(grads[3:])):.3f} ms")
     token = x[:1]
     print(f"decoding step: {milliseconds(lambda: block(token)) * 1e3:.1f} us a token")
+    served = ServedFeedForward(block)
+    y = block(x)
+    off = float((served(x).double() - y.double()).norm() / (y.double() - x.double()).norm())
+    print(f"  in 8 bits: {milliseconds(lambda: served(token)) * 1e3:.1f} us a token, {off:.2e} of the sublayer's output off")
     return worst
 
 
