@@ -143,6 +143,7 @@ struct Step {
 
 struct Layout {
     bool small;              // all steps in one launch
+    int strips, width, mp;   // or, strips > 0, a step in one launch (x[0]: X, gram and poly: A's parts)
     int m, n, ldx, lda;
     bool turned_in, turned_out;
     int blocks, lg;          // of the sums of squares
@@ -159,6 +160,10 @@ constexpr int kSmallBlocks = 10;   // 16 x 16 blocks of X a wavefront computes
 // others 15 us and more: 64 x 64 28 us against 77, 16 x 1000 48 and 75, 96 x 300 (63
 // stages) 97 and 95.
 constexpr int kSmallStages = 44;
+// The strips of a matrix of few rows: at most so many, whose parts of A every
+// workgroup reads, and so many elements, which every workgroup reads for the norm.
+constexpr int kMostStrips = 8, kStripsElements = 1 << 17;
+constexpr int kStripUnits = 8;   // 16-byte units of a strip a thread holds
 inline long long small_stages(int m, int n)
 {
     const int mb = ceil_div(m, 16), nb = ceil_div(n, 16), mt = ceil_div(m, 32), nt = ceil_div(n, 32);
@@ -206,6 +211,24 @@ inline int lay_out(const gemm_orthogonalize_params *q, Layout &l)
               q->batch < kMostGroups / 4 && small_stages(l.m, l.n) <= kSmallStages;
     if (l.small)
         return GEMM_OK;
+    const auto take = [&](size_t bytes) {
+        const size_t at = l.bytes;
+        l.bytes += round_up(bytes, kWsAlign);
+        return at;
+    };
+    l.mp = (int)mp;
+    l.width = (int)std::fmax(64.0, (l.n + 32LL * kMostStrips - 1) / (32LL * kMostStrips) * 32LL);
+    l.strips = ceil_div(l.n, l.width);
+    const int mb = ceil_div(l.m, 16);
+    if (mp <= 128 && (long long)l.m * l.n <= kStripsElements && 4 * mp * (mp + l.width) <= kSmallBytes &&
+        4 * mp * l.width <= 16 * 64 * kSmallWaves * kStripUnits && mb * (l.width / 16) <= kSmallWaves * kSmallBlocks && (long long)q->batch * l.strips < kMostGroups / 4) {
+        const size_t groups = (size_t)q->batch * l.strips;
+        l.x[0] = take(groups * 4 * l.mp * l.width);
+        l.gram = take(groups * mb * (mb + 1) / 2 * 1024);
+        l.poly = q->steps > 1 ? take(groups * mb * (mb + 1) / 2 * 1024) : l.gram;
+        return GEMM_OK;
+    }
+    l.strips = 0;
     l.ldx = pair_stride(l.n), l.lda = pair_stride(l.m);
     for (int i = 0; i < 3; ++i)
         if (!choose((Which)i, l.m, l.n, q->batch, l.way[i]))
@@ -220,11 +243,6 @@ inline int lay_out(const gemm_orthogonalize_params *q, Layout &l)
         return GEMM_ERR_INVALID_DIM;
     while (l.lg < 8 && (8 << l.lg) < cols)
         ++l.lg;
-    const auto take = [&](size_t bytes) {
-        const size_t at = l.bytes;
-        l.bytes += round_up(bytes, kWsAlign);
-        return at;
-    };
     const size_t b = (size_t)q->batch, x = 2 * b * l.m * l.ldx, a = 2 * b * l.m * l.lda;
     l.sums = take(sizeof(double) * b * l.blocks);
     l.x[0] = take(x);

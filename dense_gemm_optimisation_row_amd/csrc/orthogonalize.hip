@@ -20,6 +20,7 @@
 // Bound by the matrix cores where the tiles fill the compute units.
 #include <cstddef>
 #include <stdint.h>
+#include <type_traits>
 
 #include "orthogonalize.h"
 #include "ring.h"
@@ -29,6 +30,8 @@ namespace {
 
 using namespace newton_schulz;
 using namespace ring;
+
+typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
 
 struct OpHalf : Half16 {
     static __device__ __forceinline__ floatx4 mfma(halfx8 a, halfx8 b, floatx4 c)
@@ -907,6 +910,140 @@ __global__ __launch_bounds__(256) void newton_schulz_join_kernel(Operands p, Wor
 struct SmallStep {
     float gram, alpha[2], beta[2], diagonal[2], next;   // Finish's; of A's, P's and the next X's sums
 };
+// T: planes of 32 T rows, 0 where that is known to the call alone.
+template <int T>
+struct Planes {
+    uint8_t *lds;
+    int bytes, s16, g;        // of a plane; the lane's row or column, and its group
+    uint32_t rows, cols[2];   // the lane's part of its fragments' addresses,
+    uint32_t four, one[2];    // and of its results'
+    __device__ __forceinline__ Planes(uint8_t *at, int size, int lane)
+        : lds(at), bytes(size), s16(lane & 15), g(lane >> 4)
+    {
+        rows = (uint32_t)(s16 * 128 + ((g ^ ((s16 >> 1) & 7)) * 16));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = 8 * g + 4 * h + (s16 >> 2);
+            cols[h] = (uint32_t)(k * 128 + ((((s16 & 3) >> 1) ^ ((k >> 1) & 7)) * 16) + 8 * (s16 & 1));
+            one[h] = (uint32_t)((4 * g + 2 * h) * 128 + (((s16 >> 3) ^ ((2 * g + h) & 7)) * 16) + 2 * (s16 & 7));
+        }
+        four = (uint32_t)(s16 * 128 + (((g >> 1) ^ ((s16 >> 1) & 7)) * 16) + 8 * (g & 1));
+    }
+    __device__ __forceinline__ int plane() const { return T ? 4096 * T : bytes; }
+    // element (r, c) of planes at `base`; its lower term is 64 bytes on, by an XOR
+    __device__ __forceinline__ uint8_t *place(uint8_t *base, int r, int c) const
+    {
+        return base + (c >> 5) * plane() + r * 128 + ((((c & 31) >> 3) ^ ((r >> 1) & 7)) * 16) + 2 * (c & 7);
+    }
+    __device__ __forceinline__ uint8_t *lower(const uint8_t *q) const { return lds + ((uint32_t)(q - lds) ^ 64u); }
+    __device__ __forceinline__ void put(uint8_t *base, int r, int c, float y) const
+    {
+        uint8_t *q = place(base, r, c);
+        const _Float16 hi = (_Float16)y;
+        *reinterpret_cast<_Float16 *>(q) = hi;
+        *reinterpret_cast<_Float16 *>(lower(q)) = (_Float16)(y - (float)hi);
+    }
+    // The 16 x 16 block (bi, bj) of planes at base from its transpose as the matrix
+    // cores give it: the lane's row 16 bi + s16, four neighbours from 16 bj + 4 g.
+    __device__ __forceinline__ uint8_t *place4(uint8_t *base, int bi, int bj, int term) const
+    {
+        return base + ((bj >> 1) * plane() + 2048 * bi) + (four ^ (32u * (bj & 1) ^ 64u * term));
+    }
+    __device__ __forceinline__ void put4(uint8_t *base, int bi, int bj, floatx4 y) const
+    {
+        halfx4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = (_Float16)y[e];
+            lo[e] = (_Float16)(y[e] - (float)hi[e]);
+        }
+        *reinterpret_cast<halfx4 *>(place4(base, bi, bj, 0)) = hi;
+        *reinterpret_cast<halfx4 *>(place4(base, bi, bj, 1)) = lo;
+    }
+    __device__ __forceinline__ floatx4 get4(uint8_t *base, int bi, int bj) const
+    {
+        const halfx4 hi = *reinterpret_cast<const halfx4 *>(place4(base, bi, bj, 0));
+        const halfx4 lo = *reinterpret_cast<const halfx4 *>(place4(base, bi, bj, 1));
+        floatx4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = (float)hi[e] + (float)lo[e];
+        return y;
+    }
+    // as it is: the lane's column 16 bj + s16, rows from 16 bi + 4 g
+    __device__ __forceinline__ void put_turned(uint8_t *base, int bi, int bj, floatx4 y) const
+    {
+        uint8_t *q = base + ((bj >> 1) * plane() + 2048 * bi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t at = one[e >> 1] ^ 32u * (bj & 1);
+            const _Float16 hi = (_Float16)y[e];
+            *reinterpret_cast<_Float16 *>(q + at + 128 * (e & 1)) = hi;
+            *reinterpret_cast<_Float16 *>(q + (at ^ 64u) + 128 * (e & 1)) = (_Float16)(y[e] - (float)hi);
+        }
+    }
+    // four neighbouring elements of P, of the sums v of A A and A's own
+    // (of block (bi, bj), as it is or its transpose: both are symmetric)
+    __device__ __forceinline__ floatx4 polynomial(const SmallStep &k, bool diagonal, floatx4 v, floatx4 a) const
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool on = diagonal && s16 == 4 * g + e;
+            const float rest = __builtin_fmaf(k.alpha[1], v[e], __builtin_fmaf(k.beta[1], a[e], on ? k.diagonal[1] : 0.f));
+            v[e] = __builtin_fmaf(k.alpha[0], v[e], __builtin_fmaf(k.beta[0], a[e], on ? k.diagonal[0] : 0.f)) + rest;
+        }
+        return v;
+    }
+    // Fragments: rows 16 b .. of planes at base, k 32 t ..; and columns 16 b ...  A
+    // lane's part of the address is found once: planes start on 128 bytes, so what the
+    // term and b change in it are XORs, and the rest is the same in all lanes.
+    __device__ __forceinline__ halfx8 along(const uint8_t *base, int b, int t, int term) const
+    {
+        return *reinterpret_cast<const halfx8 *>(base + (t * plane() + 2048 * b) + (rows ^ (64u * term)));
+    }
+    __device__ __forceinline__ halfx8 across(const uint8_t *base, int b, int t, int term) const
+    {
+        const uint8_t *q = base + ((b >> 1) * plane() + 4096 * t);
+        const uint32_t flip = 64u * term ^ 32u * (b & 1);
+        shortx4 part[2];
+        part[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + (cols[0] ^ flip)));
+        part[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + (cols[1] ^ flip)));
+        return __builtin_bit_cast(halfx8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    // the sum over `stages` of a block: all four products, the cross ones apart, and
+    // two halves of the others, for fewer roundings of each (KNOWN: T stages)
+    template <bool KNOWN = false, class A, class B>
+    static __device__ __forceinline__ floatx4 block(int stages, A a_of, B b_of)
+    {
+        floatx4 sum = {0.f, 0.f, 0.f, 0.f}, other = sum, low = sum;
+        auto add = [&](int t, floatx4 &to) {
+            const halfx8 a0 = a_of(t, 0), b0 = b_of(t, 0), a1 = a_of(t, 1), b1 = b_of(t, 1);
+            to = OpHalf::mfma(a0, b0, to);
+            low = OpHalf::mfma(a1, b1, low);   // (counts in sums of few products)
+            low = OpHalf::mfma(a1, b0, low);
+            low = OpHalf::mfma(a0, b1, low);
+        };
+        auto both = [&](int t, int half) {
+            add(t, sum);
+            if (half + t < stages)
+                add(half + t, other);
+        };
+        if constexpr (T != 0 && KNOWN) {
+#pragma unroll
+            for (int t = 0; t < (T + 1) / 2; ++t)
+                both(t, (T + 1) / 2);
+        } else {
+            const int half = (stages + 1) / 2;
+            for (int t = 0; t < half; ++t)
+                both(t, half);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            sum[r] = sum[r] + other[r] + low[r];
+        return sum;
+    }
+};
+
 struct Small {
     Source g;
     int m, n, mp, np;   // mp, np: padded to multiples of 32
@@ -924,12 +1061,12 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSmallBytes];
     __shared__ double sums[kSmallWaves];
     const int lane = threadIdx.x & 63;
-    int s16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const long long matrix = blockIdx.x;
     const int mp = p.mp, plane = mp * 128, nb = (p.n + 15) / 16;
     int mb = (p.m + 15) / 16;
     uint8_t *const xs = lds, *const as = lds + p.np / 32 * plane;
+    Planes<0> w(lds, plane, lane);
 
     // G, its norm, X
     for (int i = threadIdx.x; i < (p.np + mp) / 32 * plane / 16; i += 64 * kSmallWaves)
@@ -958,17 +1095,6 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
     for (int i = 1; i < kSmallWaves; ++i)
         v += sums[i];
     const double factor = p.by / (sqrt(v) + p.eps);
-    // element (r, c) of planes at `base`; its lower term is 64 bytes on, by an XOR
-    auto place = [&](uint8_t *base, int r, int c) {
-        return base + (c >> 5) * plane + r * 128 + ((((c & 31) >> 3) ^ ((r >> 1) & 7)) * 16) + 2 * (c & 7);
-    };
-    auto lower = [&](uint8_t *q) { return lds + ((uint32_t)(q - lds) ^ 64u); };
-    auto put = [&](uint8_t *base, int r, int c, float y) {
-        uint8_t *q = place(base, r, c);
-        const _Float16 hi = (_Float16)y;
-        *reinterpret_cast<_Float16 *>(q) = hi;
-        *reinterpret_cast<_Float16 *>(lower(q)) = (_Float16)(y - (float)hi);
-    };
 #pragma unroll
     for (int t = 0; t < kSmallUnits; ++t) {
         const int id = (int)threadIdx.x + 64 * kSmallWaves * t;
@@ -977,54 +1103,16 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (c + e < p.g.cols)
-                    put(xs, p.turned_in ? c + e : r, p.turned_in ? r : c + e, (float)(f[t][e] * factor));
+                    w.put(xs, p.turned_in ? c + e : r, p.turned_in ? r : c + e, (float)(f[t][e] * factor));
         }
     }
     __syncthreads();
-
-    // fragments: rows 16 b .. of planes at base, k 32 t ..; and columns 16 b ..
-    auto along = [&](const uint8_t *base, int b, int t, int term) {
-        const uint32_t at = (uint32_t)(base - lds) + (uint32_t)(t * plane + (16 * b + s16) * 128 + ((g ^ ((s16 >> 1) & 7)) * 16));
-        return *reinterpret_cast<const halfx8 *>(lds + (at ^ (uint32_t)(64 * term)));
-    };
-    auto across_x = [&](int b, int t, int term) {
-        shortx4 part[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = 32 * t + 8 * g + 4 * h + (s16 >> 2), u = 4 * term + 2 * (b & 1) + ((s16 & 3) >> 1);
-            const uint8_t *q = xs + (b >> 1) * plane + k * 128 + ((u ^ ((k >> 1) & 7)) * 16) + 8 * (s16 & 1);
-            part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
-        }
-        return __builtin_bit_cast(halfx8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    // the sum over `stages` of a block: all four products, the cross ones apart, and
-    // two halves of the others, for fewer roundings of each
-    auto block = [&](int stages, auto a_of, auto b_of) {
-        floatx4 sum = {0.f, 0.f, 0.f, 0.f}, other = sum, low = sum;
-        auto add = [&](int t, floatx4 &to) {
-            const halfx8 a0 = a_of(t, 0), b0 = b_of(t, 0), a1 = a_of(t, 1), b1 = b_of(t, 1);
-            to = OpHalf::mfma(a0, b0, to);
-            low = OpHalf::mfma(a1, b1, low);   // (counts in sums of few products)
-            low = OpHalf::mfma(a1, b0, low);
-            low = OpHalf::mfma(a0, b1, low);
-        };
-        const int half = (stages + 1) / 2;
-        for (int t = 0; t < half; ++t) {
-            add(t, sum);
-            if (half + t < stages)
-                add(half + t, other);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            sum[r] = sum[r] + other[r] + low[r];
-        return sum;
-    };
 
     constexpr int SQUARES = 4;   // blocks of A a wavefront computes, of mp = 128
 #pragma unroll 1
     for (int i = 0; i < p.steps; ++i) {
         // (else every block's addresses are found once, kept, and spilled)
-        asm volatile("" : "+v"(s16), "+v"(g), "+s"(mb));
+        asm volatile("" : "+v"(w.s16), "+v"(w.g), "+v"(w.rows), "+v"(w.cols[0]), "+v"(w.cols[1]), "+v"(w.four), "+s"(mb));
         const int squares = mb * mb;
         // read where the argument lies: an index into it that is not a constant
         // puts a copy of it into scratch memory
@@ -1036,11 +1124,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
         const SmallStep k = {at[0], {at[1], at[2]}, {at[3], at[4]}, {at[5], at[6]}, at[7]};
         for (int id = wave; id < squares; id += kSmallWaves) {
             const int bi = id / mb, bj = id % mb;
-            const floatx4 v4 = block(p.np / 32, [&](int t, int term) { return along(xs, bi, t, term); },
-                                     [&](int t, int term) { return along(xs, bj, t, term); });
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                put(as, 16 * bi + 4 * g + r, 16 * bj + s16, k.gram * v4[r]);
+            const floatx4 v4 = Planes<0>::block(p.np / 32, [&](int t, int term) { return w.along(xs, bi, t, term); },
+                                     [&](int t, int term) { return w.along(xs, bj, t, term); });
+            w.put4(as, bj, bi, k.gram * v4);   // (symmetric)
         }
         __syncthreads();
         floatx4 held[kSmallBlocks];
@@ -1048,36 +1134,26 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
         for (int b = 0; b < SQUARES; ++b) {
             const int id = wave + kSmallWaves * b, bi = id / mb, bj = id % mb;
             if (id < squares) {
-                held[b] = block(mp / 32, [&](int t, int term) { return along(as, bi, t, term); },
-                                [&](int t, int term) { return along(as, bj, t, term); });
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * bi + 4 * g + r, col = 16 * bj + s16;
-                    uint8_t *q = place(as, row, col);
-                    const float a = (float)*reinterpret_cast<_Float16 *>(q) + (float)*reinterpret_cast<_Float16 *>(lower(q));
-                    const bool on = row == col;
-                    const float rest = __builtin_fmaf(k.alpha[1], held[b][r], __builtin_fmaf(k.beta[1], a, on ? k.diagonal[1] : 0.f));
-                    held[b][r] = __builtin_fmaf(k.alpha[0], held[b][r], __builtin_fmaf(k.beta[0], a, on ? k.diagonal[0] : 0.f)) + rest;
-                }
+                held[b] = Planes<0>::block(mp / 32, [&](int t, int term) { return w.along(as, bi, t, term); },
+                                [&](int t, int term) { return w.along(as, bj, t, term); });
+                held[b] = w.polynomial(k, bi == bj, held[b], w.get4(as, bj, bi));
             }
         }
         __syncthreads();   // A has been read
 #pragma unroll
         for (int b = 0; b < SQUARES; ++b) {
             const int id = wave + kSmallWaves * b, bi = id / mb, bj = id % mb;
-            if (id < squares) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    put(as, 16 * bi + 4 * g + r, 16 * bj + s16, held[b][r]);
-            }
+            if (id < squares)
+                w.put4(as, bj, bi, held[b]);
         }
         __syncthreads();
 #pragma unroll
         for (int b = 0; b < kSmallBlocks; ++b) {
             const int id = wave + kSmallWaves * b, bi = id % mb, bj = id / mb;
             if (id < mb * nb) {
-                held[b] = block(mp / 32, [&](int t, int term) { return along(as, bi, t, term); },
-                                [&](int t, int term) { return across_x(bj, t, term); });
+                // (X's columns first: a lane's four are neighbours)
+                held[b] = Planes<0>::block(mp / 32, [&](int t, int term) { return w.across(xs, bj, t, term); },
+                                        [&](int t, int term) { return w.along(as, bi, t, term); });
             }
         }
         __syncthreads();   // X has been read
@@ -1085,15 +1161,15 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
         for (int b = 0; b < kSmallBlocks; ++b) {
             const int id = wave + kSmallWaves * b, bi = id % mb, bj = id / mb;
             if (id < mb * nb) {
+                const int row = 16 * bi + w.s16, col = 16 * bj + 4 * w.g;
+                const floatx4 y = k.next * held[b];
+                if (i + 1 < p.steps)
+                    w.put4(xs, bi, bj, y);
+                else   // the result, as it is stored
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * bi + 4 * g + r, col = 16 * bj + s16;
-                    const float y = k.next * held[b][r];
-                    if (i + 1 < p.steps)
-                        put(xs, row, col, y);
-                    else if (row < p.m && col < p.n)   // the result, as it is stored
-                        reinterpret_cast<float *>(xs)[p.turned_out ? col * p.m + row : row * p.n + col] = y;
-                }
+                    for (int e = 0; e < 4; ++e)
+                        if (row < p.m && col + e < p.n)
+                            reinterpret_cast<float *>(xs)[p.turned_out ? (col + e) * p.m + row : row * p.n + col + e] = y[e];
             }
         }
         __syncthreads();
@@ -1106,6 +1182,249 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
         for (int e = 0; e < 8; ++e)
             y[e] = reinterpret_cast<const float *>(xs)[r * cols + min(c + e, cols - 1)];
         store8_of(p.fmt, p.out, matrix * p.out_matrix + (size_t)r * p.out_ld + c, cols - c, y);
+    }
+}
+
+// ----------------------------------------------------- matrices of few rows --
+//
+// Up to 128 rows and in too many columns for one workgroup's LDS: X stays in strips
+// of columns, a workgroup each, and a step is one launch.  It adds the strips' parts
+// of A = X X^T, computes P (each strip's workgroup all of it), its strip of P X, and
+// that strip's part of the next A.  Planes are as above; a strip lies in the
+// workspace as LDS holds it, a part of A as the lanes hold the blocks on and below
+// the diagonal.  Bound by latency as well: 10 us a step, where three launches
+// take 18 (8 of 128 x 256).
+struct Strips {
+    int m, n, width, strips;   // width: a strip's columns, a multiple of 32
+    bool turned;                   // in: X is G's transpose; out: the result's
+    uint8_t *images;               // X's strips
+    float *parts;                  // of the next A
+};
+
+__device__ __forceinline__ void block_of(int id, int &bi, int &bj)   // on and below the diagonal
+{
+    for (bi = 0; id > bi; id -= ++bi)
+        ;
+    bj = id;
+}
+
+// A strip of X and its part of A, from LDS to the workspace.
+template <int T>
+__device__ __forceinline__ void leave_strip(const Strips &p, const Planes<T> &w, const uint8_t *xs, int wave)
+{
+    const int lane = threadIdx.x & 63, mb = (p.m + 15) / 16, lower = mb * (mb + 1) / 2, bytes = 128 * T * p.width;
+    uint8_t *const image = p.images + (size_t)blockIdx.x * bytes;
+    for (int i = 16 * threadIdx.x; i < bytes; i += 16 * 64 * kSmallWaves)
+        *reinterpret_cast<u32x4 *>(image + i) = *reinterpret_cast<const u32x4 *>(xs + i);
+    float *const part = p.parts + (size_t)blockIdx.x * lower * 256;
+    for (int id = wave; id < lower; id += kSmallWaves) {
+        int bi, bj;
+        block_of(id, bi, bj);
+        *reinterpret_cast<floatx4 *>(part + 256 * id + 4 * lane) =
+            Planes<T>::block(p.width / 32, [&](int t, int term) { return w.along(xs, bi, t, term); },
+                          [&](int t, int term) { return w.along(xs, bj, t, term); });
+    }
+}
+
+template <int T>
+__global__ __launch_bounds__(64 * kSmallWaves) void strips_start_kernel(Strips p, Source g, double eps, double by)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kSmallBytes];
+    __shared__ double sums[kSmallWaves];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const long long matrix = blockIdx.x / p.strips;
+    const int first = (int)(blockIdx.x - matrix * p.strips) * p.width, plane = 4096 * T;
+    const Planes<T> w(lds, plane, lane);
+    for (int i = 16 * threadIdx.x; i < p.width / 32 * plane; i += 16 * 64 * kSmallWaves)
+        *reinterpret_cast<u32x4 *>(lds + i) = u32x4{0u, 0u, 0u, 0u};
+    // the norm, of the whole matrix: in every strip's workgroup the same
+    double v = 0;
+    const int across = (g.cols + 7) / 8, units = across * g.rows;
+    const auto add = [&](auto fmt, auto whole) {   // four units' loads in flight at once
+        constexpr int AT_ONCE = 4;
+        for (int id0 = threadIdx.x; id0 < units; id0 += 64 * kSmallWaves * AT_ONCE) {
+            float f[AT_ONCE][8];
+#pragma unroll
+            for (int t = 0; t < AT_ONCE; ++t) {
+                const int id = min(id0 + 64 * kSmallWaves * t, units - 1), r = id / across, c = 8 * (id - r * across);
+                load8_of(fmt, g.p, matrix * g.matrix + (size_t)r * g.ld + c, whole ? 8 : g.cols - c, f[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < AT_ONCE; ++t)
+                if (id0 + 64 * kSmallWaves * t < units)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v += (double)f[t][e] * (double)f[t][e];
+        }
+    };
+    const auto add_of = [&](auto fmt) {
+        if (g.cols % 8 == 0)
+            add(fmt, std::true_type());
+        else
+            add(fmt, std::false_type());
+    };
+    switch (g.fmt) {
+    case kF32: add_of(std::integral_constant<int, kF32>()); break;
+    case kF16: add_of(std::integral_constant<int, kF16>()); break;
+    default: add_of(std::integral_constant<int, kBF16>()); break;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        v += __shfl_xor(v, o, 64);
+    if (lane == 0)
+        sums[wave] = v;
+    __syncthreads();   // and LDS is zero
+    v = sums[0];
+#pragma unroll
+    for (int i = 1; i < kSmallWaves; ++i)
+        v += sums[i];
+    const double factor = by / (sqrt(v) + eps);
+    // the strip's rows and units of G: `first` of them left out
+    const int r0 = p.turned ? first : 0, c0 = p.turned ? 0 : first;
+    const int rows = p.turned ? min(p.width, g.rows - r0) : g.rows, cols = p.turned ? g.cols : min(p.width, g.cols - c0);
+    const int wide = (cols + 7) / 8;
+    for (int id = threadIdx.x; id < wide * rows; id += 64 * kSmallWaves) {
+        const int r = id / wide, c = 8 * (id % wide);
+        float f[8];
+        g.load8(matrix, r0 + r, c0 + c, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < cols)
+                w.put(lds, p.turned ? c + e : r, p.turned ? r : c + e, (float)(f[e] * factor));
+    }
+    __syncthreads();
+    leave_strip(p, w, lds, wave);
+}
+
+struct Result {
+    void *p;
+    int ld, fmt;
+    long long matrix;
+};
+
+template <int T, bool LAST>
+__global__ __launch_bounds__(64 * kSmallWaves) void strips_step_kernel(Strips p, const float *parts, SmallStep k, Result out)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kSmallBytes];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const long long matrix = blockIdx.x / p.strips;
+    const int strip = (int)(blockIdx.x - matrix * p.strips), plane = 4096 * T;
+    const int mb = (p.m + 15) / 16, lower = mb * (mb + 1) / 2, bytes = p.width / 32 * plane;
+    uint8_t *const xs = lds, *const as = lds + bytes;
+    const Planes<T> w(lds, plane, lane);
+    for (int i = 16 * threadIdx.x; i < T * plane; i += 16 * 64 * kSmallWaves)
+        *reinterpret_cast<u32x4 *>(as + i) = u32x4{0u, 0u, 0u, 0u};
+    constexpr int SQUARES = (T * (2 * T + 1) + kSmallWaves - 1) / kSmallWaves;   // blocks on and below the diagonal a wavefront holds
+    floatx4 held[kSmallBlocks];
+    parts += (size_t)matrix * p.strips * lower * 256 + 4 * lane;
+    // all loads of four strips in flight at once: those past the last strip are the
+    // last one's, and not added
+#pragma unroll
+    for (int b = 0; b < SQUARES; ++b)
+        held[b] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < p.strips; s0 += 4) {
+        floatx4 v[SQUARES][4];
+#pragma unroll
+        for (int b = 0; b < SQUARES; ++b)
+            if (wave + kSmallWaves * b < lower)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    v[b][s] = *reinterpret_cast<const floatx4 *>(
+                        parts + ((size_t)min(s0 + s, p.strips - 1) * lower + wave + kSmallWaves * b) * 256);
+#pragma unroll
+        for (int b = 0; b < SQUARES; ++b)
+            if (wave + kSmallWaves * b < lower)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    held[b] += s0 + s < p.strips ? v[b][s] : floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    __syncthreads();   // A's planes are zero
+    // a symmetric matrix's blocks, to both places
+    auto put_squares = [&](float by) {
+#pragma unroll
+        for (int b = 0; b < SQUARES; ++b) {
+            const int id = wave + kSmallWaves * b;
+            if (id < lower) {
+                int bi, bj;
+                block_of(id, bi, bj);
+                w.put4(as, bj, bi, by * held[b]);
+                if (bi != bj)
+                    w.put_turned(as, bi, bj, by * held[b]);
+            }
+        }
+    };
+    put_squares(k.gram);
+    // X is on its way while P is computed
+    u32x4 strip_x[kStripUnits];
+    const uint8_t *const image = p.images + (size_t)blockIdx.x * bytes;
+#pragma unroll
+    for (int i = 0; i < kStripUnits; ++i) {
+        const int at = 16 * ((int)threadIdx.x + 64 * kSmallWaves * i);
+        if (at < bytes)
+            strip_x[i] = *reinterpret_cast<const u32x4 *>(image + at);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < SQUARES; ++b) {
+        const int id = wave + kSmallWaves * b;
+        if (id < lower) {
+            int bi, bj;
+            block_of(id, bi, bj);
+            held[b] = Planes<T>::template block<true>(T, [&](int t, int term) { return w.along(as, bi, t, term); },
+                                    [&](int t, int term) { return w.along(as, bj, t, term); });
+            held[b] = w.polynomial(k, bi == bj, held[b], w.get4(as, bj, bi));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kStripUnits; ++i) {
+        const int at = 16 * ((int)threadIdx.x + 64 * kSmallWaves * i);
+        if (at < bytes)
+            *reinterpret_cast<u32x4 *>(xs + at) = strip_x[i];
+    }
+    __syncthreads();   // A has been read
+    put_squares(1.f);
+    __syncthreads();
+    const int blocks = mb * (p.width / 16);
+#pragma unroll
+    for (int b = 0; b < kSmallBlocks; ++b) {
+        const int id = wave + kSmallWaves * b, bi = id % mb, bj = id / mb;
+        if (id < blocks)
+            held[b] = Planes<T>::template block<true>(T, [&](int t, int term) { return w.across(xs, bj, t, term); },
+                                    [&](int t, int term) { return w.along(as, bi, t, term); });
+    }
+    __syncthreads();   // X has been read
+    const int first = strip * p.width, inside = min(p.width, p.n - first);
+#pragma unroll
+    for (int b = 0; b < kSmallBlocks; ++b) {
+        const int id = wave + kSmallWaves * b, bi = id % mb, bj = id / mb;
+        if (id < blocks) {
+            const int row = 16 * bi + w.s16, col = 16 * bj + 4 * w.g;
+            const floatx4 y = k.next * held[b];
+            if (!LAST)
+                w.put4(xs, bi, bj, y);
+            else   // the result, as it is stored
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (row < p.m && col + e < inside)
+                        reinterpret_cast<float *>(xs)[p.turned ? (col + e) * p.m + row : row * inside + col + e] = y[e];
+        }
+    }
+    __syncthreads();
+    if (!LAST) {
+        leave_strip(p, w, xs, wave);
+        return;
+    }
+    const int cols = p.turned ? p.m : inside, rows = p.turned ? inside : p.m, wide = (cols + 7) / 8;
+    const size_t at = matrix * out.matrix + (p.turned ? (size_t)first * out.ld : (size_t)first);
+    for (int id = threadIdx.x; id < wide * rows; id += 64 * kSmallWaves) {
+        const int r = id / wide, c = 8 * (id % wide);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = reinterpret_cast<const float *>(xs)[r * cols + min(c + e, cols - 1)];
+        store8_of(out.fmt, out.p, at + (size_t)r * out.ld + c, cols - c, y);
     }
 }
 
@@ -1205,6 +1524,36 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
             p.step[i].gram = gram_of(i), p.step[i].next = next_of(i);
         }
         hipLaunchKernelGGL(newton_schulz_small_kernel, dim3((unsigned)batch), dim3(64 * kSmallWaves), 0, s, p);
+        return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    }
+    if (l.strips) {
+        Strips p{l.m, l.n, l.width, l.strips, l.turned_in, base + l.x[0], nullptr};
+        float *const parts[2] = {(float *)(base + l.gram), (float *)(base + l.poly)};
+        const Result out{O, q->ldo, fmt, batch > 1 ? q->stride_o : 0};
+        const auto steps = [&](auto planes) {
+            constexpr int T = decltype(planes)::value;
+            const dim3 groups((unsigned)(batch * l.strips)), threads(64 * kSmallWaves);
+            p.parts = parts[0];
+            hipLaunchKernelGGL(strips_start_kernel<T>, groups, threads, 0, s, p, g, q->eps, std::ldexp(1.0, l.step[0].x));
+            p.turned = l.turned_out;
+            for (int i = 0; i < q->steps; ++i) {
+                SmallStep k;
+                polynomial_of(i, k);
+                k.gram = gram_of(i), k.next = next_of(i);
+                p.parts = parts[(i + 1) & 1];
+                const float *from = parts[i & 1];
+                if (i + 1 < q->steps)
+                    hipLaunchKernelGGL((strips_step_kernel<T, false>), groups, threads, 0, s, p, from, k, out);
+                else
+                    hipLaunchKernelGGL((strips_step_kernel<T, true>), groups, threads, 0, s, p, from, k, out);
+            }
+        };
+        switch (l.mp / 32) {
+        case 1: steps(std::integral_constant<int, 1>()); break;
+        case 2: steps(std::integral_constant<int, 2>()); break;
+        case 3: steps(std::integral_constant<int, 3>()); break;
+        default: steps(std::integral_constant<int, 4>()); break;
+        }
         return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
     }
     const auto pair = [&](size_t at, int ld) {

@@ -113,6 +113,20 @@ int main()
                 printf(" small\n");
                 continue;
             }
+            if (l.strips) {
+                printf(" strips");
+                // all columns, none of them empty, in what LDS and registers hold
+                const int mb = dgor::ceil_div(l.m, 16);
+                const size_t groups = (size_t)q.batch * l.strips, part = groups * mb * (mb + 1) / 2 * 1024;
+                if (l.width % 32 != 0 || l.mp % 32 != 0 || l.mp < l.m || l.strips * l.width < l.n || l.strips < 1 ||
+                    (l.strips - 1) * l.width >= l.n || 4 * l.mp * (l.width + l.mp) > dgor::kSmallBytes ||
+                    4 * l.mp * l.width > 1024 * 16 * dgor::kStripUnits ||
+                    mb * (l.width / 16) > dgor::kSmallWaves * dgor::kSmallBlocks || mb * (mb + 1) / 2 > 3 * dgor::kSmallWaves ||
+                    l.gram < l.x[0] + groups * 4 * l.mp * l.width || l.poly < l.gram + part || l.bytes < l.poly + part)
+                    printf(" BAD");
+                printf("\n");
+                continue;
+            }
             const char *names[] = {"gram", "polynomial", "update"};
             for (int i = 0; i < 3; ++i) {
                 const dgor::Way &w = l.way[i];

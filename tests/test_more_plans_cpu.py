@@ -64,7 +64,7 @@ def test_the_gpu_tests_reach_every_8_bit_kernel(plans):
 def test_the_gpu_tests_reach_every_way_of_the_update(plans):
     lines = [f"orthogonalize {batch} {M} {N}" for M, N, _ in ortho.EXACT for batch in (1, 3)]
     text = "\n".join(plans(lines))
-    assert " small" in text
+    assert " small" in text and " strips" in text
     for side in (64, 128, 256):
         for product in ("gram", "polynomial", "update"):
             assert f"{product} tile={side} " in text, (product, side)
