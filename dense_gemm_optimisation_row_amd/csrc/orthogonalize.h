@@ -156,14 +156,20 @@ struct Layout {
 constexpr int kSmallWaves = 16, kSmallBytes = 159 * 1024;
 constexpr int kSmallUnits = 6;     // units of eight of G a thread loads
 constexpr int kSmallBlocks = 10;   // 16 x 16 blocks of X a wavefront computes
-// A step of the small kernel takes about 2 us and 0.26 for each of these, of the
-// others 15 us and more: 64 x 64 28 us against 77, 16 x 1000 48 and 75, 96 x 300 (63
-// stages) 97 and 95.
-constexpr int kSmallStages = 44;
-// The strips of a matrix of few rows: at most so many, whose parts of A every
-// workgroup reads, and so many elements, which every workgroup reads for the norm.
-constexpr int kMostStrips = 8, kStripsElements = 1 << 17;
-constexpr int kStripUnits = 8;   // 16-byte units of a strip a thread holds
+// Strips of a matrix of few rows: so many at most, whose parts of A every workgroup
+// reads, and a strip's 16-byte units a thread holds.
+constexpr int kMostStrips = 8, kStripUnits = 8;
+// Which of the two, or the three products a step, by five steps in FP32, measured in
+// us as all steps in one launch / strips / products.  Up to kSmallStages of a
+// wavefront's 32-deep block products a step, one launch: 64 x 64 (6) 29 / 33 / 77,
+// 64 x 128 (10) 35 / 35.  Past it strips, 64 x 256 (18) 50 / 36, 32 x 1024 (41)
+// 71 / 35, 128 x 128 68 with strips and 91 without, 16 x 3000 41 and 174, where they
+// are one workgroup a compute unit; else again one launch where a matrix fits it: 64
+// of 64 x 512 83 / 109, 600 of 96 x 200 226 / 525 / 545.  What does not: strips up to
+// two workgroups a compute unit (64 of 64 x 800 129 and 167, 64 of 128 x 256 109 and
+// 129; 200 of each 341 and 295, 354 and 269), any number of up to 32 rows, of
+// which the products' tiles would be half empty (600 of 16 x 3000 840 and 1502).
+constexpr int kSmallStages = 16;
 inline long long small_stages(int m, int n)
 {
     const int mb = ceil_div(m, 16), nb = ceil_div(n, 16), mt = ceil_div(m, 32), nt = ceil_div(n, 32);
@@ -201,14 +207,21 @@ inline int lay_out(const gemm_orthogonalize_params *q, Layout &l)
     const bool tall = q->M > q->N;
     l.m = tall ? q->N : q->M, l.n = tall ? q->M : q->N;
     l.turned_in = tall != (q->op_g == GEMM_OP_T), l.turned_out = tall != (q->op_o == GEMM_OP_T);
-    // LDS holds X and A, 16 x 16 blocks and G's units are no more than the registers
-    // take, and a wavefront's 32-deep block products a step at most kSmallStages
+    // Strips: LDS holds one and A, the registers its units and its 16 x 16 blocks.
     const long long mp = (l.m + 31LL) / 32 * 32, np = (l.n + 31LL) / 32 * 32;
+    const int mb = ceil_div(l.m, 16);
+    l.mp = (int)mp;
+    l.width = (int)std::fmax(64.0, (l.n + 32LL * kMostStrips - 1) / (32LL * kMostStrips) * 32LL);
+    const long long groups = (long long)q->batch * ceil_div(l.n, l.width);
+    const bool strips = mp <= 128 && 4 * mp * (mp + l.width) <= kSmallBytes &&
+                        4 * mp * l.width <= 16 * 64 * kSmallWaves * kStripUnits &&
+                        (long long)mb * (l.width / 16) <= kSmallWaves * kSmallBlocks && groups < kMostGroups / 4;
+    // One launch: LDS holds X and A, the registers 16 x 16 blocks and G's units.
     const int cols = l.turned_in ? l.m : l.n, rows = l.turned_in ? l.n : l.m;
     l.small = mp <= 128 && 4 * mp * (mp + np) <= kSmallBytes &&
-              ceil_div(l.m, 16) * ceil_div(l.n, 16) <= kSmallWaves * kSmallBlocks &&
-              (long long)rows * ceil_div(cols, 8) <= 64 * kSmallWaves * kSmallUnits &&
-              q->batch < kMostGroups / 4 && small_stages(l.m, l.n) <= kSmallStages;
+              mb * ceil_div(l.n, 16) <= kSmallWaves * kSmallBlocks &&
+              (long long)rows * ceil_div(cols, 8) <= 64 * kSmallWaves * kSmallUnits && q->batch < kMostGroups / 4 &&
+              (!strips || small_stages(l.m, l.n) <= kSmallStages || groups > kUnits);
     if (l.small)
         return GEMM_OK;
     const auto take = [&](size_t bytes) {
@@ -216,19 +229,13 @@ inline int lay_out(const gemm_orthogonalize_params *q, Layout &l)
         l.bytes += round_up(bytes, kWsAlign);
         return at;
     };
-    l.mp = (int)mp;
-    l.width = (int)std::fmax(64.0, (l.n + 32LL * kMostStrips - 1) / (32LL * kMostStrips) * 32LL);
-    l.strips = ceil_div(l.n, l.width);
-    const int mb = ceil_div(l.m, 16);
-    if (mp <= 128 && (long long)l.m * l.n <= kStripsElements && 4 * mp * (mp + l.width) <= kSmallBytes &&
-        4 * mp * l.width <= 16 * 64 * kSmallWaves * kStripUnits && mb * (l.width / 16) <= kSmallWaves * kSmallBlocks && (long long)q->batch * l.strips < kMostGroups / 4) {
-        const size_t groups = (size_t)q->batch * l.strips;
-        l.x[0] = take(groups * 4 * l.mp * l.width);
-        l.gram = take(groups * mb * (mb + 1) / 2 * 1024);
-        l.poly = q->steps > 1 ? take(groups * mb * (mb + 1) / 2 * 1024) : l.gram;
+    if (strips && (groups <= 2 * kUnits || mp == 32)) {
+        l.strips = ceil_div(l.n, l.width);
+        l.x[0] = take((size_t)groups * 4 * l.mp * l.width);
+        l.gram = take((size_t)groups * mb * (mb + 1) / 2 * 1024);
+        l.poly = q->steps > 1 ? take((size_t)groups * mb * (mb + 1) / 2 * 1024) : l.gram;
         return GEMM_OK;
     }
-    l.strips = 0;
     l.ldx = pair_stride(l.n), l.lda = pair_stride(l.m);
     for (int i = 0; i < 3; ++i)
         if (!choose((Which)i, l.m, l.n, q->batch, l.way[i]))

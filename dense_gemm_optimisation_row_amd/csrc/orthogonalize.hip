@@ -902,7 +902,9 @@ __global__ __launch_bounds__(256) void newton_schulz_join_kernel(Operands p, Wor
 // A matrix that fits LDS in two terms next to its A: all steps in one launch, a
 // workgroup of 16 wavefronts a matrix.  Bound by the latency of a product's chain,
 // LDS to MFMA to LDS and a barrier, where the launches of the kernels above, three a
-// step, take 5 us each (64 x 64: 76 us).
+// step, take 5 us each (five steps of 64 x 64: 29 us, and 76).  A lane's results are
+// four neighbours of the transpose, so A and P, symmetric, are written four at a time
+// and X with its columns as the first operand.
 //
 // X is planes of 32 columns, A and P after it likewise: row r of a plane 128 bytes,
 // higher terms and then lower ones, unit c at 8 r + (c ^ ((r >> 1) & 7)).  Rows and
@@ -1187,15 +1189,18 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
 
 // ----------------------------------------------------- matrices of few rows --
 //
-// Up to 128 rows and in too many columns for one workgroup's LDS: X stays in strips
+// Up to 128 rows, in more columns than one workgroup is best for: X stays in strips
 // of columns, a workgroup each, and a step is one launch.  It adds the strips' parts
 // of A = X X^T, computes P (each strip's workgroup all of it), its strip of P X, and
 // that strip's part of the next A.  Planes are as above; a strip lies in the
 // workspace as LDS holds it, a part of A as the lanes hold the blocks on and below
-// the diagonal.  Bound by latency as well: 10 us a step, where three launches
-// take 18 (8 of 128 x 256).
+// the diagonal.  T is m's 32-row blocks: with it in the code the sums' reads have
+// constant offsets and are all in flight at once (a step 13 us, 15.5 without).
+// Bound by latency as well: of 13 us a step (8 of 128 x 256; three launches took 18)
+// 3 go into the parts of A, 2 into placing A, 2.4 each into the two products, 1.4 and
+// 1 into placing P and X, 1.5 into what is left for the next step.
 struct Strips {
-    int m, n, width, strips;   // width: a strip's columns, a multiple of 32
+    int m, n, width, strips;       // width: a strip's columns, a multiple of 32
     bool turned;                   // in: X is G's transpose; out: the result's
     uint8_t *images;               // X's strips
     float *parts;                  // of the next A

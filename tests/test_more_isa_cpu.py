@@ -10,7 +10,7 @@ from test_linear_isa_cpu import _instances
 KERNELS = {"i8_ring_kernel": ("i8_kernels.hip", 8, True), "i8_rows_kernel": ("i8_kernels.hip", 8, False),
            "newton_schulz_kernel": ("orthogonalize.hip", 12, True),
            "newton_schulz_small_kernel": ("orthogonalize.hip", 1, False),
-           "strips_start_kernel": ("orthogonalize.hip", 1, False), "strips_step_kernel": ("orthogonalize.hip", 2, False),
+           "strips_start_kernel": ("orthogonalize.hip", 4, False), "strips_step_kernel": ("orthogonalize.hip", 8, False),
            "quantize_kernel": ("quantize.hip", 36, False)}
 
 
@@ -23,7 +23,7 @@ def kernel(request, tmp_path_factory):
 def test_every_variant_is_generated(kernel):
     # four tiles, one matrix and two; one to four blocks of rows, one matrix and two;
     # three products on three tiles, and on the smallest with and without sums apart;
-    # a step of strips, and the last
+    # a step of strips and the last, of one to four blocks of 32 rows
     assert len(kernel[1]) == kernel[2]
 
 

@@ -65,6 +65,8 @@ def test_the_gpu_tests_reach_every_way_of_the_update(plans):
     lines = [f"orthogonalize {batch} {M} {N}" for M, N, _ in ortho.EXACT for batch in (1, 3)]
     text = "\n".join(plans(lines))
     assert " small" in text and " strips" in text
+    many = plans([f"orthogonalize {batch} {M} {N}" for batch, M, N in ortho.MANY])
+    assert [p.split()[0] for p in many] == ["small", "strips", "strips", "gram", "strips"]
     for side in (64, 128, 256):
         for product in ("gram", "polynomial", "update"):
             assert f"{product} tile={side} " in text, (product, side)

@@ -150,6 +150,42 @@ def test_steps(size, kind, dtype):
     near(dg.orthogonalize(g, steps=3, coefficients=each, eps=1e-3), g, each, "a triple for each step", eps=1e-3)
 
 
+# more than one, and than two, workgroups a compute unit where a matrix is strips
+MANY = [(100, 64, 200), (120, 100, 250), (80, 20, 1500), (75, 500, 128), (40, 2500, 90)]
+
+
+@pytest.mark.parametrize("size", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_many_matrices(size):
+    batch, M, N = size
+    say("orthogonalize", size)
+    x = signs(M, N, 4, M + N, batch)
+    got = dg.orthogonalize(x, steps=1, coefficients=(2.0, -1.0, 3.0), eps=0.0)
+    assert torch.equal(got, exact(x, [(2.0, -1.0, 3.0)], 0.0, 1.0).to(got.dtype))
+    g = torch.stack([matrix(M, N, i, torch.float32, "spread") for i in range(batch)])
+    got = dg.orthogonalize(g)
+    for i in (0, batch // 2, batch - 1):
+        near(got[i], g[i], [COEFFICIENTS] * 5, f"{i}")
+
+
+@pytest.mark.parametrize("size", [(20, 8000), (4090, 64), (96, 2560), (128, 1280), (1, 5000), (100, 1000), (33, 65)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_steps_of_few_rows(size):
+    M, N = size
+    say("orthogonalize", size)
+    for dtype in DTYPES.values():
+        g = matrix(M, N, M + N, dtype, "spread")
+        near(dg.orthogonalize(g), g, [COEFFICIENTS] * 5, "five steps")
+        wide = torch.zeros(M + 2, N + 9, device="cuda", dtype=dtype)   # off 16 bytes, rows with gaps
+        wide[1:-1, 3:N + 3] = g
+        assert torch.equal(dg.orthogonalize(wide[1:-1, 3:N + 3]), dg.orthogonalize(g))
+        again = g.clone()
+        assert torch.equal(dg.orthogonalize(again, out=again), dg.orthogonalize(g))
+        out = torch.full((N + 2, M + 1), 7.0, device="cuda", dtype=dtype)
+        dg.orthogonalize(g, out=out[1:-1, :-1].mT)
+        assert torch.equal(out[1:-1, :-1].mT, dg.orthogonalize(g))
+        assert bool((out[0] == 7).all()) and bool((out[-1] == 7).all()) and bool((out[:, -1] == 7).all())
+
+
 def test_stacks_and_strides():
     g = gen(4)
     flat = torch.randn(2, 3, 70, 100, generator=g, device="cuda")
