@@ -490,7 +490,7 @@ __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t
 // the two quadrants that follow, and have the two after that to land.
 //
 // Why this tile: LDS serves 128 bytes a cycle, of which a stage moves 192 KB here in
-// its 3072 cycles of MFMAs, and 96 KB on 128 x 128 in 768, which is then bound by it.
+// its 3 x 1024 cycles of MFMAs, and 96 KB on 128 x 128 in 768, which is then bound by it.
 template <bool TB>
 __device__ __forceinline__ void quad_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
                                          int steps, floatx4 (&acc)[8][8])
