@@ -227,6 +227,12 @@ def test_unusual_values():
     for by, eps in ((3e38, 1e-7), (1e-30, 0.0), (1e-30, 1e-31)):
         g = base * by
         near(dg.orthogonalize(g, eps=eps), g, [COEFFICIENTS] * 5, f"{by}", eps=eps)
+    for shape in ((2, 128, 256), (30, 3000)):   # in strips
+        assert bool((dg.orthogonalize(torch.zeros(shape, device="cuda")) == 0).all())
+        g = torch.randn(2, *shape[-2:], generator=gen(5), device="cuda")
+        g[0, 3, -1] = float("nan")
+        out = dg.orthogonalize(g)
+        assert bool(torch.isnan(out[0]).all()) and torch.equal(out[1], dg.orthogonalize(g[1]))
     one = torch.zeros(30, 20, device="cuda")
     one[7, 3] = -5.0                       # a single entry
     near(dg.orthogonalize(one), one, [COEFFICIENTS] * 5, "one entry")
@@ -255,6 +261,35 @@ def test_graphs_and_streams_share_nothing():
     got = dg.orthogonalize(xs[0], stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want[0])
+
+
+def test_graphs_and_streams_of_few_rows():
+    """All steps in one launch and a step in one, captured, replayed in turn and on two streams at once."""
+    sizes = [(64, 64), (2, 128, 256), (24, 3000), (100, 90)]
+    xs = [torch.randn(s, generator=gen(i), device="cuda") for i, s in enumerate(sizes)]
+    for x in xs:
+        dg.orthogonalize(x)
+    graphs, outs = [], []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(dg.orthogonalize(x))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(4):
+        for i, x in enumerate(xs):
+            x.copy_(torch.randn(x.shape, generator=gen(10 * turn + i), device="cuda"))
+        want = [dg.orthogonalize(x.clone()) for x in xs]
+        for graph in graphs:
+            graph.replay()
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = [dg.orthogonalize(x, stream=streams[i % 2]) for _ in range(3) for i, x in enumerate(xs)]
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), turn
+        assert all(torch.equal(a, b) for a, b in zip(got, 3 * want)), turn
 
 
 def test_a_training_step_and_its_served_weights():
