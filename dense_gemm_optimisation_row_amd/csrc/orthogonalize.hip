@@ -779,10 +779,12 @@ __global__ __launch_bounds__(256 * GROUPS) void newton_schulz_kernel(Operands p,
                             v[q][e] = sum(r * ROW + c + e);
                         }
                         f.value(row0 + r, col, v[q], a);
+                        // (rows past the matrix become P's padding, which has to be zeros:
+                        // theirs here is b A of its last row, which P's bound does not hold)
                         if (mirrored)
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                w[r * ROW + c + e] = v[q][e];
+                                w[r * ROW + c + e] = row0 + r < p.M ? v[q][e] : 0.f;
                     }
                     if (GROUPS == 1 && 32 * round + b + BATCH * STEP < HALF)
                         load_with(32 * round + b + BATCH * STEP);
