@@ -123,6 +123,13 @@ __device__ __forceinline__ double block_sum(double v, double *lds)
     return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+// What G is multiplied by, `by` / (|G| + eps), from its sum of squares, which is zero
+// for zeros alone: these stay zeros, whatever eps.
+__device__ __forceinline__ double factor_of(double by, double squares, double eps)
+{
+    return squares == 0 ? 0 : by / (sqrt(squares) + eps);
+}
+
 // Sums of squares of each of `blocks` parts of each matrix, in FP64, which
 // holds the square of any FP32.  Threads: 256 >> lg rows of 1 << lg units.
 __global__ __launch_bounds__(256) void squares_kernel(Source g, int blocks, int lg, double *sums)
@@ -157,7 +164,7 @@ __global__ __launch_bounds__(256) void start_kernel(Source g, Pair x, const doub
     for (int i = threadIdx.x; i < blocks; i += 256)
         v += sums[m * blocks + i];
     v = block_sum(v, lds);
-    const double factor = by / (sqrt(v) + eps);
+    const double factor = factor_of(by, v, eps);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int r = (int)(threadIdx.x >> 3) + 32 * t, c = 8 * (int)(threadIdx.x & 7);
@@ -1098,7 +1105,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void newton_schulz_small_kernel(S
 #pragma unroll
     for (int i = 1; i < kSmallWaves; ++i)
         v += sums[i];
-    const double factor = p.by / (sqrt(v) + p.eps);
+    const double factor = factor_of(p.by, v, p.eps);
 #pragma unroll
     for (int t = 0; t < kSmallUnits; ++t) {
         const int id = (int)threadIdx.x + 64 * kSmallWaves * t;
@@ -1286,7 +1293,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void strips_start_kernel(Strips p
 #pragma unroll
     for (int i = 1; i < kSmallWaves; ++i)
         v += sums[i];
-    const double factor = by / (sqrt(v) + eps);
+    const double factor = factor_of(by, v, eps);
     // the strip's rows and units of G: `first` of them left out
     const int r0 = p.turned ? first : 0, c0 = p.turned ? 0 : first;
     const int rows = p.turned ? min(p.width, g.rows - r0) : g.rows, cols = p.turned ? g.cols : min(p.width, g.cols - c0);
