@@ -903,7 +903,7 @@ const char *gemm_status_string(int status)
     case GEMM_ERR_INVALID_LAYOUT: return "invalid operand layout (op flag or leading dimension)";
     case GEMM_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case GEMM_ERR_INVALID_ACTIVATION: return "unknown activation";
-    case GEMM_ERR_INVALID_COEFFICIENTS: return "coefficients that are not finite, or whose steps grow too far";
+    case GEMM_ERR_INVALID_COEFFICIENTS: return "coefficients that are not finite or whose steps leave the range, or such a scale";
     case GEMM_ERR_SCRATCH_LIMIT: return "needs more scratch than the no-allocation entry point's fixed array (16 MiB)";
     default: return "unknown status";
     }

@@ -127,12 +127,18 @@ inline double multiplied(double a, double b, double c, double r)
         most = std::fmax(most, f(-b / (2 * c)));
     return most;
 }
+// What a step's bounds may be: below kLeast an operand would want a power of two whose
+// products, undone, leave FP32.
+constexpr double kLeast = 0x1p-35, kMost = 256;
+inline bool in_range(double bound) { return bound == 0 || (bound >= kLeast && bound <= kMost); }
 // The power of two at which values of at most `most` stay binary16: the rounding
 // of the sums is far below what 60000 leaves to 65504.
 inline int exponent_for(double most)
 {
+    if (most == 0)
+        return 0;
     int e = 0;
-    std::frexp(60000.0 / std::fmax(most, 1.0), &e);   // 60000 / most in [2^(e - 1), 2^e)
+    std::frexp(60000.0 / most, &e);   // 60000 / most in [2^(e - 1), 2^e)
     return e - 1;
 }
 
@@ -149,6 +155,7 @@ struct Layout {
     int blocks, lg;          // of the sums of squares
     Way way[3];
     Step step[GEMM_MAX_STEPS];
+    double last;             // `scale`, and the last step's powers of two undone
     size_t sums, x[2], gram, poly, part, bytes;   // offsets, and the whole size
 };
 
@@ -197,11 +204,16 @@ inline int lay_out(const gemm_orthogonalize_params *q, Layout &l)
         if (!std::isfinite(s.a) || !std::isfinite(s.b) || !std::isfinite(s.c))
             return GEMM_ERR_INVALID_COEFFICIENTS;
         const double p = multiplied(s.a, s.b, s.c, r), next = grown(s.a, s.b, s.c, r);
-        if (!(p <= 256) || !(next <= 256))
+        if (!in_range(p) || !in_range(next))
             return GEMM_ERR_INVALID_COEFFICIENTS;
         s.x = exponent_for(r), s.gram = exponent_for(r * r), s.poly = exponent_for(p);
         r = next;
     }
+    // what the last sums are multiplied by, a normal FP32 number
+    const Step &end = l.step[q->steps - 1];
+    l.last = std::ldexp(q->scale, -end.poly - end.x);
+    if (std::isfinite(q->scale) && q->scale != 0 && !(std::fabs(l.last) >= 0x1p-126 && std::fabs(l.last) < 0x1p127))
+        return GEMM_ERR_INVALID_COEFFICIENTS;
     if (q->batch == 0 || q->M == 0 || q->N == 0)
         return GEMM_OK;
     const bool tall = q->M > q->N;

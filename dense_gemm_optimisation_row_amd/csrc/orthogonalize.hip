@@ -13,7 +13,7 @@
 // bits at a third of the 16-bit rate, five times the FP32 one.  Terms are held at a
 // power of two: the coefficients bound the singular values of each step on the
 // host, so X, A and P have scales at which no entry overflows, and entries down to
-// 2^-18 of the bound keep all bits, smaller ones an error of 2^-40 of it.  The Gram
+// 2^-16 of the bound keep all bits, smaller ones are off by at most 2^-39 of it.  The Gram
 // matrix alone would do for long rows (P's products applied to X once), but its
 // rounding, 2^-24 of the largest eigenvalue, is a singular value of 2^-12.
 //
@@ -1515,7 +1515,7 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
     const auto gram_of = [&](int i) { return (float)std::ldexp(1.0, l.step[i].gram - 2 * l.step[i].x); };
     const auto next_of = [&](int i) {
         const int from = l.step[i].poly + l.step[i].x;
-        return i + 1 < q->steps ? (float)std::ldexp(1.0, l.step[i + 1].x - from) : (float)std::ldexp(q->scale, -from);
+        return (float)(i + 1 < q->steps ? std::ldexp(1.0, l.step[i + 1].x - from) : l.last);
     };
     const auto polynomial_of = [&](int i, auto &f) {
         const Step &k = l.step[i];

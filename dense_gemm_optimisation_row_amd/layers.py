@@ -872,7 +872,8 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     root of its sum of squares, ``steps`` Newton-Schulz steps
     X = a X + (b A + c A A) X, A = X X^T, then ``scale`` X, in g's type and
     storage.  ``coefficients`` are a, b, c, or such a triple for each step; they must not let
-    a singular value of at most 1, nor what multiplies it, grow past 256.
+    a singular value of at most 1, nor what multiplies it, grow past 256, nor hold all
+    of them below 2^-35.
     Products are computed from two float16 terms of each operand, to 2^-23 of
     its values.  g may be a transposed view (a weight gradient of
     ``linear_backward``); ``out`` may be g itself."""

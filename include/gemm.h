@@ -584,15 +584,19 @@ int gemm_gated_i8_bf16(const gemm_gated_i8_params *params, const int8_t *X, cons
  *   where M > N), with the step's own a, b, c,
  *   O = scale X.
  * The operands of the products are held as two binary16 terms each at a power of
- * two that the coefficients give, to 2^-23 of a value and 2^-39 of the largest;
- * a step's sums, A and c A A + b A are computed in FP32, |G| in FP64.
+ * two that the coefficients give, to 2^-23 of a value and 2^-39 of the bound that
+ * the steps have for it (1 for the first X, then the largest that a singular value of
+ * at most 1 becomes); a step's sums, A and c A A + b A are computed in FP32, |G| in
+ * FP64.
  * G and O are stored M x N (op GEMM_OP_N) or N x M (GEMM_OP_T), stride_g and
  * stride_o elements from a matrix to the next (read only where batch > 1).  O may
  * be G itself (same pointer, op and strides).  A matrix of zeros gives zeros; one
  * with a NaN or an infinity NaN.  steps outside [1, GEMM_MAX_STEPS] or eps
  * negative or NaN -> GEMM_ERR_INVALID_DIM; coefficients that are not finite, or
  * whose steps let a singular value of at most 1, or what multiplies it, grow past
- * 256 -> GEMM_ERR_INVALID_COEFFICIENTS. */
+ * 256 or hold all of them below 2^-35 (but for 0), and a scale so small or large
+ * that a sum's multiplier leaves FP32's normal numbers (never within 2^-26 .. 2^100)
+ * -> GEMM_ERR_INVALID_COEFFICIENTS. */
 #define GEMM_MAX_STEPS 32
 typedef struct {
     int batch, M, N;
