@@ -107,14 +107,13 @@ inline double grown(double a, double b, double c, double r)
         if (t > 0 && t < r * r)
             most = std::fmax(most, f(std::sqrt(t)));
     };
-    if (c != 0) {
-        const double d = 9 * b * b - 20 * a * c;
-        if (d >= 0) {
-            at((-3 * b + std::sqrt(d)) / (10 * c));
-            at((-3 * b - std::sqrt(d)) / (10 * c));
-        }
-    } else if (b != 0) {
-        at(-a / (3 * b));
+    // (the sum that does not cancel gives one zero and the product of both, a / 5 c, the
+    // other: a c that is next to nothing leaves the cubic's)
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0) {
+        const double q = -(3 * b + std::copysign(std::sqrt(d), b)) / 2;
+        at(q / (5 * c));   // not a number or infinite where there is none
+        at(a / q);
     }
     return most;
 }

@@ -40,3 +40,19 @@ def test_a_step_on_small_values(size):
     got = dg.orthogonalize(g, steps=2, coefficients=each, scale=1e6).double()
     ref = exact(g, each, scale=1e6)
     assert bool((got - ref).norm() <= 1000 * 2.0 ** -24 * ref.norm()), float((got - ref).norm() / ref.norm())
+
+
+@pytest.mark.parametrize("c", [1e-17, -1e-17, 0.0])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_a_cubic_whose_largest_value_is_inside(size, c):
+    """24 s - 27 s^3 is 8.7 at 0.54 and 3 at 1: two equal singular values of 0.7, and of
+    0.54 from an entry of 2^-1.3 of the norm, neither lost nor past the range."""
+    say("orthogonalize cubic", size, c)
+    for first, second in ((1.0, 1.0), (0.65, 1.0)):
+        g = torch.zeros(size, device="cuda")
+        g[0, 1], g[-1, 0] = first, second
+        got = dg.orthogonalize(g, steps=1, coefficients=(24.0, -27.0, c), eps=0.0).double()
+        ref = exact(g, [(24.0, -27.0, c)], 0.0)
+        # one product a sum: A is off by 18 x 2^-24 of itself, P by 27 times that and 6 x 2^-24 of
+        # its terms, P X by 15 x 2^-24 of itself and s times P's error: together below 570 x 2^-24
+        assert bool(((got - ref).abs() <= 600 * 2.0 ** -24).all())

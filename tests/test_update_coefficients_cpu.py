@@ -95,6 +95,17 @@ def test_drawn_coefficients_stay_within_binary16_and_use_its_range(plan):
         held(found, each)
 
 
+def test_polynomials_of_nearly_lower_degree(plan):
+    """A leading coefficient that is left over from rounding, as fits give it: the largest
+    value is inside [0, 1], where the cubic or the line has it."""
+    calls = []
+    for c in (1e-16, -1e-16, 1e-17, -1e-17, 1e-20, -1e-30, 1e-300, 0.0, -0.0):
+        calls += [[(24.0, -27.0, c)], [(3.0, -4.0, c)], [(24.0, -27.0, c), (1.5, -0.02, 0.0)], [(-6.0, 7.0, c)]]
+        calls += [[(2.0, c, -3.0)], [(2.0, c, 3.0)], [(c, -4.0, 5.0)], [(2.0, c, c)], [(c, c, 1.0)], [(c, 2.0, c)]]
+    for found, each in zip(plan([(each, 1.0) for each in calls]), calls):
+        held(found, each)
+
+
 def test_coefficients_that_leave_the_range(plan):
     ok = [[(0, 0, 0)], [(0, 0, 0), (1.5, -0.5, 0)], [(2.0 ** -35, 0, 0)], [(1e-6, 0, 0), (1e-4, 0, 0)], [(256.0, 0, 0)]]
     bad = [[(1e-11, 0, 0)], [(1e-13, 0, 0), (1.5, -0.5, 0)], [(1e-6, 0, 0), (1e-5, 0, 0)], [(1e-300, 0, 0)],
