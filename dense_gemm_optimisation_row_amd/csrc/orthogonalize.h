@@ -184,6 +184,27 @@ inline long long small_stages(int m, int n)
 
 inline bool ld_ok(int ld, int row) { return ld >= (row > 1 ? row : 1); }
 
+// Whether two of a stack's results share an element.  Matrices may lie between each
+// other's rows: one that begins d further has a row that begins d % ld into one of the
+// first's, as long as d is inside it.
+inline bool results_overlap(const gemm_orthogonalize_params &q)
+{
+    const long long rows = q.op_o ? q.N : q.M, cols = q.op_o ? q.M : q.N, ld = q.ldo;
+    if (q.batch <= 1 || rows == 0 || cols == 0)
+        return false;
+    if (q.stride_o < -(1LL << 62) || q.stride_o > (1LL << 62))
+        return true;   // past every address: the sums below would overflow
+    const long long by = q.stride_o < 0 ? -q.stride_o : q.stride_o;
+    if (by >= cols && by <= ld && (q.batch - 1) * by + cols <= ld)   // all in one row's stride
+        return false;
+    for (long long i = 1, d = by; i < q.batch && d < (rows - 1) * ld + cols; ++i, d += by) {
+        const long long row = d / ld, in = d - row * ld;
+        if (in < cols || (row + 1 < rows && ld - in < cols))
+            return true;
+    }
+    return false;
+}
+
 inline int lay_out(const gemm_orthogonalize_params *q, Layout &l)
 {
     if (!q)

@@ -1495,6 +1495,8 @@ int run(int fmt, const gemm_orthogonalize_params *q, const void *G, void *O, voi
     const int rc = lay_out(q, l);
     if (rc != GEMM_OK)
         return rc;
+    if (results_overlap(*q))
+        return GEMM_ERR_INVALID_LAYOUT;
     if (q->batch == 0 || q->M == 0 || q->N == 0)
         return GEMM_OK;
     if (!G || !O)

@@ -31,8 +31,8 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import (ACTIVATIONS, GEMM_OK, GEMM_NO_INPUT_GRADIENT, GEMM_NO_WEIGHT_GRADIENT, GEMM_ONLY_BF16,
-                      GEMM_ONLY_F16, GEMM_OP_N, GEMM_OP_T, GEMM_MAX_STEPS, GEMM_ROUND_GRADIENT, GatedBackwardParams,
+from .binding import (ACTIVATIONS, GEMM_ERR_INVALID_LAYOUT, GEMM_OK, GEMM_NO_INPUT_GRADIENT, GEMM_NO_WEIGHT_GRADIENT,
+                      GEMM_ONLY_BF16, GEMM_ONLY_F16, GEMM_OP_N, GEMM_OP_T, GEMM_MAX_STEPS, GEMM_ROUND_GRADIENT, GatedBackwardParams,
                       GatedI8Params, GatedParams, GemmError, LayerNormParams, LinearBackwardParams, LinearI8Params,
                       LinearParams, OrthogonalizeParams, QuantizeParams)
 
@@ -876,7 +876,8 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     of them below 2^-35.
     Products are computed from two float16 terms of each operand, to 2^-23 of
     its values.  g may be a transposed view (a weight gradient of
-    ``linear_backward``); ``out`` may be g itself."""
+    ``linear_backward``) and a stack's matrices may lie between each other's rows
+    (``w.view(d, heads, -1).transpose(0, 1)``); ``out`` likewise, and it may be g itself."""
     if g.requires_grad:
         _grad_unless_off()
     values = _step_coefficients(coefficients, steps)
@@ -890,7 +891,10 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
             if form.extra:
                 o = o.mT
         ws = _workspace(form, workspace, g)
-        _done(form.entry(form.ref, g.data_ptr(), o.data_ptr(), _ptr(ws), _size(ws), handle), form)
+        rc = form.entry(form.ref, g.data_ptr(), o.data_ptr(), _ptr(ws), _size(ws), handle)
+        if rc == GEMM_ERR_INVALID_LAYOUT:   # the rest of the layout has been checked
+            raise ValueError(f"out's matrices overlap (strides {o.stride()})")
+        _done(rc, form)
         return o
     return _run(form, stream, (g, out, workspace), go)
 
@@ -910,9 +914,6 @@ def _orthogonalize_form(g, steps, values, eps, scale, out):
         if out.shape != g.shape or out.dtype != g.dtype or out.device != g.device:
             raise ValueError("out must match g")
         _, op_o, ldo, stride_o = _matrices(out, "out")
-        extent = (N - 1) * ldo + M if op_o == GEMM_OP_T else (M - 1) * ldo + N
-        if batch > 1 and M and N and stride_o < extent:
-            raise ValueError(f"out's matrices overlap (strides {out.stride()})")
     params = OrthogonalizeParams(batch, M, N, op_g, op_o, ldg, ldo, steps, stride_g, stride_o, eps, scale)
     params.coefficients[:len(values)] = values
     turned = op_g == GEMM_OP_T

@@ -589,8 +589,10 @@ int gemm_gated_i8_bf16(const gemm_gated_i8_params *params, const int8_t *X, cons
  * at most 1 becomes); a step's sums, A and c A A + b A are computed in FP32, |G| in
  * FP64.
  * G and O are stored M x N (op GEMM_OP_N) or N x M (GEMM_OP_T), stride_g and
- * stride_o elements from a matrix to the next (read only where batch > 1).  O may
- * be G itself (same pointer, op and strides).  A matrix of zeros gives zeros; one
+ * stride_o elements from a matrix to the next (read only where batch > 1).  Matrices
+ * of a stack may lie between each other's rows (the heads of one weight); those of O
+ * that share an element -> GEMM_ERR_INVALID_LAYOUT.  O may be G itself (same
+ * pointer, op and strides).  A matrix of zeros gives zeros; one
  * with a NaN or an infinity NaN.  steps outside [1, GEMM_MAX_STEPS] or eps
  * negative or NaN -> GEMM_ERR_INVALID_DIM; coefficients that are not finite, or
  * whose steps let a singular value of at most 1, or what multiplies it, grow past
