@@ -881,7 +881,8 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     if g.requires_grad:
         _grad_unless_off()
     values = _step_coefficients(coefficients, steps)
-    key = ("orthogonalize", g.shape, g.stride(), g.dtype, g.device, steps, values, eps, scale, _sig(out))
+    # (eps and scale, which a schedule changes from call to call, are not of the form)
+    key = ("orthogonalize", g.shape, g.stride(), g.dtype, g.device, steps, values, _sig(out))
     form = _FORMS.get(key) or _keep(key, _orthogonalize_form(g, steps, values, eps, scale, out))
 
     def go(handle):
@@ -891,7 +892,9 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
             if form.extra:
                 o = o.mT
         ws = _workspace(form, workspace, g)
-        rc = form.entry(form.ref, g.data_ptr(), o.data_ptr(), _ptr(ws), _size(ws), handle)
+        params = OrthogonalizeParams.from_buffer_copy(form.params)   # the call's own
+        params.eps, params.scale = eps, scale
+        rc = form.entry(ctypes.byref(params), g.data_ptr(), o.data_ptr(), _ptr(ws), _size(ws), handle)
         if rc == GEMM_ERR_INVALID_LAYOUT:   # the rest of the layout has been checked
             raise ValueError(f"out's matrices overlap (strides {o.stride()})")
         _done(rc, form)
