@@ -857,6 +857,8 @@ def _matrices(t, name):
 
 def _step_coefficients(coefficients, steps):
     """a, b, c of every step, one after another."""
+    if not 1 <= steps <= GEMM_MAX_STEPS:
+        raise ValueError(f"steps must be 1 to {GEMM_MAX_STEPS}, not {steps}")
     triples = list(coefficients)
     if triples and not hasattr(triples[0], "__len__"):
         triples = [tuple(triples)] * steps
@@ -907,8 +909,6 @@ def _orthogonalize_form(g, steps, values, eps, scale, out):
     kind = _kind_of(g.dtype, "g")
     if g.dim() < 2:
         raise ValueError("g must be a matrix or a stack of them")
-    if not 1 <= steps <= GEMM_MAX_STEPS:
-        raise ValueError(f"steps must be 1 to {GEMM_MAX_STEPS}, not {steps}")
     M, N = g.shape[-2:]
     batch, op_g, ldg, stride_g = _matrices(g, "g")
     if out is None:

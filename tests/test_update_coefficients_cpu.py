@@ -11,6 +11,7 @@ import pytest
 
 import linear_plan
 from dense_gemm_optimisation_row_amd import binding as b
+from dense_gemm_optimisation_row_amd import layers
 
 ROOT = linear_plan.ROOT
 pytestmark = pytest.mark.skipif(linear_plan.hipcc() is None, reason="needs hipcc")
@@ -122,3 +123,9 @@ def test_scales_that_leave_fp32(plan):
         assert found[0] == (b.GEMM_OK if any(scale is s for s in ok) else b.GEMM_ERR_INVALID_COEFFICIENTS), scale
     for small in ([(2.0 ** -35, 0, 0)], [(256.0, 0, 0)]):
         assert all(rc == b.GEMM_OK for rc, _ in plan([(small, 2.0 ** -26), (small, 2.0 ** 100)]))
+
+
+def test_steps_out_of_range_are_refused_before_their_coefficients_are_made():
+    for steps in (0, -1, 33, 10 ** 12):   # (10^12 triples are 8 TB)
+        with pytest.raises(ValueError, match="steps must be"):
+            layers._step_coefficients((3.4445, -4.775, 2.0315), steps)
