@@ -1,8 +1,9 @@
 """Build the HIP libraries in-tree, beside this file: ``libdgor_gemm.so`` (the
 product), ``libdgor_calibrate.so`` (the benchmark's matrix-core calibration
 kernel) and ``libdgor_gemm_poison.so`` (the product built with LDS poisoning,
-for the race tests); and ``_marshal.so``, the extension module through which
-short calls of the layers reach the product (host code, against torch).
+for the race tests); and, where torch and the headers are there,
+``_marshal.so``, the extension module through which short calls of the layers reach
+the product (host code, against torch).
 
 Every source in ``csrc/`` is compiled for gfx950 with hipcc (in parallel),
 then linked into one shared library that exports the C ABI of
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -81,8 +83,30 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
-def _marshal() -> None:
-    """Compile the extension module against the installed torch."""
+def _without() -> str | None:
+    """What the extension module's build lacks, if anything."""
+    import sysconfig
+
+    try:
+        from torch.utils.cpp_extension import include_paths
+        include = include_paths()
+    except Exception as e:   # no torch, or one that does not load
+        return f"torch ({e})"
+    if not any(os.path.exists(os.path.join(p, "torch", "csrc", "autograd", "python_variable.h")) for p in include):
+        return "torch's headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None if shutil.which("g++") else "g++"
+
+
+def _marshal() -> str | None:
+    """Compile the extension module against the installed torch; returns what is
+    missing for it (there is no module then, not even an older one)."""
+    missing = _without()
+    if missing is not None:
+        if os.path.exists(MARSHAL_LIB):
+            os.remove(MARSHAL_LIB)
+        return missing
     import sysconfig
 
     import torch
@@ -90,7 +114,7 @@ def _marshal() -> None:
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = MARSHAL_LIB + ".tmp"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{p}" for p in include_paths()), f"-I{sysconfig.get_paths()['include']}",
            os.path.join(CSRC, "marshal.cpp"), "-o", tmp, f"-L{lib}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
@@ -98,24 +122,29 @@ def _marshal() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL_LIB)
+    return None
 
 
 def build(verbose: bool = False) -> str:
-    """Compile all sources, link the GEMM library, the calibration library and
-    the extension module; return the GEMM library's path."""
+    """Compile all sources, link the GEMM library, the calibration library and the
+    poisoned one, which need neither torch nor Python's headers, and, where these are
+    there, the extension module; return the GEMM library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     jobs_list = [(src, False) for src in SOURCES + CAL_SOURCES] + [(src, True) for src in SOURCES]
     jobs = min(len(jobs_list), max(1, min(8, os.cpu_count() or 1)))
     with ThreadPoolExecutor(jobs) as ex:
         marshal = ex.submit(_marshal)
         objs = list(ex.map(lambda j: _compile(*j), jobs_list))
-        marshal.result()
     n = len(SOURCES)
     _link(objs[:n], LIB)
     _link(objs[n:n + len(CAL_SOURCES)], CAL_LIB)
     _link(objs[n + len(CAL_SOURCES):], POISON_LIB)
+    missing = marshal.result()   # (raised only now: the libraries are whole without it)
+    if missing is not None:
+        warnings.warn(f"{os.path.basename(MARSHAL_LIB)} is not built without {missing}: short calls of the layers "
+                      "take the longer way through Python", RuntimeWarning)
     if verbose:
-        print(f"built {LIB}, {CAL_LIB}, {POISON_LIB} and {MARSHAL_LIB}")
+        print(f"built {LIB}, {CAL_LIB}, {POISON_LIB}" + (f" and {MARSHAL_LIB}" if missing is None else ""))
     return LIB
 
 
