@@ -185,6 +185,26 @@ __device__ __forceinline__ void store8_f32(float *p, int n, const float (&f)[8])
             p[e] = f[e];
 }
 
+// The same of an array whose format is known to the call alone: eight elements from
+// element `at`.
+enum Format { kF32, kF16, kBF16 };
+__device__ __forceinline__ void load8_of(int fmt, const void *p, size_t at, int n, float (&f)[8])
+{
+    if (fmt == kF32)
+        load8_f32((const float *)p + at, n, f);
+    else if (fmt == kF16)
+        unpack8<Half16>(load8_16((const uint16_t *)p + at, n), f);
+    else
+        unpack8<Brain16>(load8_16((const uint16_t *)p + at, n), f);
+}
+__device__ __forceinline__ void store8_of(int fmt, void *p, size_t at, int n, const float (&f)[8])
+{
+    if (fmt == kF32)
+        store8_f32((float *)p + at, n, f);
+    else
+        store8_16((uint16_t *)p + at, n, fmt == kF16 ? pack8<Half16>(f) : pack8<Brain16>(f));
+}
+
 // ---- activations, in binary32.  exp is the hardware's base-2 exponential
 // (one unit in the last place; the scaled argument adds |z| 2^-24 relative);
 // the logistic function's quotient the hardware reciprocal.  A large

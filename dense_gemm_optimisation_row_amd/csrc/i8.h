@@ -9,13 +9,12 @@ namespace dgor {
 // What follows a product's INT32 sums: the scales of their row and column, bias,
 // activation (or the gate's product) and residual, in FP32, and the rounding to
 // the output's format.
-enum I8Format { kI8F32, kI8F16, kI8BF16 };
 struct I8Epilogue {
     const float *row, *col, *up;   // scales: M; N; N of the second matrix (gated)
     const float *bias;             // N, or null
     const void *R;                 // residual in the output's format, or null
     void *Y;
-    int ldy, ldr, act, fmt;
+    int ldy, ldr, act, fmt;   // fmt: a Format
 };
 
 // The sum of a product of int8 operands overflows INT32 past this K: a code may

@@ -46,23 +46,6 @@ struct Columns {
     }
 };
 
-__device__ __forceinline__ void load8_as(int fmt, const void *p, size_t at, int n, float (&f)[8])
-{
-    if (fmt == kI8F32)
-        load8_f32((const float *)p + at, n, f);
-    else if (fmt == kI8F16)
-        unpack8<Half16>(load8_16((const uint16_t *)p + at, n), f);
-    else
-        unpack8<Brain16>(load8_16((const uint16_t *)p + at, n), f);
-}
-__device__ __forceinline__ void store8_as(int fmt, void *p, size_t at, int n, const float (&f)[8])
-{
-    if (fmt == kI8F32)
-        store8_f32((float *)p + at, n, f);
-    else
-        store8_16((uint16_t *)p + at, n, fmt == kI8F16 ? pack8<Half16>(f) : pack8<Brain16>(f));
-}
-
 // Eight neighbouring outputs of each of the rows row, row + step, ... below M: v
 // (and u, gated) the INT32 sums' bits.  The residual is read by the lane that
 // writes the same elements of Y, so Y may be the residual itself.
@@ -77,7 +60,7 @@ __device__ __forceinline__ void emit_i8(const I8Epilogue &e, int row, int step, 
         const int at = row + i * step < M ? row + i * step : row;
         s[i] = e.row[at];
         if (!GATED && e.R)
-            load8_as(e.fmt, e.R, (size_t)at * e.ldr + col, n, r[i]);
+            load8_of(e.fmt, e.R, (size_t)at * e.ldr + col, n, r[i]);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -92,7 +75,7 @@ __device__ __forceinline__ void emit_i8(const I8Epilogue &e, int row, int step, 
                 v[i][c] += r[i][c];
         }
         if (row + i * step < M)
-            store8_as(e.fmt, e.Y, (size_t)(row + i * step) * e.ldy + col, n, v[i]);
+            store8_of(e.fmt, e.Y, (size_t)(row + i * step) * e.ldy + col, n, v[i]);
     }
 }
 

@@ -223,19 +223,19 @@ int gemm_linear_i8_f32(const gemm_linear_i8_params *params, const int8_t *X, con
                        const float *w_scale, const float *bias, const float *R, float *Y, void *workspace,
                        size_t workspace_bytes, void *stream)
 {
-    return run_linear(dgor::kI8F32, params, X, x_scale, W, w_scale, bias, R, Y, workspace, workspace_bytes, stream);
+    return run_linear(dgor::kF32, params, X, x_scale, W, w_scale, bias, R, Y, workspace, workspace_bytes, stream);
 }
 int gemm_linear_i8_f16(const gemm_linear_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *W,
                        const float *w_scale, const float *bias, const uint16_t *R, uint16_t *Y, void *workspace,
                        size_t workspace_bytes, void *stream)
 {
-    return run_linear(dgor::kI8F16, params, X, x_scale, W, w_scale, bias, R, Y, workspace, workspace_bytes, stream);
+    return run_linear(dgor::kF16, params, X, x_scale, W, w_scale, bias, R, Y, workspace, workspace_bytes, stream);
 }
 int gemm_linear_i8_bf16(const gemm_linear_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *W,
                         const float *w_scale, const float *bias, const uint16_t *R, uint16_t *Y, void *workspace,
                         size_t workspace_bytes, void *stream)
 {
-    return run_linear(dgor::kI8BF16, params, X, x_scale, W, w_scale, bias, R, Y, workspace, workspace_bytes, stream);
+    return run_linear(dgor::kBF16, params, X, x_scale, W, w_scale, bias, R, Y, workspace, workspace_bytes, stream);
 }
 
 int gemm_gated_i8_workspace(const gemm_gated_i8_params *params, size_t *bytes) { return workspace(params, bytes); }
@@ -243,21 +243,21 @@ int gemm_gated_i8_f32(const gemm_gated_i8_params *params, const int8_t *X, const
                       const float *wg_scale, const int8_t *Wu, const float *wu_scale, float *H, void *workspace,
                       size_t workspace_bytes, void *stream)
 {
-    return run_gated(dgor::kI8F32, params, X, x_scale, Wg, wg_scale, Wu, wu_scale, H, workspace, workspace_bytes,
+    return run_gated(dgor::kF32, params, X, x_scale, Wg, wg_scale, Wu, wu_scale, H, workspace, workspace_bytes,
                      stream);
 }
 int gemm_gated_i8_f16(const gemm_gated_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *Wg,
                       const float *wg_scale, const int8_t *Wu, const float *wu_scale, uint16_t *H, void *workspace,
                       size_t workspace_bytes, void *stream)
 {
-    return run_gated(dgor::kI8F16, params, X, x_scale, Wg, wg_scale, Wu, wu_scale, H, workspace, workspace_bytes,
+    return run_gated(dgor::kF16, params, X, x_scale, Wg, wg_scale, Wu, wu_scale, H, workspace, workspace_bytes,
                      stream);
 }
 int gemm_gated_i8_bf16(const gemm_gated_i8_params *params, const int8_t *X, const float *x_scale, const int8_t *Wg,
                        const float *wg_scale, const int8_t *Wu, const float *wu_scale, uint16_t *H, void *workspace,
                        size_t workspace_bytes, void *stream)
 {
-    return run_gated(dgor::kI8BF16, params, X, x_scale, Wg, wg_scale, Wu, wu_scale, H, workspace, workspace_bytes,
+    return run_gated(dgor::kBF16, params, X, x_scale, Wg, wg_scale, Wu, wu_scale, H, workspace, workspace_bytes,
                      stream);
 }
 

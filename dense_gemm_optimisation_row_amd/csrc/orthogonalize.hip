@@ -33,32 +33,6 @@ using namespace ring;
 
 typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
 
-struct OpHalf : Half16 {
-    static __device__ __forceinline__ floatx4 mfma(halfx8 a, halfx8 b, floatx4 c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-    }
-};
-
-enum Format { kF32, kF16, kBF16 };
-
-__device__ __forceinline__ void load8_of(int fmt, const void *p, size_t at, int n, float (&f)[8])
-{
-    if (fmt == kF32)
-        load8_f32((const float *)p + at, n, f);
-    else if (fmt == kF16)
-        unpack8<Half16>(load8_16((const uint16_t *)p + at, n), f);
-    else
-        unpack8<Brain16>(load8_16((const uint16_t *)p + at, n), f);
-}
-__device__ __forceinline__ void store8_of(int fmt, void *p, size_t at, int n, const float (&f)[8])
-{
-    if (fmt == kF32)
-        store8_f32((float *)p + at, n, f);
-    else
-        store8_16((uint16_t *)p + at, n, fmt == kF16 ? pack8<Half16>(f) : pack8<Brain16>(f));
-}
-
 // Matrices in two terms.  A row is groups of 32 columns, each 64 bytes of higher
 // terms and then 64 of lower ones, so that what a 32-deep stage takes of a row is
 // one whole line of 128 bytes: a compute unit takes about as many pieces a
