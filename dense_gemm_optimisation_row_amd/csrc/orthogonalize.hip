@@ -278,62 +278,56 @@ __device__ __forceinline__ void tile_of(const Work &w, int id, int &tm, int &tn)
 template <int BM, int BN>
 constexpr int stage_bytes() { return (BM + BN) * 32 * 2 * 2; }
 
-// `steps` stages from s0, those from `stop` on zeros, by the four wavefronts of
-// one of the workgroup's groups; `lds` is the group's.  LOW: the cross products
-// have sums of their own, `low`, to which the lower terms' products belong too.  Each
-// MFMA rounds its sum four times, and the higher terms' sum is then rounded by a
-// third as many.
-template <int BM, int BN, int NB, bool TB, bool LOW>
-__device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
-                                         int stop, int steps, floatx4 (&acc)[BM / 32][BN / 32],
-                                         floatx4 (&low)[LOW ? BM / 32 : 1][LOW ? BN / 32 : 1])
-{
-    constexpr int BK = 32, HM = BM / 2, HN = BN / 2, FA = HM / 16, FB = HN / 16, W = HN / 4;
-    constexpr int LPA = BM / 32, LPB = BN / 32, LOADS = LPA + LPB;   // a wavefront's, of a stage
-    constexpr int HALF_B = HN * 128, B_AT = BM * 128, STAGE = stage_bytes<BM, BN>();
-    const uint32_t ring = lds_address(lds);
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) & 3);
-    const int lda = p.a.ld, ldb = p.b.ld;
-    const int a_left = p.M - m0, end = min(p.K, BK * stop);   // what is past `end` reads as zero
-
-    // ---- loads.  Of rows along k eight a load: unit (lane % 8) of row lane / 8,
-    // which holds k's unit `unit` & 3 of the term unit / 4
-    const int lhalf = wave >> 1;
-    uint32_t a_off[2], b_off[TB ? 2 : LPB];
-    int kc[2];
+// A wavefront's loads of a stage: of rows along k eight a load, LPA of A's and (B as N x
+// K) LPB of B's; of B as K x N 64 / W k rows a load, of one half of the tile's columns.
+template <int BM, int BN, bool TB>
+struct StageLoads {
+    static constexpr int BK = 32, HN = BN / 2, W = HN / 4;
+    static constexpr int LPA = BM / 32, LPB = BN / 32, LOADS = LPA + LPB;
+    static constexpr int HALF_B = HN * 128, B_AT = BM * 128;
+    uint32_t a_off[2], b_off[TB ? 2 : LPB], a_rows, b_rows, at_a, at_b;
+    int kc[2], lda, ldb, a_left, b_left, k_left;
+    size_t b_step;   // elements from a k to the next
+    const uint16_t *ap, *bp;
+    // of tile (m0, n0) of matrix m, from stage s0; what is past k `end` reads as zero
+    __device__ __forceinline__ StageLoads(const Operands &p, long long m, int m0, int n0, int s0, int end, int lane,
+                                          int wave)
+        : lda(p.a.ld), ldb(p.b.ld), a_left(p.M - m0), k_left(end - BK * s0)
+    {
+        const int lhalf = wave >> 1;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int unit = (lane & 7) ^ ((4 * q + (lane >> 4)) & 7);
-        kc[q] = 8 * (unit & 3);
-        a_off[q] = (uint32_t)((8 * (LPA * wave + q) + (lane >> 3)) * lda + 8 * unit) * 2u;
-        if (TB)
-            b_off[q] = (uint32_t)((8 * (LPB * wave + q) + (lane >> 3)) * ldb + 8 * unit) * 2u;
-    }
-    const uint32_t a_rows = (uint32_t)(16 * lda) * 2u, b_rows = (uint32_t)(16 * ldb) * 2u;
-    const int bcol = TB ? n0 : n0 + HN * lhalf, b_left = p.N - bcol;
-    if (!TB)
-#pragma unroll
-        for (int q = 0; q < LPB; ++q) {
-            const int k = (64 / W) * (LPB * (wave & 1) + q) + lane / W, u = (lane % W) ^ row_swizzle<W>(k);
-            b_off[TB ? 0 : q] = 32 * (u >> 3) + 8 * (u & 3) < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
+        for (int q = 0; q < 2; ++q) {
+            // unit (lane % 8) of row lane / 8 holds k's unit `unit` & 3 of the term unit / 4
+            const int unit = (lane & 7) ^ ((4 * q + (lane >> 4)) & 7);
+            kc[q] = 8 * (unit & 3);
+            a_off[q] = (uint32_t)((8 * (LPA * wave + q) + (lane >> 3)) * lda + 8 * unit) * 2u;
+            if (TB)
+                b_off[q] = (uint32_t)((8 * (LPB * wave + q) + (lane >> 3)) * ldb + 8 * unit) * 2u;
         }
-    const size_t b_step = TB ? 2 : (size_t)ldb;   // elements from a k to the next
-    const uint16_t *ap = p.a.p + m * p.a.matrix + (size_t)m0 * lda + (size_t)(2 * BK) * s0;
-    const uint16_t *bp = p.b.p + m * p.b.matrix + (TB ? (size_t)bcol * ldb : (size_t)(2 * bcol)) + BK * s0 * b_step;
-    int k_left = end - BK * s0;
-    uint32_t to = ring;   // the buffer that the next loads fill
-    const uint32_t at_a = (uint32_t)(LPA * wave * 1024);
-    const uint32_t at_b = (uint32_t)(B_AT + (TB ? LPB * wave * 1024 : lhalf * HALF_B + LPB * (wave & 1) * 1024));
-    struct Loads {
+        a_rows = (uint32_t)(16 * lda) * 2u, b_rows = (uint32_t)(16 * ldb) * 2u;
+        const int bcol = TB ? n0 : n0 + HN * lhalf;
+        b_left = p.N - bcol;
+        if (!TB)
+#pragma unroll
+            for (int q = 0; q < LPB; ++q) {
+                const int k = (64 / W) * (LPB * (wave & 1) + q) + lane / W;
+                const int u = (lane % W) ^ row_swizzle<(W < 16 ? W : 16)>(k);
+                b_off[TB ? 0 : q] = 32 * (u >> 3) + 8 * (u & 3) < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
+            }
+        b_step = TB ? 2 : (size_t)ldb;
+        ap = p.a.p + m * p.a.matrix + (size_t)m0 * lda + (size_t)(2 * BK) * s0;
+        bp = p.b.p + m * p.b.matrix + (TB ? (size_t)bcol * ldb : (size_t)(2 * bcol)) + BK * s0 * b_step;
+        at_a = (uint32_t)(LPA * wave * 1024);
+        at_b = (uint32_t)(B_AT + (TB ? LPB * wave * 1024 : lhalf * HALF_B + LPB * (wave & 1) * 1024));
+    }
+    struct Stage {
         intx4 a, b;
         int k_left;
-        uint32_t to;
     };
-    auto loads = [&]() {   // of the next stage
-        Loads L;
+    __device__ __forceinline__ Stage next()
+    {
+        Stage L;
         L.k_left = k_left;
-        L.to = to;
         L.a = rsrc_words(ap, 0);
         L.b = rsrc_words(bp, 0);
         L.a.z = k_left <= 0 ? 0 : (a_left >= BM ? 0x7fffffff : (a_left - 1) * lda * 2 + 128);
@@ -345,52 +339,100 @@ __device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t
         ap += 2 * BK;
         bp += BK * b_step;
         k_left -= BK;
-        to = to == ring + (uint32_t)((NB - 1) * STAGE) ? ring : to + STAGE;
         return L;
-    };
-    auto load = [&](const Loads &L, int i) {   // load i of the stage
+    }
+    // load i of a stage, into the buffer at the LDS address `to`
+    __device__ __forceinline__ void load(const Stage &L, uint32_t to, int i) const
+    {
         if (i < LPA)
-            load_to_lds(L.a, L.to + at_a + (uint32_t)(i * 1024),
+            load_to_lds(L.a, to + at_a + (uint32_t)(i * 1024),
                         kc[i & 1] >= L.k_left ? kOutside : a_off[i & 1] + (uint32_t)(i >> 1) * a_rows);
         else if (TB)
-            load_to_lds(L.b, L.to + at_b + (uint32_t)((i - LPA) * 1024),
+            load_to_lds(L.b, to + at_b + (uint32_t)((i - LPA) * 1024),
                         kc[i & 1] >= L.k_left ? kOutside : b_off[(i - LPA) & 1] + (uint32_t)((i - LPA) >> 1) * b_rows);
         else
-            load_to_lds(L.b, L.to + at_b + (uint32_t)((i - LPA) * 1024), b_off[TB ? 0 : i - LPA]);
-    };
+            load_to_lds(L.b, to + at_b + (uint32_t)((i - LPA) * 1024), b_off[TB ? 0 : i - LPA]);
+    }
     static_assert(LPA % 2 == 0 && LPB % 2 == 0, "");
+};
 
-    // ---- fragments.  Lane (g, s) = (lane / 16, lane % 16): k 8 g .. 8 g + 7 of
-    // row s of A's block and column s of B's
-    const int s16 = lane & 15, g = lane >> 4;
-    const uint32_t row_lane = (uint32_t)(s16 * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
-    const uint32_t a_lane = row_lane + (uint32_t)((wave >> 1) * HM * 128);
-    const int kr = 8 * g + (s16 >> 2);
-    const uint32_t b_lane = (uint32_t)B_AT + (TB ? row_lane + (uint32_t)((wave & 1) * HN * 128)
-                                                 : (uint32_t)(kr * (W * 16) + 8 * (s16 & 1) + (wave & 1) * HALF_B));
-    uint32_t b_unit[TB ? 1 : FB];   // of the higher terms; the lower ones are four units on
-    if (!TB)
+// Where a lane's fragments begin in a stage buffer.  Lane (g, s) = (lane / 16, lane %
+// 16): k 8 g .. 8 g + 7 of row s of A's block and column s of B's.
+template <int BM, int BN, bool TB>
+struct StageLanes {
+    static constexpr int HM = BM / 2, HN = BN / 2, W = HN / 4;
+    static constexpr int UNITS = HN / 16 < 4 ? HN / 16 : 4;   // B's blocks from the fifth on are sixteen units on
+    uint32_t a, b, b_unit[TB ? 1 : UNITS];   // b_unit: of the higher terms; the lower ones are four units on
+    __device__ __forceinline__ StageLanes(int lane, int wave)
+    {
+        const int s16 = lane & 15, g = lane >> 4, kr = 8 * g + (s16 >> 2);
+        const uint32_t row = (uint32_t)(s16 * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
+        a = row + (uint32_t)((wave >> 1) * HM * 128);
+        b = (uint32_t)(BM * 128) + (TB ? row + (uint32_t)((wave & 1) * HN * 128)
+                                       : (uint32_t)(kr * (W * 16) + 8 * (s16 & 1) + (wave & 1) * HN * 128));
+        if (!TB)
 #pragma unroll
-        for (int j = 0; j < FB; ++j)
-            b_unit[TB ? 0 : j] = (uint32_t)(((8 * (j >> 1) + 2 * (j & 1) + ((s16 & 3) >> 1)) ^ row_swizzle<W>(kr)) * 16);
-    auto read_b = [&](uint32_t at, int j, int term) -> halfx8 {
+            for (int j = 0; j < UNITS; ++j)
+                b_unit[TB ? 0 : j] = (uint32_t)(
+                    ((8 * (j >> 1) + 2 * (j & 1) + ((s16 & 3) >> 1)) ^ row_swizzle<(W < 16 ? W : 16)>(kr)) * 16);
+    }
+    // term of A's block i and B's block j, of the buffer at byte `at`
+    __device__ __forceinline__ halfx8 read_a(const uint8_t *lds, uint32_t at, int i, int term) const
+    {
+        return *reinterpret_cast<const halfx8 *>(lds + ((a ^ (uint32_t)(64 * term)) + (at + (uint32_t)(i * 2048))));
+    }
+    __device__ __forceinline__ halfx8 read_b(const uint8_t *lds, uint32_t at, int j, int term) const
+    {
         if (TB)
-            return *reinterpret_cast<const halfx8 *>(lds + at + ((b_lane ^ (uint32_t)(64 * term)) + (uint32_t)(j * 2048)));
-        const uint8_t *q = lds + at + b_lane + (b_unit[TB ? 0 : j] ^ (uint32_t)(64 * term));
+            return *reinterpret_cast<const halfx8 *>(lds + ((b ^ (uint32_t)(64 * term)) + (at + (uint32_t)(j * 2048))));
+        const uint8_t *q = lds + (b + (b_unit[TB ? 0 : j & (UNITS - 1)] ^ (uint32_t)(64 * term)) +
+                                  (at + (uint32_t)(j / UNITS * 256)));
         const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
         const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * (W * 16)));
         return __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// `steps` stages from s0, those from `stop` on zeros, by the four wavefronts of
+// one of the workgroup's groups; `lds` is the group's.  LOW: the cross products
+// have sums of their own, `low`, to which the lower terms' products belong too.  Each
+// MFMA rounds its sum four times, and the higher terms' sum is then rounded by a
+// third as many.
+template <int BM, int BN, int NB, bool TB, bool LOW>
+__device__ __forceinline__ void pair_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
+                                         int stop, int steps, floatx4 (&acc)[BM / 32][BN / 32],
+                                         floatx4 (&low)[LOW ? BM / 32 : 1][LOW ? BN / 32 : 1])
+{
+    constexpr int BK = 32, FA = BM / 32, FB = BN / 32;
+    constexpr int STAGE = stage_bytes<BM, BN>();
+    typedef StageLoads<BM, BN, TB> From;
+    constexpr int LOADS = From::LOADS;   // a wavefront's, of a stage
+    const uint32_t ring = lds_address(lds);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) & 3);
+    From from(p, m, m0, n0, s0, min(p.K, BK * stop), lane, wave);
+    const StageLanes<BM, BN, TB> lanes(lane, wave);
+    uint32_t to = ring;   // the buffer that the next loads fill
+    struct Loads {
+        typename From::Stage stage;
+        uint32_t to;
     };
+    auto loads = [&]() {   // of the next stage
+        const Loads L{from.next(), to};
+        to = to == ring + (uint32_t)((NB - 1) * STAGE) ? ring : to + STAGE;
+        return L;
+    };
+    auto load = [&](const Loads &L, int i) { from.load(L.stage, L.to, i); };   // load i of the stage
+
     struct Fragments {
         halfx8 a[2][FA], b[2][FB];
     };
     constexpr int READS = 2 * (FA + FB);
     auto read = [&](uint32_t at, int r, Fragments &f) {   // read r of the stage in the buffer at `at`
         if (r < 2 * FA)
-            f.a[r / FA][r % FA] = *reinterpret_cast<const halfx8 *>(
-                lds + at + ((a_lane ^ (uint32_t)(64 * (r / FA))) + (uint32_t)((r % FA) * 2048)));
+            f.a[r / FA][r % FA] = lanes.read_a(lds, at, r % FA, r / FA);
         else
-            f.b[(r - 2 * FA) / FB][(r - 2 * FA) % FB] = read_b(at, (r - 2 * FA) % FB, (r - 2 * FA) / FB);
+            f.b[(r - 2 * FA) / FB][(r - 2 * FA) % FB] = lanes.read_b(lds, at, (r - 2 * FA) % FB, (r - 2 * FA) / FB);
     };
 
 #pragma unroll
@@ -476,100 +518,26 @@ template <bool TB>
 __device__ __forceinline__ void quad_sum(const Operands &p, long long m, uint8_t *lds, int m0, int n0, int s0,
                                          int steps, floatx4 (&acc)[8][8])
 {
-    constexpr int BK = 32, SIDE = 256, HALF = 128, LP = SIDE / 32;
-    constexpr int HALF_B = HALF * 128, B_AT = SIDE * 128, STAGE = stage_bytes<SIDE, SIDE>();
+    constexpr int BK = 32, SIDE = 256, STAGE = stage_bytes<SIDE, SIDE>();
+    typedef StageLoads<SIDE, SIDE, TB> From;
     const uint32_t ring = lds_address(lds);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int lda = p.a.ld, ldb = p.b.ld;
-    const int a_left = p.M - m0, end = min(p.K, BK * (s0 + steps));
-
-    // ---- loads, as in pair_sum
-    const int lhalf = wave >> 1;
-    uint32_t a_off[2], b_off[TB ? 2 : LP];
-    int kc[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int unit = (lane & 7) ^ ((4 * q + (lane >> 4)) & 7), row = 8 * (LP * wave + q) + (lane >> 3);
-        kc[q] = 8 * (unit & 3);
-        a_off[q] = (uint32_t)(row * lda + 8 * unit) * 2u;
-        if (TB)
-            b_off[q] = (uint32_t)(row * ldb + 8 * unit) * 2u;
-    }
-    const uint32_t a_rows = (uint32_t)(16 * lda) * 2u, b_rows = (uint32_t)(16 * ldb) * 2u;
-    const int bcol = TB ? n0 : n0 + HALF * lhalf, b_left = p.N - bcol;
-    if (!TB)
-#pragma unroll
-        for (int q = 0; q < LP; ++q) {
-            const int k = 2 * (LP * (wave & 1) + q) + (lane >> 5), u = (lane & 31) ^ row_swizzle<16>(k);
-            b_off[TB ? 0 : q] = 32 * (u >> 3) + 8 * (u & 3) < b_left ? (uint32_t)(k * ldb + 8 * u) * 2u : kOutside;
-        }
-    const size_t b_step = TB ? 2 : (size_t)ldb;
-    const uint16_t *ap = p.a.p + m * p.a.matrix + (size_t)m0 * lda + (size_t)(2 * BK) * s0;
-    const uint16_t *bp = p.b.p + m * p.b.matrix + (TB ? (size_t)bcol * ldb : (size_t)(2 * bcol)) + BK * s0 * b_step;
-    int k_left = end - BK * s0;
-    const uint32_t at_a = ring + (uint32_t)(LP * wave * 1024);
-    const uint32_t at_b = ring + (uint32_t)(B_AT + (TB ? LP * wave * 1024 : lhalf * HALF_B + LP * (wave & 1) * 1024));
-    struct Loads {
-        intx4 a, b;
-        int k_left;
-    };
-    auto loads = [&]() {
-        Loads L;
-        L.k_left = k_left;
-        L.a = rsrc_words(ap, 0);
-        L.b = rsrc_words(bp, 0);
-        L.a.z = k_left <= 0 ? 0 : (a_left >= SIDE ? 0x7fffffff : (a_left - 1) * lda * 2 + 128);
-        if (TB)
-            L.b.z = k_left <= 0 ? 0 : (b_left >= SIDE ? 0x7fffffff : (b_left - 1) * ldb * 2 + 128);
-        else
-            L.b.z = k_left >= BK || b_left <= 0 ? 0x7fffffff
-                                                : (k_left <= 0 ? 0 : (k_left - 1) * ldb * 2 + 4 * ((b_left + 31) & ~31));
-        ap += 2 * BK;
-        bp += BK * b_step;
-        k_left -= BK;
-        return L;
-    };
-    auto load = [&](const Loads &L, int buffer, int i) {
-        const uint32_t to = (uint32_t)(buffer * STAGE + (i % LP) * 1024);
-        if (i < LP)
-            load_to_lds(L.a, at_a + to, kc[i & 1] >= L.k_left ? kOutside : a_off[i & 1] + (uint32_t)(i >> 1) * a_rows);
-        else if (TB)
-            load_to_lds(L.b, at_b + to,
-                        kc[i & 1] >= L.k_left ? kOutside : b_off[i & 1] + (uint32_t)((i - LP) >> 1) * b_rows);
-        else
-            load_to_lds(L.b, at_b + to, b_off[TB ? 0 : i - LP]);
+    From from(p, m, m0, n0, s0, min(p.K, BK * (s0 + steps)), lane, wave);
+    const StageLanes<SIDE, SIDE, TB> lanes(lane, wave);
+    auto load = [&](const typename From::Stage &L, int buffer, int i) {
+        from.load(L, ring + (uint32_t)(buffer * STAGE), i);
     };
 
-    // ---- fragments, as in pair_sum; half h of A's and B's blocks is four
-    const int s16 = lane & 15, g = lane >> 4;
-    const uint32_t row_lane = (uint32_t)(s16 * 128) | (uint32_t)((g ^ ((s16 >> 1) & 7)) * 16);
-    const uint32_t a_lane = row_lane + (uint32_t)((wave >> 1) * HALF * 128);
-    const int kr = 8 * g + (s16 >> 2);
-    const uint32_t b_lane = (uint32_t)B_AT + (TB ? row_lane + (uint32_t)((wave & 1) * HALF * 128)
-                                                 : (uint32_t)(kr * 512 + 8 * (s16 & 1) + (wave & 1) * HALF_B));
-    uint32_t b_unit[TB ? 1 : 4];   // of blocks 0 to 3; 4 to 7 are sixteen units on
-    if (!TB)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            b_unit[TB ? 0 : j] = (uint32_t)(((8 * (j >> 1) + 2 * (j & 1) + ((s16 & 3) >> 1)) ^ row_swizzle<16>(kr)) * 16);
+    // fragments; half h of A's and B's blocks is four
     halfx8 fa[2][8], fb[2][8];
     auto read_a = [&](int buffer, int h, int r) {   // read r of 8 of A's half h
         const int t = r >> 2, i = 4 * h + (r & 3);
-        fa[t][i] = *reinterpret_cast<const halfx8 *>(
-            lds + ((a_lane ^ (uint32_t)(64 * t)) + (uint32_t)(buffer * STAGE + i * 2048)));
+        fa[t][i] = lanes.read_a(lds, (uint32_t)(buffer * STAGE), i, t);
     };
     auto read_b = [&](int buffer, int h, int r) {
         const int t = r >> 2, j = 4 * h + (r & 3);
-        if (TB) {
-            fb[t][j] = *reinterpret_cast<const halfx8 *>(
-                lds + ((b_lane ^ (uint32_t)(64 * t)) + (uint32_t)(buffer * STAGE + j * 2048)));
-            return;
-        }
-        const uint8_t *q = lds + (b_lane + (b_unit[TB ? 0 : j & 3] ^ (uint32_t)(64 * t)) + (uint32_t)(buffer * STAGE + (j >> 2) * 256));
-        const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)q);
-        const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(q + 4 * 512));
-        fb[t][j] = __builtin_bit_cast(halfx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        fb[t][j] = lanes.read_b(lds, (uint32_t)(buffer * STAGE), j, t);
     };
 
 #pragma unroll
@@ -603,7 +571,7 @@ __device__ __forceinline__ void quad_sum(const Operands &p, long long m, uint8_t
         // everyone's
         __builtin_amdgcn_s_waitcnt(wait_vmcnt_lgkm0(0));
         __builtin_amdgcn_s_barrier();
-        const Loads L = loads();
+        const auto L = from.next();
         __builtin_amdgcn_sched_barrier(0);
         quadrant(1, o, [&](int r) { read_a(o, 0, r); }, [&](int l) { load(L, parity, l); });
         quadrant(1, f, [&](int r) { read_b(o, o, r); }, [&](int l) { load(L, parity, 8 + l); });
@@ -611,12 +579,12 @@ __device__ __forceinline__ void quad_sum(const Operands &p, long long m, uint8_t
 
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-        const Loads L = loads();
+        const auto L = from.next();
 #pragma unroll
-        for (int i = 0; i < 2 * LP; ++i)
+        for (int i = 0; i < From::LOADS; ++i)
             load(L, st, i);
     }
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * LP));
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(From::LOADS));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
