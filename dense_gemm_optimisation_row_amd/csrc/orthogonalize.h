@@ -43,10 +43,10 @@ struct Way {
 
 // Microseconds of a tile: its ends (with A's part in the polynomial's), and each
 // stage, where up to 64 compute units work and where 192 and more do (between them
-// in between: 136 tiles of 256 x 256 take 2.0).  From 1 to 2080 tiles and
-// sums of 256 to 4096 (128 x 256 to 4096 x 4096, batches of 1 to 8); over those what
-// is chosen takes at most 1.15 times the shortest of the three tiles, with and
-// without runs.
+// in between: 136 tiles of 256 x 256 take 2.0).  Over 102 products (129 to 4096 rows,
+// sums of 128 to 8192, batches of 1 to 30) what is chosen is the shortest of the three
+// tiles, with and without runs, for 95, at most 1.12 times it for 100, and 1.22 and 1.19
+// times for two long sums in few 64 x 64 tiles, which runs do not shorten.
 struct TileCost {
     Tile tile;
     double ends, polynomial, few, all;
