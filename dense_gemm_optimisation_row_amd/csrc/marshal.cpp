@@ -8,6 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <ATen/ATen.h>
 #include <ATen/core/grad_mode.h>
+#include <pybind11/gil.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -60,7 +61,7 @@ struct Form {
     uintptr_t entry;
     int64_t workspace;        // bytes; -1: the entry point takes none
 };
-std::unordered_multimap<uint64_t, std::unique_ptr<Form>> forms;
+std::unordered_multimap<uint64_t, std::shared_ptr<Form>> forms;   // under the interpreter's lock
 
 // The key of a call; false where it is not one for here: another kind of tensor,
 // or one that requires grad where torch records gradients (layers.py refuses it).
@@ -112,12 +113,12 @@ bool unpack(PyObject *tensors, PyObject *extra, const at::Tensor *(&found)[16])
     return true;
 }
 
-Form *find(const Key &k)
+std::shared_ptr<Form> find(const Key &k)
 {
     const auto range = forms.equal_range(k.hash());
     for (auto it = range.first; it != range.second; ++it)
         if ((int)it->second->key.size() == k.n && memcmp(it->second->key.data(), k.v, sizeof(int64_t) * k.n) == 0)
-            return it->second.get();
+            return it->second;
     return nullptr;
 }
 
@@ -151,7 +152,7 @@ PyObject *keep(PyObject *, PyObject *args)
     if (!unpack(tensors, extra, found))
         return nullptr;
     Key k;
-    auto f = std::make_unique<Form>();
+    auto f = std::make_shared<Form>();
     const Py_ssize_t n = PyTuple_Size(slots), outs = PyTuple_Size(outputs);
     const int total = 1 + (int)n + (workspace >= 0 ? 2 : 0) + 1;
     if (n < 0 || outs < 0 || (total != 5 && total != 11)) {
@@ -220,9 +221,12 @@ PyObject *run(PyObject *, PyObject *const *args, Py_ssize_t nargs)
             return nullptr;
         Py_RETURN_NONE;
     }
-    Form *f = find(k);
+    const std::shared_ptr<Form> f = find(k);   // held, should another thread drop the forms
     if (!f)
         Py_RETURN_NONE;
+    const uintptr_t stream = (uintptr_t)PyLong_AsUnsignedLongLong(args[4]);
+    if (PyErr_Occurred())
+        return nullptr;
     const auto options = at::TensorOptions().device(at::Device(at::kCUDA, (c10::DeviceIndex)device));
     at::Tensor made[4], space;
     const at::Tensor *out[4];
@@ -231,29 +235,33 @@ PyObject *run(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         PyErr_SetString(PyExc_ValueError, "too many outputs");
         return nullptr;
     }
-    for (int i = 0; i < outs; ++i) {
-        const Output &o = f->outputs[i];
-        if (o.given < 0)
-            made[i] = at::empty(o.sizes, options.dtype(o.type));
-        out[i] = o.given < 0 ? &made[i] : found[o.given];
+    int rc;
+    {
+        // without the lock, as torch's and ctypes' calls: an allocation or a launch may
+        // wait for the GPU, and that for another thread.  The caller holds the tensors.
+        pybind11::gil_scoped_release unlocked;
+        for (int i = 0; i < outs; ++i) {
+            const Output &o = f->outputs[i];
+            if (o.given < 0)
+                made[i] = at::empty(o.sizes, options.dtype(o.type));
+            out[i] = o.given < 0 ? &made[i] : found[o.given];
+        }
+        uintptr_t a[kMostPointers + 4];
+        int n = 0;
+        a[n++] = (uintptr_t)f->params.data();
+        for (const int s : f->slots) {
+            const at::Tensor *t = s >= 0 ? found[s] : out[-1 - s];
+            a[n++] = t ? (uintptr_t)t->data_ptr() : 0;
+        }
+        if (f->workspace >= 0) {
+            if (f->workspace > 0)
+                space = at::empty({f->workspace}, options.dtype(at::kByte));
+            a[n++] = f->workspace > 0 ? (uintptr_t)space.data_ptr() : 0;
+            a[n++] = (uintptr_t)f->workspace;
+        }
+        a[n++] = stream;
+        rc = call(f->entry, a, n);
     }
-    uintptr_t a[kMostPointers + 4];
-    int n = 0;
-    a[n++] = (uintptr_t)f->params.data();
-    for (const int s : f->slots) {
-        const at::Tensor *t = s >= 0 ? found[s] : out[-1 - s];
-        a[n++] = t ? (uintptr_t)t->data_ptr() : 0;
-    }
-    if (f->workspace >= 0) {
-        if (f->workspace > 0)
-            space = at::empty({f->workspace}, options.dtype(at::kByte));
-        a[n++] = f->workspace > 0 ? (uintptr_t)space.data_ptr() : 0;
-        a[n++] = (uintptr_t)f->workspace;
-    }
-    a[n++] = (uintptr_t)PyLong_AsUnsignedLongLong(args[4]);
-    if (PyErr_Occurred())
-        return nullptr;
-    const int rc = call(f->entry, a, n);
     if (rc != 0)
         return PyLong_FromLong(rc);
     if (outs == 1)
