@@ -4,7 +4,7 @@
 // point.  A form is made, checked and kept by layers.py; what is not known here is
 // left to it.  Nothing of a tensor is kept, neither its address nor its identity.
 //
-// In Python a call of six tensors takes 9.2 us, 3.4 of them the launch.
+// In Python a call of six tensors takes 8.0 us, so 4.5, of which the launch is 2.6.
 #define PY_SSIZE_T_CLEAN
 #include <ATen/ATen.h>
 #include <ATen/core/grad_mode.h>

@@ -8,10 +8,13 @@
 // Precision.  A step multiplies small singular values by a, five by 485, so what
 // is rounded off X at the start grows by that against directions that grow less:
 // operands rounded to 16 bits once leave errors of 2^-9 and more in the result.
-// So each operand is two binary16 terms, hi + lo, and a product three on the matrix
-// cores, hi hi + lo hi + hi lo (lo lo is below the terms' own error): 22 to 23
-// bits at a third of the 16-bit rate, five times the FP32 one.  Terms are held at a
-// power of two: the coefficients bound the singular values of each step on the
+// So each operand is two binary16 terms, hi + lo, which hold a value to 2^-23 (FP32
+// would to 2^-24), and a product three on the matrix cores, hi hi + lo hi + hi lo, at a
+// third of the 16-bit rate, five times the FP32 one; lo lo, at most 2^-22 of a product,
+// is added where the sums are of few.  Over 160 sizes the result's error is 0.61 times
+// that of FP32 products at the median and 1.03 times at most, up to 1.23 times where the
+// directions fall off as 1 / k; a third term would take twice the products.  Terms are
+// held at a power of two: the coefficients bound the singular values of each step on the
 // host, so X, A and P have scales at which no entry overflows, and entries down to
 // 2^-16 of the bound keep all bits, smaller ones are off by at most 2^-39 of it.  The Gram
 // matrix alone would do for long rows (P's products applied to X once), but its

@@ -589,7 +589,7 @@ def _layer_norm_backward_form(dy, x, weight, mean, rstd, need_weight, dx, dweigh
 # --------------------------------------------- calls of forms seen before --
 #
 # The kernels of a few rows on 8-bit operands take 3 to 5 us, less than a call's
-# checks, allocations and marshalling in Python (8 to 9 us with the launch): the
+# checks, allocations and marshalling in Python (7 to 8 us with the launch): the
 # extension module does these for a form that a call in Python has made and kept.
 
 _marshal = None   # the module; False where there is none
@@ -609,7 +609,7 @@ def _again(op, stem, tensors, extra):
             from . import _marshal as module
         except ImportError as e:
             module = False
-            warnings.warn(f"calls of quantize_i8, linear_i8 and gated_i8 take 3 to 4 us longer without the extension "
+            warnings.warn(f"calls of quantize_i8, linear_i8 and gated_i8 take about 3 us longer without the extension "
                           f"module _marshal.so ({e}): `python -m dense_gemm_optimisation_row_amd.build` makes it",
                           RuntimeWarning)
         _marshal = module

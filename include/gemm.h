@@ -592,7 +592,7 @@ int gemm_gated_i8_bf16(const gemm_gated_i8_params *params, const int8_t *X, cons
  * stride_o elements from a matrix to the next (read only where batch > 1).  Matrices
  * of a stack may lie between each other's rows (the heads of one weight); those of O
  * that share an element -> GEMM_ERR_INVALID_LAYOUT.  O may be G itself (same
- * pointer, op and strides).  A matrix of zeros gives zeros; one
+ * pointer, op and strides) and shares nothing with it otherwise.  A matrix of zeros gives zeros; one
  * with a NaN or an infinity NaN.  steps outside [1, GEMM_MAX_STEPS] or eps
  * negative or NaN -> GEMM_ERR_INVALID_DIM; coefficients that are not finite, or
  * whose steps let a singular value of at most 1, or what multiplies it, grow past
