@@ -24,7 +24,7 @@ def kept(op, seconds):
 
 
 def test_other_threads_run_while_a_call_waits():
-    kept(1000, 0.5)
+    kept(1000, 2.0)
     assert marshal.run(1001, NOTHING, (), 0, 0) is None      # of no such form
     done = threading.Event()
     t = threading.Thread(target=lambda: (marshal.run(1000, NOTHING, (), 0, 0), done.set()))
@@ -32,7 +32,7 @@ def test_other_threads_run_while_a_call_waits():
     t.start()
     while time.perf_counter() - start < 0.1:
         time.sleep(0.001)
-    waiting = not done.is_set() and time.perf_counter() - start < 0.4
+    waiting = not done.is_set() and time.perf_counter() - start < 1.5
     t.join()
     assert waiting, "the interpreter stood still during the call"
 
